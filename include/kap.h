@@ -62,6 +62,20 @@ typedef struct {
   float *k_summary;     /* [num_pages][Hkv][d] fp32 block-mean keys (K-summary cache); may be NULL if unused */
 } kap_kv_pool;
 
+/* A pool with packed pages beside its 16-bit ones. Physical page ids below pool.num_pages name 16-bit pages (bf16),
+ * ids num_pages + j name packed page j, so one block table or view mixes both and every call that only moves ids
+ * (views, slot mappings, tables) takes it as it is. A packed page holds K and V in 4 bits: for nb = head_dim / 64
+ * blocks of 64 dims, the chunk of one (page, KV head) is
+ *   K codes [nb][16 tokens][32 bytes], V codes alike, K params [nb][16][2] bf16, V params alike,
+ * kap_packed_chunk_bytes(head_dim) = 1152 * nb bytes. Byte b of a token's block holds dim 2b in its low and dim 2b + 1
+ * in its high four bits; params are (scale, lowest value) and code c stands for lowest + scale * c. */
+typedef struct {
+  kap_kv_pool pool;   /* the 16-bit pages; dtype must be KAP_BF16. k_summary, when given, has
+                         num_pages + num_packed rows, one per physical page id */
+  int32_t num_packed; /* packed pages (0 or more) */
+  void *packed;       /* [num_packed][Hkv][kap_packed_chunk_bytes(head_dim)], 16-byte aligned */
+} kap_packed_pool;
+
 /* Page map M and lengths. Logical page j of request r covers positions 16j .. 16j+15. */
 typedef struct {
   int32_t num_seqs;           /* R */
@@ -329,6 +343,100 @@ size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
 kap_status kap_attn_propose_noalloc(const kap_kv_pool *pool, const kap_page_map *map, const kap_view *view,
                                     const void *q_dev, void *out, float *lse, kap_stream stream);
 size_t kap_noalloc_scratch_bytes(void);
+
+/* ---------------------------------------------------------------------------------------------------------
+ * Packed pages. The pages describe caches of 16-bit keys and values only; what they do describe is that decode is bound
+ * by the bytes of the KV it reads (KAP paper, cost model), which packing divides by 3.6.
+ *
+ * Packing: for each i < num_listed, 16-bit page src_pages_dev[i] becomes packed page dst_pages_dev[i] (both physical
+ * ids, dst >= pool.num_pages). Every group of 64 dims of one token, KV head and tensor is coded by itself:
+ *   lowest = min x;  scale = the least bf16 number that is not below (max x - min x) / 15;
+ *   code = (x - lowest) / scale rounded to nearest, ties to even (0 when scale is 0),
+ * decided exactly, with no rounding in between. A group that holds an infinity or a NaN reads back as NaN
+ * throughout. All 16 token rows are packed, whatever the page's length. When k_summary is
+ * given, the source page's summary is copied to the destination's row, so that routing scores stay as they were.
+ * Unpacking: packed page src_pages_dev[i] to 16-bit page dst_pages_dev[i]: each element is lowest + scale * code in
+ * fp32 (one rounding), then rounded to bf16; the summary is copied back.
+ * Source and destination lists have num_listed int32 entries on the device; destinations must be distinct.
+ * Errors: KAP_EINVAL for null or misaligned pointers or a negative count; KAP_EUNSUPPORTED for an fp32 pool. An id
+ * outside its pool is skipped and sets device error bit 1. */
+size_t kap_packed_chunk_bytes(int32_t head_dim);
+kap_status kap_pack_pages(const kap_packed_pool *pool, const int32_t *src_pages_dev, const int32_t *dst_pages_dev,
+                          int32_t num_listed, kap_stream stream);
+kap_status kap_unpack_pages(const kap_packed_pool *pool, const int32_t *src_pages_dev, const int32_t *dst_pages_dev,
+                            int32_t num_listed, kap_stream stream);
+
+/* Attention over a pool with packed pages: kap_attn_propose and kap_attn_verify with the same arguments, visibility
+ * rules and outputs, over pages of both kinds. Keys and values are those that the codes stand for (lowest + scale *
+ * code, not rounded); sums and softmax statistics are fp32, probabilities enter the product with the values as fp16
+ * (packed pages) or as two bf16 terms (16-bit pages). The value scales of one (request, KV head) should span less than
+ * a factor of 2^20: a packed token whose probability times scale is 2^-20 of the largest scale or less loses bits.
+ * Every group size G in 1..8 is supported. kap_view.settled is not read. A hidden or skipped token adds nothing,
+ * whatever its codes, parameters or 16-bit values hold. A query row that sees no token gets zeros and lse -infinity
+ * (and, for the proposal, device error bit 4).
+ *   workspace >= kap_packed_workspace_size(R, Hkv, Hq, d, max_q) bytes (max_q = 1 for the proposal), zero-filled once
+ *   before first use; the kernels leave its counters at zero. Calls that may run at the same time, captured graphs
+ *   among them, need a workspace each. */
+kap_status kap_attn_propose_packed(const kap_packed_pool *pool, const kap_page_map *map, const kap_view *view,
+                                   const void *q_dev, void *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, kap_stream stream);
+kap_status kap_attn_verify_packed(const kap_packed_pool *pool, const kap_page_map *map, const kap_verify_policy *vp,
+                                  const void *q_dev, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                  kap_stream stream);
+size_t kap_packed_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
+                                 int32_t max_q);
+
+/* Log probabilities of given tokens, beside the acceptance of verify windows: how sure the verifier is of each token,
+ * which kap_accept_commit reduces to a yes or no. For each row of logits x over the vocabulary, in fp32:
+ *   lse = log sum exp x;  logprob_out = x[token] - lse;  entropy_out = -sum p log p with p = exp(x - lse);
+ *   rank_out = how many tokens come before the given one (kap_accept_commit's order: logit descending, lower token id
+ *   first, NaN last);  top_ids, top_logprobs [rows][top_n] = the first top_n tokens of that order.
+ * logits_dev [rows] rows of `vocab` values (KAP_BF16 or KAP_F32), row_stride elements apart, at any element alignment;
+ * tokens_dev [rows] int32. entropy_out and rank_out may be NULL; top_ids and top_logprobs are used when top_n > 0.
+ * A logit of -infinity has probability 0 and adds nothing. A row with a NaN or +infinity, or with -infinity
+ * throughout, has no distribution: its log probabilities and entropy are NaN, ranks and ids hold. A token outside
+ * [0, vocab) gets -infinity and rank vocab.
+ *   workspace >= kap_logprobs_workspace_size(rows, vocab) bytes, zero-filled once before first use; the call leaves its
+ *   counters at zero. Calls that may run at the same time need a workspace each.
+ * Errors: KAP_EINVAL for null pointers, rows < 0, vocab < 1, row_stride < vocab, top_n outside [0, min(32, vocab)];
+ * KAP_EUNSUPPORTED for another dtype or vocab > 2^24; KAP_ECAPACITY for a small workspace. */
+kap_status kap_token_logprobs(const void *logits_dev, int32_t logits_dtype, int32_t vocab, int64_t row_stride,
+                              int32_t rows, const int32_t *tokens_dev, int32_t top_n, float *logprob_out,
+                              float *entropy_out, int32_t *rank_out, int32_t *top_ids, float *top_logprobs,
+                              void *workspace, size_t workspace_bytes, kap_stream stream);
+size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab);
+
+/* Block tables and slot maps from request lengths. KAP paper, compiler and executor (block tables and slot mappings
+ * are plan objects of fixed shape): the tables grow and the slots of a step are found on the device, from the lengths
+ * and a stack of free pages (free_pages[0 .. free_count-1], its top last), without a copy to the host.
+ *
+ * kap_extend_tables: request r holds seq_len[r] tokens on the first ceil(seq_len / 16) entries of its block_table row
+ * and takes new_tokens[r] more. Requests are served in order: with need[r] the new pages that r wants, r is granted
+ * when need[r] is 0 or the needs of all requests up to and including r fit free_count. A granted request's new entries
+ * are written, in page order, from the stack's top down; a request that wants a row longer than max_pages counts as
+ * need 0, is not granted and sets device error bit 2.
+ *   tok_offsets [R+1] = exclusive sums of new_tokens; token tok_offsets[r] + i sits at pos_out = seq_len[r] + i and, when
+ *   r is granted, at slot_out = page * 16 + pos % 16 (-1 when not granted or when its page is negative). Tokens past
+ *   max_tokens are not written (device error bit 2); entries of slot_out and pos_out past the last token are left as
+ *   they are. seq_len_out[r] = seq_len[r] + new_tokens[r] when granted, else seq_len[r]; granted_out[r] = 1 or 0;
+ *   free_count_out = free_count less the pages taken.
+ * kap_release_tables: the pages of every request with released[r] != 0 (the first ceil(seq_len / 16) entries of its row)
+ * are pushed on the stack in request and then page order; seq_len_out[r] = 0 for these and seq_len[r] for the others;
+ * free_count_out = free_count plus the pages pushed. Pages past free_capacity are dropped (device error bit 2). The
+ * rows themselves are left as they are.
+ * Output arrays must not alias the inputs (seq_len_out, free_count_out). A negative length or count counts as 0 and a
+ * free_count past free_capacity as free_capacity (device error bits 4 and 2). All arrays are int32 on the device,
+ * slot_out is int64. Errors: KAP_EINVAL for null pointers, num_seqs or max_pages < 1, negative capacities or aliased
+ * outputs. */
+kap_status kap_extend_tables(int32_t num_seqs, int32_t max_pages, int32_t *block_table, const int32_t *seq_len,
+                             const int32_t *new_tokens, const int32_t *free_pages, int32_t free_capacity,
+                             const int32_t *free_count, int32_t *free_count_out, int32_t *tok_offsets,
+                             int64_t *slot_out, int32_t *pos_out, int32_t max_tokens, int32_t *seq_len_out,
+                             int32_t *granted_out, kap_stream stream);
+kap_status kap_release_tables(int32_t num_seqs, int32_t max_pages, const int32_t *block_table,
+                              const int32_t *seq_len, const int32_t *released, int32_t *free_pages,
+                              int32_t free_capacity, const int32_t *free_count, int32_t *free_count_out,
+                              int32_t *seq_len_out, kap_stream stream);
 
 /* Check of the bounded waits. Every wait of a kernel on an mbarrier (a copy landing, a slot freed, an MMA done)
  * gives up after at most about a second, sets bit 8 of the device error word and lets the kernel return, so that a

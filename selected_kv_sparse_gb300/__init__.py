@@ -14,4 +14,9 @@ from ._binding import (  # noqa: F401
 from ._binding import kap_append_propose, kap_attn_propose_noalloc, kap_noalloc_scratch_bytes  # noqa: F401
 from ._binding import kap_accept_commit, kap_accept_workspace_size, kap_materialize_view, kap_prior_topk  # noqa: F401
 from ._binding import kap_refresh_summaries, kap_score_topk_view, kap_selftest_wait_timeout  # noqa: F401
+from ._binding import (  # noqa: F401
+    PackedPool, kap_attn_propose_packed, kap_attn_verify_packed, kap_extend_tables, kap_logprobs_workspace_size,
+    kap_pack_pages, kap_packed_chunk_bytes, kap_packed_workspace_size, kap_release_tables, kap_token_logprobs,
+    kap_unpack_pages,
+)
 from .pipeline import DecodeCycle, DecodeLoop, SideFlowDecode  # noqa: F401

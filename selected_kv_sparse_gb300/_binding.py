@@ -61,6 +61,10 @@ class _Verify(ctypes.Structure):
                 ("q_start_pos", ctypes.c_void_p)]
 
 
+class _Packed(ctypes.Structure):
+    _fields_ = [("pool", _Pool), ("num_packed", ctypes.c_int32), ("packed", ctypes.c_void_p)]
+
+
 def _declare(lib):
     P, I, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     F = ctypes.c_float
@@ -89,6 +93,16 @@ def _declare(lib):
         "kap_attn_propose_noalloc": ([P, P, P, P, P, P, P], I),
         "kap_noalloc_scratch_bytes": ([], Z),
         "kap_rope_inv_freq": ([I, ctypes.c_double, P], I),
+        "kap_packed_chunk_bytes": ([I], Z),
+        "kap_pack_pages": ([P, P, P, I, P], I),
+        "kap_unpack_pages": ([P, P, P, I, P], I),
+        "kap_packed_workspace_size": ([I, I, I, I, I], Z),
+        "kap_attn_propose_packed": ([P, P, P, P, P, P, P, Z, P], I),
+        "kap_attn_verify_packed": ([P, P, P, P, P, P, P, Z, P], I),
+        "kap_logprobs_workspace_size": ([I, I], Z),
+        "kap_token_logprobs": ([P, I, I, ctypes.c_int64, I, P, I, P, P, P, P, P, P, Z, P], I),
+        "kap_extend_tables": ([I, I, P, P, P, P, I, P, P, P, P, P, I, P, P, P], I),
+        "kap_release_tables": ([I, I, P, P, P, P, I, P, P, P, P], I),
         "kap_selftest_wait_timeout": ([ctypes.c_uint32, ctypes.c_uint32, P, P], I),
     }
     for name, (args, res) in sig.items():
@@ -133,6 +147,13 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on_current_device(*tensors):
+    """All tensors on the current CUDA device: the calls launch there."""
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"expected tensors on the current CUDA device, got one on {t.device}")
 
 
 def _i32(t, name):
@@ -241,6 +262,67 @@ class VerifyPolicy:
 
     def _c(self) -> _Verify:
         return _Verify(self.max_q, self.total_q, _i32(self.q_offsets, "q_offsets"), _i32(self.q_start_pos, "q_start_pos"))
+
+
+@dataclass
+class PackedPool:
+    """A pool with packed 4-bit pages beside its 16-bit ones. Physical page ids below the pool's page count name its
+    bf16 pages, the ids after them the packed pages: packed uint8 [num_packed][Hkv][kap_packed_chunk_bytes(d)].
+    k_summary, when given, is fp32 [num_pages + num_packed][Hkv][d], one row per physical id; the pool's own k_summary
+    is not used through this class (it may be the first num_pages rows of this one)."""
+    pool: KVPool
+    packed: torch.Tensor
+    k_summary: Optional[torch.Tensor] = None
+
+    def _base(self) -> _Pool:
+        p = self.pool._c()
+        if self.pool.dtype != torch.bfloat16:
+            raise TypeError("a pool with packed pages must be bfloat16")
+        if self.k_summary is not None and (self.k_summary.dtype != torch.float32 or tuple(self.k_summary.shape) != (
+                p.num_pages + self.packed.shape[0], p.num_kv_heads, p.head_dim)):
+            raise ValueError("k_summary must be fp32 [num_pages + num_packed][Hkv][d]")
+        p.k_summary = _ptr(self.k_summary)
+        return p
+
+    def _c(self) -> _Packed:
+        p = self._base()
+        x = self.packed
+        if x.dtype != torch.uint8 or x.dim() != 3 or tuple(x.shape[1:]) != (
+                p.num_kv_heads, int(load().kap_packed_chunk_bytes(p.head_dim))):
+            raise ValueError("packed must be uint8 [num_packed][Hkv][kap_packed_chunk_bytes(d)]")
+        _on_current_device(x, self.pool.k_pages, self.pool.v_pages, self.k_summary)
+        return _Packed(p, x.shape[0], _ptr(x))
+
+    @property
+    def dtype(self):
+        return self.pool.dtype
+
+    @property
+    def first_packed(self) -> int:
+        """The physical id of packed page 0."""
+        return int(self.pool.k_pages.shape[0])
+
+    def routing(self) -> "_RoutingPool":
+        """The pool that page scoring (kap_score_topk, kap_score_topk_view) takes: summaries of both kinds of page."""
+        if self.k_summary is None:
+            raise ValueError("routing needs k_summary")
+        return _RoutingPool(self)
+
+
+class _RoutingPool:
+    """Stands for a KVPool in the scoring calls, which read summaries only: its page count covers the packed pages."""
+
+    def __init__(self, owner: PackedPool):
+        self._owner = owner
+
+    def _c(self) -> _Pool:
+        p = self._owner._base()
+        p.num_pages += int(self._owner.packed.shape[0])
+        return p
+
+    @property
+    def dtype(self):
+        return self._owner.dtype
 
 
 # ------------------------------------------------------------------------------------------------- calls
@@ -465,6 +547,152 @@ def kap_attn_verify(pool: KVPool, pmap: PageMap, vp: VerifyPolicy, q: torch.Tens
     _check("kap_attn_verify", lib.kap_attn_verify(ctypes.byref(p), ctypes.byref(m), ctypes.byref(v), _ptr(q),
                                                   _ptr(out), _ptr(lse), _ptr(workspace),
                                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kap_packed_chunk_bytes(d: int) -> int:
+    """Bytes of the packed chunk of one (page, KV head); 0 for a head_dim without a packed form."""
+    return int(load().kap_packed_chunk_bytes(int(d)))
+
+
+def _pack(fn: str, pool: PackedPool, src: torch.Tensor, dst: torch.Tensor, stream):
+    lib = load()
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src_pages and dst_pages must be 1-D and of equal length")
+    _on_current_device(src, dst)
+    p = pool._c()
+    _check(fn, getattr(lib, fn)(ctypes.byref(p), _i32(src, "src_pages"), _i32(dst, "dst_pages"), src.numel(),
+                                _stream(stream)))
+
+
+def kap_pack_pages(pool: PackedPool, src_pages: torch.Tensor, dst_pages: torch.Tensor, stream=None):
+    """16-bit pages src_pages[i] become packed pages dst_pages[i] (physical ids, dst >= pool.first_packed, distinct)."""
+    _pack("kap_pack_pages", pool, src_pages, dst_pages, stream)
+
+
+def kap_unpack_pages(pool: PackedPool, src_pages: torch.Tensor, dst_pages: torch.Tensor, stream=None):
+    """Packed pages src_pages[i] (physical ids) read back into 16-bit pages dst_pages[i] (distinct)."""
+    _pack("kap_unpack_pages", pool, src_pages, dst_pages, stream)
+
+
+def kap_packed_workspace_size(R: int, hkv: int, hq: int, d: int, max_q: int = 1) -> int:
+    return int(load().kap_packed_workspace_size(R, hkv, hq, d, max_q))
+
+
+def _check_attention(pool: PackedPool, rows: int, q, out, lse, workspace):
+    hq, d = pool.pool.num_q_heads, int(pool.pool.k_pages.shape[3])
+    if q.dtype != pool.dtype or out.dtype != pool.dtype or lse.dtype != torch.float32:
+        raise TypeError("q/out must have the pool dtype and lse fp32")
+    if tuple(q.shape) != (rows, hq, d) or out.shape != q.shape or tuple(lse.shape) != (rows, hq):
+        raise ValueError(f"q and out must be [{rows}][{hq}][{d}] and lse [{rows}][{hq}]")
+    _on_current_device(q, out, lse, workspace)
+
+
+def kap_attn_propose_packed(pool: PackedPool, pmap: PageMap, view: View, q: torch.Tensor, out: torch.Tensor,
+                            lse: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """kap_attn_propose over a pool with packed pages (workspace: kap_packed_workspace_size(..., max_q=1))."""
+    lib = load()
+    _check_attention(pool, int(pmap.block_table.shape[0]), q, out, lse, workspace)
+    p, m, v = pool._c(), pmap._c(), view._c()
+    _check("kap_attn_propose_packed", lib.kap_attn_propose_packed(
+        ctypes.byref(p), ctypes.byref(m), ctypes.byref(v), _ptr(q), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kap_attn_verify_packed(pool: PackedPool, pmap: PageMap, vp: VerifyPolicy, q: torch.Tensor, out: torch.Tensor,
+                           lse: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """kap_attn_verify over a pool with packed pages; windows of one row are decode attention over the whole table."""
+    lib = load()
+    _check_attention(pool, vp.total_q, q, out, lse, workspace)
+    R = int(pmap.block_table.shape[0])
+    if vp.q_offsets.numel() != R + 1 or vp.q_start_pos.numel() != R:
+        raise ValueError("q_offsets must have R + 1 and q_start_pos R entries")
+    p, m, v = pool._c(), pmap._c(), vp._c()
+    _check("kap_attn_verify_packed", lib.kap_attn_verify_packed(
+        ctypes.byref(p), ctypes.byref(m), ctypes.byref(v), _ptr(q), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kap_logprobs_workspace_size(rows: int, vocab: int) -> int:
+    return int(load().kap_logprobs_workspace_size(int(rows), int(vocab)))
+
+
+def kap_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.Tensor, workspace: torch.Tensor,
+                       entropy: Optional[torch.Tensor] = None, rank: Optional[torch.Tensor] = None,
+                       top_ids: Optional[torch.Tensor] = None, top_logprobs: Optional[torch.Tensor] = None,
+                       stream=None):
+    """Log probabilities of tokens [rows] (int32) under logits [rows][vocab] (bf16 or fp32, rows any stride apart), into
+    logprobs [rows]; optionally each row's entropy, the token's rank and the top_ids.shape[1] best alternatives."""
+    lib = load()
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda:
+        raise TypeError("logits must be a [rows][vocab] bf16 or fp32 CUDA tensor")
+    rows, vocab = int(logits.shape[0]), int(logits.shape[1])
+    stride = int(logits.stride(0)) if rows > 1 else vocab
+    if (vocab > 1 and logits.stride(1) != 1) or stride < vocab:
+        raise ValueError("a row of logits must be contiguous and rows must not overlap")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    top_n = int(top_ids.shape[1]) if top_ids is not None and top_ids.dim() == 2 else 0
+    for name, t, dt, shape in (("tokens", tokens, torch.int32, (rows,)), ("logprobs", logprobs, torch.float32, (rows,)),
+                               ("entropy", entropy, torch.float32, (rows,)), ("rank", rank, torch.int32, (rows,)),
+                               ("top_ids", top_ids, torch.int32, (rows, top_n)),
+                               ("top_logprobs", top_logprobs, torch.float32, (rows, top_n))):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be {dt} of shape {shape}")
+    _on_current_device(logits, tokens, logprobs, workspace, entropy, rank, top_ids, top_logprobs)
+    dt = KAP_BF16 if logits.dtype == torch.bfloat16 else KAP_F32
+    _check("kap_token_logprobs", lib.kap_token_logprobs(
+        ctypes.c_void_p(logits.data_ptr()), dt, vocab, stride, rows, _ptr(tokens), top_n, _ptr(logprobs),
+        _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _check_tables(R: int, **tensors):
+    for name, (t, n) in tensors.items():
+        if t.dim() != 1 or (n is not None and t.numel() != n):
+            raise ValueError(f"{name} must be 1-D" + (f" with {n} entries" if n is not None else ""))
+    _on_current_device(*(t for t, _ in tensors.values()))
+
+
+def kap_extend_tables(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: torch.Tensor,
+                      free_pages: torch.Tensor, free_count: torch.Tensor, free_count_out: torch.Tensor,
+                      tok_offsets: torch.Tensor, slot_out: torch.Tensor, pos_out: torch.Tensor,
+                      seq_len_out: torch.Tensor, granted: torch.Tensor, stream=None):
+    """Grows block_table [R][max_pages] by the pages that new_tokens [R] need, taken from the stack free_pages whose
+    length is free_count [1], and writes the new tokens' slots and positions (room for slot_out.numel() of them)."""
+    lib = load()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R][max_pages]")
+    R, mp = int(block_table.shape[0]), int(block_table.shape[1])
+    if slot_out.dtype != torch.int64:
+        raise TypeError("slot_out must be int64")
+    _check_tables(R, seq_len=(seq_len, R), new_tokens=(new_tokens, R), free_pages=(free_pages, None),
+                  free_count=(free_count, 1), free_count_out=(free_count_out, 1), tok_offsets=(tok_offsets, R + 1),
+                  slot_out=(slot_out, None), pos_out=(pos_out, slot_out.numel()), seq_len_out=(seq_len_out, R),
+                  granted=(granted, R))
+    _on_current_device(block_table)
+    _check("kap_extend_tables", lib.kap_extend_tables(
+        R, mp, _i32(block_table, "block_table"), _i32(seq_len, "seq_len"), _i32(new_tokens, "new_tokens"),
+        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count"),
+        _i32(free_count_out, "free_count_out"), _i32(tok_offsets, "tok_offsets"), _ptr(slot_out),
+        _i32(pos_out, "pos_out"), slot_out.numel(), _i32(seq_len_out, "seq_len_out"), _i32(granted, "granted"),
+        _stream(stream)))
+
+
+def kap_release_tables(block_table: torch.Tensor, seq_len: torch.Tensor, released: torch.Tensor,
+                       free_pages: torch.Tensor, free_count: torch.Tensor, free_count_out: torch.Tensor,
+                       seq_len_out: torch.Tensor, stream=None):
+    """Pushes the pages of the requests with released[r] != 0 on the stack free_pages and sets their length to 0."""
+    lib = load()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R][max_pages]")
+    R, mp = int(block_table.shape[0]), int(block_table.shape[1])
+    _check_tables(R, seq_len=(seq_len, R), released=(released, R), free_pages=(free_pages, None),
+                  free_count=(free_count, 1), free_count_out=(free_count_out, 1), seq_len_out=(seq_len_out, R))
+    _on_current_device(block_table)
+    _check("kap_release_tables", lib.kap_release_tables(
+        R, mp, _i32(block_table, "block_table"), _i32(seq_len, "seq_len"), _i32(released, "released"),
+        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count"),
+        _i32(free_count_out, "free_count_out"), _i32(seq_len_out, "seq_len_out"), _stream(stream)))
 
 
 def kap_selftest_wait_timeout(polls: int, suspend_ns: int, timed_out: torch.Tensor, stream=None):

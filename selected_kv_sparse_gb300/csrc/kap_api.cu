@@ -389,6 +389,146 @@ kap_status kap_attn_verify(const kap_kv_pool *pool, const kap_page_map *map, con
                                    cs(stream)));
 }
 
+namespace {
+kap_status check_packed(const kap_packed_pool *p) {
+  if (!p) return KAP_EINVAL;
+  const kap_status st = check_pool(&p->pool, false);
+  if (st != KAP_OK) return st;
+  if (p->pool.dtype != KAP_BF16) return KAP_EUNSUPPORTED;
+  if (p->num_packed < 0 || (p->num_packed > 0 && !p->packed) || !aligned16(p->packed)) return KAP_EINVAL;
+  if ((static_cast<int64_t>(p->pool.num_pages) + p->num_packed) * p->pool.num_kv_heads * 16 >= (int64_t(1) << 31))
+    return KAP_EUNSUPPORTED;
+  return KAP_OK;
+}
+
+PackedArgs packed_args(const kap_packed_pool *p) { return PackedArgs{pool_args(&p->pool), p->num_packed, p->packed}; }
+
+kap_status pack_common(const kap_packed_pool *pool, bool pack, const int32_t *src, const int32_t *dst, int32_t n,
+                       kap_stream stream) {
+  const kap_status st = check_packed(pool);
+  if (st != KAP_OK) return st;
+  if (n < 0) return KAP_EINVAL;
+  if (n == 0) return KAP_OK;
+  if (!src || !dst) return KAP_EINVAL;
+  return cuda_status(launch_pack(packed_args(pool), pack, src, dst, n, error_word(), cs(stream)));
+}
+}  // namespace
+
+size_t kap_packed_chunk_bytes(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? static_cast<size_t>(packed_chunk_bytes(head_dim)) : 0;
+}
+
+kap_status kap_pack_pages(const kap_packed_pool *pool, const int32_t *src_pages_dev, const int32_t *dst_pages_dev,
+                          int32_t num_listed, kap_stream stream) {
+  return pack_common(pool, true, src_pages_dev, dst_pages_dev, num_listed, stream);
+}
+
+kap_status kap_unpack_pages(const kap_packed_pool *pool, const int32_t *src_pages_dev, const int32_t *dst_pages_dev,
+                            int32_t num_listed, kap_stream stream) {
+  return pack_common(pool, false, src_pages_dev, dst_pages_dev, num_listed, stream);
+}
+
+size_t kap_packed_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
+                                 int32_t max_q) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_q <= 0) return 0;
+  return packed_workspace_bytes(num_seqs, num_kv_heads, num_q_heads, head_dim, max_q);
+}
+
+kap_status kap_attn_propose_packed(const kap_packed_pool *pool, const kap_page_map *map, const kap_view *view,
+                                   const void *q_dev, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                   kap_stream stream) {
+  kap_status st = check_packed(pool);
+  if (st != KAP_OK) return st;
+  if ((st = check_map(map, true)) != KAP_OK) return st;
+  if (!view || !q_dev || !out || !lse || !workspace) return KAP_EINVAL;
+  if (!view->block_table || !view->logical_page || !view->n_entries || !view->n_selected) return KAP_EINVAL;
+  if (view->cap <= 0) return KAP_EINVAL;
+  if (view->rows_per_seq != 1 && view->rows_per_seq != pool->pool.num_kv_heads) return KAP_ESHAPE;
+  if (!aligned16(q_dev) || !aligned16(out) || !aligned16(workspace)) return KAP_EINVAL;
+  if (workspace_bytes < packed_workspace_bytes(map->num_seqs, pool->pool.num_kv_heads, pool->pool.num_q_heads,
+                                               pool->pool.head_dim, 1))
+    return KAP_ECAPACITY;
+  const ViewArgs va{view->rows_per_seq, view->cap, view->block_table, view->logical_page, view->n_entries,
+                    view->n_selected, 0};
+  return cuda_status(launch_propose_packed(packed_args(pool), map_args(map), va, q_dev, out, lse, workspace,
+                                           error_word(), cs(stream)));
+}
+
+kap_status kap_attn_verify_packed(const kap_packed_pool *pool, const kap_page_map *map, const kap_verify_policy *vp,
+                                  const void *q_dev, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                  kap_stream stream) {
+  kap_status st = check_packed(pool);
+  if (st != KAP_OK) return st;
+  if ((st = check_map(map, false)) != KAP_OK) return st;
+  if (!vp || !q_dev || !out || !lse || !workspace) return KAP_EINVAL;
+  if (!vp->q_offsets || !vp->q_start_pos) return KAP_EINVAL;
+  if (vp->max_q <= 0 || vp->total_q < 0) return KAP_EINVAL;
+  if (pool->pool.num_q_heads / pool->pool.num_kv_heads * static_cast<int64_t>(vp->max_q) > 64)
+    return KAP_EUNSUPPORTED;
+  if (!aligned16(q_dev) || !aligned16(out) || !aligned16(workspace)) return KAP_EINVAL;
+  if (workspace_bytes < packed_workspace_bytes(map->num_seqs, pool->pool.num_kv_heads, pool->pool.num_q_heads,
+                                               pool->pool.head_dim, vp->max_q))
+    return KAP_ECAPACITY;
+  if (vp->total_q == 0) return KAP_OK;
+  return cuda_status(launch_verify_packed(packed_args(pool), map_args(map), vp->max_q, vp->total_q, vp->q_offsets,
+                                          vp->q_start_pos, q_dev, out, lse, workspace, error_word(), cs(stream)));
+}
+
+size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab) {
+  if (rows <= 0 || vocab <= 0) return 0;
+  return logprobs_workspace_bytes(rows, vocab);
+}
+
+kap_status kap_token_logprobs(const void *logits_dev, int32_t logits_dtype, int32_t vocab, int64_t row_stride,
+                              int32_t rows, const int32_t *tokens_dev, int32_t top_n, float *logprob_out,
+                              float *entropy_out, int32_t *rank_out, int32_t *top_ids, float *top_logprobs,
+                              void *workspace, size_t workspace_bytes, kap_stream stream) {
+  if (logits_dtype != KAP_BF16 && logits_dtype != KAP_F32) return KAP_EUNSUPPORTED;
+  if (rows < 0 || vocab <= 0 || row_stride < vocab) return KAP_EINVAL;
+  if (vocab > (1 << 24)) return KAP_EUNSUPPORTED;
+  if (top_n < 0 || top_n > 32 || top_n > vocab) return KAP_EINVAL;
+  if (rows == 0) return KAP_OK;
+  if (!logits_dev || !tokens_dev || !logprob_out || !workspace) return KAP_EINVAL;
+  if (top_n > 0 && (!top_ids || !top_logprobs)) return KAP_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(logits_dev) & (logits_dtype == KAP_BF16 ? 1u : 3u)) || !aligned16(workspace))
+    return KAP_EINVAL;
+  if (workspace_bytes < logprobs_workspace_bytes(rows, vocab)) return KAP_ECAPACITY;
+  return cuda_status(launch_logprobs(logits_dev, logits_dtype, vocab, row_stride, rows, tokens_dev, top_n,
+                                     logprob_out, entropy_out, rank_out, top_ids, top_logprobs, workspace,
+                                     cs(stream)));
+}
+
+kap_status kap_extend_tables(int32_t num_seqs, int32_t max_pages, int32_t *block_table, const int32_t *seq_len,
+                             const int32_t *new_tokens, const int32_t *free_pages, int32_t free_capacity,
+                             const int32_t *free_count, int32_t *free_count_out, int32_t *tok_offsets,
+                             int64_t *slot_out, int32_t *pos_out, int32_t max_tokens, int32_t *seq_len_out,
+                             int32_t *granted_out, kap_stream stream) {
+  if (num_seqs <= 0 || max_pages <= 0 || free_capacity < 0 || max_tokens < 0) return KAP_EINVAL;
+  if (max_pages > (1 << 26)) return KAP_EUNSUPPORTED;
+  if (!block_table || !seq_len || !new_tokens || !free_count || !free_count_out || !tok_offsets || !seq_len_out ||
+      !granted_out || (free_capacity > 0 && !free_pages) || (max_tokens > 0 && (!slot_out || !pos_out)))
+    return KAP_EINVAL;
+  if (seq_len_out == seq_len || free_count_out == free_count) return KAP_EINVAL;
+  return cuda_status(launch_extend_tables(num_seqs, max_pages, block_table, seq_len, new_tokens, free_pages,
+                                          free_capacity, free_count, free_count_out, tok_offsets, slot_out, pos_out,
+                                          max_tokens, seq_len_out, granted_out, error_word(), cs(stream)));
+}
+
+kap_status kap_release_tables(int32_t num_seqs, int32_t max_pages, const int32_t *block_table,
+                              const int32_t *seq_len, const int32_t *released, int32_t *free_pages,
+                              int32_t free_capacity, const int32_t *free_count, int32_t *free_count_out,
+                              int32_t *seq_len_out, kap_stream stream) {
+  if (num_seqs <= 0 || max_pages <= 0 || free_capacity < 0) return KAP_EINVAL;
+  if (max_pages > (1 << 26)) return KAP_EUNSUPPORTED;
+  if (!block_table || !seq_len || !released || !free_count || !free_count_out || !seq_len_out ||
+      (free_capacity > 0 && !free_pages))
+    return KAP_EINVAL;
+  if (seq_len_out == seq_len || free_count_out == free_count) return KAP_EINVAL;
+  return cuda_status(launch_release_tables(num_seqs, max_pages, block_table, seq_len, released, free_pages,
+                                           free_capacity, free_count, free_count_out, seq_len_out, error_word(),
+                                           cs(stream)));
+}
+
 const char *kap_status_str(kap_status s) {
   switch (s) {
     case KAP_OK: return "ok";

@@ -87,6 +87,40 @@ cudaError_t launch_verify(const PoolArgs &p, const MapArgs &m, int max_q, int to
                           const int32_t *q_start, const void *q, void *out, float *lse, void *ws, size_t ws_bytes,
                           int *err, cudaStream_t s);
 
+// packed pages (k_packed.cu) and attention over them (k_attn_packed.cu)
+struct PackedArgs {
+  PoolArgs pool;   // the 16-bit pages; physical id num_pages + j is packed page j
+  int num_packed;
+  void *packed;    // [num_packed][hkv][packed_chunk_bytes(d)]
+};
+constexpr int packed_chunk_bytes(int d) { return d / 64 * 1152; }
+// pack: 16-bit page src[i] -> packed page dst[i]; otherwise packed page src[i] -> 16-bit page dst[i]
+cudaError_t launch_pack(const PackedArgs &p, bool pack, const int32_t *src, const int32_t *dst, int n, int *err,
+                        cudaStream_t s);
+size_t packed_workspace_bytes(int R, int hkv, int hq, int d, int max_q);
+cudaError_t launch_propose_packed(const PackedArgs &p, const MapArgs &m, const ViewArgs &v, const void *q, void *out,
+                                  float *lse, void *ws, int *err, cudaStream_t s);
+cudaError_t launch_verify_packed(const PackedArgs &p, const MapArgs &m, int max_q, int total_q,
+                                 const int32_t *q_offsets, const int32_t *q_start, const void *q, void *out,
+                                 float *lse, void *ws, int *err, cudaStream_t s);
+
+// log probabilities of given tokens (k_logprobs.cu)
+size_t logprobs_workspace_bytes(int rows, int vocab);
+cudaError_t launch_logprobs(const void *logits, int dtype, int V, int64_t stride, int rows, const int32_t *tokens,
+                            int top_n, float *lp, float *ent, int32_t *rank, int32_t *top_ids, float *top_lp, void *ws,
+                            cudaStream_t s);
+
+// block tables and slot maps from request lengths (k_tables.cu)
+cudaError_t launch_extend_tables(int R, int max_pages, int32_t *bt, const int32_t *seq_len, const int32_t *new_tokens,
+                                 const int32_t *free_pages, int free_cap, const int32_t *free_count,
+                                 int32_t *free_count_out, int32_t *tok_offsets, int64_t *slot_out, int32_t *pos_out,
+                                 int max_tokens, int32_t *seq_len_out, int32_t *granted_out, int *err,
+                                 cudaStream_t s);
+cudaError_t launch_release_tables(int R, int max_pages, const int32_t *bt, const int32_t *seq_len,
+                                  const int32_t *released, int32_t *free_pages, int free_cap,
+                                  const int32_t *free_count, int32_t *free_count_out, int32_t *seq_len_out, int *err,
+                                  cudaStream_t s);
+
 // number of SMs of the current device (cached per device)
 int device_sm_count();
 
