@@ -1,15 +1,44 @@
-// k_attn_packed.cu - attention over a pool with packed 4-bit pages (sm_103a).
+// k_attn_packed.cu - attention over a pool with packed 4-bit pages (sm_103a): proposal (one query a request, the pages
+// of a compact view) and verification (a causal window, the whole block table; windows of one row are plain decode).
 //
-// One warp per (query row, query head) walks its visible tokens with a running maximum and sum; a lane holds d / 32
-// dims. Proposal: the entries of the request's view row. Verification: the logical pages of the block table.
+// Mathematics. With code c, scale s and lowest value l of a group of 64 dims, a logit is
+//   sum_blocks ( s_k * sum_i q_i c_i + l_k * sum_i q_i ),
+// so the inner product runs over the bare codes and the parameters join it once per token and block, in fp32; and
+//   out = sum_tokens p v = sum_tokens (p s_v) c + sum_tokens p l_v,
+// so p s_v (rounded to fp16, 2^-11) meets the bare codes and the second sum is one number per block and query.
+// A code in the low bits of an fp16 is the subnormal c * 2^-24, or c * 2^-20 four bits further up: masking a word of
+// codes gives tensor-core operands with no conversion and no subtraction. The factor 16 of every second code goes
+// into the query (keys) or into the result (values); the power of two comes off the accumulators.
+//
+// Tile. A page is 16 tokens: the M of mma.m16n8k16. Logits are S^T[16 tokens x 8 queries] = codes . q^T, and
+// O^T[16 dims x 8 queries] = codes^T . p^T; p moves from one to the other inside registers (movmatrix). Queries of one
+// KV head (G heads x window rows) are the columns, in tiles of 8. Why mma.sync and registers: a (page, head) is 2304
+// bytes, 98 SM cycles of HBM at the measured copy rate, and 65536 codes; as 16-bit operands in shared memory for
+// tcgen05 those would be 8 KiB written and read again, more than the page's time at 128 bytes a cycle. Fragments masked
+// out of the packed words cost 0.6 instructions a pair.
+//
+// Split. The pages of all (request, KV head) rows form one line that is cut into equal shares, one a CTA. In a share
+// the warps take pages in turn, each with its own ring of bulk copies (a whole page-head each), its own running maximum
+// and accumulators; they are joined at the end of a row's part, and the last CTA to finish a row merges the parts in
+// their order.
+//
+// Statistics. A warp keeps a reference per query column (at most 2^8 below the running maximum) and one for the value
+// scales (at most 2^6 below the largest), so that p s_v stays inside fp16; both move only when a page exceeds them.
 #include "kap_launch.h"
 #include "kap_packed.cuh"
+
+#include <algorithm>
 
 namespace kap {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;      // reference of a column that has seen nothing
+constexpr float kMaxSlack = 8.0f;     // log2 units a logit may exceed its reference by
+constexpr float kScaleSlack = 64.0f;  // factor a value scale may exceed its reference by
+
+constexpr int kMaxCtas = 320;  // records of a launch beside one per row: CTAs of the widest grid
 
 struct AParams {
   const __nv_bfloat16 *k, *v;
@@ -17,113 +46,836 @@ struct AParams {
   int P16, P4, hkv, hq, R;
   const int32_t *bt;
   int max_pages;
-  const int32_t *ctx_len, *seq_len;           // proposal
-  ViewArgs view;                              // proposal
-  const int32_t *q_offsets, *q_start;         // verification
-  int rows;                                   // query rows: R, or total_q
+  const int32_t *ctx_len, *seq_len;    // proposal
+  ViewArgs view;                       // proposal
+  const int32_t *q_offsets, *q_start;  // verification
+  int max_q, total_q;
   const __nv_bfloat16 *q;
   __nv_bfloat16 *out;
   float *lse;
+  int *counters;  // one per row
+  float2 *ml;     // [slot][columns]
+  float *part;    // [slot][columns][d]
+  int ncol;       // columns of a record: G * max_q
   int *err;
 };
 
-template <int D, bool kView>
-__global__ void __launch_bounds__(256) attn_kernel(const AParams p) {
-  using L = PackedChunk<D>;
-  constexpr int PL = D / 32;
-  grid_dependency_sync();
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (wid >= static_cast<int64_t>(p.rows) * p.hq) return;
-  const int row = static_cast<int>(wid / p.hq), head = static_cast<int>(wid - static_cast<int64_t>(row) * p.hq);
-  const int h = head / (p.hq / p.hkv);
-  int r = row, last, nent, nsel = 0, ctx = 0;
-  const int32_t *ids, *lps = nullptr;
-  if (kView) {
-    const int vr = r * p.view.rows_per_seq + (p.view.rows_per_seq > 1 ? h : 0);
-    last = p.seq_len[r] - 1;
-    ctx = p.ctx_len[r];
-    nent = p.view.n_entries[vr];
-    nsel = p.view.n_selected[vr];
-    if (nent > p.view.cap) {
-      if (lane == 0) set_error(p.err, kErrCapacity);
-      nent = p.view.cap;
-    }
-    ids = p.view.bt + static_cast<size_t>(vr) * p.view.cap;
-    lps = p.view.lp + static_cast<size_t>(vr) * p.view.cap;
-  } else {
-    int lo = 0, hi = p.R - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.q_offsets[mid] <= row) lo = mid; else hi = mid - 1;
-    }
-    r = lo;
-    if (row >= p.q_offsets[r + 1] || row < p.q_offsets[r]) return;
-    last = p.q_start[r] + (row - p.q_offsets[r]);
-    nent = last < 0 ? 0 : last / kPage + 1;
-    if (nent > p.max_pages) {
-      if (lane == 0) set_error(p.err, kErrPage);
-      nent = p.max_pages;
-    }
-    ids = p.bt + static_cast<size_t>(r) * p.max_pages;
+template <int D, int NTL, int CS>
+struct Cfg {
+  static constexpr int kWarps = NTL == 2 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kCtas = NTL == 1 ? 2 : 1;         // resident CTAs an SM
+  static constexpr int PW = kWarps / CS;                 // warps that take pages in turn
+  static constexpr int N = NTL * CS * 8;                 // query columns
+  static constexpr int NB = D / 64;
+  static constexpr int KS = NB * 4;                      // k-steps of the logits
+  static constexpr int kChunk = PackedChunk<D>::BYTES;
+  static constexpr int kStages = (D == 128 ? 5 : 8) * CS;
+  static constexpr int kQStride = D + 8;                 // bf16 elements of a raw query row
+  static constexpr int OFF_RING = 0;
+  static constexpr int kRing = PW * kStages * kChunk;
+  static constexpr int kAcc = NTL * NB * 16;             // accumulators of a lane
+  static constexpr int kJoin = (kAcc + NTL * 4) * 32 * 4;  // bytes a warp hands over
+  static constexpr int kJoinAll = (kWarps / 2 + 1) * kJoin;
+  static constexpr int kMaxGrid = 160 * kCtas;            // CTAs, so parts of a row
+  static constexpr int kWeights = kMaxGrid * N * 8;       // (maximum, sum) of every part and column
+  static constexpr int kArea = kRing > kJoinAll ? (kRing > kWeights ? kRing : kWeights)
+                                                : (kJoinAll > kWeights ? kJoinAll : kWeights);
+  static constexpr int OFF_QRAW = (kArea + 127) / 128 * 128;
+  static constexpr int OFF_QF = OFF_QRAW + (N * kQStride * 2 + 15) / 16 * 16;  // fp16 fragments [tile][k-step][lane]
+  static constexpr int OFF_QS = OFF_QF + NTL * CS * KS * 32 * 8;               // [N] scale, [N][NB] block sums
+  static constexpr int OFF_BAR = OFF_QS + N * (1 + NB) * 4;
+  static constexpr int BYTES = OFF_BAR + PW * kStages * 8;
+  static_assert(BYTES <= 227 * 1024 / kCtas, "shared memory");
+};
+
+// One row's part: pages [p0, p1) of (request r, head h).
+struct Seg {
+  int r, h, row, n, p0, p1, nq, qoff, last0, ctx, nsel;
+  const int32_t *ids, *lps;
+};
+
+__device__ __forceinline__ int atom_add_acq_rel_gpu(int *p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+// Leaves a page to the producer: the warps of all column groups have read it. Returns whether any of them gave up.
+template <int CS, int PW>
+__device__ __forceinline__ bool release_page(int pw, bool dead) {
+  if (CS == 1) {
+    __syncwarp();
+    return dead;
   }
-  const size_t qo = (static_cast<size_t>(row) * p.hq + head) * D;
-  float qv[PL], ov[PL];
-  const float sc = rsqrtf(static_cast<float>(D)) * kLog2e;
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(1 + pw), "r"(32 * CS), "r"(dead ? 1 : 0)
+      : "memory");
+  return any != 0;
+}
+// Over the eight lanes that hold one column: lanes l, l ^ 4, l ^ 8, l ^ 16.
+__device__ __forceinline__ float column_max(float v) {
 #pragma unroll
-  for (int k = 0; k < PL; ++k) {
-    qv[k] = to_f(p.q[qo + lane + 32 * k]) * sc;
-    ov[k] = 0.0f;
+  for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float column_sum(float v) {
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Units are what has a page list of its own: a request (every head walks the same list), or a row of a per-head view.
+template <bool kView>
+struct Units {
+  const AParams &p;
+  __device__ __forceinline__ int count() const { return kView ? p.R * p.view.rows_per_seq : p.R; }
+  __device__ __forceinline__ int heads() const { return kView && p.view.rows_per_seq > 1 ? 1 : p.hkv; }
+  // Window of request r, kept inside the query array whatever the device data say.
+  __device__ __forceinline__ int window(int r, int &qoff, bool &bad) const {
+    if (kView) {
+      qoff = r;
+      return 1;
+    }
+    const int a = p.q_offsets[r], b = p.q_offsets[r + 1];
+    qoff = min(max(a, 0), p.total_q);
+    const int nq = max(min(b, p.total_q) - qoff, 0);
+    bad = a != qoff || b < a || b > p.total_q || nq > p.max_q;
+    return min(nq, p.max_q);
   }
-  float mx = -INFINITY, l = 0.0f;
-  for (int e = 0; e < nent; ++e) {
-    const int id = ids[e], pos0 = (kView ? lps[e] : e) * kPage;
-    if (id < 0 || id >= p.P16 + p.P4) {
-      if (lane == 0) set_error(p.err, kErrPage);
+  __device__ __forceinline__ int pages(int u, int &bad) const {
+    if (kView) {
+      const int n = p.view.n_entries[u];
+      if (n > p.view.cap) bad |= kErrCapacity;
+      return min(max(n, 0), p.view.cap);
+    }
+    int qoff;
+    bool wbad = false;
+    const int nq = window(u, qoff, wbad);
+    if (wbad) bad |= kErrLength;
+    if (nq <= 0) return 0;
+    const int64_t end = static_cast<int64_t>(p.q_start[u]) + nq;
+    const int64_t n = end <= 0 ? 0 : (end + kPage - 1) / kPage;
+    if (n > p.max_pages) bad |= kErrPage;
+    return static_cast<int>(min(n, static_cast<int64_t>(p.max_pages)));
+  }
+};
+
+template <int D, int NTL, int CS, bool kView>
+__global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kCtas) attn_kernel(const AParams p) {
+  using C = Cfg<D, NTL, CS>;
+  using L = PackedChunk<D>;
+  constexpr int NB = C::NB;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_scan[C::kWarps], s_total, s_base;
+  __shared__ int s_unit, s_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pw = warp % C::PW, cg = warp / C::PW;  // which pages, which group of NTL column tiles
+  const int g = lane >> 2, t = lane & 3;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + pw * C::kStages;
+  unsigned char *ring = smem + C::OFF_RING + pw * C::kStages * C::kChunk;
+  __nv_bfloat16 *qraw = reinterpret_cast<__nv_bfloat16 *>(smem + C::OFF_QRAW);
+  uint2 *qfrag = reinterpret_cast<uint2 *>(smem + C::OFF_QF);
+  float *qscale = reinterpret_cast<float *>(smem + C::OFF_QS);
+  float *qsum = qscale + C::N;
+
+  if (cg == 0 && lane < C::kStages) mbar_init(&bars[lane], 1);
+  fence_barrier_init();
+  grid_dependency_sync();
+
+  // ---- this CTA's share of the line of pages, and the unit that it starts in
+  const Units<kView> units{p};
+  const int U = units.count(), H = units.heads();
+  int64_t total = 0;
+  int bad = 0;
+  for (int base = 0; base < U; base += C::kThreads) {
+    const int u = base + tid;
+    const int64_t n = u < U ? static_cast<int64_t>(units.pages(u, bad)) * H : 0;
+    const int64_t incl = block_inclusive_scan<int64_t>(n, s_scan);
+    if (tid == C::kThreads - 1) s_total = incl;
+    __syncthreads();
+    total += s_total;
+    __syncthreads();
+    if (u < U && n == 0 && u % gridDim.x == blockIdx.x) {  // a row without pages: zeros
+      const int r = kView ? u / p.view.rows_per_seq : u;
+      const int h0 = H == 1 ? u - r * p.view.rows_per_seq : 0;
+      int qoff;
+      bool wb = false;
+      const int nq = units.window(r, qoff, wb), G = p.hq / p.hkv;
+      for (int i = 0; i < nq; ++i)
+        for (int a = h0 * G; a < (h0 + H) * G; ++a) {
+          const size_t o = static_cast<size_t>(qoff + i) * p.hq + a;
+          p.lse[o] = -INFINITY;
+          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(p.out + o * D + c) = make_uint4(0, 0, 0, 0);
+        }
+      if (kView) bad |= kErrLength;
+    }
+  }
+  if (bad && blockIdx.x == 0) set_error(p.err, bad);
+  else if (bad & kErrLength) set_error(p.err, kErrLength);
+  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(C::PW));
+  int64_t x = share * blockIdx.x;
+  const int64_t x1 = min(x + share, total);
+  if (x >= x1) return;
+  {
+    int64_t before = 0;
+    int dummy = 0;
+    for (int base = 0; base < U; base += C::kThreads) {
+      const int u = base + tid;
+      const int64_t n = u < U ? static_cast<int64_t>(units.pages(u, dummy)) * H : 0;
+      const int64_t incl = before + block_inclusive_scan<int64_t>(n, s_scan);
+      if (incl - n <= x && x < incl) {
+        s_unit = u;
+        s_base = incl - n;
+      }
+      if (tid == C::kThreads - 1) s_total = incl;
+      __syncthreads();
+      before = s_total;
+      __syncthreads();
+      if (before > x) break;
+    }
+  }
+  int unit = s_unit;
+  int64_t ubase = s_base;
+
+  const int G = p.hq / p.hkv;
+  const float qk = rsqrtf(static_cast<float>(D)) * kLog2e;
+  const int tokA = (g >> 1) + 4 * (g & 1), tokB = tokA + 8;  // tokens of this lane's two logit rows
+  uint32_t issued = 0, consumed = 0;
+  bool dead = false;
+
+  while (x < x1) {
+    // ---- the row at x and its part in this share
+    Seg s;
+    int dummy = 0;
+    s.n = units.pages(unit, dummy);
+    if (x >= ubase + static_cast<int64_t>(s.n) * H) {
+      ubase += static_cast<int64_t>(s.n) * H;
+      ++unit;
       continue;
     }
-    const unsigned char *chunk = p.packed + (static_cast<size_t>(id - p.P16) * p.hkv + h) * L::BYTES;
-    const size_t o16 = (static_cast<size_t>(id) * p.hkv + h) * (kPage * D);
-    for (int t = 0; t < kPage; ++t) {
-      const int pos = pos0 + t;
-      if (pos > last || (kView && e >= nsel && pos < ctx)) continue;
-      float s = 0.0f, vv[PL];
-#pragma unroll
-      for (int k = 0; k < PL; ++k) {
-        const int i = lane + 32 * k;
-        float kk;
-        if (id >= p.P16) {
-          const int blk = i >> 6, at = blk * L::kBlock + t * 32 + ((i & 63) >> 1), sh = (i & 1) * 4;
-          const uint32_t kp = *reinterpret_cast<const uint32_t *>(chunk + L::OFF_KPAR + (blk * kPage + t) * 4);
-          const uint32_t vp = *reinterpret_cast<const uint32_t *>(chunk + L::OFF_VPAR + (blk * kPage + t) * 4);
-          kk = fmaf(param_scale(kp), static_cast<float>((chunk[at] >> sh) & 15), param_low(kp));
-          vv[k] = fmaf(param_scale(vp), static_cast<float>((chunk[L::OFF_V + at] >> sh) & 15), param_low(vp));
-        } else {
-          kk = to_f(p.k[o16 + t * D + i]);
-          vv[k] = to_f(p.v[o16 + t * D + i]);
-        }
-        s = fmaf(qv[k], kk, s);
+    {
+      const int64_t in = x - ubase;
+      const int hh = static_cast<int>(in / s.n);
+      s.r = kView ? unit / p.view.rows_per_seq : unit;
+      s.h = H == 1 && kView ? unit - s.r * p.view.rows_per_seq : hh;
+      s.row = s.r * p.hkv + s.h;
+      s.p0 = static_cast<int>(in - static_cast<int64_t>(hh) * s.n);
+      s.p1 = static_cast<int>(min(static_cast<int64_t>(s.n), s.p0 + (x1 - x)));
+      bool wb = false;
+      s.nq = units.window(s.r, s.qoff, wb);
+      if (kView) {
+        s.last0 = p.seq_len[s.r] - 1;
+        s.ctx = p.ctx_len[s.r];
+        s.nsel = p.view.n_selected[unit];
+        s.ids = p.view.bt + static_cast<size_t>(unit) * p.view.cap;
+        s.lps = p.view.lp + static_cast<size_t>(unit) * p.view.cap;
+      } else {
+        s.last0 = p.q_start[s.r];
+        s.ctx = 0;
+        s.nsel = 0;
+        s.ids = p.bt + static_cast<size_t>(s.r) * p.max_pages;
+        s.lps = nullptr;
       }
-      s = warp_sum(s);
-      const float mn = fmaxf(mx, s);
-      const float a = exp2f(mx - mn), w = exp2f(s - mn);
-      l = l * a + w;
-#pragma unroll
-      for (int k = 0; k < PL; ++k) ov[k] = ov[k] * a + w * vv[k];
-      mx = mn;
     }
-  }
+    const int64_t rb = x - s.p0, re = rb + s.n;  // the row's pages on the line
+    const int M = G * s.nq;
+
+    // ---- this warp's items: pages p0 + pw, p0 + pw + PW, ...; ids of 32 items a load, two loads held
+    const int nit = s.p1 - s.p0 > pw ? (s.p1 - s.p0 - pw + C::PW - 1) / C::PW : 0;
+    auto load_ids = [&](int batch, int &id, int &lp) {
+      const int j = batch * 32 + lane;
+      id = -1;
+      lp = 0;
+      if (j < nit) {
+        const int e = s.p0 + pw + C::PW * j;
+        id = s.ids[e];
+        if (kView) lp = s.lps[e];
+      }
+    };
+    int idc, lpc, idn, lpn, batch = 0, ahead = 0;
+    load_ids(0, idc, lpc);
+    load_ids(1, idn, lpn);
+    auto issue = [&](int k) {  // copies for items below k + 24, as far as the ring has room
+      while (ahead < nit && ahead < k + 24 && issued - consumed < C::kStages) {
+        const int id = __shfl_sync(0xffffffffu, (ahead >> 5) == batch ? idc : idn, ahead & 31);
+        if (id >= p.P16 && id < p.P16 + p.P4) {
+          if (lane == 0 && cg == 0) {
+            const uint32_t st = issued % C::kStages;
+            mbar_arrive_expect_tx(&bars[st], C::kChunk);
+            bulk_g2s(ring + st * C::kChunk, p.packed + (static_cast<size_t>(id - p.P16) * p.hkv + s.h) * C::kChunk,
+                     C::kChunk, &bars[st]);
+          }
+          ++issued;
+        }
+        ++ahead;
+      }
+    };
+    if (!dead && CS == 1) issue(0);
+
+    // ---- queries: raw rows, their power-of-two scales, block sums, then the fp16 fragments
+    for (int c = warp; c < C::N; c += C::kWarps) {
+      float v[D / 32];
+      float mx = 0.0f, sum = 0.0f;
+      const int i = c / G, a = c - i * G;
+      const size_t o = (static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + a) * D + lane * (D / 32);
 #pragma unroll
-  for (int k = 0; k < PL; ++k) p.out[qo + lane + 32 * k] = from_f<__nv_bfloat16>(l != 0.0f ? ov[k] / l : 0.0f);
-  if (lane == 0) {
-    p.lse[static_cast<size_t>(row) * p.hq + head] = l != 0.0f ? (mx + log2f(l)) * kLn2 : -INFINITY;
-    if (kView && l == 0.0f) set_error(p.err, kErrLength);
+      for (int k = 0; k < D / 32; ++k) {
+        const __nv_bfloat16 b = c < M ? p.q[o + k] : __float2bfloat16(0.0f);
+        qraw[c * C::kQStride + lane * (D / 32) + k] = b;
+        v[k] = to_f(b);
+        mx = fmaxf(mx, fabsf(v[k]));
+        sum += v[k];
+      }
+      mx = warp_max(mx);
+      constexpr int kHalf = NB == 2 ? 8 : 16;  // lanes of one block: 16 of two, or all
+#pragma unroll
+      for (int o2 = kHalf; o2 >= 1; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+      // largest magnitude to [2^14, 2^15): every bf16 down to 2^-24 of it is exact in fp16, a sixteenth too
+      const int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255);
+      const int sh = e == 0 || e == 255 ? 0 : min(141 - e, 126);
+      if (lane == 0) qscale[c] = __uint_as_float(static_cast<uint32_t>(127 + max(sh, -126)) << 23);
+      if (NB == 1 ? lane == 0 : (lane & 15) == 0) qsum[c * NB + (NB == 1 ? 0 : lane >> 4)] = sum * qk;
+    }
+    __syncthreads();
+    for (int f = tid; f < NTL * CS * C::KS * 32; f += C::kThreads) {
+      const int ln = f & 31, ks = (f >> 5) % C::KS, tile = (f >> 5) / C::KS;
+      const int c = tile * 8 + (ln >> 2);
+      const int d0 = (ks >> 2) * 64 + (ln & 3) * 16 + ((ks >> 1) & 1) * 8 + (ks & 1) * 2;
+      const __nv_bfloat16 *qr = qraw + c * C::kQStride + d0;
+      const float sc = qscale[c], s16 = sc * 0.0625f;
+      qfrag[f] = make_uint2(pack_f16(to_f(qr[0]) * sc, to_f(qr[4]) * sc), pack_f16(to_f(qr[1]) * s16, to_f(qr[5]) * s16));
+    }
+    __syncthreads();
+    // CS > 1: the first column group's lane issues for both, so its partner must have left the ring (barrier above)
+    if (!dead && CS > 1) issue(0);
+
+    // per column of this lane (two a tile): logit factor, block sums, reference, sum, sum p * lowest
+    float cq[NTL][2], qs[NTL][2][NB], mref[NTL][2], lsum[NTL][2], lv[NTL][2][NB], acc[NTL][NB][4][4];
+#pragma unroll
+    for (int j = 0; j < NTL; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = (cg * NTL + j) * 8 + 2 * t + c;
+        cq[j][c] = qk * 0x1p24f / qscale[col];
+        mref[j][c] = kNoMax;
+        lsum[j][c] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          qs[j][c][b] = qsum[col * NB + b];
+          lv[j][c][b] = 0.0f;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < NTL; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[j][b][m][c] = 0.0f;
+    float inv_e = 1.0f;       // 1 / reference of the value scales, a power of two
+    bool scaled = false;      // whether a packed page has set it
+    uint2 qreg[NTL == 1 ? C::KS : 1];
+    if (NTL == 1) {
+#pragma unroll
+      for (int ks = 0; ks < C::KS; ++ks) qreg[ks] = qfrag[(cg * C::KS + ks) * 32 + lane];
+    }
+
+    for (int k = 0; k < nit; ++k) {
+      if (k > 0 && (k & 31) == 0) {
+        idc = idn;
+        lpc = lpn;
+        load_ids(++batch + 1, idn, lpn);
+      }
+      if (!dead) issue(k);
+      const int id = __shfl_sync(0xffffffffu, idc, k & 31);
+      const int e = s.p0 + pw + C::PW * k;
+      const int pos0 = (kView ? __shfl_sync(0xffffffffu, lpc, k & 31) : e) * kPage;
+      if (id < 0 || id >= p.P16 + p.P4) {
+        if (lane == 0) set_error(p.err, kErrPage);
+        continue;
+      }
+      const bool is4 = id >= p.P16;
+      // tokens hidden from every column, and pages on which some column sees only a part
+      const int last_all = s.last0 + s.nq - 1;
+      const int first = kView && e >= s.nsel ? s.ctx : 0;
+      const bool edge = pos0 + kPage - 1 > s.last0 || pos0 < first;
+      float sc[NTL][4];  // logits (log2 units), then probabilities
+      uint32_t vpA[NB], vpB[NB];
+      const unsigned char *ch = ring + (consumed % C::kStages) * C::kChunk;
+      if (is4) {
+        if (dead) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[consumed % C::kStages], (consumed / C::kStages) & 1, p.err))) {
+          dead = release_page<CS, C::PW>(pw, true);  // nothing more is read; copies in flight are waited for below
+          continue;
+        }
+        float sb[NTL][NB][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint2 wA = *reinterpret_cast<const uint2 *>(ch + b * L::kBlock + tokA * 32 + t * 8);
+          const uint2 wB = *reinterpret_cast<const uint2 *>(ch + b * L::kBlock + tokB * 32 + t * 8);
+          const uint32_t a[4] = {wA.x, wA.x >> 8, wA.y, wA.y >> 8}, bb[4] = {wB.x, wB.x >> 8, wB.y, wB.y >> 8};
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) sb[j][b][0] = sb[j][b][1] = sb[j][b][2] = sb[j][b][3] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = a[i] & 0x000f000fu, a1 = bb[i] & 0x000f000fu, a2 = a[i] & 0x00f000f0u,
+                           a3 = bb[i] & 0x00f000f0u;
+#pragma unroll
+            for (int j = 0; j < NTL; ++j) {
+              const uint2 q = NTL == 1 ? qreg[b * 4 + i] : qfrag[((cg * NTL + j) * C::KS + b * 4 + i) * 32 + lane];
+              mma_f16(sb[j][b], a0, a1, a2, a3, q.x, q.y);
+            }
+          }
+        }
+        float sA[NB], sB[NB], lA[NB], lB[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t kA = *reinterpret_cast<const uint32_t *>(ch + L::OFF_KPAR + (b * kPage + tokA) * 4);
+          const uint32_t kB = *reinterpret_cast<const uint32_t *>(ch + L::OFF_KPAR + (b * kPage + tokB) * 4);
+          vpA[b] = *reinterpret_cast<const uint32_t *>(ch + L::OFF_VPAR + (b * kPage + tokA) * 4);
+          vpB[b] = *reinterpret_cast<const uint32_t *>(ch + L::OFF_VPAR + (b * kPage + tokB) * 4);
+          sA[b] = param_scale(kA), lA[b] = param_low(kA), sB[b] = param_scale(kB), lB[b] = param_low(kB);
+        }
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float a = sb[j][0][c] * sA[0], b = sb[j][0][2 + c] * sB[0];
+            float la = lA[0] * qs[j][c][0], lb = lB[0] * qs[j][c][0];
+#pragma unroll
+            for (int z = 1; z < NB; ++z) {
+              a = fmaf(sb[j][z][c], sA[z], a);
+              b = fmaf(sb[j][z][2 + c], sB[z], b);
+              la = fmaf(lA[z], qs[j][c][z], la);
+              lb = fmaf(lB[z], qs[j][c][z], lb);
+            }
+            sc[j][c] = fmaf(a, cq[j][c], la);
+            sc[j][2 + c] = fmaf(b, cq[j][c], lb);
+          }
+      } else {
+        const __nv_bfloat16 *kp = p.k + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
+#pragma unroll
+        for (int j = 0; j < NTL; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+#pragma unroll
+        for (int z = 0; z < D / 32; ++z) {
+          const uint4 kA = *reinterpret_cast<const uint4 *>(kp + tokA * D + z * 32 + t * 8);
+          const uint4 kB = *reinterpret_cast<const uint4 *>(kp + tokB * D + z * 32 + t * 8);
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(qraw + ((cg * NTL + j) * 8 + g) * C::kQStride + z * 32 + t * 8);
+            mma_bf16(sc[j], kA.x, kB.x, kA.y, kB.y, q.x, q.y);
+            mma_bf16(sc[j], kA.z, kB.z, kA.w, kB.w, q.z, q.w);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[j][c] *= qk;
+      }
+      if (edge) {
+        const int pA = pos0 + tokA, pB = pos0 + tokB;
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int last = s.last0 + ((cg * NTL + j) * 8 + 2 * t + c) / G;
+            if (pA > last || pA < first) sc[j][c] = -INFINITY;
+            if (pB > last || pB < first) sc[j][2 + c] = -INFINITY;
+          }
+        if (is4) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            if (pA > last_all || pA < first) vpA[b] = 0u;
+            if (pB > last_all || pB < first) vpB[b] = 0u;
+          }
+        }
+      }
+      // ---- references: moved when a logit or a value scale of this page is too far above its own
+      bool up = false;
+#pragma unroll
+      for (int j = 0; j < NTL; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) up |= sc[j][c] > mref[j][c & 1] + kMaxSlack;
+      float svA[NB], svB[NB];
+      if (is4) {
+        up |= !scaled;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          svA[b] = param_scale(vpA[b]);
+          svB[b] = param_scale(vpB[b]);
+          up |= fmaxf(svA[b], svB[b]) * inv_e > kScaleSlack;
+        }
+      }
+      if (__any_sync(0xffffffffu, up)) {
+        float ratio = 1.0f;
+        if (is4) {
+          float mx = 0.0f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(svA[b], svB[b]));
+          mx = column_max(mx);  // the lanes of a column hold all 16 tokens
+          if (!scaled || mx * inv_e > kScaleSlack) {
+            scaled = true;
+            const float ie = 1.0f / fmaxf(__uint_as_float(__float_as_uint(mx) & 0x7f800000u), 0x1p-100f);
+            ratio = ie / inv_e;
+            inv_e = ie;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float m = fmaxf(mref[j][c], column_max(fmaxf(sc[j][c], sc[j][2 + c])));
+            const float f = fast_exp2(mref[j][c] - m);
+            mref[j][c] = m;
+            lsum[j][c] *= f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              lv[j][c][b] *= f;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                acc[j][b][z][c] *= f * ratio;
+                acc[j][b][z][2 + c] *= f * ratio;
+              }
+            }
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NTL; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[j][c] = fast_exp2(sc[j][c] - mref[j][c & 1]);
+#pragma unroll
+      for (int j = 0; j < NTL; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) lsum[j][c] += sc[j][c] + sc[j][2 + c];
+
+      if (is4) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float lA = param_low(vpA[b]), lB = param_low(vpB[b]);
+          const float eA = svA[b] * inv_e, eB = svB[b] * inv_e;
+          uint32_t pb[NTL][2];
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              lv[j][c][b] = fmaf(sc[j][c], lA, fmaf(sc[j][2 + c], lB, lv[j][c][b]));
+            pb[j][0] = transpose8x8(pack_f16(sc[j][0] * eA, sc[j][1] * eA));
+            pb[j][1] = transpose8x8(pack_f16(sc[j][2] * eB, sc[j][3] * eB));
+          }
+          const unsigned char *vb = ch + L::OFF_V + b * L::kBlock + g * 4;
+          const uint32_t v0 = *reinterpret_cast<const uint32_t *>(vb + t * 32);
+          const uint32_t v1 = *reinterpret_cast<const uint32_t *>(vb + (t + 4) * 32);
+          const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vb + (t + 8) * 32);
+          const uint32_t v3 = *reinterpret_cast<const uint32_t *>(vb + (t + 12) * 32);
+          const uint32_t x0 = __byte_perm(v0, v1, 0x5410), x1w = __byte_perm(v0, v1, 0x7632);
+          const uint32_t y0 = __byte_perm(v2, v3, 0x5410), y1w = __byte_perm(v2, v3, 0x7632);
+          const uint32_t xs[4] = {x0, x0 >> 8, x1w, x1w >> 8}, ys[4] = {y0, y0 >> 8, y1w, y1w >> 8};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t a0 = xs[m] & 0x000f000fu, a1 = xs[m] & 0x00f000f0u, a2 = ys[m] & 0x000f000fu,
+                           a3 = ys[m] & 0x00f000f0u;
+#pragma unroll
+            for (int j = 0; j < NTL; ++j) mma_f16(acc[j][b][m], a0, a1, a2, a3, pb[j][0], pb[j][1]);
+          }
+        }
+        ++consumed;
+        dead = release_page<CS, C::PW>(pw, false);
+      } else {
+        // p as two bf16 terms, in the accumulators' unit (2^-24 of the value over the scale reference)
+        const __nv_bfloat16 *vp = p.v + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
+        const float unit16 = 0x1p-24f * inv_e;
+        uint32_t ph[NTL][2], pl[NTL][2];
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float u0 = sc[j][2 * z] * unit16, u1 = sc[j][2 * z + 1] * unit16;
+            const uint32_t hi = pack_bf16(u0, u1);
+            pl[j][z] = transpose8x8(pack_bf16(u0 - __uint_as_float(hi << 16), u1 - __uint_as_float(hi & 0xffff0000u)));
+            ph[j][z] = transpose8x8(hi);
+          }
+        bool see[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int pos = pos0 + t + 4 * z;
+          see[z] = pos <= last_all && pos >= first;
+        }
+        const __nv_bfloat162 sixteen = __floats2bfloat162_rn(16.0f, 16.0f);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint4 w[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            w[z] = see[z] ? *reinterpret_cast<const uint4 *>(vp + (t + 4 * z) * D + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t u[4] = {(&w[0].x)[m], (&w[1].x)[m], (&w[2].x)[m], (&w[3].x)[m]};
+            const uint32_t a0 = __byte_perm(u[0], u[1], 0x5410), a2 = __byte_perm(u[2], u[3], 0x5410);
+            uint32_t a1 = __byte_perm(u[0], u[1], 0x7632), a3 = __byte_perm(u[2], u[3], 0x7632);
+            const __nv_bfloat162 s1 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a1), sixteen);
+            const __nv_bfloat162 s3 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a3), sixteen);
+            a1 = *reinterpret_cast<const uint32_t *>(&s1);
+            a3 = *reinterpret_cast<const uint32_t *>(&s3);
+#pragma unroll
+            for (int j = 0; j < NTL; ++j) {
+              mma_bf16(acc[j][b][m], a0, a1, a2, a3, ph[j][0], ph[j][1]);
+              mma_bf16(acc[j][b][m], a0, a1, a2, a3, pl[j][0], pl[j][1]);
+            }
+          }
+        }
+      }
+    }
+    // a wait that ran out leaves copies in flight: each is waited for (with a limit) before its slot's memory is reused
+    if (dead) {
+      while (consumed != issued) {
+        mbar_wait(&bars[consumed % C::kStages], (consumed / C::kStages) & 1, p.err);
+        ++consumed;
+      }
+    }
+
+    // ---- values in their own unit, columns summed over their lanes
+    const float unit_e = 0x1p24f / inv_e;
+#pragma unroll
+    for (int j = 0; j < NTL; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        lsum[j][c] = column_sum(lsum[j][c]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float l = column_sum(lv[j][c][b]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            acc[j][b][m][c] = fmaf(acc[j][b][m][c], unit_e, l);
+            acc[j][b][m][2 + c] = fmaf(acc[j][b][m][2 + c], unit_e * 0.0625f, l);
+          }
+        }
+      }
+    // ---- warps joined pairwise, always in the same order; a lane hands over to the same lane
+    __syncthreads();  // the ring is idle
+#pragma unroll 1
+    for (int n = C::PW; n > 1; n = (n + 1) / 2) {
+      const int half = (n + 1) / 2;
+      float4 *buf = reinterpret_cast<float4 *>(smem + ((pw % half) + cg * (C::PW / 2)) * C::kJoin);
+      if (pw >= half && pw < n) {
+#pragma unroll
+        for (int j = 0; j < NTL; ++j) {
+          buf[j * 32 + lane] = make_float4(mref[j][0], mref[j][1], lsum[j][0], lsum[j][1]);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              buf[(NTL + (j * NB + b) * 4 + m) * 32 + lane] =
+                  make_float4(acc[j][b][m][0], acc[j][b][m][1], acc[j][b][m][2], acc[j][b][m][3]);
+        }
+      }
+      __syncthreads();
+      if (pw < n - half) {
+#pragma unroll
+        for (int j = 0; j < NTL; ++j) {
+          const float4 o = buf[j * 32 + lane];
+          const float m0 = fmaxf(mref[j][0], o.x), m1 = fmaxf(mref[j][1], o.y);
+          const float a0 = fast_exp2(mref[j][0] - m0), a1 = fast_exp2(mref[j][1] - m1);
+          const float b0 = fast_exp2(o.x - m0), b1 = fast_exp2(o.y - m1);
+          mref[j][0] = m0;
+          mref[j][1] = m1;
+          lsum[j][0] = fmaf(lsum[j][0], a0, o.z * b0);
+          lsum[j][1] = fmaf(lsum[j][1], a1, o.w * b1);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float4 v = buf[(NTL + (j * NB + b) * 4 + m) * 32 + lane];
+              acc[j][b][m][0] = fmaf(acc[j][b][m][0], a0, v.x * b0);
+              acc[j][b][m][1] = fmaf(acc[j][b][m][1], a1, v.y * b1);
+              acc[j][b][m][2] = fmaf(acc[j][b][m][2], a0, v.z * b0);
+              acc[j][b][m][3] = fmaf(acc[j][b][m][3], a1, v.w * b1);
+            }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- the row's result, or a record of its part
+    const int c_first = static_cast<int>(rb / share), c_last = static_cast<int>((re - 1) / share);
+    const size_t slot = static_cast<size_t>(blockIdx.x) + s.row;
+    if (pw == 0) {
+#pragma unroll
+      for (int j = 0; j < NTL; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = (cg * NTL + j) * 8 + 2 * t + c;
+          if (col >= M) continue;
+          const float l = lsum[j][c];
+          if (c_first == c_last) {
+            const int i = col / G;
+            const size_t o = static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + (col - i * G);
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            if (g == 0) {
+              p.lse[o] = l != 0.0f ? (mref[j][c] + log2f(l)) * kLn2 : -INFINITY;
+              if (kView && l == 0.0f) set_error(p.err, kErrLength);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              float v[8];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                v[2 * m] = acc[j][b][m][c] * inv;
+                v[2 * m + 1] = acc[j][b][m][2 + c] * inv;
+              }
+              *reinterpret_cast<uint4 *>(p.out + o * D + b * 64 + g * 8) = Vec16<__nv_bfloat16>::pack(v);
+            }
+          } else {
+            float *rec = p.part + (slot * p.ncol + col) * D + g * 8;
+            if (g == 0) __stcg(&p.ml[slot * p.ncol + col], make_float2(mref[j][c], l));
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              __stcg(reinterpret_cast<float4 *>(rec + b * 64),
+                     make_float4(acc[j][b][0][c], acc[j][b][0][2 + c], acc[j][b][1][c], acc[j][b][1][2 + c]));
+              __stcg(reinterpret_cast<float4 *>(rec + b * 64 + 4),
+                     make_float4(acc[j][b][2][c], acc[j][b][2][2 + c], acc[j][b][3][c], acc[j][b][3][2 + c]));
+            }
+          }
+        }
+    }
+    if (c_first != c_last) {
+      __syncthreads();
+      if (tid == 0) {
+        const int parts = c_last - c_first + 1;
+        const int old = atom_add_acq_rel_gpu(&p.counters[s.row], 1);
+        s_flag = old == parts - 1;
+        if (s_flag) p.counters[s.row] = 0;  // left at zero for the next call
+      }
+      __syncthreads();
+      if (s_flag) {
+        // part k of the row lies in slot c_first + k + row; weights first, then every thread sums its values in order
+        const int parts = c_last - c_first + 1;
+        const size_t slot0 = static_cast<size_t>(c_first) + s.row;
+        float *w = reinterpret_cast<float *>(smem);  // [parts][M] weights over the row's sum
+        float2 *mls = reinterpret_cast<float2 *>(smem);
+        // the maxima and sums come in as pairs; a column's thread turns them into weights in place (first half of a pair)
+        for (int i = tid; i < parts * M; i += C::kThreads) {
+          const int k = i / M, col = i - k * M;
+          mls[i] = __ldcg(&p.ml[(slot0 + k) * p.ncol + col]);
+        }
+        __syncthreads();
+        for (int col = tid; col < M; col += C::kThreads) {
+          float m = kNoMax, l = 0.0f;
+          for (int k = 0; k < parts; ++k) m = fmaxf(m, mls[k * M + col].x);
+          for (int k = 0; k < parts; ++k) {
+            const float2 z = mls[k * M + col];
+            const float f = fast_exp2(z.x - m);
+            l = fmaf(z.y, f, l);
+            w[2 * (k * M + col)] = f;
+          }
+          const int i = col / G;
+          p.lse[static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + (col - i * G)] =
+              l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          if (kView && l == 0.0f) set_error(p.err, kErrLength);
+          w[2 * col + 1] = l != 0.0f ? 1.0f / l : 0.0f;  // of part 0's pair: the factor of the whole column
+        }
+        __syncthreads();
+        for (int i = tid; i < M * (D / 8); i += C::kThreads) {
+          const int col = i / (D / 8), d0 = (i - col * (D / 8)) * 8;
+          float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+          for (int k = 0; k < parts; ++k) {
+            const float *rec = p.part + ((slot0 + k) * p.ncol + col) * D + d0;
+            const float4 a = __ldcg(reinterpret_cast<const float4 *>(rec));
+            const float4 b = __ldcg(reinterpret_cast<const float4 *>(rec + 4));
+            const float f = w[2 * (k * M + col)];
+            v[0] = fmaf(a.x, f, v[0]), v[1] = fmaf(a.y, f, v[1]), v[2] = fmaf(a.z, f, v[2]), v[3] = fmaf(a.w, f, v[3]);
+            v[4] = fmaf(b.x, f, v[4]), v[5] = fmaf(b.y, f, v[5]), v[6] = fmaf(b.z, f, v[6]), v[7] = fmaf(b.w, f, v[7]);
+          }
+          const float inv = w[2 * col + 1];
+#pragma unroll
+          for (int z = 0; z < 8; ++z) v[z] *= inv;
+          const int qi = col / G;
+          const size_t o = static_cast<size_t>(s.qoff + qi) * p.hq + s.h * G + (col - qi * G);
+          *reinterpret_cast<uint4 *>(p.out + o * D + d0) = Vec16<__nv_bfloat16>::pack(v);
+        }
+      }
+    }
+    // the next part's copies write the memory that the joins used: order this proxy's accesses before theirs
+    fence_proxy_async_smem();
+    __syncthreads();
+    x += s.p1 - s.p0;
   }
 }
 
-template <bool kView>
-cudaError_t launch(const PackedArgs &pa, AParams &p, const MapArgs &m, const void *q, void *out, float *lse, int *err,
-                   cudaStream_t s) {
+template <int D, int NTL, int CS, bool kView>
+cudaError_t launch(const AParams &p, cudaStream_t s) {
+  using C = Cfg<D, NTL, CS>;
+  static_assert(C::kMaxGrid <= kMaxCtas, "record slots");
+  static bool ready[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!ready[dev & 63]) {
+    e = cudaFuncSetAttribute(attn_kernel<D, NTL, CS, kView>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+    if (e != cudaSuccess) return e;
+    ready[dev & 63] = true;
+  }
+  return launch_pdl(attn_kernel<D, NTL, CS, kView>, dim3(std::min(device_sm_count() * C::kCtas, C::kMaxGrid)), dim3(C::kThreads), C::BYTES, s,
+                    p);
+}
+
+// Column tiles of 8: up to 4 a warp; wider windows go to two groups of warps that read the same pages.
+template <int D, bool kView>
+cudaError_t launch_tiles(const AParams &p, cudaStream_t s) {
+  const int tiles = (p.ncol + 7) / 8;
+  if (kView || tiles == 1) return launch<D, 1, 1, kView>(p, s);
+  if (tiles == 2) return launch<D, 2, 1, false>(p, s);
+  if (tiles == 3) return launch<D, 3, 1, false>(p, s);
+  if (tiles == 4) return launch<D, 4, 1, false>(p, s);
+  if (tiles <= 6) return launch<D, 3, 2, false>(p, s);
+  return launch<D, 4, 2, false>(p, s);
+}
+
+
+AParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *out, float *lse, void *ws, int ncol,
+               int *err) {
+  AParams p{};
   p.k = static_cast<const __nv_bfloat16 *>(pa.pool.k);
   p.v = static_cast<const __nv_bfloat16 *>(pa.pool.v);
   p.packed = static_cast<const unsigned char *>(pa.packed);
@@ -139,38 +891,44 @@ cudaError_t launch(const PackedArgs &pa, AParams &p, const MapArgs &m, const voi
   p.q = static_cast<const __nv_bfloat16 *>(q);
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
+  p.ncol = ncol;
   p.err = err;
-  const int64_t blocks = (static_cast<int64_t>(p.rows) * p.hq + 7) / 8;
-  if (pa.pool.d == 128)
-    return launch_pdl(attn_kernel<128, kView>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
-  return launch_pdl(attn_kernel<64, kView>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
+  const size_t rows = static_cast<size_t>(m.R) * p.hkv, slots = rows + kMaxCtas;
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  p.counters = reinterpret_cast<int *>(w);
+  w += (rows * 4 + 255) / 256 * 256;
+  p.ml = reinterpret_cast<float2 *>(w);
+  w += (slots * ncol * 8 + 255) / 256 * 256;
+  p.part = reinterpret_cast<float *>(w);
+  return p;
 }
 
 }  // namespace
 
 size_t packed_workspace_bytes(int R, int hkv, int hq, int d, int max_q) {
-  (void)R, (void)hkv, (void)hq, (void)d, (void)max_q;
-  return 256;
+  const size_t rows = static_cast<size_t>(R) * hkv, slots = rows + kMaxCtas;
+  const size_t ncol = static_cast<size_t>(hq / hkv) * max_q;
+  return (rows * 4 + 255) / 256 * 256 + (slots * ncol * 8 + 255) / 256 * 256 + slots * ncol * d * 4;
 }
 
 cudaError_t launch_propose_packed(const PackedArgs &pa, const MapArgs &m, const ViewArgs &v, const void *q, void *out,
                                   float *lse, void *ws, int *err, cudaStream_t s) {
-  (void)ws;
-  AParams p{};
+  AParams p = params(pa, m, q, out, lse, ws, pa.pool.hq / pa.pool.hkv, err);
   p.view = v;
-  p.rows = m.R;
-  return launch<true>(pa, p, m, q, out, lse, err, s);
+  p.max_q = 1;
+  p.total_q = m.R;
+  return pa.pool.d == 128 ? launch_tiles<128, true>(p, s) : launch_tiles<64, true>(p, s);
 }
 
 cudaError_t launch_verify_packed(const PackedArgs &pa, const MapArgs &m, int max_q, int total_q,
                                  const int32_t *q_offsets, const int32_t *q_start, const void *q, void *out,
                                  float *lse, void *ws, int *err, cudaStream_t s) {
-  (void)ws, (void)max_q;
-  AParams p{};
+  AParams p = params(pa, m, q, out, lse, ws, pa.pool.hq / pa.pool.hkv * max_q, err);
   p.q_offsets = q_offsets;
   p.q_start = q_start;
-  p.rows = total_q;
-  return launch<false>(pa, p, m, q, out, lse, err, s);
+  p.max_q = max_q;
+  p.total_q = total_q;
+  return pa.pool.d == 128 ? launch_tiles<128, false>(p, s) : launch_tiles<64, false>(p, s);
 }
 
 }  // namespace kap
