@@ -23,6 +23,7 @@ KAP_FALLBACK_FULL = 1
 KAP_BF16 = 0
 KAP_F32 = 1
 PAGE = 16
+_PACKED_BLOCK = 1152  # bytes of a packed block: 64 dims of K and V of 16 tokens, codes and parameters
 
 _lock = threading.Lock()
 _lib = None
@@ -114,6 +115,8 @@ def _declare(lib):
 def load():
     """Loads libkap.so (in-tree). Raises if it is missing: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -141,7 +144,7 @@ def _ptr(t: Optional[torch.Tensor]):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
@@ -149,11 +152,32 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on_current_device(*tensors):
-    """All tensors on the current CUDA device: the calls launch there."""
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
-            raise ValueError(f"expected tensors on the current CUDA device, got one on {t.device}")
+def _here(t: torch.Tensor) -> int:
+    """The current CUDA device, on which a call launches and on which `t`, its first tensor, has to be."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
+        raise ValueError(f"expected tensors on the current CUDA device {dev}, got one on {t.device}")
+    return dev
+
+
+def _at(t: Optional[torch.Tensor], dev: int, dtype: Optional[torch.dtype] = None, name: str = "a tensor"):
+    """Address of a contiguous tensor on device `dev` (None for None)."""
+    if t is None:
+        return None
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device {dev}, got one on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; the device's current stream without building a Python object for it."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _i32(t, name):
@@ -274,24 +298,24 @@ class PackedPool:
     packed: torch.Tensor
     k_summary: Optional[torch.Tensor] = None
 
-    def _base(self) -> _Pool:
-        p = self.pool._c()
-        if self.pool.dtype != torch.bfloat16:
+    def _base(self, dev: Optional[int] = None) -> _Pool:
+        pool, ks = self.pool, self.k_summary
+        k, v, x = pool.k_pages, pool.v_pages, self.packed
+        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
             raise TypeError("a pool with packed pages must be bfloat16")
-        if self.k_summary is not None and (self.k_summary.dtype != torch.float32 or tuple(self.k_summary.shape) != (
-                p.num_pages + self.packed.shape[0], p.num_kv_heads, p.head_dim)):
-            raise ValueError("k_summary must be fp32 [num_pages + num_packed][Hkv][d]")
-        p.k_summary = _ptr(self.k_summary)
-        return p
-
-    def _c(self) -> _Packed:
-        p = self._base()
-        x = self.packed
-        if x.dtype != torch.uint8 or x.dim() != 3 or tuple(x.shape[1:]) != (
-                p.num_kv_heads, int(load().kap_packed_chunk_bytes(p.head_dim))):
+        if k.dim() != 4 or k.shape != v.shape or k.shape[2] != PAGE:
+            raise ValueError("k_pages/v_pages must both be [num_pages][Hkv][16][d]")
+        P, hkv, _, d = k.shape
+        if x.dtype != torch.uint8 or x.dim() != 3 or x.shape[1] != hkv or x.shape[2] != d // 64 * _PACKED_BLOCK:
             raise ValueError("packed must be uint8 [num_packed][Hkv][kap_packed_chunk_bytes(d)]")
-        _on_current_device(x, self.pool.k_pages, self.pool.v_pages, self.k_summary)
-        return _Packed(p, x.shape[0], _ptr(x))
+        if ks is not None and (ks.dtype != torch.float32 or tuple(ks.shape) != (P + x.shape[0], hkv, d)):
+            raise ValueError("k_summary must be fp32 [num_pages + num_packed][Hkv][d]")
+        dev = _here(k) if dev is None else dev
+        return _Pool(P, PAGE, hkv, pool.num_q_heads, d, KAP_BF16, _at(k, dev), _at(v, dev), _at(ks, dev))
+
+    def _c(self, dev: Optional[int] = None) -> _Packed:
+        dev = _here(self.packed) if dev is None else dev
+        return _Packed(self._base(dev), self.packed.shape[0], _at(self.packed, dev))
 
     @property
     def dtype(self):
@@ -555,13 +579,14 @@ def kap_packed_chunk_bytes(d: int) -> int:
 
 
 def _pack(fn: str, pool: PackedPool, src: torch.Tensor, dst: torch.Tensor, stream):
-    lib = load()
+    f = getattr(load(), fn)
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src_pages and dst_pages must be 1-D and of equal length")
-    _on_current_device(src, dst)
-    p = pool._c()
-    _check(fn, getattr(lib, fn)(ctypes.byref(p), _i32(src, "src_pages"), _i32(dst, "dst_pages"), src.numel(),
-                                _stream(stream)))
+    dev = _here(pool.packed)
+    s, d = _at(src, dev, torch.int32, "src_pages"), _at(dst, dev, torch.int32, "dst_pages")
+    st = f(ctypes.byref(pool._c(dev)), s, d, src.shape[0], _raw_stream(stream, dev))
+    if st:
+        _check(fn, st)
 
 
 def kap_pack_pages(pool: PackedPool, src_pages: torch.Tensor, dst_pages: torch.Tensor, stream=None):
@@ -578,38 +603,62 @@ def kap_packed_workspace_size(R: int, hkv: int, hq: int, d: int, max_q: int = 1)
     return int(load().kap_packed_workspace_size(R, hkv, hq, d, max_q))
 
 
-def _check_attention(pool: PackedPool, rows: int, q, out, lse, workspace):
-    hq, d = pool.pool.num_q_heads, int(pool.pool.k_pages.shape[3])
-    if q.dtype != pool.dtype or out.dtype != pool.dtype or lse.dtype != torch.float32:
-        raise TypeError("q/out must have the pool dtype and lse fp32")
-    if tuple(q.shape) != (rows, hq, d) or out.shape != q.shape or tuple(lse.shape) != (rows, hq):
-        raise ValueError(f"q and out must be [{rows}][{hq}][{d}] and lse [{rows}][{hq}]")
-    _on_current_device(q, out, lse, workspace)
+def _attention_args(pool: PackedPool, rows: int, q, out, lse, workspace):
+    """(device, addresses of q, out, lse, workspace, bytes of the workspace) after their checks."""
+    k = pool.pool.k_pages
+    shape = (rows, pool.pool.num_q_heads, k.shape[3])
+    if tuple(q.shape) != shape or tuple(out.shape) != shape or tuple(lse.shape) != shape[:2]:
+        raise ValueError(f"q and out must be {list(shape)} and lse {list(shape[:2])}")
+    dev = _here(pool.packed)
+    bf16 = torch.bfloat16
+    return (dev, _at(q, dev, bf16, "q"), _at(out, dev, bf16, "out"), _at(lse, dev, torch.float32, "lse"),
+            _at(workspace, dev, None, "workspace"), workspace.nbytes)
+
+
+def _map_c(m: PageMap, dev: int) -> _Map:
+    bt, i32 = m.block_table, torch.int32
+    if bt.dim() != 2:
+        raise ValueError("block_table must be [R][max_pages]")
+    R, mp = bt.shape
+    if m.ctx_len.numel() != R or (m.seq_len is not None and m.seq_len.numel() != R):
+        raise ValueError("ctx_len/seq_len must have R entries")
+    return _Map(R, mp, _at(bt, dev, i32, "block_table"), _at(m.ctx_len, dev, i32, "ctx_len"),
+                _at(m.seq_len, dev, i32, "seq_len"))
 
 
 def kap_attn_propose_packed(pool: PackedPool, pmap: PageMap, view: View, q: torch.Tensor, out: torch.Tensor,
                             lse: torch.Tensor, workspace: torch.Tensor, stream=None):
     """kap_attn_propose over a pool with packed pages (workspace: kap_packed_workspace_size(..., max_q=1))."""
-    lib = load()
-    _check_attention(pool, int(pmap.block_table.shape[0]), q, out, lse, workspace)
-    p, m, v = pool._c(), pmap._c(), view._c()
-    _check("kap_attn_propose_packed", lib.kap_attn_propose_packed(
-        ctypes.byref(p), ctypes.byref(m), ctypes.byref(v), _ptr(q), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    f = load().kap_attn_propose_packed
+    R, i32 = pmap.block_table.shape[0], torch.int32
+    dev, aq, ao, al, aw, nw = _attention_args(pool, R, q, out, lse, workspace)
+    rows, cap = view.rows_per_seq, view.cap
+    if tuple(view.block_table.shape) != (R, rows, cap) or view.logical_page.shape != view.block_table.shape or \
+            tuple(view.n_entries.shape) != (R, rows) or view.n_selected.shape != view.n_entries.shape:
+        raise ValueError("the view's tensors must be [R][rows_per_seq][cap] and [R][rows_per_seq]")
+    v = _View(rows, cap, _at(view.block_table, dev, i32, "view.block_table"),
+              _at(view.logical_page, dev, i32, "view.logical_page"), _at(view.n_entries, dev, i32, "view.n_entries"),
+              _at(view.n_selected, dev, i32, "view.n_selected"), 0)
+    st = f(ctypes.byref(pool._c(dev)), ctypes.byref(_map_c(pmap, dev)), ctypes.byref(v), aq, ao, al, aw, nw,
+           _raw_stream(stream, dev))
+    if st:
+        _check("kap_attn_propose_packed", st)
 
 
 def kap_attn_verify_packed(pool: PackedPool, pmap: PageMap, vp: VerifyPolicy, q: torch.Tensor, out: torch.Tensor,
                            lse: torch.Tensor, workspace: torch.Tensor, stream=None):
     """kap_attn_verify over a pool with packed pages; windows of one row are decode attention over the whole table."""
-    lib = load()
-    _check_attention(pool, vp.total_q, q, out, lse, workspace)
-    R = int(pmap.block_table.shape[0])
+    f = load().kap_attn_verify_packed
+    R, i32 = pmap.block_table.shape[0], torch.int32
+    dev, aq, ao, al, aw, nw = _attention_args(pool, vp.total_q, q, out, lse, workspace)
     if vp.q_offsets.numel() != R + 1 or vp.q_start_pos.numel() != R:
         raise ValueError("q_offsets must have R + 1 and q_start_pos R entries")
-    p, m, v = pool._c(), pmap._c(), vp._c()
-    _check("kap_attn_verify_packed", lib.kap_attn_verify_packed(
-        ctypes.byref(p), ctypes.byref(m), ctypes.byref(v), _ptr(q), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    v = _Verify(vp.max_q, vp.total_q, _at(vp.q_offsets, dev, i32, "q_offsets"),
+                _at(vp.q_start_pos, dev, i32, "q_start_pos"))
+    st = f(ctypes.byref(pool._c(dev)), ctypes.byref(_map_c(pmap, dev)), ctypes.byref(v), aq, ao, al, aw, nw,
+           _raw_stream(stream, dev))
+    if st:
+        _check("kap_attn_verify_packed", st)
 
 
 def kap_logprobs_workspace_size(rows: int, vocab: int) -> int:
@@ -622,35 +671,40 @@ def kap_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: tor
                        stream=None):
     """Log probabilities of tokens [rows] (int32) under logits [rows][vocab] (bf16 or fp32, rows any stride apart), into
     logprobs [rows]; optionally each row's entropy, the token's rank and the top_ids.shape[1] best alternatives."""
-    lib = load()
+    f = load().kap_token_logprobs
     if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda:
         raise TypeError("logits must be a [rows][vocab] bf16 or fp32 CUDA tensor")
-    rows, vocab = int(logits.shape[0]), int(logits.shape[1])
-    stride = int(logits.stride(0)) if rows > 1 else vocab
-    if (vocab > 1 and logits.stride(1) != 1) or stride < vocab:
+    dev = _here(logits)
+    rows, vocab = logits.shape
+    stride, step = logits.stride()
+    if rows <= 1:
+        stride = vocab
+    if (vocab > 1 and step != 1) or stride < vocab:
         raise ValueError("a row of logits must be contiguous and rows must not overlap")
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
-    top_n = int(top_ids.shape[1]) if top_ids is not None and top_ids.dim() == 2 else 0
-    for name, t, dt, shape in (("tokens", tokens, torch.int32, (rows,)), ("logprobs", logprobs, torch.float32, (rows,)),
-                               ("entropy", entropy, torch.float32, (rows,)), ("rank", rank, torch.int32, (rows,)),
-                               ("top_ids", top_ids, torch.int32, (rows, top_n)),
-                               ("top_logprobs", top_logprobs, torch.float32, (rows, top_n))):
-        if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
-            raise ValueError(f"{name} must be {dt} of shape {shape}")
-    _on_current_device(logits, tokens, logprobs, workspace, entropy, rank, top_ids, top_logprobs)
-    dt = KAP_BF16 if logits.dtype == torch.bfloat16 else KAP_F32
-    _check("kap_token_logprobs", lib.kap_token_logprobs(
-        ctypes.c_void_p(logits.data_ptr()), dt, vocab, stride, rows, _ptr(tokens), top_n, _ptr(logprobs),
-        _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    top_n = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != rows or top_logprobs.shape != top_ids.shape:
+            raise ValueError("top_ids and top_logprobs must be [rows][top_n]")
+        top_n = top_ids.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    for t, dt in ((tokens, i32), (logprobs, f32), (entropy, f32), (rank, i32)):
+        if t is not None and (t.dtype != dt or t.dim() != 1 or t.shape[0] != rows):
+            raise ValueError("tokens and rank must be int32, logprobs and entropy fp32, each [rows]")
+    st = f(logits.data_ptr(), KAP_BF16 if logits.dtype == torch.bfloat16 else KAP_F32, vocab, stride, rows,
+           _at(tokens, dev, None, "tokens"), top_n, _at(logprobs, dev, None, "logprobs"),
+           _at(entropy, dev, None, "entropy"), _at(rank, dev, None, "rank"), _at(top_ids, dev, i32, "top_ids"),
+           _at(top_logprobs, dev, f32, "top_logprobs"), _at(workspace, dev, None, "workspace"), workspace.nbytes,
+           _raw_stream(stream, dev))
+    if st:
+        _check("kap_token_logprobs", st)
 
 
-def _check_tables(R: int, **tensors):
-    for name, (t, n) in tensors.items():
-        if t.dim() != 1 or (n is not None and t.numel() != n):
-            raise ValueError(f"{name} must be 1-D" + (f" with {n} entries" if n is not None else ""))
-    _on_current_device(*(t for t, _ in tensors.values()))
+def _vector(t: torch.Tensor, n: Optional[int], dev: int, name: str, dtype=torch.int32):
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be 1-D" + (f" with {n} entries" if n is not None else ""))
+    return _at(t, dev, dtype, name)
 
 
 def kap_extend_tables(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: torch.Tensor,
@@ -659,40 +713,37 @@ def kap_extend_tables(block_table: torch.Tensor, seq_len: torch.Tensor, new_toke
                       seq_len_out: torch.Tensor, granted: torch.Tensor, stream=None):
     """Grows block_table [R][max_pages] by the pages that new_tokens [R] need, taken from the stack free_pages whose
     length is free_count [1], and writes the new tokens' slots and positions (room for slot_out.numel() of them)."""
-    lib = load()
+    f = load().kap_extend_tables
     if block_table.dim() != 2:
         raise ValueError("block_table must be [R][max_pages]")
-    R, mp = int(block_table.shape[0]), int(block_table.shape[1])
-    if slot_out.dtype != torch.int64:
-        raise TypeError("slot_out must be int64")
-    _check_tables(R, seq_len=(seq_len, R), new_tokens=(new_tokens, R), free_pages=(free_pages, None),
-                  free_count=(free_count, 1), free_count_out=(free_count_out, 1), tok_offsets=(tok_offsets, R + 1),
-                  slot_out=(slot_out, None), pos_out=(pos_out, slot_out.numel()), seq_len_out=(seq_len_out, R),
-                  granted=(granted, R))
-    _on_current_device(block_table)
-    _check("kap_extend_tables", lib.kap_extend_tables(
-        R, mp, _i32(block_table, "block_table"), _i32(seq_len, "seq_len"), _i32(new_tokens, "new_tokens"),
-        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count"),
-        _i32(free_count_out, "free_count_out"), _i32(tok_offsets, "tok_offsets"), _ptr(slot_out),
-        _i32(pos_out, "pos_out"), slot_out.numel(), _i32(seq_len_out, "seq_len_out"), _i32(granted, "granted"),
-        _stream(stream)))
+    dev = _here(block_table)
+    R, mp = block_table.shape
+    n = slot_out.shape[0] if slot_out.dim() == 1 else 0
+    st = f(R, mp, _at(block_table, dev, torch.int32, "block_table"), _vector(seq_len, R, dev, "seq_len"),
+           _vector(new_tokens, R, dev, "new_tokens"), _vector(free_pages, None, dev, "free_pages"),
+           free_pages.shape[0], _vector(free_count, 1, dev, "free_count"),
+           _vector(free_count_out, 1, dev, "free_count_out"), _vector(tok_offsets, R + 1, dev, "tok_offsets"),
+           _vector(slot_out, None, dev, "slot_out", torch.int64), _vector(pos_out, n, dev, "pos_out"), n,
+           _vector(seq_len_out, R, dev, "seq_len_out"), _vector(granted, R, dev, "granted"), _raw_stream(stream, dev))
+    if st:
+        _check("kap_extend_tables", st)
 
 
 def kap_release_tables(block_table: torch.Tensor, seq_len: torch.Tensor, released: torch.Tensor,
                        free_pages: torch.Tensor, free_count: torch.Tensor, free_count_out: torch.Tensor,
                        seq_len_out: torch.Tensor, stream=None):
     """Pushes the pages of the requests with released[r] != 0 on the stack free_pages and sets their length to 0."""
-    lib = load()
+    f = load().kap_release_tables
     if block_table.dim() != 2:
         raise ValueError("block_table must be [R][max_pages]")
-    R, mp = int(block_table.shape[0]), int(block_table.shape[1])
-    _check_tables(R, seq_len=(seq_len, R), released=(released, R), free_pages=(free_pages, None),
-                  free_count=(free_count, 1), free_count_out=(free_count_out, 1), seq_len_out=(seq_len_out, R))
-    _on_current_device(block_table)
-    _check("kap_release_tables", lib.kap_release_tables(
-        R, mp, _i32(block_table, "block_table"), _i32(seq_len, "seq_len"), _i32(released, "released"),
-        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count"),
-        _i32(free_count_out, "free_count_out"), _i32(seq_len_out, "seq_len_out"), _stream(stream)))
+    dev = _here(block_table)
+    R, mp = block_table.shape
+    st = f(R, mp, _at(block_table, dev, torch.int32, "block_table"), _vector(seq_len, R, dev, "seq_len"),
+           _vector(released, R, dev, "released"), _vector(free_pages, None, dev, "free_pages"), free_pages.shape[0],
+           _vector(free_count, 1, dev, "free_count"), _vector(free_count_out, 1, dev, "free_count_out"),
+           _vector(seq_len_out, R, dev, "seq_len_out"), _raw_stream(stream, dev))
+    if st:
+        _check("kap_release_tables", st)
 
 
 def kap_selftest_wait_timeout(polls: int, suspend_ns: int, timed_out: torch.Tensor, stream=None):
