@@ -28,6 +28,7 @@
 #include "kap_packed.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kap {
 namespace {
@@ -71,6 +72,7 @@ struct Cfg {
   static constexpr int KS = NB * 4;                      // k-steps of the logits
   static constexpr int kChunk = PackedChunk<D>::BYTES;
   static constexpr int kStages = (D == 128 ? 5 : 8) * CS;
+  static constexpr bool kPairs = NTL <= 2;               // two pages at once: more independent work a warp
   static constexpr int kQStride = D + 8;                 // bf16 elements of a raw query row
   static constexpr int OFF_RING = 0;
   static constexpr int kRing = PW * kStages * kChunk;
@@ -82,7 +84,7 @@ struct Cfg {
   static constexpr int kArea = kRing > kJoinAll ? (kRing > kWeights ? kRing : kWeights)
                                                 : (kJoinAll > kWeights ? kJoinAll : kWeights);
   static constexpr int OFF_QRAW = (kArea + 127) / 128 * 128;
-  static constexpr int OFF_QF = OFF_QRAW + (N * kQStride * 2 + 15) / 16 * 16;  // fp16 fragments [tile][k-step][lane]
+  static constexpr int OFF_QF = OFF_QRAW + (N * kQStride * 2 + 15) / 16 * 16;  // fp16 fragments [tile][k-step / 2][lane][2]
   static constexpr int OFF_QS = OFF_QF + NTL * CS * KS * 32 * 8;               // [N] scale, [N][NB] block sums
   static constexpr int OFF_BAR = OFF_QS + N * (1 + NB) * 4;
   static constexpr int BYTES = OFF_BAR + PW * kStages * 8;
@@ -111,6 +113,42 @@ __device__ __forceinline__ void mma_f16(float *c, uint32_t a0, uint32_t a1, uint
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+      "%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Pairs of fp32: the two columns of a lane in one instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(F2 x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 __device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -215,6 +253,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
   unsigned char *ring = smem + C::OFF_RING + pw * C::kStages * C::kChunk;
   __nv_bfloat16 *qraw = reinterpret_cast<__nv_bfloat16 *>(smem + C::OFF_QRAW);
   uint2 *qfrag = reinterpret_cast<uint2 *>(smem + C::OFF_QF);
+  const uint4 *qfrag4 = reinterpret_cast<const uint4 *>(smem + C::OFF_QF);  // two k-steps
   float *qscale = reinterpret_cast<float *>(smem + C::OFF_QS);
   float *qsum = qscale + C::N;
 
@@ -280,8 +319,16 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
   const int G = p.hq / p.hkv;
   const float qk = rsqrtf(static_cast<float>(D)) * kLog2e;
   const int tokA = (g >> 1) + 4 * (g & 1), tokB = tokA + 8;  // tokens of this lane's two logit rows
-  uint32_t issued = 0, consumed = 0;
+  uint32_t issued = 0, consumed = 0;               // packed pages copied and used by this warp
+  uint32_t in_st = 0, out_st = 0, out_parity = 0;  // their ring slots
   bool dead = false;
+  auto advance = [&]() {
+    ++consumed;
+    if (++out_st == C::kStages) {
+      out_st = 0;
+      out_parity ^= 1;
+    }
+  };
 
   while (x < x1) {
     // ---- the row at x and its part in this share
@@ -333,19 +380,31 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
       }
     };
     int idc, lpc, idn, lpn, batch = 0, ahead = 0;
+    unsigned m4c, m4n, whole;  // packed pages of the two loads; those of the first that every column sees in full
+    auto is_packed = [&](int id) { return id >= p.P16 && id < p.P16 + p.P4; };
+    auto classify = [&]() {
+      const int e = s.p0 + pw + C::PW * (batch * 32 + lane);
+      const int pos0 = (kView ? lpc : e) * kPage, first = kView && e >= s.nsel ? s.ctx : 0;
+      m4c = __ballot_sync(0xffffffffu, is_packed(idc));
+      m4n = __ballot_sync(0xffffffffu, is_packed(idn));
+      whole = m4c & __ballot_sync(0xffffffffu, pos0 + kPage - 1 <= s.last0 && pos0 >= first);
+    };
     load_ids(0, idc, lpc);
     load_ids(1, idn, lpn);
-    auto issue = [&](int k) {  // copies for items below k + 24, as far as the ring has room
-      while (ahead < nit && ahead < k + 24 && issued - consumed < C::kStages) {
-        const int id = __shfl_sync(0xffffffffu, (ahead >> 5) == batch ? idc : idn, ahead & 31);
-        if (id >= p.P16 && id < p.P16 + p.P4) {
-          if (lane == 0 && cg == 0) {
-            const uint32_t st = issued % C::kStages;
-            mbar_arrive_expect_tx(&bars[st], C::kChunk);
-            bulk_g2s(ring + st * C::kChunk, p.packed + (static_cast<size_t>(id - p.P16) * p.hkv + s.h) * C::kChunk,
-                     C::kChunk, &bars[st]);
+    classify();
+    // Copies for items below k + 24, as far as the ring has room; the lane that holds an item's id starts its copy.
+    auto issue = [&](int k) {
+      while (ahead < nit && ahead < k + 24 && issued != consumed + C::kStages) {
+        const bool cur = (ahead >> 5) == batch;
+        if ((cur ? m4c : m4n) >> (ahead & 31) & 1) {
+          if (lane == (ahead & 31) && cg == 0) {
+            const int id = cur ? idc : idn;
+            mbar_arrive_expect_tx(&bars[in_st], C::kChunk);
+            bulk_g2s(ring + in_st * C::kChunk, p.packed + (static_cast<size_t>(id - p.P16) * p.hkv + s.h) * C::kChunk,
+                     C::kChunk, &bars[in_st]);
           }
           ++issued;
+          in_st = in_st + 1 == C::kStages ? 0 : in_st + 1;
         }
         ++ahead;
       }
@@ -378,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     }
     __syncthreads();
     for (int f = tid; f < NTL * CS * C::KS * 32; f += C::kThreads) {
-      const int ln = f & 31, ks = (f >> 5) % C::KS, tile = (f >> 5) / C::KS;
+      const int ln = (f >> 1) & 31, ks = ((f >> 6) % (C::KS / 2)) * 2 + (f & 1), tile = (f >> 6) / (C::KS / 2);
       const int c = tile * 8 + (ln >> 2);
       const int d0 = (ks >> 2) * 64 + (ln & 3) * 16 + ((ks >> 1) & 1) * 8 + (ks & 1) * 2;
       const __nv_bfloat16 *qr = qraw + c * C::kQStride + d0;
@@ -390,21 +449,20 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     if (!dead && CS > 1) issue(0);
 
     // per column of this lane (two a tile): logit factor, block sums, reference, sum, sum p * lowest
-    float cq[NTL][2], qs[NTL][2][NB], mref[NTL][2], lsum[NTL][2], lv[NTL][2][NB], acc[NTL][NB][4][4];
+    F2 cq[NTL], qs[NTL][NB], lsum[NTL], lv[NTL][NB];
+    float mref[NTL][2], acc[NTL][NB][4][4];
 #pragma unroll
-    for (int j = 0; j < NTL; ++j)
+    for (int j = 0; j < NTL; ++j) {
+      const int col = (cg * NTL + j) * 8 + 2 * t;
+      cq[j] = f2(qk * 0x1p24f / qscale[col], qk * 0x1p24f / qscale[col + 1]);
+      mref[j][0] = mref[j][1] = kNoMax;
+      lsum[j] = f2(0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = (cg * NTL + j) * 8 + 2 * t + c;
-        cq[j][c] = qk * 0x1p24f / qscale[col];
-        mref[j][c] = kNoMax;
-        lsum[j][c] = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          qs[j][c][b] = qsum[col * NB + b];
-          lv[j][c][b] = 0.0f;
-        }
+      for (int b = 0; b < NB; ++b) {
+        qs[j][b] = f2(qsum[col * NB + b], qsum[(col + 1) * NB + b]);
+        lv[j][b] = f2(0.0f, 0.0f);
       }
+    }
 #pragma unroll
     for (int j = 0; j < NTL; ++j)
 #pragma unroll
@@ -414,196 +472,194 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[j][b][m][c] = 0.0f;
     float inv_e = 1.0f;       // 1 / reference of the value scales, a power of two
-    bool scaled = false;      // whether a packed page has set it
-    uint2 qreg[NTL == 1 ? C::KS : 1];
-    if (NTL == 1) {
-#pragma unroll
-      for (int ks = 0; ks < C::KS; ++ks) qreg[ks] = qfrag[(cg * C::KS + ks) * 32 + lane];
-    }
+    float sv_limit = -1.0f;   // largest scale that it admits; the first packed page sets both
 
-    for (int k = 0; k < nit; ++k) {
-      if (k > 0 && (k & 31) == 0) {
-        idc = idn;
-        lpc = lpn;
-        load_ids(++batch + 1, idn, lpn);
-      }
-      if (!dead) issue(k);
-      const int id = __shfl_sync(0xffffffffu, idc, k & 31);
-      const int e = s.p0 + pw + C::PW * k;
-      const int pos0 = (kView ? __shfl_sync(0xffffffffu, lpc, k & 31) : e) * kPage;
-      if (id < 0 || id >= p.P16 + p.P4) {
-        if (lane == 0) set_error(p.err, kErrPage);
-        continue;
-      }
-      const bool is4 = id >= p.P16;
-      // tokens hidden from every column, and pages on which some column sees only a part
-      const int last_all = s.last0 + s.nq - 1;
-      const int first = kView && e >= s.nsel ? s.ctx : 0;
-      const bool edge = pos0 + kPage - 1 > s.last0 || pos0 < first;
-      float sc[NTL][4];  // logits (log2 units), then probabilities
-      uint32_t vpA[NB], vpB[NB];
-      const unsigned char *ch = ring + (consumed % C::kStages) * C::kChunk;
-      if (is4) {
-        if (dead) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[consumed % C::kStages], (consumed / C::kStages) & 1, p.err))) {
-          dead = release_page<CS, C::PW>(pw, true);  // nothing more is read; copies in flight are waited for below
-          continue;
-        }
-        float sb[NTL][NB][4];
+    // Moves the references up where a page's logits (page[n][j][4]) or value scales exceed them by too much, and turns
+    // the logits into probabilities over the references (pairs of columns of this lane's two tokens).
+    const int last_all = s.last0 + s.nq - 1;
+    auto probabilities = [&](auto np, float (*sc)[NTL][4], float svmax, F2 (*pA)[NTL], F2 (*pB)[NTL]) {
+      constexpr int NP = decltype(np)::value;
+      auto distances = [&]() {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint2 wA = *reinterpret_cast<const uint2 *>(ch + b * L::kBlock + tokA * 32 + t * 8);
-          const uint2 wB = *reinterpret_cast<const uint2 *>(ch + b * L::kBlock + tokB * 32 + t * 8);
-          const uint32_t a[4] = {wA.x, wA.x >> 8, wA.y, wA.y >> 8}, bb[4] = {wB.x, wB.x >> 8, wB.y, wB.y >> 8};
+        for (int j = 0; j < NTL; ++j) {
+          const F2 m = f2(-mref[j][0], -mref[j][1]);
 #pragma unroll
-          for (int j = 0; j < NTL; ++j) sb[j][b][0] = sb[j][b][1] = sb[j][b][2] = sb[j][b][3] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = a[i] & 0x000f000fu, a1 = bb[i] & 0x000f000fu, a2 = a[i] & 0x00f000f0u,
-                           a3 = bb[i] & 0x00f000f0u;
-#pragma unroll
-            for (int j = 0; j < NTL; ++j) {
-              const uint2 q = NTL == 1 ? qreg[b * 4 + i] : qfrag[((cg * NTL + j) * C::KS + b * 4 + i) * 32 + lane];
-              mma_f16(sb[j][b], a0, a1, a2, a3, q.x, q.y);
-            }
+          for (int n = 0; n < NP; ++n) {
+            pA[n][j] = add2(f2(sc[n][j][0], sc[n][j][1]), m);
+            pB[n][j] = add2(f2(sc[n][j][2], sc[n][j][3]), m);
           }
         }
-        float sA[NB], sB[NB], lA[NB], lB[NB];
+      };
+      distances();
+      float over = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t kA = *reinterpret_cast<const uint32_t *>(ch + L::OFF_KPAR + (b * kPage + tokA) * 4);
-          const uint32_t kB = *reinterpret_cast<const uint32_t *>(ch + L::OFF_KPAR + (b * kPage + tokB) * 4);
-          vpA[b] = *reinterpret_cast<const uint32_t *>(ch + L::OFF_VPAR + (b * kPage + tokA) * 4);
-          vpB[b] = *reinterpret_cast<const uint32_t *>(ch + L::OFF_VPAR + (b * kPage + tokB) * 4);
-          sA[b] = param_scale(kA), lA[b] = param_low(kA), sB[b] = param_scale(kB), lB[b] = param_low(kB);
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int j = 0; j < NTL; ++j) {
+          float a, b, c, d;
+          split(pA[n][j], a, b);
+          split(pB[n][j], c, d);
+          over = fmaxf(over, fmaxf(fmaxf(a, b), fmaxf(c, d)));
+        }
+      if (__any_sync(0xffffffffu, over > kMaxSlack || svmax > sv_limit)) {
+        float ratio = 1.0f;
+        const float mx = column_max(svmax);  // the lanes of a column hold all tokens
+        if (mx > sv_limit) {
+          const float ie = 1.0f / fmaxf(__uint_as_float(__float_as_uint(mx) & 0x7f800000u), 0x1p-100f);
+          ratio = ie / inv_e;
+          inv_e = ie;
+          sv_limit = kScaleSlack / ie;
         }
 #pragma unroll
-        for (int j = 0; j < NTL; ++j)
+        for (int j = 0; j < NTL; ++j) {
+          float f[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float a = sb[j][0][c] * sA[0], b = sb[j][0][2 + c] * sB[0];
-            float la = lA[0] * qs[j][c][0], lb = lB[0] * qs[j][c][0];
+            float m = mref[j][c];
 #pragma unroll
-            for (int z = 1; z < NB; ++z) {
-              a = fmaf(sb[j][z][c], sA[z], a);
-              b = fmaf(sb[j][z][2 + c], sB[z], b);
-              la = fmaf(lA[z], qs[j][c][z], la);
-              lb = fmaf(lB[z], qs[j][c][z], lb);
-            }
-            sc[j][c] = fmaf(a, cq[j][c], la);
-            sc[j][2 + c] = fmaf(b, cq[j][c], lb);
+            for (int n = 0; n < NP; ++n) m = fmaxf(m, fmaxf(sc[n][j][c], sc[n][j][2 + c]));
+            m = column_max(m);
+            f[c] = fast_exp2(mref[j][c] - m);
+            mref[j][c] = m;
           }
-      } else {
-        const __nv_bfloat16 *kp = p.k + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
-#pragma unroll
-        for (int j = 0; j < NTL; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
-#pragma unroll
-        for (int z = 0; z < D / 32; ++z) {
-          const uint4 kA = *reinterpret_cast<const uint4 *>(kp + tokA * D + z * 32 + t * 8);
-          const uint4 kB = *reinterpret_cast<const uint4 *>(kp + tokB * D + z * 32 + t * 8);
-#pragma unroll
-          for (int j = 0; j < NTL; ++j) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(qraw + ((cg * NTL + j) * 8 + g) * C::kQStride + z * 32 + t * 8);
-            mma_bf16(sc[j], kA.x, kB.x, kA.y, kB.y, q.x, q.y);
-            mma_bf16(sc[j], kA.z, kB.z, kA.w, kB.w, q.z, q.w);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NTL; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[j][c] *= qk;
-      }
-      if (edge) {
-        const int pA = pos0 + tokA, pB = pos0 + tokB;
-#pragma unroll
-        for (int j = 0; j < NTL; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int last = s.last0 + ((cg * NTL + j) * 8 + 2 * t + c) / G;
-            if (pA > last || pA < first) sc[j][c] = -INFINITY;
-            if (pB > last || pB < first) sc[j][2 + c] = -INFINITY;
-          }
-        if (is4) {
+          const F2 ff = f2(f[0], f[1]);
+          lsum[j] = mul2(lsum[j], ff);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            if (pA > last_all || pA < first) vpA[b] = 0u;
-            if (pB > last_all || pB < first) vpB[b] = 0u;
+            lv[j][b] = mul2(lv[j][b], ff);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[j][b][z][c] *= f[c & 1] * ratio;
           }
         }
+        distances();
       }
-      // ---- references: moved when a logit or a value scale of this page is too far above its own
-      bool up = false;
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int j = 0; j < NTL; ++j) {
+          float a, b, c, d;
+          split(pA[n][j], a, b);
+          split(pB[n][j], c, d);
+          pA[n][j] = f2(fast_exp2(a), fast_exp2(b));
+          pB[n][j] = f2(fast_exp2(c), fast_exp2(d));
+          lsum[j] = add2(lsum[j], add2(pA[n][j], pB[n][j]));
+        }
+    };
+    // Hides what lies past a column's last token or before `first`.
+    auto hide = [&](float (*sc)[4], int pos0, int first) {
+      const int pA = pos0 + tokA, pB = pos0 + tokB;
 #pragma unroll
       for (int j = 0; j < NTL; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) up |= sc[j][c] > mref[j][c & 1] + kMaxSlack;
-      float svA[NB], svB[NB];
-      if (is4) {
-        up |= !scaled;
+        for (int c = 0; c < 2; ++c) {
+          const int last = s.last0 + ((cg * NTL + j) * 8 + 2 * t + c) / G;
+          if (pA > last || pA < first) sc[j][c] = -INFINITY;
+          if (pB > last || pB < first) sc[j][2 + c] = -INFINITY;
+        }
+    };
+
+    // NP packed pages at once; `edge` (one page only): part of it is hidden from some column.
+    auto packed_pages = [&](auto np, const unsigned char *const *chs, bool edge, int pos0, int first) {
+      constexpr int NP = decltype(np)::value;
+      float sc[NP][NTL][4];
+      uint32_t vpA[NP][NB], vpB[NP][NB];
+      {
+        float sb[NP][NTL][NB][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          svA[b] = param_scale(vpA[b]);
-          svB[b] = param_scale(vpB[b]);
-          up |= fmaxf(svA[b], svB[b]) * inv_e > kScaleSlack;
-        }
-      }
-      if (__any_sync(0xffffffffu, up)) {
-        float ratio = 1.0f;
-        if (is4) {
-          float mx = 0.0f;
+          uint32_t a[NP][4], bb[NP][4];
 #pragma unroll
-          for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(svA[b], svB[b]));
-          mx = column_max(mx);  // the lanes of a column hold all 16 tokens
-          if (!scaled || mx * inv_e > kScaleSlack) {
-            scaled = true;
-            const float ie = 1.0f / fmaxf(__uint_as_float(__float_as_uint(mx) & 0x7f800000u), 0x1p-100f);
-            ratio = ie / inv_e;
-            inv_e = ie;
+          for (int n = 0; n < NP; ++n) {
+            const uint2 wA = *reinterpret_cast<const uint2 *>(chs[n] + b * L::kBlock + tokA * 32 + t * 8);
+            const uint2 wB = *reinterpret_cast<const uint2 *>(chs[n] + b * L::kBlock + tokB * 32 + t * 8);
+            a[n][0] = wA.x, a[n][1] = wA.x >> 8, a[n][2] = wA.y, a[n][3] = wA.y >> 8;
+            bb[n][0] = wB.x, bb[n][1] = wB.x >> 8, bb[n][2] = wB.y, bb[n][3] = wB.y >> 8;
           }
-        }
 #pragma unroll
-        for (int j = 0; j < NTL; ++j)
+          for (int i = 0; i < 4; i += 2) {
+            uint4 q[NTL];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float m = fmaxf(mref[j][c], column_max(fmaxf(sc[j][c], sc[j][2 + c])));
-            const float f = fast_exp2(mref[j][c] - m);
-            mref[j][c] = m;
-            lsum[j][c] *= f;
+            for (int j = 0; j < NTL; ++j) q[j] = qfrag4[((cg * NTL + j) * (C::KS / 2) + b * 2 + i / 2) * 32 + lane];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              lv[j][c][b] *= f;
+            for (int n = 0; n < NP; ++n) {
+              const uint32_t a0 = a[n][i] & 0x000f000fu, a1 = bb[n][i] & 0x000f000fu, a2 = a[n][i] & 0x00f000f0u,
+                             a3 = bb[n][i] & 0x00f000f0u;
+              const uint32_t e0 = a[n][i + 1] & 0x000f000fu, e1 = bb[n][i + 1] & 0x000f000fu,
+                             e2 = a[n][i + 1] & 0x00f000f0u, e3 = bb[n][i + 1] & 0x00f000f0u;
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                acc[j][b][z][c] *= f * ratio;
-                acc[j][b][z][2 + c] *= f * ratio;
+              for (int j = 0; j < NTL; ++j) {
+                if (i == 0) mma_f16_zero(sb[n][j][b], a0, a1, a2, a3, q[j].x, q[j].y);
+                else mma_f16(sb[n][j][b], a0, a1, a2, a3, q[j].x, q[j].y);
+                mma_f16(sb[n][j][b], e0, e1, e2, e3, q[j].z, q[j].w);
               }
             }
           }
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+          F2 sA[NB], sB[NB], lA[NB], lB[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t kA = *reinterpret_cast<const uint32_t *>(chs[n] + L::OFF_KPAR + (b * kPage + tokA) * 4);
+            const uint32_t kB = *reinterpret_cast<const uint32_t *>(chs[n] + L::OFF_KPAR + (b * kPage + tokB) * 4);
+            vpA[n][b] = *reinterpret_cast<const uint32_t *>(chs[n] + L::OFF_VPAR + (b * kPage + tokA) * 4);
+            vpB[n][b] = *reinterpret_cast<const uint32_t *>(chs[n] + L::OFF_VPAR + (b * kPage + tokB) * 4);
+            sA[b] = f2(param_scale(kA), param_scale(kA)), lA[b] = f2(param_low(kA), param_low(kA));
+            sB[b] = f2(param_scale(kB), param_scale(kB)), lB[b] = f2(param_low(kB), param_low(kB));
+          }
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) {
+            F2 a = mul2(f2(sb[n][j][0][0], sb[n][j][0][1]), sA[0]), b = mul2(f2(sb[n][j][0][2], sb[n][j][0][3]), sB[0]);
+            F2 la = mul2(lA[0], qs[j][0]), lb = mul2(lB[0], qs[j][0]);
+#pragma unroll
+            for (int z = 1; z < NB; ++z) {
+              a = fma2(f2(sb[n][j][z][0], sb[n][j][z][1]), sA[z], a);
+              b = fma2(f2(sb[n][j][z][2], sb[n][j][z][3]), sB[z], b);
+              la = fma2(lA[z], qs[j][z], la);
+              lb = fma2(lB[z], qs[j][z], lb);
+            }
+            split(fma2(a, cq[j], la), sc[n][j][0], sc[n][j][1]);
+            split(fma2(b, cq[j], lb), sc[n][j][2], sc[n][j][3]);
+          }
+        }
       }
-#pragma unroll
-      for (int j = 0; j < NTL; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[j][c] = fast_exp2(sc[j][c] - mref[j][c & 1]);
-#pragma unroll
-      for (int j = 0; j < NTL; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) lsum[j][c] += sc[j][c] + sc[j][2 + c];
-
-      if (is4) {
+      if (NP == 1 && edge) {
+        hide(sc[0], pos0, first);
+        // a token that no column sees: its parameters may hold anything
+        const bool hA = pos0 + tokA > last_all || pos0 + tokA < first, hB = pos0 + tokB > last_all || pos0 + tokB < first;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float lA = param_low(vpA[b]), lB = param_low(vpB[b]);
-          const float eA = svA[b] * inv_e, eB = svB[b] * inv_e;
+          if (hA) vpA[0][b] = 0u;
+          if (hB) vpB[0][b] = 0u;
+        }
+      }
+      float svmax = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) svmax = fmaxf(svmax, fmaxf(param_scale(vpA[n][b]), param_scale(vpB[n][b])));
+      F2 pA[NP][NTL], pB[NP][NTL];
+      probabilities(np, sc, svmax, pA, pB);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+          const float fA = param_low(vpA[n][b]), fB = param_low(vpB[n][b]);
+          const float ea = param_scale(vpA[n][b]) * inv_e, eb = param_scale(vpB[n][b]) * inv_e;
+          const F2 lA = f2(fA, fA), lB = f2(fB, fB), eA = f2(ea, ea), eB = f2(eb, eb);
           uint32_t pb[NTL][2];
 #pragma unroll
           for (int j = 0; j < NTL; ++j) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              lv[j][c][b] = fmaf(sc[j][c], lA, fmaf(sc[j][2 + c], lB, lv[j][c][b]));
-            pb[j][0] = transpose8x8(pack_f16(sc[j][0] * eA, sc[j][1] * eA));
-            pb[j][1] = transpose8x8(pack_f16(sc[j][2] * eB, sc[j][3] * eB));
+            lv[j][b] = fma2(pA[n][j], lA, fma2(pB[n][j], lB, lv[j][b]));
+            float x, y;
+            split(mul2(pA[n][j], eA), x, y);
+            pb[j][0] = transpose8x8(pack_f16(x, y));
+            split(mul2(pB[n][j], eB), x, y);
+            pb[j][1] = transpose8x8(pack_f16(x, y));
           }
-          const unsigned char *vb = ch + L::OFF_V + b * L::kBlock + g * 4;
+          const unsigned char *vb = chs[n] + L::OFF_V + b * L::kBlock + g * 4;
           const uint32_t v0 = *reinterpret_cast<const uint32_t *>(vb + t * 32);
           const uint32_t v1 = *reinterpret_cast<const uint32_t *>(vb + (t + 4) * 32);
           const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vb + (t + 8) * 32);
@@ -619,78 +675,161 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
             for (int j = 0; j < NTL; ++j) mma_f16(acc[j][b][m], a0, a1, a2, a3, pb[j][0], pb[j][1]);
           }
         }
-        ++consumed;
-        dead = release_page<CS, C::PW>(pw, false);
-      } else {
-        // p as two bf16 terms, in the accumulators' unit (2^-24 of the value over the scale reference)
-        const __nv_bfloat16 *vp = p.v + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
-        const float unit16 = 0x1p-24f * inv_e;
-        uint32_t ph[NTL][2], pl[NTL][2];
+      }
+    };
+
+    // One 16-bit page, straight from global memory: these are the few a view's or a table's tail has.
+    auto page16 = [&](int id, bool edge, int pos0, int first) {
+      float sc[1][NTL][4];
+      const __nv_bfloat16 *kp = p.k + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
 #pragma unroll
-        for (int j = 0; j < NTL; ++j)
+      for (int j = 0; j < NTL; ++j) sc[0][j][0] = sc[0][j][1] = sc[0][j][2] = sc[0][j][3] = 0.0f;
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const float u0 = sc[j][2 * z] * unit16, u1 = sc[j][2 * z + 1] * unit16;
-            const uint32_t hi = pack_bf16(u0, u1);
-            pl[j][z] = transpose8x8(pack_bf16(u0 - __uint_as_float(hi << 16), u1 - __uint_as_float(hi & 0xffff0000u)));
-            ph[j][z] = transpose8x8(hi);
-          }
-        bool see[4];
+      for (int z = 0; z < D / 32; ++z) {
+        const uint4 kA = *reinterpret_cast<const uint4 *>(kp + tokA * D + z * 32 + t * 8);
+        const uint4 kB = *reinterpret_cast<const uint4 *>(kp + tokB * D + z * 32 + t * 8);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int pos = pos0 + t + 4 * z;
-          see[z] = pos <= last_all && pos >= first;
+        for (int j = 0; j < NTL; ++j) {
+          const uint4 q = *reinterpret_cast<const uint4 *>(qraw + ((cg * NTL + j) * 8 + g) * C::kQStride + z * 32 + t * 8);
+          mma_bf16(sc[0][j], kA.x, kB.x, kA.y, kB.y, q.x, q.y);
+          mma_bf16(sc[0][j], kA.z, kB.z, kA.w, kB.w, q.z, q.w);
         }
-        const __nv_bfloat162 sixteen = __floats2bfloat162_rn(16.0f, 16.0f);
+      }
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          uint4 w[4];
+      for (int j = 0; j < NTL; ++j)
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            w[z] = see[z] ? *reinterpret_cast<const uint4 *>(vp + (t + 4 * z) * D + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 4; ++c) sc[0][j][c] *= qk;
+      if (edge) hide(sc[0], pos0, first);
+      F2 pA[1][NTL], pB[1][NTL];
+      probabilities(std::integral_constant<int, 1>{}, sc, -INFINITY, pA, pB);
+      // p as two bf16 terms, in the accumulators' unit (2^-24 of the value over the scale reference)
+      const __nv_bfloat16 *vp = p.v + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
+      const float unit16 = 0x1p-24f * inv_e;
+      uint32_t ph[NTL][2], pl[NTL][2];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t u[4] = {(&w[0].x)[m], (&w[1].x)[m], (&w[2].x)[m], (&w[3].x)[m]};
-            const uint32_t a0 = __byte_perm(u[0], u[1], 0x5410), a2 = __byte_perm(u[2], u[3], 0x5410);
-            uint32_t a1 = __byte_perm(u[0], u[1], 0x7632), a3 = __byte_perm(u[2], u[3], 0x7632);
-            const __nv_bfloat162 s1 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a1), sixteen);
-            const __nv_bfloat162 s3 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a3), sixteen);
-            a1 = *reinterpret_cast<const uint32_t *>(&s1);
-            a3 = *reinterpret_cast<const uint32_t *>(&s3);
+      for (int j = 0; j < NTL; ++j)
 #pragma unroll
-            for (int j = 0; j < NTL; ++j) {
-              mma_bf16(acc[j][b][m], a0, a1, a2, a3, ph[j][0], ph[j][1]);
-              mma_bf16(acc[j][b][m], a0, a1, a2, a3, pl[j][0], pl[j][1]);
+        for (int z = 0; z < 2; ++z) {
+          float u0, u1;
+          split(z ? pB[0][j] : pA[0][j], u0, u1);
+          u0 *= unit16, u1 *= unit16;
+          const uint32_t hi = pack_bf16(u0, u1);
+          pl[j][z] = transpose8x8(pack_bf16(u0 - __uint_as_float(hi << 16), u1 - __uint_as_float(hi & 0xffff0000u)));
+          ph[j][z] = transpose8x8(hi);
+        }
+      bool see[4];  // rows that no column sees may hold anything
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int pos = pos0 + t + 4 * z;
+        see[z] = pos <= last_all && pos >= first;
+      }
+      const __nv_bfloat162 sixteen = __floats2bfloat162_rn(16.0f, 16.0f);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint4 w[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          w[z] = see[z] ? *reinterpret_cast<const uint4 *>(vp + (t + 4 * z) * D + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t u[4] = {(&w[0].x)[m], (&w[1].x)[m], (&w[2].x)[m], (&w[3].x)[m]};
+          const uint32_t a0 = __byte_perm(u[0], u[1], 0x5410), a2 = __byte_perm(u[2], u[3], 0x5410);
+          uint32_t a1 = __byte_perm(u[0], u[1], 0x7632), a3 = __byte_perm(u[2], u[3], 0x7632);
+          const __nv_bfloat162 s1 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a1), sixteen);
+          const __nv_bfloat162 s3 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a3), sixteen);
+          a1 = *reinterpret_cast<const uint32_t *>(&s1);
+          a3 = *reinterpret_cast<const uint32_t *>(&s3);
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) {
+            mma_bf16(acc[j][b][m], a0, a1, a2, a3, ph[j][0], ph[j][1]);
+            mma_bf16(acc[j][b][m], a0, a1, a2, a3, pl[j][0], pl[j][1]);
+          }
+        }
+      }
+    };
+
+    // Waits for the next page of the ring; false (for every lane) when the wait ran out.
+    auto arrived = [&]() { return __all_sync(0xffffffffu, mbar_wait(&bars[out_st], out_parity, p.err)) != 0; };
+    for (int k = 0; k < nit;) {
+      if ((k >> 5) != batch) {
+        idc = idn;
+        lpc = lpn;
+        load_ids(++batch + 1, idn, lpn);
+        classify();
+      }
+      if (!dead) issue(k);
+      const int kk = k & 31;
+      if (whole >> kk & 1) {
+        const bool two = C::kPairs && (whole >> kk & 3) == 3;
+        if (!dead) {
+          const unsigned char *chs[2] = {ring + out_st * C::kChunk, nullptr};
+          bool ok = arrived();
+          if (ok) advance();
+          if (ok && two) {
+            chs[1] = ring + out_st * C::kChunk;
+            ok = arrived();
+            if (ok) {
+              advance();
+              packed_pages(std::integral_constant<int, 2>{}, chs, false, 0, 0);
             }
+          } else if (ok) {
+            packed_pages(std::integral_constant<int, 1>{}, chs, false, 0, 0);
           }
+          dead = release_page<CS, C::PW>(pw, !ok);  // from then on nothing is read; what is in flight is waited for below
         }
+        k += two ? 2 : 1;
+        continue;
+      }
+      const int id = __shfl_sync(0xffffffffu, idc, kk);
+      const int e = s.p0 + pw + C::PW * k;
+      const int pos0 = (kView ? __shfl_sync(0xffffffffu, lpc, kk) : e) * kPage, first = kView && e >= s.nsel ? s.ctx : 0;
+      ++k;
+      if (m4c >> kk & 1) {
+        if (dead) continue;
+        const unsigned char *chs[1] = {ring + out_st * C::kChunk};
+        const bool ok = arrived();
+        if (ok) {
+          advance();
+          packed_pages(std::integral_constant<int, 1>{}, chs, true, pos0, first);
+        }
+        dead = release_page<CS, C::PW>(pw, !ok);
+      } else if (id >= 0 && id < p.P16) {
+        page16(id, pos0 + kPage - 1 > s.last0 || pos0 < first, pos0, first);
+      } else if (lane == 0) {
+        set_error(p.err, kErrPage);
       }
     }
     // a wait that ran out leaves copies in flight: each is waited for (with a limit) before its slot's memory is reused
     if (dead) {
       while (consumed != issued) {
-        mbar_wait(&bars[consumed % C::kStages], (consumed / C::kStages) & 1, p.err);
-        ++consumed;
+        mbar_wait(&bars[out_st], out_parity, p.err);
+        advance();
       }
     }
 
     // ---- values in their own unit, columns summed over their lanes
     const float unit_e = 0x1p24f / inv_e;
+    float lr[NTL][2];
 #pragma unroll
-    for (int j = 0; j < NTL; ++j)
+    for (int j = 0; j < NTL; ++j) {
+      split(lsum[j], lr[j][0], lr[j][1]);
+      lr[j][0] = column_sum(lr[j][0]);
+      lr[j][1] = column_sum(lr[j][1]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        lsum[j][c] = column_sum(lsum[j][c]);
+      for (int b = 0; b < NB; ++b) {
+        float l[2];
+        split(lv[j][b], l[0], l[1]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float l = column_sum(lv[j][c][b]);
+        for (int c = 0; c < 2; ++c) {
+          l[c] = column_sum(l[c]);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            acc[j][b][m][c] = fmaf(acc[j][b][m][c], unit_e, l);
-            acc[j][b][m][2 + c] = fmaf(acc[j][b][m][2 + c], unit_e * 0.0625f, l);
+            acc[j][b][m][c] = fmaf(acc[j][b][m][c], unit_e, l[c]);
+            acc[j][b][m][2 + c] = fmaf(acc[j][b][m][2 + c], unit_e * 0.0625f, l[c]);
           }
         }
       }
+    }
     // ---- warps joined pairwise, always in the same order; a lane hands over to the same lane
     __syncthreads();  // the ring is idle
 #pragma unroll 1
@@ -700,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
       if (pw >= half && pw < n) {
 #pragma unroll
         for (int j = 0; j < NTL; ++j) {
-          buf[j * 32 + lane] = make_float4(mref[j][0], mref[j][1], lsum[j][0], lsum[j][1]);
+          buf[j * 32 + lane] = make_float4(mref[j][0], mref[j][1], lr[j][0], lr[j][1]);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -719,8 +858,8 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
           const float b0 = fast_exp2(o.x - m0), b1 = fast_exp2(o.y - m1);
           mref[j][0] = m0;
           mref[j][1] = m1;
-          lsum[j][0] = fmaf(lsum[j][0], a0, o.z * b0);
-          lsum[j][1] = fmaf(lsum[j][1], a1, o.w * b1);
+          lr[j][0] = fmaf(lr[j][0], a0, o.z * b0);
+          lr[j][1] = fmaf(lr[j][1], a1, o.w * b1);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -746,7 +885,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         for (int c = 0; c < 2; ++c) {
           const int col = (cg * NTL + j) * 8 + 2 * t + c;
           if (col >= M) continue;
-          const float l = lsum[j][c];
+          const float l = lr[j][c];
           if (c_first == c_last) {
             const int i = col / G;
             const size_t o = static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + (col - i * G);
