@@ -1,110 +1,481 @@
 // k_logprobs.cu - log probabilities of given tokens, entropy, rank and the best alternatives (sm_103a).
 //
-// One CTA per row: the row's maximum, then sum exp(x - max), the entropy's sum and the token's rank in a second pass,
-// then one pass per alternative for the next token in the order (logit descending, lower id first, NaN last).
+// Mathematics, in base 2 (c = log2 e): with a reference M, y_i = x_i c - M, S = sum 2^y_i and T = sum 2^y_i y_i,
+//   log p_t = ln 2 (y_t - log2 S),   entropy = ln 2 (log2 S - T / S).
+// M is a number of its own (the rounded product of a maximum and c), so y_i has one rounding and partial sums of
+// different references join by powers of two. Logits below -1e7 are lifted there on the way in: their 2^y is 0 all the
+// same and the entropy's 0 * y stays 0 for -infinity. Rows whose maximum lies outside (-9e5, 1e6), where that would
+// distort or M's own rounding would leave a large y, are summed again from x - max.
+// Rank: tokens before the given one count with >= on the pieces of the row that lie before it and with > behind it.
+// Alternatives: the row is cut into at most 257 tiles whose maxima are kept. A token among the first n of the order lies
+// in one of the first n tiles by (maximum, position): every tile before its own holds a token that comes before it. So
+// only those n tiles are read again (from L2), and the n-th tile's maximum bars nearly all of their tokens.
+//
+// Bound by HBM: one pass over the logits; at bf16 the exponential unit (16 a cycle and SM) would allow 1.36 times the
+// measured copy rate, so the loop is kept to about 7 instructions a logit with packed bf16 compares and maxima. A warp
+// streams chunks of 512 logits with the next chunk's loads in flight and its own running sums: no barriers. Rows that are
+// too few to fill the GPU are split over CTAs; the last one to finish a row joins the parts in their order.
 #include "kap_device.cuh"
 #include "kap_launch.h"
+
+#include <algorithm>
 
 namespace kap {
 namespace {
 
 constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kChunk = 512;              // logits of a warp's step, 16 a lane
+constexpr int kMaxTiles = 257;           // tiles of a row whose maxima are kept
+constexpr int kMaxSplit = 32;            // CTAs of a row
+constexpr int kSplitRows = 512;          // from here on there is a CTA a row
+constexpr float kC = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -1e7f;         // logits are lifted to it
+constexpr float kNoRef = -1e6f;          // reference before any logit: above what is lifted
+constexpr float kSlack = 10.0f;          // how far a logit may exceed a lane's reference
 
-__device__ __forceinline__ unsigned long long rank_key(float x, int t) {
-  return (static_cast<unsigned long long>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
+struct LParams {
+  const void *logits;
+  int V, rows, top_n, split, tile_chunks;  // a tile is tile_chunks chunks
+  int64_t stride;
+  const int32_t *tokens;
+  float *lp, *ent;
+  int32_t *rank, *top_ids;
+  float *top_lp;
+  int *counters;
+  float4 *parts;    // [row][kMaxSplit]: maximum, reference sum S, T, tokens before (bits)
+  uint32_t *keys;   // [row][kMaxTiles]
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long rank_key(uint32_t k, int t) {
+  return (static_cast<unsigned long long>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
+}
+__device__ __forceinline__ float key_value(uint32_t k) {  // inverse of order_key
+  return k == 0u ? NAN : __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-template <class V, class F>
-__device__ __forceinline__ V block_reduce(V v, F f, V *scratch) {
+// M of one reference less M of another, from above -1e30: also where both overflow (such rows are summed again).
+__device__ __forceinline__ float shift(float from, float to) {
+  return fmaxf(__fmul_rn(from, kC) - __fmul_rn(to, kC), -1e30f);
+}
+
+// Running sums of a lane: true maximum, reference (a logit), S and T.
+struct Sums {
+  float mx = -INFINITY, ref = kNoRef, s = 0.0f, t = 0.0f;
+  __device__ __forceinline__ void lift(float m) {  // raises the reference to a new chunk's maximum where it must
+    if (m > ref + kSlack || (s == 0.0f && m > ref)) {
+      const float d = shift(ref, m), f = exp2_fast(d);
+      t = fmaf(t, f, s * f * d);  // sum 2^(y + d) (y + d)
+      s *= f;
+      ref = m;
+    }
+  }
+};
+// b joined to a: sums over the larger reference.
+__device__ __forceinline__ void join(Sums &a, const Sums &b) {
+  a.mx = fmaxf(a.mx, b.mx);
+  const float r = fmaxf(a.ref, b.ref);
+  const float da = shift(a.ref, r), db = shift(b.ref, r);
+  const float fa = exp2_fast(da), fb = exp2_fast(db);
+  a.t = fmaf(fa, a.t, a.s * fa * da) + fmaf(fb, b.t, b.s * fb * db);
+  a.s = fmaf(fa, a.s, fb * b.s);
+  a.ref = r;
+}
+
+// 16 logits of a lane: VEC 16-byte loads of EPV logits, vector (j * 32 + lane) of the chunk.
+template <class T>
+struct Lane16 {
+  static constexpr int EPV = Vec16<T>::N, VEC = 16 / EPV;
+  uint4 v[VEC];
+  __device__ __forceinline__ void load(const T *chunk, int lane) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = scratch[0];
-  for (int w = 1; w < kLpThreads / 32; ++w) v = f(v, scratch[w]);
-  __syncthreads();
-  return v;
+    for (int j = 0; j < VEC; ++j) {
+      const T *a = chunk + (j * 32 + lane) * EPV;
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                   : "l"(a));
+    }
+  }
+  // position in the chunk of value i
+  __device__ __forceinline__ static int at(int i, int lane) { return ((i / EPV) * 32 + lane) * EPV + i % EPV; }
+  __device__ __forceinline__ void values(float *x) const {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) Vec16<T>::unpack(v[j], x + j * EPV);
+  }
+};
+
+// A whole chunk: maximum, sums, and how many logits are above xt (or at least xt when `ge`).
+__device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, float xt, bool ge, int &before) {
+  float x[16];
+  c.values(x);
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) m = fmaxf(m, x[i]);
+  u.lift(m);
+  const float M = u.ref * kC;
+  if (ge) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) before += x[i] >= xt ? 1 : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) before += x[i] > xt ? 1 : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float y = fmaf(max_nan(x[i], kLowest), kC, -M);
+    const float e = exp2_fast(y);
+    u.s += e;
+    u.t = fmaf(e, y, u.t);
+  }
+  return m;
+}
+__device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums &u, float xt, bool ge, int &before) {
+  const uint32_t w[8] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w, c.v[1].x, c.v[1].y, c.v[1].z, c.v[1].w};
+  __nv_bfloat162 h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+  const __nv_bfloat162 m2 = __hmax2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])),
+                                    __hmax2(__hmax2(h[4], h[5]), __hmax2(h[6], h[7])));
+  const float m = fmaxf(__low2float(m2), __high2float(m2));
+  u.lift(m);
+  const float M = u.ref * kC;
+  const __nv_bfloat162 t2 = __float2bfloat162_rn(xt), low = __float2bfloat162_rn(kLowest);  // xt is a bf16
+  __nv_bfloat162 cnt = __float2bfloat162_rn(0.0f);  // counts to 8: exact
+  if (ge) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cnt = __hadd2(cnt, __hge2(h[i], t2));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cnt = __hadd2(cnt, __hgt2(h[i], t2));
+  }
+  before += static_cast<int>(__low2float(cnt) + __high2float(cnt));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 l = __hmax2_nan(h[i], low);
+    const uint32_t b = *reinterpret_cast<const uint32_t *>(&l);
+    const float y0 = fmaf(__uint_as_float(b << 16), kC, -M), y1 = fmaf(__uint_as_float(b & 0xffff0000u), kC, -M);
+    const float e0 = exp2_fast(y0), e1 = exp2_fast(y1);
+    u.s += e0;
+    u.t = fmaf(e0, y0, u.t);
+    u.s += e1;
+    u.t = fmaf(e1, y1, u.t);
+  }
+  return m;
 }
 
 template <class T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T *__restrict__ logits, int V, int64_t stride,
-                                                              const int32_t *__restrict__ tokens, int top_n,
-                                                              float *__restrict__ lp, float *__restrict__ ent,
-                                                              int32_t *__restrict__ rank,
-                                                              int32_t *__restrict__ top_ids,
-                                                              float *__restrict__ top_lp) {
-  __shared__ unsigned long long s_u[kLpThreads / 32];
-  __shared__ float s_f[kLpThreads / 32];
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p) {
+  __shared__ Sums s_sums[kLpWarps];
+  __shared__ int s_before[kLpWarps], s_last;
+  __shared__ uint32_t s_key[kMaxTiles];
+  __shared__ int s_tile[32];
+  __shared__ unsigned long long s_list[kLpThreads];
+  __shared__ float s_ref, s_logz;
+  __shared__ int s_kind;
   grid_dependency_sync();
-  const int row = blockIdx.x;
-  const T *x = logits + row * stride;
-  const int tok = tokens[row];
-  const bool has = tok >= 0 && tok < V;
-  const float xt = has ? to_f(x[tok]) : -INFINITY;
-  const unsigned long long kt = has ? rank_key(xt, tok) : 0ull;
-  float m = -INFINITY, bad = 0.0f;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / p.split, part = blockIdx.x - row * p.split;
+  const T *x = static_cast<const T *>(p.logits) + row * p.stride;
+  // positions are counted from the 16-byte boundary at or before the row: `off` of them lie before it
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  const T *base = x - off;
+  const int end = off + p.V;
+  const int chunks = (end + kChunk - 1) / kChunk, tiles = (chunks + p.tile_chunks - 1) / p.tile_chunks;
+  const int tok = p.tokens[row];
+  const bool has = tok >= 0 && tok < p.V;
+  const int tpos = off + tok;
+  uint32_t *keys = p.split > 1 ? p.keys + static_cast<size_t>(row) * kMaxTiles : s_key;
+
+  // ---- this warp's tiles: every (split * warps)-th
+  Sums u;
   int before = 0;
-  for (int t = threadIdx.x; t < V; t += kLpThreads) {
-    const float v = to_f(x[t]);
-    m = fmaxf(m, v);
-    if (!(v < INFINITY)) bad = 1.0f;
-    before += rank_key(v, t) > kt;
-  }
-  auto fmx = [](float a, float b) { return fmaxf(a, b); };
-  auto add = [](float a, float b) { return a + b; };
-  m = block_reduce(m, fmx, s_f);
-  bad = block_reduce(bad, fmx, s_f);
-  before = static_cast<int>(block_reduce<unsigned long long>(
-      before, [](unsigned long long a, unsigned long long b) { return a + b; }, s_u));
-  const bool none = bad != 0.0f || m == -INFINITY;
-  float s = 0.0f, h = 0.0f;
-  for (int t = threadIdx.x; t < V; t += kLpThreads) {
-    const float d = to_f(x[t]) - m, e = expf(d);
-    s += e;
-    if (e > 0.0f) h = fmaf(e, d, h);
-  }
-  s = block_reduce(s, add, s_f);
-  h = block_reduce(h, add, s_f);
-  const float ls = logf(s);
-  if (threadIdx.x == 0) {
-    lp[row] = !has ? -INFINITY : none ? NAN : (xt - m) - ls;
-    if (ent) ent[row] = none ? NAN : ls - h / s;
-    if (rank) rank[row] = has ? before : V;
-  }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < top_n; ++k) {
-    unsigned long long best = 0;
-    for (int t = threadIdx.x; t < V; t += kLpThreads) {
-      const unsigned long long key = rank_key(to_f(x[t]), t);
-      if (key < last && key > best) best = key;
+  const int w0 = part * kLpWarps + warp, ws = p.split * kLpWarps;
+  const bool first_whole = off == 0;
+  auto whole = [&](int c) { return (c > 0 || first_whole) && (c + 1) * kChunk <= end; };
+  float xt = 0.0f;
+  Lane16<T> cur, nxt;
+  int tile = w0, c = tile * p.tile_chunks;
+  bool cw = tile < tiles && whole(c);
+  if (cw) cur.load(base + c * kChunk, lane);
+  if (has) xt = to_f(x[tok]);
+  float tmax = -INFINITY;
+  bool any_nan_only = true;  // no logit of the tile is a number so far
+  while (tile < tiles) {
+    // the next chunk: of this tile, or of the warp's next one
+    const int tend = min((tile + 1) * p.tile_chunks, chunks);
+    int nc = c + 1, nt = tile;
+    if (nc >= tend) nt = tile + ws, nc = nt * p.tile_chunks;
+    const bool nw = nt < tiles && whole(nc);
+    if (nw) nxt.load(base + nc * kChunk, lane);
+    const bool at_token = has && tpos / kChunk == c;
+    if (cw && !at_token && xt == xt) {
+      const float m = chunk_pass(cur, u, xt, has && c * kChunk < tpos, before);
+      u.mx = fmaxf(u.mx, m);
+      if (m == m) {
+        tmax = fmaxf(tmax, m);
+        any_nan_only = false;
+      }
+    } else {  // the row's ends, the chunk of the given token, and rows whose token is a NaN: one by one
+      const uint32_t kt = order_key(xt);
+      float m = -INFINITY;
+      float v[16];
+      bool in[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int pos = c * kChunk + Lane16<T>::at(i, lane);
+        in[i] = pos >= off && pos < end;
+        v[i] = in[i] ? to_f(base[pos]) : 0.0f;
+        if (in[i] && v[i] == v[i]) {
+          m = fmaxf(m, v[i]);
+          any_nan_only = false;
+        }
+        if (in[i] && has) {
+          const uint32_t k = order_key(v[i]);
+          before += k > kt || (k == kt && pos < tpos) ? 1 : 0;
+        }
+      }
+      u.mx = fmaxf(u.mx, m);
+      tmax = fmaxf(tmax, m);
+      u.lift(m);
+      const float M = u.ref * kC;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (!in[i]) continue;
+        const float y = fmaf(max_nan(v[i], kLowest), kC, -M);
+        const float e = exp2_fast(y);
+        u.s += e;
+        u.t = fmaf(e, y, u.t);
+      }
     }
-    best = block_reduce(best, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; }, s_u);
-    const int t = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-    if (threadIdx.x == 0) {
-      top_ids[row * top_n + k] = t;
-      top_lp[row * top_n + k] = none ? NAN : (to_f(x[t]) - m) - ls;
+    if (nt != tile) {
+      const uint32_t k = __reduce_max_sync(0xffffffffu, any_nan_only ? 0u : order_key(tmax));
+      if (lane == 0) keys[tile] = k;
+      tmax = -INFINITY;
+      any_nan_only = true;
     }
-    last = best;
+    cur = nxt;
+    cw = nw;
+    tile = nt;
+    c = nc;
+  }
+  // ---- lanes, then warps, joined in a fixed order
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    Sums b;
+    b.mx = __shfl_xor_sync(0xffffffffu, u.mx, o);
+    b.ref = __shfl_xor_sync(0xffffffffu, u.ref, o);
+    b.s = __shfl_xor_sync(0xffffffffu, u.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, u.t, o);
+    join(u, b);
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    s_sums[warp] = u;
+    s_before[warp] = before;
+  }
+  __syncthreads();
+  if (p.split > 1) {
+    if (tid == 0) {
+      for (int w = 1; w < kLpWarps; ++w) {
+        join(u, s_sums[w]);
+        before += s_before[w];
+      }
+      p.parts[static_cast<size_t>(row) * kMaxSplit * 2 + part * 2] = make_float4(u.mx, u.ref, u.s, u.t);
+      p.parts[static_cast<size_t>(row) * kMaxSplit * 2 + part * 2 + 1] = make_float4(__int_as_float(before), 0, 0, 0);
+      int old;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p.counters + row), "r"(1) : "memory");
+      s_last = old == p.split - 1;
+      if (s_last) p.counters[row] = 0;  // left at zero for the next call
+    }
+    __syncthreads();
+    if (!s_last) return;
+    for (int i = tid; i < tiles; i += kLpThreads) s_key[i] = __ldcg(keys + i);
+  }
+  // ---- the row's sums
+  if (warp == 0) {
+    Sums r;
+    int b = 0;
+    const int n = p.split > 1 ? p.split : kLpWarps;
+    if (p.split > 1) {
+      float4 q = make_float4(-INFINITY, kNoRef, 0.0f, 0.0f);
+      if (lane < n) {
+        q = __ldcg(&p.parts[static_cast<size_t>(row) * kMaxSplit * 2 + lane * 2]);
+        b = __float_as_int(__ldcg(&p.parts[static_cast<size_t>(row) * kMaxSplit * 2 + lane * 2 + 1].x));
+      }
+      r.mx = q.x, r.ref = q.y, r.s = q.z, r.t = q.w;
+    } else if (lane < n) {
+      r = s_sums[lane];
+      b = s_before[lane];
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      Sums q;
+      q.mx = __shfl_xor_sync(0xffffffffu, r.mx, o);
+      q.ref = __shfl_xor_sync(0xffffffffu, r.ref, o);
+      q.s = __shfl_xor_sync(0xffffffffu, r.s, o);
+      q.t = __shfl_xor_sync(0xffffffffu, r.t, o);
+      join(r, q);
+    }
+    b = __reduce_add_sync(0xffffffffu, b);
+    if (lane == 0) {
+      // kind 0: sums hold; 1: no distribution (NaN, an infinity on top, nothing left); 2: sum again from x - max
+      int kind = 0;
+      if (r.mx == INFINITY || r.mx == -INFINITY) kind = 1;
+      else if (!(r.mx > -9e5f && r.mx < 1e6f)) kind = 2;  // which looks for NaN itself
+      else if (r.s != r.s) kind = 1;
+      s_kind = kind;
+      // log p = (x - ref) - (log S of the terms over ref): no product that a far logit overflows
+      const float l2 = log2f(r.s), res = fmaf(r.ref, kC, -__fmul_rn(r.ref, kC));
+      s_ref = kind == 2 ? r.mx : r.ref;
+      s_logz = (l2 - res) * kLn2;
+      if (p.rank) p.rank[row] = has ? b : p.V;
+      if (kind != 2) {
+        p.lp[row] = !has ? -INFINITY : kind == 1 ? NAN : (xt - r.ref) - s_logz;
+        if (p.ent) p.ent[row] = kind == 1 ? NAN : (l2 - r.t / r.s) * kLn2;
+      }
+    }
+  }
+  __syncthreads();
+  if (s_kind == 2) {
+    // far logits: sums of 2^((x - max) c), every term from the difference
+    const float mx = s_ref;
+    float a = 0.0f, b = 0.0f;
+    bool bad = false;
+    for (int t = tid; t < p.V; t += kLpThreads) {
+      const float v = to_f(x[t]);
+      bad |= v != v;
+      const float d = fmaxf((v - mx) * kC, -1e30f), e = exp2_fast(d);
+      a += e;
+      b = fmaf(e, d, b);
+    }
+    if (bad) a = NAN;
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if (lane == 0) s_sums[warp].s = a, s_sums[warp].t = b;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kLpWarps; ++w) a += s_sums[w].s, b += s_sums[w].t;
+      const float l2 = log2f(a);
+      s_logz = l2 * kLn2;
+      p.lp[row] = !has ? -INFINITY : (xt - mx) - s_logz;
+      if (p.ent) p.ent[row] = (l2 - b / a) * kLn2;
+    }
+    __syncthreads();
+  }
+  if (p.top_n == 0) return;
+
+  // ---- the first top_n tiles by (maximum, position), by counting
+  const int n = p.top_n, nt = min(n, tiles);
+  for (int i = tid; i < tiles; i += kLpThreads) {
+    const uint32_t k = s_key[i];
+    int r = 0;
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t o = s_key[j];
+      r += o > k || (o == k && j < i) ? 1 : 0;
+    }
+    if (r < nt) s_tile[r] = i;
+  }
+  __syncthreads();
+  // ---- their tokens, into a sorted list a warp (lane i: its i-th); nothing below the n-th tile's maximum can be in it
+  const uint32_t bar = tiles >= n ? s_key[s_tile[n - 1]] : 0u;
+  unsigned long long list = 0ull;
+  for (int z = warp; z < nt; z += kLpWarps) {
+    const int c0 = s_tile[z] * p.tile_chunks, c1 = min(c0 + p.tile_chunks, chunks);
+    for (int cc = c0; cc < c1; ++cc) {
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int pos = cc * kChunk + i * 32 + lane;
+        unsigned long long key = 0ull;
+        if (pos >= off && pos < end) {
+          const uint32_t k = order_key(to_f(base[pos]));
+          if (k >= bar) key = rank_key(k, pos - off);
+        }
+        unsigned long long worst = __shfl_sync(0xffffffffu, list, n - 1);
+        unsigned m = __ballot_sync(0xffffffffu, key > worst);
+        while (m) {
+          const int src = __ffs(m) - 1;
+          const unsigned long long k = __shfl_sync(0xffffffffu, key, src);
+          const int at = __popc(__ballot_sync(0xffffffffu, list > k));
+          const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
+          list = lane < at ? list : lane == at ? k : up;
+          worst = __shfl_sync(0xffffffffu, list, n - 1);
+          m &= __ballot_sync(0xffffffffu, key > worst) & ~(1u << src);
+        }
+      }
+    }
+  }
+  s_list[tid] = lane < n ? list : 0ull;
+  __syncthreads();
+  {
+    const unsigned long long k = s_list[tid];
+    if (k != 0ull) {
+      int r = 0;
+      for (int j = 0; j < kLpThreads; ++j) r += s_list[j] > k ? 1 : 0;
+      if (r < n) {
+        const float v = key_value(static_cast<uint32_t>(k >> 32));
+        const size_t o = static_cast<size_t>(row) * n + r;
+        p.top_ids[o] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
+        p.top_lp[o] = s_kind == 1 ? NAN : (v - s_ref) - s_logz;
+      }
+    }
   }
 }
+
+int tile_chunks_of(int V) { return (V / kChunk + 1 + 255) / 256; }
 
 }  // namespace
 
 size_t logprobs_workspace_bytes(int rows, int vocab) {
   (void)vocab;
-  return static_cast<size_t>(rows) * 16;
+  const size_t n = static_cast<size_t>(std::min(rows, kSplitRows));
+  return (n * 4 + 255) / 256 * 256 + n * kMaxSplit * 32 + n * kMaxTiles * 4;
 }
 
 cudaError_t launch_logprobs(const void *logits, int dtype, int V, int64_t stride, int rows, const int32_t *tokens,
                             int top_n, float *lp, float *ent, int32_t *rank, int32_t *top_ids, float *top_lp, void *ws,
                             cudaStream_t s) {
-  (void)ws;
+  LParams p{};
+  p.logits = logits;
+  p.V = V;
+  p.rows = rows;
+  p.top_n = top_n;
+  p.stride = stride;
+  p.tokens = tokens;
+  p.lp = lp;
+  p.ent = ent;
+  p.rank = rank;
+  p.top_ids = top_ids;
+  p.top_lp = top_lp;
+  p.tile_chunks = tile_chunks_of(V);
+  p.split = 1;
+  if (rows < kSplitRows) {
+    // about four CTAs an SM, each warp with one tile at least
+    const int tiles = (V / kChunk + 1) / p.tile_chunks + 1;
+    p.split = std::max(1, std::min({(4 * device_sm_count() + rows - 1) / rows, tiles / kLpWarps, kMaxSplit}));
+  }
+  const size_t n = static_cast<size_t>(std::min(rows, kSplitRows));
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  p.counters = reinterpret_cast<int *>(w);
+  w += (n * 4 + 255) / 256 * 256;
+  p.parts = reinterpret_cast<float4 *>(w);
+  w += n * kMaxSplit * 32;
+  p.keys = reinterpret_cast<uint32_t *>(w);
+  const int64_t grid = static_cast<int64_t>(rows) * p.split;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   if (dtype == 0)
-    return launch_pdl(logprobs_kernel<__nv_bfloat16>, dim3(rows), dim3(kLpThreads), 0, s,
-                      static_cast<const __nv_bfloat16 *>(logits), V, stride, tokens, top_n, lp, ent, rank, top_ids,
-                      top_lp);
-  return launch_pdl(logprobs_kernel<float>, dim3(rows), dim3(kLpThreads), 0, s, static_cast<const float *>(logits), V,
-                    stride, tokens, top_n, lp, ent, rank, top_ids, top_lp);
+    return launch_pdl(logprobs_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(grid)), dim3(kLpThreads), 0, s, p);
+  return launch_pdl(logprobs_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(kLpThreads), 0, s, p);
 }
 
 }  // namespace kap
