@@ -7,7 +7,7 @@
 // same and the entropy's 0 * y stays 0 for -infinity. Rows whose maximum lies outside (-9e5, 1e6), where that would
 // distort or M's own rounding would leave a large y, are summed again from x - max.
 // Rank: tokens before the given one count with >= on the pieces of the row that lie before it and with > behind it.
-// Alternatives: the row is cut into at most 257 tiles whose maxima are kept. A token among the first n of the order lies
+// Alternatives: the row is cut into at most 256 tiles whose maxima are kept. A token among the first n of the order lies
 // in one of the first n tiles by (maximum, position): every tile before its own holds a token that comes before it. So
 // only those n tiles are read again (from L2), and the n-th tile's maximum bars nearly all of their tokens.
 //
@@ -26,7 +26,7 @@ namespace {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kChunk = 512;              // logits of a warp's step, 16 a lane
-constexpr int kMaxTiles = 257;           // tiles of a row whose maxima are kept
+constexpr int kMaxTiles = kLpThreads;    // tiles of a row whose maxima are kept: one a thread
 constexpr int kMaxSplit = 32;            // CTAs of a row
 constexpr int kSplitRows = 512;          // from here on there is a CTA a row
 constexpr float kC = 1.4426950408889634f;
@@ -174,12 +174,42 @@ __device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums
   return m;
 }
 
+// Keys of a warp in descending order (bitonic).
+template <class K>
+__device__ __forceinline__ K warp_sort_desc(K k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d >= 1; d >>= 1) {
+      const K o = __shfl_xor_sync(0xffffffffu, k, d);
+      const bool keep_max = ((lane & d) == 0) == ((lane & size) == 0);
+      k = keep_max ? (o > k ? o : k) : (o > k ? k : o);
+    }
+  return k;
+}
+// How many keys of the block's sorted warps (32 a warp, descending, distinct or 0) come before k, the lane-th of its own.
+template <class K>
+__device__ __forceinline__ int block_rank(const K *lists, K k, int warp, int lane) {
+  int r = lane;
+#pragma unroll
+  for (int w = 0; w < kLpWarps; ++w) {
+    if (w == warp) continue;
+    int n = 0;
+#pragma unroll
+    for (int step = 16; step >= 1; step >>= 1) n += lists[w * 32 + n + step - 1] > k ? step : 0;
+    n += lists[w * 32 + n] > k ? 1 : 0;
+    r += n;
+  }
+  return r;
+}
+
 template <class T>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p) {
   __shared__ Sums s_sums[kLpWarps];
   __shared__ int s_before[kLpWarps], s_last;
   __shared__ uint32_t s_key[kMaxTiles];
-  __shared__ int s_tile[32];
+  __shared__ int s_tile[kMaxTiles], s_ntile, s_ncand;
+  __shared__ uint32_t s_sorted[kMaxTiles], s_bar;
   __shared__ unsigned long long s_list[kLpThreads];
   __shared__ float s_ref, s_logz;
   __shared__ int s_kind;
@@ -201,52 +231,41 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   Sums u;
   int before = 0;
   const int w0 = part * kLpWarps + warp, ws = p.split * kLpWarps;
-  const bool first_whole = off == 0;
-  auto whole = [&](int c) { return (c > 0 || first_whole) && (c + 1) * kChunk <= end; };
+  // chunks [c_lo, c_hi) lie inside the row; the chunk of the given token is apart, and so is a row whose token is a NaN
+  const int c_lo = off ? 1 : 0, c_hi = end / kChunk;
+  auto whole = [&](int c) { return c >= c_lo && c < c_hi; };
+  const int c_tok = has ? tpos / kChunk : -1;
   float xt = 0.0f;
   Lane16<T> cur, nxt;
   int tile = w0, c = tile * p.tile_chunks;
-  bool cw = tile < tiles && whole(c);
-  if (cw) cur.load(base + c * kChunk, lane);
+  if (tile < tiles && whole(c)) cur.load(base + c * kChunk, lane);
   if (has) xt = to_f(x[tok]);
-  float tmax = -INFINITY;
-  bool any_nan_only = true;  // no logit of the tile is a number so far
+  const bool odd = xt != xt;
+  float tmax = NAN;  // maximum of the tile's numbers
   while (tile < tiles) {
     // the next chunk: of this tile, or of the warp's next one
-    const int tend = min((tile + 1) * p.tile_chunks, chunks);
     int nc = c + 1, nt = tile;
-    if (nc >= tend) nt = tile + ws, nc = nt * p.tile_chunks;
-    const bool nw = nt < tiles && whole(nc);
-    if (nw) nxt.load(base + nc * kChunk, lane);
-    const bool at_token = has && tpos / kChunk == c;
-    if (cw && !at_token && xt == xt) {
-      const float m = chunk_pass(cur, u, xt, has && c * kChunk < tpos, before);
-      u.mx = fmaxf(u.mx, m);
-      if (m == m) {
-        tmax = fmaxf(tmax, m);
-        any_nan_only = false;
-      }
-    } else {  // the row's ends, the chunk of the given token, and rows whose token is a NaN: one by one
+    if (nc == (tile + 1) * p.tile_chunks || nc >= chunks) nt = tile + ws, nc = nt * p.tile_chunks;
+    if (whole(nc)) nxt.load(base + nc * kChunk, lane);
+    float m;
+    if (whole(c) && c != c_tok && !odd) {
+      m = chunk_pass(cur, u, xt, c < c_tok, before);
+    } else {  // one by one
       const uint32_t kt = order_key(xt);
-      float m = -INFINITY;
       float v[16];
       bool in[16];
+      m = NAN;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int pos = c * kChunk + Lane16<T>::at(i, lane);
         in[i] = pos >= off && pos < end;
-        v[i] = in[i] ? to_f(base[pos]) : 0.0f;
-        if (in[i] && v[i] == v[i]) {
-          m = fmaxf(m, v[i]);
-          any_nan_only = false;
-        }
+        v[i] = in[i] ? to_f(base[pos]) : NAN;
+        m = fmaxf(m, v[i]);
         if (in[i] && has) {
           const uint32_t k = order_key(v[i]);
           before += k > kt || (k == kt && pos < tpos) ? 1 : 0;
         }
       }
-      u.mx = fmaxf(u.mx, m);
-      tmax = fmaxf(tmax, m);
       u.lift(m);
       const float M = u.ref * kC;
 #pragma unroll
@@ -258,14 +277,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
         u.t = fmaf(e, y, u.t);
       }
     }
+    tmax = fmaxf(tmax, m);
     if (nt != tile) {
-      const uint32_t k = __reduce_max_sync(0xffffffffu, any_nan_only ? 0u : order_key(tmax));
-      if (lane == 0) keys[tile] = k;
-      tmax = -INFINITY;
-      any_nan_only = true;
+      u.mx = fmaxf(u.mx, tmax);
+      if (p.top_n > 0) {
+        const uint32_t k = __reduce_max_sync(0xffffffffu, order_key(tmax));
+        if (lane == 0) keys[tile] = k;
+      }
+      tmax = NAN;
     }
     cur = nxt;
-    cw = nw;
     tile = nt;
     c = nc;
   }
@@ -375,64 +396,94 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   }
   if (p.top_n == 0) return;
 
-  // ---- the first top_n tiles by (maximum, position), by counting
-  const int n = p.top_n, nt = min(n, tiles);
-  for (int i = tid; i < tiles; i += kLpThreads) {
-    const uint32_t k = s_key[i];
-    int r = 0;
-    for (int j = 0; j < tiles; ++j) {
-      const uint32_t o = s_key[j];
-      r += o > k || (o == k && j < i) ? 1 : 0;
-    }
-    if (r < nt) s_tile[r] = i;
+  // ---- a bar that top_n tokens reach: the top_n-th of the tiles' maxima, without its low bits (which a bf16 does not
+  // have), so that a maximum and its tile make one distinct word to sort. Tiles that reach it are read again.
+  const int n = p.top_n;
+  {
+    uint32_t k = tid < tiles ? (s_key[tid] & ~255u) | (255u - tid) : 0u;
+    k = warp_sort_desc(k, lane);
+    const int own = k != 0u ? 255 - static_cast<int>(k & 255u) : tiles == kMaxTiles ? 255 : tiles;
+    s_sorted[tid] = k;
+    if (tid == 0) s_bar = 0u, s_ntile = 0, s_ncand = 0;
+    __syncthreads();
+    if ((k != 0u || tiles == kMaxTiles) && tiles >= n && block_rank(s_sorted, k, warp, lane) == n - 1) s_bar = k & ~255u;
+    __syncthreads();
+    if (own < tiles && (k & ~255u) >= s_bar) s_tile[atomicAdd(&s_ntile, 1)] = own;
+    __syncthreads();
   }
-  __syncthreads();
-  // ---- their tokens, into a sorted list a warp (lane i: its i-th); nothing below the n-th tile's maximum can be in it
-  const uint32_t bar = tiles >= n ? s_key[s_tile[n - 1]] : 0u;
-  unsigned long long list = 0ull;
+  const uint32_t bar = s_bar;
+  const int nt = s_ntile;
+  // ---- their tokens that reach the bar: hardly more than top_n where logits differ
   for (int z = warp; z < nt; z += kLpWarps) {
     const int c0 = s_tile[z] * p.tile_chunks, c1 = min(c0 + p.tile_chunks, chunks);
     for (int cc = c0; cc < c1; ++cc) {
-#pragma unroll 4
+      float v[16];
+      if (whole(cc)) {
+        cur.load(base + cc * kChunk, lane);
+        cur.values(v);
+      }
+#pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int pos = cc * kChunk + i * 32 + lane;
-        unsigned long long key = 0ull;
-        if (pos >= off && pos < end) {
-          const uint32_t k = order_key(to_f(base[pos]));
-          if (k >= bar) key = rank_key(k, pos - off);
-        }
-        unsigned long long worst = __shfl_sync(0xffffffffu, list, n - 1);
-        unsigned m = __ballot_sync(0xffffffffu, key > worst);
-        while (m) {
-          const int src = __ffs(m) - 1;
-          const unsigned long long k = __shfl_sync(0xffffffffu, key, src);
-          const int at = __popc(__ballot_sync(0xffffffffu, list > k));
-          const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
-          list = lane < at ? list : lane == at ? k : up;
-          worst = __shfl_sync(0xffffffffu, list, n - 1);
-          m &= __ballot_sync(0xffffffffu, key > worst) & ~(1u << src);
+        const int pos = cc * kChunk + Lane16<T>::at(i, lane);
+        const bool in = whole(cc) || (pos >= off && pos < end);
+        if (!whole(cc)) v[i] = in ? to_f(base[pos]) : 0.0f;
+        const uint32_t k = order_key(v[i]);
+        if (in && k >= bar) {
+          const int at = atomicAdd(&s_ncand, 1);
+          if (at < kLpThreads) s_list[at] = rank_key(k, pos - off);
         }
       }
     }
   }
-  s_list[tid] = lane < n ? list : 0ull;
   __syncthreads();
-  {
-    const unsigned long long k = s_list[tid];
-    if (k != 0ull) {
-      int r = 0;
-      for (int j = 0; j < kLpThreads; ++j) r += s_list[j] > k ? 1 : 0;
-      if (r < n) {
-        const float v = key_value(static_cast<uint32_t>(k >> 32));
-        const size_t o = static_cast<size_t>(row) * n + r;
-        p.top_ids[o] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
-        p.top_lp[o] = s_kind == 1 ? NAN : (v - s_ref) - s_logz;
+  unsigned long long k = 0ull;
+  int r = lane;
+  if (s_ncand <= 32) {  // one warp's sort is the order
+    if (warp != 0) return;
+    k = warp_sort_desc(lane < s_ncand ? s_list[lane] : 0ull, lane);
+  } else {
+    if (s_ncand <= kLpThreads) {
+      k = warp_sort_desc(tid < s_ncand ? s_list[tid] : 0ull, lane);
+      __syncthreads();
+    } else {
+      // many equal logits: every warp inserts its tiles' tokens into a sorted list of its own (lane i: its i-th)
+      for (int z = warp; z < nt; z += kLpWarps) {
+        const int p0 = s_tile[z] * p.tile_chunks * kChunk, p1 = min(p0 + p.tile_chunks * kChunk, chunks * kChunk);
+        for (int pos = p0 + lane; pos < p1; pos += 32) {
+          unsigned long long key = 0ull;
+          if (pos >= off && pos < end) {
+            const uint32_t u32 = order_key(to_f(base[pos]));
+            if (u32 >= bar) key = rank_key(u32, pos - off);
+          }
+          unsigned long long worst = __shfl_sync(0xffffffffu, k, n - 1);
+          unsigned m = __ballot_sync(0xffffffffu, key > worst);
+          while (m) {
+            const int src = __ffs(m) - 1;
+            const unsigned long long q = __shfl_sync(0xffffffffu, key, src);
+            const int at = __popc(__ballot_sync(0xffffffffu, k > q));
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, k, 1);
+            k = lane < at ? k : lane == at ? q : up;
+            worst = __shfl_sync(0xffffffffu, k, n - 1);
+            m &= __ballot_sync(0xffffffffu, key > worst) & ~(1u << src);
+          }
+        }
       }
+      __syncthreads();
     }
+    s_list[tid] = k;
+    __syncthreads();
+    if (k != 0ull) r = block_rank(s_list, k, warp, lane);
+  }
+  if (k != 0ull && r < n) {
+    const float v = key_value(static_cast<uint32_t>(k >> 32));
+    const size_t o = static_cast<size_t>(row) * n + r;
+    p.top_ids[o] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
+    p.top_lp[o] = s_kind == 1 ? NAN : (v - s_ref) - s_logz;
   }
 }
 
-int tile_chunks_of(int V) { return (V / kChunk + 1 + 255) / 256; }
+// A row has at most V / kChunk + 2 chunks, wherever it starts in memory.
+int tile_chunks_of(int V) { return (V / kChunk + 2 + kMaxTiles - 1) / kMaxTiles; }
 
 }  // namespace
 
