@@ -115,6 +115,23 @@ struct Lane16 {
   }
 };
 
+// Two logits into the running pairs of S and T.
+__device__ __forceinline__ void add_pair(F2 x, F2 c, F2 m, F2 &s, F2 &t) {
+  const F2 y = fma2(x, c, m);
+  float a, b;
+  split(y, a, b);
+  const F2 e = f2(exp2_fast(a), exp2_fast(b));
+  s = add2(s, e);
+  t = fma2(e, y, t);
+}
+__device__ __forceinline__ void close_pairs(Sums &u, F2 s, F2 t) {
+  float a, b;
+  split(s, a, b);
+  u.s += a + b;
+  split(t, a, b);
+  u.t += a + b;
+}
+
 // A whole chunk: maximum, sums, and how many logits are above xt (or at least xt when `ge`).
 __device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, float xt, bool ge, int &before) {
   float x[16];
@@ -131,13 +148,11 @@ __device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, flo
 #pragma unroll
     for (int i = 0; i < 16; ++i) before += x[i] > xt ? 1 : 0;
   }
+  F2 s = f2(0.0f, 0.0f), t = s;
+  const F2 cc = f2(kC, kC), mm = f2(-M, -M);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float y = fmaf(max_nan(x[i], kLowest), kC, -M);
-    const float e = exp2_fast(y);
-    u.s += e;
-    u.t = fmaf(e, y, u.t);
-  }
+  for (int i = 0; i < 16; i += 2) add_pair(f2(max_nan(x[i], kLowest), max_nan(x[i + 1], kLowest)), cc, mm, s, t);
+  close_pairs(u, s, t);
   return m;
 }
 __device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums &u, float xt, bool ge, int &before) {
@@ -160,17 +175,15 @@ __device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums
     for (int i = 0; i < 8; ++i) cnt = __hadd2(cnt, __hgt2(h[i], t2));
   }
   before += static_cast<int>(__low2float(cnt) + __high2float(cnt));
+  F2 s = f2(0.0f, 0.0f), t = s;
+  const F2 cc = f2(kC, kC), mm = f2(-M, -M);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const __nv_bfloat162 l = __hmax2_nan(h[i], low);
     const uint32_t b = *reinterpret_cast<const uint32_t *>(&l);
-    const float y0 = fmaf(__uint_as_float(b << 16), kC, -M), y1 = fmaf(__uint_as_float(b & 0xffff0000u), kC, -M);
-    const float e0 = exp2_fast(y0), e1 = exp2_fast(y1);
-    u.s += e0;
-    u.t = fmaf(e0, y0, u.t);
-    u.s += e1;
-    u.t = fmaf(e1, y1, u.t);
+    add_pair(f2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), cc, mm, s, t);
   }
+  close_pairs(u, s, t);
   return m;
 }
 
@@ -422,16 +435,25 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
         cur.load(base + cc * kChunk, lane);
         cur.values(v);
       }
+      // above the key of -infinity the bar is a number and one compare decides; NaN counts only below it
+      unsigned hit = 0u;
+      if (whole(cc) && bar > 0x007fffffu) {
+        const float b = key_value(bar);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int pos = cc * kChunk + Lane16<T>::at(i, lane);
-        const bool in = whole(cc) || (pos >= off && pos < end);
-        if (!whole(cc)) v[i] = in ? to_f(base[pos]) : 0.0f;
-        const uint32_t k = order_key(v[i]);
-        if (in && k >= bar) {
-          const int at = atomicAdd(&s_ncand, 1);
-          if (at < kLpThreads) s_list[at] = rank_key(k, pos - off);
+        for (int i = 0; i < 16; ++i) hit |= v[i] >= b ? 1u << i : 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int pos = cc * kChunk + Lane16<T>::at(i, lane);
+          const bool in = pos >= off && pos < end;
+          hit |= in && order_key(to_f(base[in ? pos : off])) >= bar ? 1u << i : 0u;
         }
+      }
+      while (hit) {
+        const int i = __ffs(hit) - 1, pos = cc * kChunk + Lane16<T>::at(i, lane);
+        hit &= hit - 1;
+        const int at = atomicAdd(&s_ncand, 1);
+        if (at < kLpThreads) s_list[at] = rank_key(order_key(to_f(base[pos])), pos - off);
       }
     }
   }
