@@ -58,31 +58,35 @@ struct AParams {
   float2 *ml;     // [slot][columns]
   float *part;    // [slot][columns][d]
   int ncol;       // columns of a record: G * max_q
+  int by_row;     // a CTA a row, no shares
   int *err;
 };
 
 template <int D, int NTL, int CS>
 struct Cfg {
-  static constexpr int kWarps = NTL == 2 ? 12 : 8;
+  static constexpr int kWarps = NTL == 2 ? 10 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kCtas = NTL == 1 ? 2 : 1;         // resident CTAs an SM
   static constexpr int PW = kWarps / CS;                 // warps that take pages in turn
   static constexpr int N = NTL * CS * 8;                 // query columns
   static constexpr int NB = D / 64;
   static constexpr int KS = NB * 4;                      // k-steps of the logits
+  static constexpr int kQPer = (N * (D / 8) + kThreads - 1) / kThreads;  // 8-dim pieces of the queries a thread takes
   static constexpr int kChunk = PackedChunk<D>::BYTES;
-  static constexpr int kStages = (D == 128 ? 5 : 8) * CS;
+  static constexpr int kStages = (D == 64 ? 8 : NTL == 1 ? 4 : 5) * CS;
   static constexpr bool kPairs = NTL <= 2;               // two pages at once: more independent work a warp
   static constexpr int kQStride = D + 8;                 // bf16 elements of a raw query row
-  static constexpr int OFF_RING = 0;
+  static constexpr bool kApart = NTL <= 2;               // joins have memory of their own, beside the ring
   static constexpr int kRing = PW * kStages * kChunk;
-  static constexpr int kAcc = NTL * NB * 16;             // accumulators of a lane
-  static constexpr int kJoin = (kAcc + NTL * 4) * 32 * 4;  // bytes a warp hands over
-  static constexpr int kJoinAll = (kWarps / 2 + 1) * kJoin;
-  static constexpr int kMaxGrid = 160 * kCtas;            // CTAs, so parts of a row
-  static constexpr int kWeights = kMaxGrid * N * 8;       // (maximum, sum) of every part and column
-  static constexpr int kArea = kRing > kJoinAll ? (kRing > kWeights ? kRing : kWeights)
-                                                : (kJoinAll > kWeights ? kJoinAll : kWeights);
+  static constexpr int kSlots = (PW + 1) / 2;            // joined warps: the others are added to one of these first
+  static constexpr int kColStride = D + 8;               // floats of a joined column
+  static constexpr int kJoin = kSlots * N * (kColStride + 2) * 4;
+  static constexpr int kMaxGrid = 160 * kCtas;           // CTAs, so parts of a row
+  static constexpr int kWeights = kMaxGrid * N * 8;      // (maximum, sum) of every part and column
+  static constexpr int kJoinArea = kJoin > kWeights ? kJoin : kWeights;
+  static constexpr int OFF_RING = 0;
+  static constexpr int OFF_JOIN = kApart ? kRing : 0;
+  static constexpr int kArea = kApart ? kRing + kJoinArea : (kRing > kJoinArea ? kRing : kJoinArea);
   static constexpr int OFF_QRAW = (kArea + 127) / 128 * 128;
   static constexpr int OFF_QF = OFF_QRAW + (N * kQStride * 2 + 15) / 16 * 16;  // fp16 fragments [tile][k-step / 2][lane][2]
   static constexpr int OFF_QS = OFF_QF + NTL * CS * KS * 32 * 8;               // [N] scale, [N][NB] block sums
@@ -91,10 +95,11 @@ struct Cfg {
   static_assert(BYTES <= 227 * 1024 / kCtas, "shared memory");
 };
 
-// One row's part: pages [p0, p1) of (request r, head h).
+// One row's part: pages [p0, p1) of (request r, head h), whose pages lie at [rb, re) of the line.
 struct Seg {
-  int r, h, row, n, p0, p1, nq, qoff, last0, ctx, nsel;
+  int r, h, row, p0, p1, nq, qoff, last0, ctx, nsel;
   const int32_t *ids, *lps;
+  int64_t rb, re;
 };
 
 __device__ __forceinline__ int atom_add_acq_rel_gpu(int *p, int v) {
@@ -219,14 +224,14 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_scan[C::kWarps], s_total, s_base;
   __shared__ int s_unit, s_flag;
+  __shared__ Seg s_seg;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pw = warp % C::PW, cg = warp / C::PW;  // which pages, which group of NTL column tiles
   const int g = lane >> 2, t = lane & 3;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + pw * C::kStages;
   unsigned char *ring = smem + C::OFF_RING + pw * C::kStages * C::kChunk;
   __nv_bfloat16 *qraw = reinterpret_cast<__nv_bfloat16 *>(smem + C::OFF_QRAW);
-  uint2 *qfrag = reinterpret_cast<uint2 *>(smem + C::OFF_QF);
-  const uint4 *qfrag4 = reinterpret_cast<const uint4 *>(smem + C::OFF_QF);  // two k-steps
+  uint4 *qfrag4 = reinterpret_cast<uint4 *>(smem + C::OFF_QF);  // two k-steps
   float *qscale = reinterpret_cast<float *>(smem + C::OFF_QS);
   float *qsum = qscale + C::N;
 
@@ -237,57 +242,116 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
   // ---- this CTA's share of the line of pages, and the unit that it starts in
   const Units<kView> units{p};
   const int U = units.count(), H = units.heads();
-  int64_t total = 0;
-  int bad = 0;
-  for (int base = 0; base < U; base += C::kThreads) {
-    const int u = base + tid;
-    const int64_t n = u < U ? static_cast<int64_t>(units.pages(u, bad)) * H : 0;
-    const int64_t incl = block_inclusive_scan<int64_t>(n, s_scan);
-    if (tid == C::kThreads - 1) s_total = incl;
-    __syncthreads();
-    total += s_total;
-    __syncthreads();
-    if (u < U && n == 0 && u % gridDim.x == blockIdx.x) {  // a row without pages: zeros
-      const int r = kView ? u / p.view.rows_per_seq : u;
-      const int h0 = H == 1 ? u - r * p.view.rows_per_seq : 0;
-      int qoff;
-      bool wb = false;
-      const int nq = units.window(r, qoff, wb), G = p.hq / p.hkv;
-      for (int i = 0; i < nq; ++i)
-        for (int a = h0 * G; a < (h0 + H) * G; ++a) {
-          const size_t o = static_cast<size_t>(qoff + i) * p.hq + a;
-          p.lse[o] = -INFINITY;
-          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(p.out + o * D + c) = make_uint4(0, 0, 0, 0);
-        }
-      if (kView) bad |= kErrLength;
+  // Zeros for the heads [h0, h0 + heads) of a request whose rows have no pages.
+  auto empty_rows = [&](int r, int h0, int heads) {
+    int qoff;
+    bool wb = false;
+    const int nq = units.window(r, qoff, wb), per = heads * (p.hq / p.hkv);
+    for (int i = 0; i < nq * per; ++i) {
+      const size_t o = static_cast<size_t>(qoff + i / per) * p.hq + h0 * (p.hq / p.hkv) + i % per;
+      p.lse[o] = -INFINITY;
+      for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(p.out + o * D + c) = make_uint4(0, 0, 0, 0);
     }
-  }
-  if (bad && blockIdx.x == 0) set_error(p.err, bad);
-  else if (bad & kErrLength) set_error(p.err, kErrLength);
-  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(C::PW));
-  int64_t x = share * blockIdx.x;
-  const int64_t x1 = min(x + share, total);
-  if (x >= x1) return;
-  {
-    int64_t before = 0;
+    if (kView) set_error(p.err, kErrLength);
+  };
+  // The rest of a part's description; by one thread, into s_seg.
+  auto describe = [&](int unit, int head, int p0, int p1, int n, int64_t rb) {
+    Seg s;
+    s.r = kView ? unit / p.view.rows_per_seq : unit;
+    s.h = H == 1 && kView ? unit - s.r * p.view.rows_per_seq : head;
+    s.row = s.r * p.hkv + s.h;
+    s.p0 = p0;
+    s.p1 = p1;
+    s.rb = rb;
+    s.re = rb + n;
+    bool wb = false;
+    s.nq = units.window(s.r, s.qoff, wb);
+    if (kView) {
+      s.last0 = p.seq_len[s.r] - 1;
+      s.ctx = p.ctx_len[s.r];
+      s.nsel = p.view.n_selected[unit];
+      s.ids = p.view.bt + static_cast<size_t>(unit) * p.view.cap;
+      s.lps = p.view.lp + static_cast<size_t>(unit) * p.view.cap;
+    } else {
+      s.last0 = p.q_start[s.r];
+      s.ctx = 0;
+      s.nsel = 0;
+      s.ids = p.bt + static_cast<size_t>(s.r) * p.max_pages;
+      s.lps = nullptr;
+    }
+    s_seg = s;
+  };
+  int64_t x = 0, x1 = 0, share = 1;
+  // The part at x, from the unit at or before it (its pages start at base).
+  auto find_part = [&](int unit, int64_t base, int64_t x) {
     int dummy = 0;
+    int n = units.pages(unit, dummy);
+    while (x >= base + static_cast<int64_t>(n) * H) {
+      base += static_cast<int64_t>(n) * H;
+      n = units.pages(++unit, dummy);
+    }
+    const int64_t in = x - base;
+    const int head = in < n ? 0 : static_cast<int>(in / n), p0 = static_cast<int>(in - static_cast<int64_t>(head) * n);
+    describe(unit, head, p0, static_cast<int>(min(static_cast<int64_t>(n), p0 + (x1 - x))), n, x - p0);
+    s_unit = unit;
+    s_base = base;
+  };
+  if (p.by_row) {
+    const int unit = blockIdx.x / H, head = blockIdx.x - unit * H;
+    int bad = 0;
+    const int n = units.pages(unit, bad);
+    if (tid == 0) {
+      if (bad) set_error(p.err, bad);
+      const int r = kView ? unit / p.view.rows_per_seq : unit;
+      if (n == 0) empty_rows(r, H == 1 && kView ? unit - r * p.view.rows_per_seq : head, 1);
+      else describe(unit, head, 0, n, n, 0);
+    }
+    if (n == 0) return;
+    x1 = share = n;
+  } else {
+    int64_t total = 0, incl = 0, n_own = 0;
+    int bad = 0;
     for (int base = 0; base < U; base += C::kThreads) {
       const int u = base + tid;
-      const int64_t n = u < U ? static_cast<int64_t>(units.pages(u, dummy)) * H : 0;
-      const int64_t incl = before + block_inclusive_scan<int64_t>(n, s_scan);
-      if (incl - n <= x && x < incl) {
-        s_unit = u;
-        s_base = incl - n;
-      }
+      n_own = u < U ? static_cast<int64_t>(units.pages(u, bad)) * H : 0;
+      incl = block_inclusive_scan<int64_t>(n_own, s_scan);
       if (tid == C::kThreads - 1) s_total = incl;
       __syncthreads();
-      before = s_total;
+      total += s_total;
       __syncthreads();
-      if (before > x) break;
+      if (u < U && n_own == 0 && u % gridDim.x == blockIdx.x) {
+        const int r = kView ? u / p.view.rows_per_seq : u;
+        empty_rows(r, H == 1 && kView ? u - r * p.view.rows_per_seq : 0, H == 1 && kView ? 1 : p.hkv);
+      }
+    }
+    if (bad && blockIdx.x == 0) set_error(p.err, bad);
+    // equal shares, of two pages a warp at least
+    share = total < (1 << 30) ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x
+                              : (total + gridDim.x - 1) / gridDim.x;
+    share = max(share, static_cast<int64_t>(2 * C::PW));
+    x = share * blockIdx.x;
+    x1 = min(x + share, total);
+    if (x >= x1) return;
+    if (U <= C::kThreads) {  // the scan above still stands
+      if (incl - n_own <= x && x < incl) find_part(tid, incl - n_own, x);
+    } else {
+      int64_t before = 0;
+      int dummy = 0;
+      for (int base = 0; base < U; base += C::kThreads) {
+        const int u = base + tid;
+        const int64_t n = u < U ? static_cast<int64_t>(units.pages(u, dummy)) * H : 0;
+        const int64_t upto = before + block_inclusive_scan<int64_t>(n, s_scan);
+        if (upto - n <= x && x < upto) find_part(u, upto - n, x);
+        if (tid == C::kThreads - 1) s_total = upto;
+        __syncthreads();
+        before = s_total;
+        __syncthreads();
+        if (before > x) break;
+      }
     }
   }
-  int unit = s_unit;
-  int64_t ubase = s_base;
+  __syncthreads();
+  Seg s = s_seg;
 
   const int G = p.hq / p.hkv;
   const float qk = rsqrtf(static_cast<float>(D)) * kLog2e;
@@ -303,123 +367,112 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     }
   };
 
-  while (x < x1) {
-    // ---- the row at x and its part in this share
-    Seg s;
-    int dummy = 0;
-    s.n = units.pages(unit, dummy);
-    if (x >= ubase + static_cast<int64_t>(s.n) * H) {
-      ubase += static_cast<int64_t>(s.n) * H;
-      ++unit;
-      continue;
+  // This warp's items of a part: pages p0 + pw, p0 + pw + PW, ...; ids of 32 items a load, two loads held.
+  int nit = 0, idc = -1, lpc = 0, idn = -1, lpn = 0, batch = 0, ahead = 0;
+  unsigned m4c = 0u, m4n = 0u, whole = 0u;  // packed pages of the two loads; those of the first that every column sees in full
+  auto load_ids = [&](int b, int &id, int &lp) {
+    const int j = b * 32 + lane;
+    id = -1;
+    lp = 0;
+    if (j < nit) {
+      const int e = s.p0 + pw + C::PW * j;
+      id = s.ids[e];
+      if (kView) lp = s.lps[e];
     }
-    {
-      const int64_t in = x - ubase;
-      const int hh = static_cast<int>(in / s.n);
-      s.r = kView ? unit / p.view.rows_per_seq : unit;
-      s.h = H == 1 && kView ? unit - s.r * p.view.rows_per_seq : hh;
-      s.row = s.r * p.hkv + s.h;
-      s.p0 = static_cast<int>(in - static_cast<int64_t>(hh) * s.n);
-      s.p1 = static_cast<int>(min(static_cast<int64_t>(s.n), s.p0 + (x1 - x)));
-      bool wb = false;
-      s.nq = units.window(s.r, s.qoff, wb);
-      if (kView) {
-        s.last0 = p.seq_len[s.r] - 1;
-        s.ctx = p.ctx_len[s.r];
-        s.nsel = p.view.n_selected[unit];
-        s.ids = p.view.bt + static_cast<size_t>(unit) * p.view.cap;
-        s.lps = p.view.lp + static_cast<size_t>(unit) * p.view.cap;
-      } else {
-        s.last0 = p.q_start[s.r];
-        s.ctx = 0;
-        s.nsel = 0;
-        s.ids = p.bt + static_cast<size_t>(s.r) * p.max_pages;
-        s.lps = nullptr;
-      }
-    }
-    const int64_t rb = x - s.p0, re = rb + s.n;  // the row's pages on the line
-    const int M = G * s.nq;
-
-    // ---- this warp's items: pages p0 + pw, p0 + pw + PW, ...; ids of 32 items a load, two loads held
-    const int nit = s.p1 - s.p0 > pw ? (s.p1 - s.p0 - pw + C::PW - 1) / C::PW : 0;
-    auto load_ids = [&](int batch, int &id, int &lp) {
-      const int j = batch * 32 + lane;
-      id = -1;
-      lp = 0;
-      if (j < nit) {
-        const int e = s.p0 + pw + C::PW * j;
-        id = s.ids[e];
-        if (kView) lp = s.lps[e];
-      }
-    };
-    int idc, lpc, idn, lpn, batch = 0, ahead = 0;
-    unsigned m4c, m4n, whole;  // packed pages of the two loads; those of the first that every column sees in full
-    auto is_packed = [&](int id) { return id >= p.P16 && id < p.P16 + p.P4; };
-    auto classify = [&]() {
-      const int e = s.p0 + pw + C::PW * (batch * 32 + lane);
-      const int pos0 = (kView ? lpc : e) * kPage, first = kView && e >= s.nsel ? s.ctx : 0;
-      m4c = __ballot_sync(0xffffffffu, is_packed(idc));
-      m4n = __ballot_sync(0xffffffffu, is_packed(idn));
-      whole = m4c & __ballot_sync(0xffffffffu, pos0 + kPage - 1 <= s.last0 && pos0 >= first);
-    };
+  };
+  auto is_packed = [&](int id) { return id >= p.P16 && id < p.P16 + p.P4; };
+  auto classify = [&]() {
+    const int e = s.p0 + pw + C::PW * (batch * 32 + lane);
+    const int pos0 = (kView ? lpc : e) * kPage, first = kView && e >= s.nsel ? s.ctx : 0;
+    m4c = __ballot_sync(0xffffffffu, is_packed(idc));
+    m4n = __ballot_sync(0xffffffffu, is_packed(idn));
+    whole = m4c & __ballot_sync(0xffffffffu, pos0 + kPage - 1 <= s.last0 && pos0 >= first);
+  };
+  auto open_part = [&]() {
+    nit = s.p1 - s.p0 > pw ? (s.p1 - s.p0 - pw + C::PW - 1) / C::PW : 0;
+    batch = 0;
+    ahead = 0;
     load_ids(0, idc, lpc);
     load_ids(1, idn, lpn);
-    classify();
-    // Copies for items below k + 24, as far as the ring has room; the lane that holds an item's id starts its copy.
-    auto issue = [&](int k) {
-      while (ahead < nit && ahead < k + 24 && issued != consumed + C::kStages) {
-        const bool cur = (ahead >> 5) == batch;
-        if ((cur ? m4c : m4n) >> (ahead & 31) & 1) {
-          if (lane == (ahead & 31) && cg == 0) {
-            const int id = cur ? idc : idn;
-            mbar_arrive_expect_tx(&bars[in_st], C::kChunk);
-            bulk_g2s(ring + in_st * C::kChunk, p.packed + (static_cast<size_t>(id - p.P16) * p.hkv + s.h) * C::kChunk,
-                     C::kChunk, &bars[in_st]);
-          }
-          ++issued;
-          in_st = in_st + 1 == C::kStages ? 0 : in_st + 1;
-        }
-        ++ahead;
-      }
-    };
-    if (!dead && CS == 1) issue(0);
+  };
+  // Copies for the items from `ahead` on that are held, as far as the ring has room: the lane that holds an item's id
+  // starts its copy, in the slot of its rank among them.
+  auto issue_from = [&](unsigned held, int ids, int first_item) {
+    const unsigned m = held & (~0u << (ahead - first_item));
+    const int room = C::kStages - static_cast<int>(issued - consumed);
+    const int rank = __popc(m & ((1u << lane) - 1u));
+    const bool mine = (m >> lane & 1) && rank < room;
+    if (mine && cg == 0) {
+      const int st = in_st + rank < C::kStages ? in_st + rank : in_st + rank - C::kStages;
+      mbar_arrive_expect_tx(&bars[st], C::kChunk);
+      bulk_g2s(ring + st * C::kChunk, p.packed + (static_cast<size_t>(ids - p.P16) * p.hkv + s.h) * C::kChunk, C::kChunk,
+               &bars[st]);
+    }
+    const unsigned started = __ballot_sync(0xffffffffu, mine);
+    const int n = __popc(started);
+    issued += n;
+    in_st = in_st + n < C::kStages ? in_st + n : in_st + n - C::kStages;
+    ahead = first_item + (started == m ? 32 : 32 - __clz(started));  // with room there is a start unless m is empty
+  };
+  auto issue = [&]() {
+    if (issued - consumed >= C::kStages) return;
+    if (ahead < (batch + 1) * 32) issue_from(m4c, idc, batch * 32);
+    if (ahead >= (batch + 1) * 32 && ahead < (batch + 2) * 32 && issued - consumed < C::kStages)
+      issue_from(m4n, idn, (batch + 1) * 32);
+  };
+  // The queries' loads, asked for before the pages: behind those they would wait for the whole ring.
+  uint4 qv[C::kQPer];
+  auto load_queries = [&]() {
+#pragma unroll
+    for (int k = 0; k < C::kQPer; ++k) {
+      const int i = tid + k * C::kThreads, c = i / (D / 8), piece = i % (D / 8);
+      const int w = c / G, a = c - w * G;
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (c < G * s.nq)
+        qv[k] = *reinterpret_cast<const uint4 *>(p.q + (static_cast<size_t>(s.qoff + w) * p.hq + s.h * G + a) * D + piece * 8);
+    }
+  };
+  load_queries();
+  open_part();
+  classify();
+  if (!dead) issue();
 
-    // ---- queries: raw rows, their power-of-two scales, block sums, then the fp16 fragments
-    for (int c = warp; c < C::N; c += C::kWarps) {
-      float v[D / 32];
-      float mx = 0.0f, sum = 0.0f;
-      const int i = c / G, a = c - i * G;
-      const size_t o = (static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + a) * D + lane * (D / 32);
+  while (true) {
+    const int M = G * s.nq;
+    // ---- queries: a thread takes 8 dims of a column, whose fp16 operands are one entry of the fragment array
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const __nv_bfloat16 b = c < M ? p.q[o + k] : __float2bfloat16(0.0f);
-        qraw[c * C::kQStride + lane * (D / 32) + k] = b;
-        v[k] = to_f(b);
-        mx = fmaxf(mx, fabsf(v[k]));
-        sum += v[k];
+    for (int k = 0; k < C::kQPer; ++k) {
+      const int i = tid + k * C::kThreads, c = i / (D / 8), piece = i % (D / 8);
+      if (c < C::N) {  // whole columns: D / 8 neighbouring lanes
+        float v[8];
+        Vec16<__nv_bfloat16>::unpack(qv[k], v);
+        float mx = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          mx = fmaxf(mx, fabsf(v[z]));
+          sum += v[z];
+        }
+        const unsigned peers = __activemask();
+#pragma unroll
+        for (int o = D / 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(peers, mx, o));
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(peers, sum, o);
+        // largest magnitude to [2^14, 2^15): every bf16 down to 2^-24 of it is exact in fp16, a sixteenth too
+        const int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255);
+        const int sh = e == 0 || e == 255 ? 0 : min(141 - e, 126);
+        const float sc = __uint_as_float(static_cast<uint32_t>(127 + max(sh, -126)) << 23), s16 = sc * 0.0625f;
+        if (piece == 0) qscale[c] = sc;
+        if ((piece & 7) == 0) qsum[c * NB + (piece >> 3)] = sum * qk;
+        *reinterpret_cast<uint4 *>(qraw + c * C::kQStride + piece * 8) = qv[k];
+        // piece = 8 b + 2 t + i: dims 64 b + 16 t + 8 i .. + 7, k-steps 4 b + 2 i and the next, lane (c % 8, t)
+        qfrag4[((c >> 3) * (C::KS / 2) + (piece >> 3) * 2 + (piece & 1)) * 32 + (c & 7) * 4 + ((piece >> 1) & 3)] =
+            make_uint4(pack_f16(v[0] * sc, v[4] * sc), pack_f16(v[1] * s16, v[5] * s16), pack_f16(v[2] * sc, v[6] * sc),
+                       pack_f16(v[3] * s16, v[7] * s16));
       }
-      mx = warp_max(mx);
-      constexpr int kHalf = NB == 2 ? 8 : 16;  // lanes of one block: 16 of two, or all
-#pragma unroll
-      for (int o2 = kHalf; o2 >= 1; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
-      // largest magnitude to [2^14, 2^15): every bf16 down to 2^-24 of it is exact in fp16, a sixteenth too
-      const int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255);
-      const int sh = e == 0 || e == 255 ? 0 : min(141 - e, 126);
-      if (lane == 0) qscale[c] = __uint_as_float(static_cast<uint32_t>(127 + max(sh, -126)) << 23);
-      if (NB == 1 ? lane == 0 : (lane & 15) == 0) qsum[c * NB + (NB == 1 ? 0 : lane >> 4)] = sum * qk;
     }
     __syncthreads();
-    for (int f = tid; f < NTL * CS * C::KS * 32; f += C::kThreads) {
-      const int ln = (f >> 1) & 31, ks = ((f >> 6) % (C::KS / 2)) * 2 + (f & 1), tile = (f >> 6) / (C::KS / 2);
-      const int c = tile * 8 + (ln >> 2);
-      const int d0 = (ks >> 2) * 64 + (ln & 3) * 16 + ((ks >> 1) & 1) * 8 + (ks & 1) * 2;
-      const __nv_bfloat16 *qr = qraw + c * C::kQStride + d0;
-      const float sc = qscale[c], s16 = sc * 0.0625f;
-      qfrag[f] = make_uint2(pack_f16(to_f(qr[0]) * sc, to_f(qr[4]) * sc), pack_f16(to_f(qr[1]) * s16, to_f(qr[5]) * s16));
-    }
-    __syncthreads();
-    // CS > 1: the first column group's lane issues for both, so its partner must have left the ring (barrier above)
-    if (!dead && CS > 1) issue(0);
+    const bool more = x + (s.p1 - s.p0) < x1;
+    if (more && tid == C::kThreads - 1) find_part(s_unit, s_base, x + (s.p1 - s.p0));  // its loads run beside the pages
 
     // per column of this lane (two a tile): logit factor, block sums, reference, sum, sum p * lowest
     F2 cq[NTL], qs[NTL][NB], lsum[NTL], lv[NTL][NB];
@@ -730,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         load_ids(++batch + 1, idn, lpn);
         classify();
       }
-      if (!dead) issue(k);
+      if (!dead) issue();
       const int kk = k & 31;
       if (whole >> kk & 1) {
         const bool two = C::kPairs && (whole >> kk & 3) == 3;
@@ -803,108 +856,121 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         }
       }
     }
-    // ---- warps joined pairwise, always in the same order; a lane hands over to the same lane
-    __syncthreads();  // the ring is idle
-#pragma unroll 1
-    for (int n = C::PW; n > 1; n = (n + 1) / 2) {
-      const int half = (n + 1) / 2;
-      float4 *buf = reinterpret_cast<float4 *>(smem + ((pw % half) + cg * (C::PW / 2)) * C::kJoin);
-      if (pw >= half && pw < n) {
-#pragma unroll
-        for (int j = 0; j < NTL; ++j) {
-          buf[j * 32 + lane] = make_float4(mref[j][0], mref[j][1], lr[j][0], lr[j][1]);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              buf[(NTL + (j * NB + b) * 4 + m) * 32 + lane] =
-                  make_float4(acc[j][b][m][0], acc[j][b][m][1], acc[j][b][m][2], acc[j][b][m][3]);
-        }
-      }
-      __syncthreads();
-      if (pw < n - half) {
-#pragma unroll
-        for (int j = 0; j < NTL; ++j) {
-          const float4 o = buf[j * 32 + lane];
-          const float m0 = fmaxf(mref[j][0], o.x), m1 = fmaxf(mref[j][1], o.y);
-          const float a0 = fast_exp2(mref[j][0] - m0), a1 = fast_exp2(mref[j][1] - m1);
-          const float b0 = fast_exp2(o.x - m0), b1 = fast_exp2(o.y - m1);
-          mref[j][0] = m0;
-          mref[j][1] = m1;
-          lr[j][0] = fmaf(lr[j][0], a0, o.z * b0);
-          lr[j][1] = fmaf(lr[j][1], a1, o.w * b1);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const float4 v = buf[(NTL + (j * NB + b) * 4 + m) * 32 + lane];
-              acc[j][b][m][0] = fmaf(acc[j][b][m][0], a0, v.x * b0);
-              acc[j][b][m][1] = fmaf(acc[j][b][m][1], a1, v.y * b1);
-              acc[j][b][m][2] = fmaf(acc[j][b][m][2], a0, v.z * b0);
-              acc[j][b][m][3] = fmaf(acc[j][b][m][3], a1, v.w * b1);
-            }
-        }
-      }
-      __syncthreads();
-    }
-
-    // ---- the row's result, or a record of its part
-    const int c_first = static_cast<int>(rb / share), c_last = static_cast<int>((re - 1) / share);
+    // ---- warps joined, always in the same order: the upper half hands its sums to the lower half, whose sums then lie
+    // side by side for all threads to add
+    const bool small = s.re < (1 << 30);  // 32-bit division where it will do
+    const int c_first = small ? static_cast<uint32_t>(s.rb) / static_cast<uint32_t>(share) : static_cast<int>(s.rb / share);
+    const int c_last =
+        small ? static_cast<uint32_t>(s.re - 1) / static_cast<uint32_t>(share) : static_cast<int>((s.re - 1) / share);
     const size_t slot = static_cast<size_t>(blockIdx.x) + s.row;
-    if (pw == 0) {
+    const Seg done = s;
+    float *joined = reinterpret_cast<float *>(smem + C::OFF_JOIN);      // [slot][column][kColStride]
+    float *jml = joined + C::kSlots * C::N * C::kColStride;             // [slot][column] maximum, sum
+    if (!C::kApart) __syncthreads();  // the ring is idle
+    float *mine = joined + static_cast<size_t>(pw < C::kSlots ? pw : pw - C::kSlots) * C::N * C::kColStride;
+    float *mml = jml + (pw < C::kSlots ? pw : pw - C::kSlots) * C::N * 2;
+    auto put = [&]() {
 #pragma unroll
       for (int j = 0; j < NTL; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = (cg * NTL + j) * 8 + 2 * t + c;
-          if (col >= M) continue;
-          const float l = lr[j][c];
-          if (c_first == c_last) {
-            const int i = col / G;
-            const size_t o = static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + (col - i * G);
-            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-            if (g == 0) {
-              p.lse[o] = l != 0.0f ? (mref[j][c] + log2f(l)) * kLn2 : -INFINITY;
-              if (kView && l == 0.0f) set_error(p.err, kErrLength);
-            }
+          if (g == 0) *reinterpret_cast<float2 *>(mml + col * 2) = make_float2(mref[j][c], lr[j][c]);
+          float *o = mine + col * C::kColStride + g * 8;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              float v[8];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                v[2 * m] = acc[j][b][m][c] * inv;
-                v[2 * m + 1] = acc[j][b][m][2 + c] * inv;
-              }
-              *reinterpret_cast<uint4 *>(p.out + o * D + b * 64 + g * 8) = Vec16<__nv_bfloat16>::pack(v);
-            }
-          } else {
-            float *rec = p.part + (slot * p.ncol + col) * D + g * 8;
-            if (g == 0) __stcg(&p.ml[slot * p.ncol + col], make_float2(mref[j][c], l));
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              __stcg(reinterpret_cast<float4 *>(rec + b * 64),
-                     make_float4(acc[j][b][0][c], acc[j][b][0][2 + c], acc[j][b][1][c], acc[j][b][1][2 + c]));
-              __stcg(reinterpret_cast<float4 *>(rec + b * 64 + 4),
-                     make_float4(acc[j][b][2][c], acc[j][b][2][2 + c], acc[j][b][3][c], acc[j][b][3][2 + c]));
-            }
+          for (int b = 0; b < NB; ++b) {
+            *reinterpret_cast<float4 *>(o + b * 64) =
+                make_float4(acc[j][b][0][c], acc[j][b][0][2 + c], acc[j][b][1][c], acc[j][b][1][2 + c]);
+            *reinterpret_cast<float4 *>(o + b * 64 + 4) =
+                make_float4(acc[j][b][2][c], acc[j][b][2][2 + c], acc[j][b][3][c], acc[j][b][3][2 + c]);
           }
         }
+    };
+    if (pw >= C::kSlots) put();
+    __syncthreads();
+    if (more) {
+      x += s.p1 - s.p0;
+      s = s_seg;
+      load_queries();
+      open_part();  // the next part's ids, and below its first copies, come in beside the joins
+    }
+    if (pw < C::kSlots) {
+      if (pw + C::kSlots < C::PW) {
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = (cg * NTL + j) * 8 + 2 * t + c;
+            const float2 o = *reinterpret_cast<const float2 *>(mml + col * 2);
+            const float m = fmaxf(mref[j][c], o.x), fa = fast_exp2(mref[j][c] - m), fb = fast_exp2(o.x - m);
+            mref[j][c] = m;
+            lr[j][c] = fmaf(lr[j][c], fa, o.y * fb);
+            const float *v = mine + col * C::kColStride + g * 8;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                acc[j][b][z][c] = fmaf(acc[j][b][z][c], fa, v[b * 64 + 2 * z] * fb);
+                acc[j][b][z][2 + c] = fmaf(acc[j][b][z][2 + c], fa, v[b * 64 + 2 * z + 1] * fb);
+              }
+          }
+        __syncwarp();
+      }
+      put();
+    }
+    if (more) {
+      classify();
+      if (C::kApart && !dead) issue();
+    }
+    __syncthreads();
+    // ---- the row's result, or a record of its part
+    for (int i = tid; i < M * (D / 8); i += C::kThreads) {
+      const int col = i / (D / 8), d0 = (i - col * (D / 8)) * 8;
+      float m = kNoMax, l = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < C::kSlots; ++w) m = fmaxf(m, jml[(w * C::N + col) * 2]);
+#pragma unroll
+      for (int w = 0; w < C::kSlots; ++w) {
+        const float f = fast_exp2(jml[(w * C::N + col) * 2] - m);
+        l = fmaf(jml[(w * C::N + col) * 2 + 1], f, l);
+        const float *o = joined + (w * C::N + col) * C::kColStride + d0;
+        const float4 a = *reinterpret_cast<const float4 *>(o), b = *reinterpret_cast<const float4 *>(o + 4);
+        v[0] = fmaf(a.x, f, v[0]), v[1] = fmaf(a.y, f, v[1]), v[2] = fmaf(a.z, f, v[2]), v[3] = fmaf(a.w, f, v[3]);
+        v[4] = fmaf(b.x, f, v[4]), v[5] = fmaf(b.y, f, v[5]), v[6] = fmaf(b.z, f, v[6]), v[7] = fmaf(b.w, f, v[7]);
+      }
+      if (c_first == c_last) {
+        const int qi = col / G;
+        const size_t o = static_cast<size_t>(done.qoff + qi) * p.hq + done.h * G + (col - qi * G);
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) v[z] *= inv;
+        *reinterpret_cast<uint4 *>(p.out + o * D + d0) = Vec16<__nv_bfloat16>::pack(v);
+        if (d0 == 0) {
+          p.lse[o] = l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          if (kView && l == 0.0f) set_error(p.err, kErrLength);
+        }
+      } else {
+        float *rec = p.part + (slot * p.ncol + col) * D + d0;
+        __stcg(reinterpret_cast<float4 *>(rec), make_float4(v[0], v[1], v[2], v[3]));
+        __stcg(reinterpret_cast<float4 *>(rec + 4), make_float4(v[4], v[5], v[6], v[7]));
+        if (d0 == 0) __stcg(&p.ml[slot * p.ncol + col], make_float2(m, l));
+      }
     }
     if (c_first != c_last) {
       __syncthreads();
       if (tid == 0) {
         const int parts = c_last - c_first + 1;
-        const int old = atom_add_acq_rel_gpu(&p.counters[s.row], 1);
+        const int old = atom_add_acq_rel_gpu(&p.counters[done.row], 1);
         s_flag = old == parts - 1;
-        if (s_flag) p.counters[s.row] = 0;  // left at zero for the next call
+        if (s_flag) p.counters[done.row] = 0;  // left at zero for the next call
       }
       __syncthreads();
       if (s_flag) {
         // part k of the row lies in slot c_first + k + row; weights first, then every thread sums its values in order
         const int parts = c_last - c_first + 1;
-        const size_t slot0 = static_cast<size_t>(c_first) + s.row;
-        float *w = reinterpret_cast<float *>(smem);  // [parts][M] weights over the row's sum
-        float2 *mls = reinterpret_cast<float2 *>(smem);
+        const size_t slot0 = static_cast<size_t>(c_first) + done.row;
+        float *w = joined;  // [parts][M] weights over the row's sum
+        float2 *mls = reinterpret_cast<float2 *>(joined);
         // the maxima and sums come in as pairs; a column's thread turns them into weights in place (first half of a pair)
         for (int i = tid; i < parts * M; i += C::kThreads) {
           const int k = i / M, col = i - k * M;
@@ -921,7 +987,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
             w[2 * (k * M + col)] = f;
           }
           const int i = col / G;
-          p.lse[static_cast<size_t>(s.qoff + i) * p.hq + s.h * G + (col - i * G)] =
+          p.lse[static_cast<size_t>(done.qoff + i) * p.hq + done.h * G + (col - i * G)] =
               l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
           if (kView && l == 0.0f) set_error(p.err, kErrLength);
           w[2 * col + 1] = l != 0.0f ? 1.0f / l : 0.0f;  // of part 0's pair: the factor of the whole column
@@ -930,7 +996,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         for (int i = tid; i < M * (D / 8); i += C::kThreads) {
           const int col = i / (D / 8), d0 = (i - col * (D / 8)) * 8;
           float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
           for (int k = 0; k < parts; ++k) {
             const float *rec = p.part + ((slot0 + k) * p.ncol + col) * D + d0;
             const float4 a = __ldcg(reinterpret_cast<const float4 *>(rec));
@@ -943,15 +1009,15 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 #pragma unroll
           for (int z = 0; z < 8; ++z) v[z] *= inv;
           const int qi = col / G;
-          const size_t o = static_cast<size_t>(s.qoff + qi) * p.hq + s.h * G + (col - qi * G);
+          const size_t o = static_cast<size_t>(done.qoff + qi) * p.hq + done.h * G + (col - qi * G);
           *reinterpret_cast<uint4 *>(p.out + o * D + d0) = Vec16<__nv_bfloat16>::pack(v);
         }
       }
     }
-    // the next part's copies write the memory that the joins used: order this proxy's accesses before theirs
-    fence_proxy_async_smem();
+    if (!more) break;
+    if (!C::kApart) fence_proxy_async_smem();  // the next copies write the memory that the joins used
     __syncthreads();
-    x += s.p1 - s.p0;
+    if (!C::kApart && !dead) issue();
   }
 }
 
@@ -968,8 +1034,14 @@ cudaError_t launch(const AParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
-  return launch_pdl(attn_kernel<D, NTL, CS, kView>, dim3(std::min(device_sm_count() * C::kCtas, C::kMaxGrid)), dim3(C::kThreads), C::BYTES, s,
-                    p);
+  // Short rows that fit the GPU side by side get a CTA each: up to 8 pages a warp take no longer than the records, the
+  // atomic and the merge of a split row.
+  AParams q = p;
+  const int grid = std::min(device_sm_count() * C::kCtas, C::kMaxGrid);
+  const int64_t rows = static_cast<int64_t>(p.R) * (kView && p.view.rows_per_seq == 1 ? p.hkv : kView ? p.view.rows_per_seq : p.hkv);
+  q.by_row = rows <= grid && (kView ? p.view.cap : p.max_pages) <= 8 * C::PW;
+  return launch_pdl(attn_kernel<D, NTL, CS, kView>, dim3(q.by_row ? static_cast<int>(rows) : grid), dim3(C::kThreads),
+                    C::BYTES, s, q);
 }
 
 // Column tiles of 8: up to 4 a warp; wider windows go to two groups of warps that read the same pages.
