@@ -11,6 +11,10 @@ With overlap (the default), a proposal call that does not directly follow the pl
 kernel then scans the view and starts streaming the selected prompt pages while the previous kernel finishes. The
 cycle tracks its own launches for this; a caller that launches kernels writing the view, the page map or prompt
 tokens on the same stream between the cycle's calls must pass overlap=False.
+
+With `packed` (a PackedPool whose 16-bit part is `pool`), block tables may name packed 4-bit pages: routing reads the
+packed pool's summaries, appends write the 16-bit pages, and both attentions are the packed calls. A step is then the
+append (which rotates its queries in place, as with fused=False) followed by the attention.
 """
 from __future__ import annotations
 
@@ -29,9 +33,12 @@ class DecodeCycle:
                  spans: Optional[torch.Tensor] = None, span_offsets: Optional[torch.Tensor] = None,
                  sel_cap: Optional[int] = None, s_max: float = 1.0, fused: bool = True,
                  outputs: Optional[dict] = None, overlap: bool = True,
-                 workspace_pages: Optional[tuple] = None):
+                 workspace_pages: Optional[tuple] = None, packed: Optional[kb.PackedPool] = None):
         dev = block_table.device
-        self.fused = bool(fused)
+        if packed is not None and (packed.pool is not pool or workspace_pages is not None):
+            raise ValueError("packed must hold this pool, and has no materialised workspace")
+        self.packed = packed
+        self.fused = bool(fused) and packed is None
         # (first pool page, pages per request) of a materialised compact workspace, or None for the zero-copy view
         self.workspace_pages = tuple(workspace_pages) if workspace_pages is not None else None
         self.overlap = bool(overlap)
@@ -84,8 +91,12 @@ class DecodeCycle:
         # workspaces (zero-filled once)
         mp = int(block_table.shape[1])
         self.ws_score = kb.workspace(kb.kap_score_workspace_size(self.R, self.rows, mp), dev)
-        self.ws_prop = kb.workspace(kb.kap_propose_workspace_size(self.R, self.Hkv, self.Hq, self.d), dev)
-        self.ws_ver = kb.workspace(kb.kap_verify_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.max_q), dev)
+        if packed is None:
+            self.ws_prop = kb.workspace(kb.kap_propose_workspace_size(self.R, self.Hkv, self.Hq, self.d), dev)
+            self.ws_ver = kb.workspace(kb.kap_verify_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.max_q), dev)
+        else:
+            self.ws_prop = kb.workspace(kb.kap_packed_workspace_size(self.R, self.Hkv, self.Hq, self.d, 1), dev)
+            self.ws_ver = kb.workspace(kb.kap_packed_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.max_q), dev)
         # outputs (caller-provided tensors of these shapes may be passed in `outputs`, e.g. views of one buffer)
         shapes = self.output_shapes()
         outputs = outputs or {}
@@ -112,14 +123,14 @@ class DecodeCycle:
         if self.spans is not None:
             kb.kap_select_spans(self.map_plan, self.spans, self.span_offsets, self.policy, self.sel_ids, self.n_sel,
                                 stream)
-        elif self.fused:
-            kb.kap_score_topk_view(self.pool, self.map_plan, q_route, self.policy, self.sel_ids, self.n_sel,
+        elif self.fused or self.packed is not None:
+            kb.kap_score_topk_view(self.pool if self.packed is None else self.packed.routing(), self.map_plan, q_route, self.policy, self.sel_ids, self.n_sel,
                                    self.ws_score, self.horizon, self.view, self.fallback, self.s_max, self.slots_prop,
                                    self.pos_prop, stream)
         else:
             kb.kap_score_topk(self.pool, self.map_plan, q_route, self.policy, self.sel_ids, self.n_sel, self.ws_score,
                               stream)
-        if self.spans is not None or not self.fused:
+        if self.spans is not None or not (self.fused or self.packed is not None):
             kb.kap_compile_view(self.map_plan, self.sel_ids, self.n_sel, self.horizon, self.view, self.fallback,
                                 self.s_max, self.slots_prop, self.pos_prop, stream)
         if not self.window_is_horizon:
@@ -145,6 +156,11 @@ class DecodeCycle:
 
     def propose(self, i: int, q: torch.Tensor, stream=None, settled: Optional[bool] = None):
         """Proposal step i, second half: q = 1 attention over the compact view."""
+        if self.packed is not None:
+            kb.kap_attn_propose_packed(self.packed, self.map_steps[i], self.view, q, self.o_prop[i], self.lse_prop[i],
+                                       self.ws_prop, stream)
+            self._view_fresh = False
+            return
         kb.kap_attn_propose(self.pool, self.map_steps[i], self.view, q, self.o_prop[i], self.lse_prop[i], self.ws_prop,
                             stream, settled=self._settled(settled))
 
@@ -170,7 +186,11 @@ class DecodeCycle:
         """Causal attention of the window over the full table (after append_window when k_new/v_new are given)."""
         if k_new is not None:
             self.append_window(q, k_new, v_new, stream)
-        kb.kap_attn_verify(self.pool, self.map_full, self.vpol, q, self.o_ver, self.lse_ver, self.ws_ver, stream)
+        if self.packed is not None:
+            kb.kap_attn_verify_packed(self.packed, self.map_full, self.vpol, q, self.o_ver, self.lse_ver, self.ws_ver,
+                                      stream)
+        else:
+            kb.kap_attn_verify(self.pool, self.map_full, self.vpol, q, self.o_ver, self.lse_ver, self.ws_ver, stream)
         self._view_fresh = False
 
     def run(self, q_route, q_prop, k_new_prop, v_new_prop, q_ver, k_new_ver, v_new_ver, stream=None):
@@ -184,7 +204,7 @@ class DecodeCycle:
         top-K and view; or spans and view), a separate window slot mapping when the windows differ from the
         horizon, per step one fused kernel (or an append and a proposal kernel), then the window append and
         verification; plus the materialisation when a workspace is used."""
-        sel_view = 2 if self.spans is not None else (2 if self.fused else 3)
+        sel_view = 2 if self.spans is not None else (2 if self.fused or self.packed is not None else 3)
         sel_view += 1 if self.workspace_pages is not None else 0
         slots = 0 if self.window_is_horizon else 1
         per_step = 1 if self.fused else 2
@@ -251,8 +271,12 @@ class DecodeLoop:
     """
 
     def __init__(self, pool: kb.KVPool, block_table: torch.Tensor, ctx_len: torch.Tensor, seq_len0: torch.Tensor,
-                 steps: int, inv_freq: torch.Tensor, policy: kb.AccessPolicy, s_max: float = 1.0):
+                 steps: int, inv_freq: torch.Tensor, policy: kb.AccessPolicy, s_max: float = 1.0,
+                 packed: Optional[kb.PackedPool] = None):
         dev = block_table.device
+        if packed is not None and packed.pool is not pool:
+            raise ValueError("packed must hold this pool")
+        self.packed = packed   # block tables may name packed pages; propose_step then rotates its queries in place
         self.pool, self.policy, self.inv_freq, self.s_max = pool, policy, inv_freq, s_max
         self.steps = int(steps)
         self.R = int(block_table.shape[0])
@@ -274,7 +298,8 @@ class DecodeLoop:
         self.pos = torch.zeros(self.R, **i32)
         mp = int(block_table.shape[1])
         self.ws_score = kb.workspace(kb.kap_score_workspace_size(self.R, self.rows, mp), dev)
-        self.ws_prop = kb.workspace(kb.kap_propose_workspace_size(self.R, self.Hkv, self.Hq, self.d), dev)
+        self.ws_prop = kb.workspace(kb.kap_propose_workspace_size(self.R, self.Hkv, self.Hq, self.d) if packed is None
+                                    else kb.kap_packed_workspace_size(self.R, self.Hkv, self.Hq, self.d, 1), dev)
         self.o = torch.empty(self.steps, self.R, self.Hq, self.d, dtype=pool.dtype, device=dev)
         self.lse = torch.empty(self.steps, self.R, self.Hq, dtype=torch.float32, device=dev)
         self.t = 0
@@ -282,7 +307,8 @@ class DecodeLoop:
 
     def plan(self, q_route: torch.Tensor, stream=None):
         """Routing of step t: scores on q_route [R][Hq][d], A/R/K top-K and the view at length seq_len0 + t."""
-        kb.kap_score_topk_view(self.pool, self.maps[self.t], q_route, self.policy, self.sel_ids, self.n_sel,
+        kb.kap_score_topk_view(self.pool if self.packed is None else self.packed.routing(), self.maps[self.t], q_route,
+                               self.policy, self.sel_ids, self.n_sel,
                                self.ws_score, 1, self.view, self.fallback, self.s_max, self.slots, self.pos, stream)
         self._routed = True
 
@@ -292,6 +318,12 @@ class DecodeLoop:
         view; outputs o[t], lse[t]. i is the step's index within a cycle and must be 0 (one token per step)."""
         if i != 0:
             raise ValueError("a decode step proposes one token")
+        if self.packed is not None:
+            kb.kap_append_kv(self.pool, k_new, v_new, q, self.pos, self.slots, self.inv_freq, stream=stream)
+            kb.kap_attn_propose_packed(self.packed, self.maps[self.t + 1], self.view, q, self.o[self.t],
+                                       self.lse[self.t], self.ws_prop, stream)
+            self._routed = False
+            return
         st = (not self._routed) if settled is None else bool(settled)
         kb.kap_append_propose(self.pool, self.maps[self.t + 1], self.view, q, k_new, v_new, self.inv_freq,
                               self.o[self.t], self.lse[self.t], self.ws_prop, stream, settled=st)
