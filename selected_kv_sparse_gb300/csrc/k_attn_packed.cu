@@ -24,7 +24,7 @@
 //
 // Statistics. A warp keeps a reference per query column (at most 2^8 below the running maximum) and one for the value
 // scales (at most 2^6 below the largest), so that p s_v stays inside fp16; both move only when a page exceeds them.
-#include "kap_attn_packed.h"
+#include "kap_launch.h"
 #include "kap_packed.cuh"
 
 #include <algorithm>
@@ -35,8 +35,32 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;      // reference of a column that has seen nothing
 constexpr float kMaxSlack = 8.0f;     // log2 units a logit may exceed its reference by
 constexpr float kScaleSlack = 64.0f;  // factor a value scale may exceed its reference by
+
+constexpr int kMaxCtas = 320;  // records of a launch beside one per row: CTAs of the widest grid
+
+struct AParams {
+  const __nv_bfloat16 *k, *v;
+  const unsigned char *packed;
+  int P16, P4, hkv, hq, R;
+  const int32_t *bt;
+  int max_pages;
+  const int32_t *ctx_len, *seq_len;    // proposal
+  ViewArgs view;                       // proposal
+  const int32_t *q_offsets, *q_start;  // verification
+  int max_q, total_q;
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  float *lse;
+  int *counters;  // one per row
+  float2 *ml;     // [slot][columns]
+  float *part;    // [slot][columns][d]
+  int ncol;       // columns of a record: G * max_q
+  int by_row;     // a CTA a row, no shares
+  int *err;
+};
 
 template <int D, int NTL, int CS>
 struct Cfg {
@@ -159,7 +183,7 @@ __device__ __forceinline__ float column_sum(float v) {
 // Units are what has a page list of its own: a request (every head walks the same list), or a row of a per-head view.
 template <bool kView>
 struct Units {
-  const AttnParams &p;
+  const AParams &p;
   __device__ __forceinline__ int count() const { return kView ? p.R * p.view.rows_per_seq : p.R; }
   __device__ __forceinline__ int heads() const { return kView && p.view.rows_per_seq > 1 ? 1 : p.hkv; }
   // Window of request r, kept inside the query array whatever the device data say.
@@ -193,7 +217,7 @@ struct Units {
 };
 
 template <int D, int NTL, int CS, bool kView>
-__global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kCtas) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kCtas) attn_kernel(const AParams p) {
   using C = Cfg<D, NTL, CS>;
   using L = PackedChunk<D>;
   constexpr int NB = C::NB;
@@ -272,18 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     s_unit = unit;
     s_base = base;
   };
-  if (p.rest > 0) {
-    const int row = blockIdx.x / p.rest, slice = blockIdx.x - row * p.rest, unit = row / p.hkv;
-    int bad = 0;
-    const int n = units.pages(unit, bad);
-    if (tid == 0) {
-      if (bad) set_error(p.err, bad);
-      const int p0 = static_cast<int>(static_cast<int64_t>(n) * slice / p.rest);
-      describe(unit, row - unit * p.hkv, p0, static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / p.rest), n, 0);
-    }
-    x1 = n;  // one part
-    x = n;
-  } else if (p.by_row) {
+  if (p.by_row) {
     const int unit = blockIdx.x / H, head = blockIdx.x - unit * H;
     int bad = 0;
     const int n = units.pages(unit, bad);
@@ -356,7 +369,6 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 
   // This warp's items of a part: pages p0 + pw, p0 + pw + PW, ...; ids of 32 items a load, two loads held.
   int nit = 0, idc = -1, lpc = 0, idn = -1, lpn = 0, batch = 0, ahead = 0;
-  unsigned skip = 0u;  // of the first load: pages that are the other kernel's
   unsigned m4c = 0u, m4n = 0u, whole = 0u;  // packed pages of the two loads; those of the first that every column sees in full
   auto load_ids = [&](int b, int &id, int &lp) {
     const int j = b * 32 + lane;
@@ -375,12 +387,6 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     m4c = __ballot_sync(0xffffffffu, is_packed(idc));
     m4n = __ballot_sync(0xffffffffu, is_packed(idn));
     whole = m4c & __ballot_sync(0xffffffffu, pos0 + kPage - 1 <= s.last0 && pos0 >= first);
-    if (!kView && p.rest > 0) {
-      skip = whole;
-      whole = 0u;
-      m4c &= ~skip;
-      m4n &= __ballot_sync(0xffffffffu, pos0 + 32 * C::PW * kPage + kPage - 1 > s.last0);
-    }
   };
   auto open_part = [&]() {
     nit = s.p1 - s.p0 > pw ? (s.p1 - s.p0 - pw + C::PW - 1) / C::PW : 0;
@@ -779,10 +785,6 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
       }
       if (!dead) issue();
       const int kk = k & 31;
-      if (!kView && (skip >> kk & 1)) {
-        ++k;
-        continue;
-      }
       if (whole >> kk & 1) {
         const bool two = C::kPairs && (whole >> kk & 3) == 3;
         if (!dead) {
@@ -856,12 +858,11 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     }
     // ---- warps joined, always in the same order: the upper half hands its sums to the lower half, whose sums then lie
     // side by side for all threads to add
-    const bool record_only = !kView && p.rest > 0;
     const bool small = s.re < (1 << 30);  // 32-bit division where it will do
     const int c_first = small ? static_cast<uint32_t>(s.rb) / static_cast<uint32_t>(share) : static_cast<int>(s.rb / share);
     const int c_last =
         small ? static_cast<uint32_t>(s.re - 1) / static_cast<uint32_t>(share) : static_cast<int>((s.re - 1) / share);
-    const size_t slot = record_only ? p.rest_slot + blockIdx.x : static_cast<size_t>(blockIdx.x) + s.row;
+    const size_t slot = static_cast<size_t>(blockIdx.x) + s.row;
     const Seg done = s;
     float *joined = reinterpret_cast<float *>(smem + C::OFF_JOIN);      // [slot][column][kColStride]
     float *jml = joined + C::kSlots * C::N * C::kColStride;             // [slot][column] maximum, sum
@@ -937,7 +938,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         v[0] = fmaf(a.x, f, v[0]), v[1] = fmaf(a.y, f, v[1]), v[2] = fmaf(a.z, f, v[2]), v[3] = fmaf(a.w, f, v[3]);
         v[4] = fmaf(b.x, f, v[4]), v[5] = fmaf(b.y, f, v[5]), v[6] = fmaf(b.z, f, v[6]), v[7] = fmaf(b.w, f, v[7]);
       }
-      if (c_first == c_last && !record_only) {
+      if (c_first == c_last) {
         const int qi = col / G;
         const size_t o = static_cast<size_t>(done.qoff + qi) * p.hq + done.h * G + (col - qi * G);
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
@@ -955,7 +956,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         if (d0 == 0) __stcg(&p.ml[slot * p.ncol + col], make_float2(m, l));
       }
     }
-    if (c_first != c_last && !record_only) {
+    if (c_first != c_last) {
       __syncthreads();
       if (tid == 0) {
         const int parts = c_last - c_first + 1;
@@ -1021,7 +1022,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 }
 
 template <int D, int NTL, int CS, bool kView>
-cudaError_t launch(const AttnParams &p, cudaStream_t s) {
+cudaError_t launch(const AParams &p, cudaStream_t s) {
   using C = Cfg<D, NTL, CS>;
   static_assert(C::kMaxGrid <= kMaxCtas, "record slots");
   static bool ready[64] = {false};
@@ -1035,12 +1036,9 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   }
   // Short rows that fit the GPU side by side get a CTA each: up to 8 pages a warp take no longer than the records, the
   // atomic and the merge of a split row.
-  AttnParams q = p;
+  AParams q = p;
   const int grid = std::min(device_sm_count() * C::kCtas, C::kMaxGrid);
   const int64_t rows = static_cast<int64_t>(p.R) * (kView && p.view.rows_per_seq == 1 ? p.hkv : kView ? p.view.rows_per_seq : p.hkv);
-  if (p.rest > 0)
-    return launch_pdl(attn_kernel<D, NTL, CS, kView>, dim3(static_cast<unsigned>(rows * p.rest)), dim3(C::kThreads),
-                      C::BYTES, s, q);
   q.by_row = rows <= grid && (kView ? p.view.cap : p.max_pages) <= 8 * C::PW;
   return launch_pdl(attn_kernel<D, NTL, CS, kView>, dim3(q.by_row ? static_cast<int>(rows) : grid), dim3(C::kThreads),
                     C::BYTES, s, q);
@@ -1048,7 +1046,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
 
 // Column tiles of 8: up to 4 a warp; wider windows go to two groups of warps that read the same pages.
 template <int D, bool kView>
-cudaError_t launch_tiles(const AttnParams &p, cudaStream_t s) {
+cudaError_t launch_tiles(const AParams &p, cudaStream_t s) {
   const int tiles = (p.ncol + 7) / 8;
   if (kView || tiles == 1) return launch<D, 1, 1, kView>(p, s);
   if (tiles == 2) return launch<D, 2, 1, false>(p, s);
@@ -1059,12 +1057,9 @@ cudaError_t launch_tiles(const AttnParams &p, cudaStream_t s) {
 }
 
 
-// Slots of records: one per row and CTA, and the slices of rows in the launch before the tensor-core one.
-size_t record_slots(size_t rows) { return 2 * rows + kMaxCtas + 160; }
-
-AttnParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *out, float *lse, void *ws, int ncol,
+AParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *out, float *lse, void *ws, int ncol,
                int *err) {
-  AttnParams p{};
+  AParams p{};
   p.k = static_cast<const __nv_bfloat16 *>(pa.pool.k);
   p.v = static_cast<const __nv_bfloat16 *>(pa.pool.v);
   p.packed = static_cast<const unsigned char *>(pa.packed);
@@ -1082,8 +1077,7 @@ AttnParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *o
   p.lse = lse;
   p.ncol = ncol;
   p.err = err;
-  const size_t rows = static_cast<size_t>(m.R) * p.hkv, slots = record_slots(rows);
-  p.rest_slot = rows + kMaxCtas;
+  const size_t rows = static_cast<size_t>(m.R) * p.hkv, slots = rows + kMaxCtas;
   unsigned char *w = static_cast<unsigned char *>(ws);
   p.counters = reinterpret_cast<int *>(w);
   w += (rows * 4 + 255) / 256 * 256;
@@ -1096,14 +1090,14 @@ AttnParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *o
 }  // namespace
 
 size_t packed_workspace_bytes(int R, int hkv, int hq, int d, int max_q) {
-  const size_t rows = static_cast<size_t>(R) * hkv, slots = record_slots(rows);
+  const size_t rows = static_cast<size_t>(R) * hkv, slots = rows + kMaxCtas;
   const size_t ncol = static_cast<size_t>(hq / hkv) * max_q;
   return (rows * 4 + 255) / 256 * 256 + (slots * ncol * 8 + 255) / 256 * 256 + slots * ncol * d * 4;
 }
 
 cudaError_t launch_propose_packed(const PackedArgs &pa, const MapArgs &m, const ViewArgs &v, const void *q, void *out,
                                   float *lse, void *ws, int *err, cudaStream_t s) {
-  AttnParams p = params(pa, m, q, out, lse, ws, pa.pool.hq / pa.pool.hkv, err);
+  AParams p = params(pa, m, q, out, lse, ws, pa.pool.hq / pa.pool.hkv, err);
   p.view = v;
   p.max_q = 1;
   p.total_q = m.R;
@@ -1113,19 +1107,12 @@ cudaError_t launch_propose_packed(const PackedArgs &pa, const MapArgs &m, const 
 cudaError_t launch_verify_packed(const PackedArgs &pa, const MapArgs &m, int max_q, int total_q,
                                  const int32_t *q_offsets, const int32_t *q_start, const void *q, void *out,
                                  float *lse, void *ws, int *err, cudaStream_t s) {
-  AttnParams p = params(pa, m, q, out, lse, ws, pa.pool.hq / pa.pool.hkv * max_q, err);
+  AParams p = params(pa, m, q, out, lse, ws, pa.pool.hq / pa.pool.hkv * max_q, err);
   p.q_offsets = q_offsets;
   p.q_start = q_start;
   p.max_q = max_q;
   p.total_q = total_q;
-  if (pa.pool.d == 64) return launch_tiles<64, false>(p, s);
-  if (p.ncol <= 8) return launch_tiles<128, false>(p, s);
-  // wider windows: what is not a wholly visible packed page here (a few pages a row, as a rule), those on the 5th-generation
-  // tensor cores; enough slices that a cache of 16-bit pages keeps the GPU busy too
-  const int64_t rows = static_cast<int64_t>(m.R) * pa.pool.hkv;
-  p.rest = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({152 / rows, kMaxRest, (m.max_pages + 7) / 8})));
-  const cudaError_t e = launch_tiles<128, false>(p, s);
-  return e != cudaSuccess ? e : launch_attn_packed_tc(p, s);
+  return pa.pool.d == 128 ? launch_tiles<128, false>(p, s) : launch_tiles<64, false>(p, s);
 }
 
 }  // namespace kap
