@@ -64,7 +64,7 @@ struct AParams {
 
 template <int D, int NTL, int CS>
 struct Cfg {
-  static constexpr int kWarps = NTL == 2 ? 10 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kCtas = NTL == 1 ? 2 : 1;         // resident CTAs an SM
   static constexpr int PW = kWarps / CS;                 // warps that take pages in turn
@@ -1034,12 +1034,13 @@ cudaError_t launch(const AParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
-  // Short rows that fit the GPU side by side get a CTA each: up to 8 pages a warp take no longer than the records, the
-  // atomic and the merge of a split row.
+  // Rows of up to 16 pages a warp get a CTA each, which needs no scan, records, atomic or merge; longer ones are shared
+  // out. Both sides on a GB300, proposals over 32, 256 and 2400 rows, us by row / shared out: 60 pages 10 / 15, 17 / 26,
+  // 114 / 126; 120 pages 16 / 17, 25 / 30, 161 / 175 (110 pages); 150 pages over 32 rows 18 / 16.
   AParams q = p;
   const int grid = std::min(device_sm_count() * C::kCtas, C::kMaxGrid);
-  const int64_t rows = static_cast<int64_t>(p.R) * (kView && p.view.rows_per_seq == 1 ? p.hkv : kView ? p.view.rows_per_seq : p.hkv);
-  q.by_row = rows <= grid && (kView ? p.view.cap : p.max_pages) <= 8 * C::PW;
+  const int64_t rows = static_cast<int64_t>(p.R) * p.hkv;
+  q.by_row = (kView ? p.view.cap : p.max_pages) <= 16 * C::PW && rows <= 0x7fffffff;
   return launch_pdl(attn_kernel<D, NTL, CS, kView>, dim3(q.by_row ? static_cast<int>(rows) : grid), dim3(C::kThreads),
                     C::BYTES, s, q);
 }
