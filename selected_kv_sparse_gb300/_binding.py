@@ -166,13 +166,13 @@ def _at(t: Optional[torch.Tensor], dev: int, dtype: Optional[torch.dtype] = None
     """Address of a contiguous tensor on device `dev` (None for None)."""
     if t is None:
         return None
-    if dtype is not None and t.dtype != dtype:
+    if (dtype is None or t.dtype is dtype) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype)[6:]}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on the current CUDA device {dev}, got one on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -298,24 +298,28 @@ class PackedPool:
     packed: torch.Tensor
     k_summary: Optional[torch.Tensor] = None
 
-    def _base(self, dev: Optional[int] = None) -> _Pool:
+    def _base(self, dev: int) -> _Pool:
         pool, ks = self.pool, self.k_summary
-        k, v, x = pool.k_pages, pool.v_pages, self.packed
-        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        k, v = pool.k_pages, pool.v_pages
+        shape, packed = k.shape, self.packed.shape
+        if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
             raise TypeError("a pool with packed pages must be bfloat16")
-        if k.dim() != 4 or k.shape != v.shape or k.shape[2] != PAGE:
+        if len(shape) != 4 or shape != v.shape or shape[2] != PAGE:
             raise ValueError("k_pages/v_pages must both be [num_pages][Hkv][16][d]")
-        P, hkv, _, d = k.shape
-        if x.dtype != torch.uint8 or x.dim() != 3 or x.shape[1] != hkv or x.shape[2] != d // 64 * _PACKED_BLOCK:
+        P, hkv, _, d = shape
+        if self.packed.dtype is not torch.uint8 or len(packed) != 3 or packed[1] != hkv or \
+                packed[2] != d // 64 * _PACKED_BLOCK:
             raise ValueError("packed must be uint8 [num_packed][Hkv][kap_packed_chunk_bytes(d)]")
-        if ks is not None and (ks.dtype != torch.float32 or tuple(ks.shape) != (P + x.shape[0], hkv, d)):
+        if ks is not None and (ks.dtype is not torch.float32 or tuple(ks.shape) != (P + packed[0], hkv, d)):
             raise ValueError("k_summary must be fp32 [num_pages + num_packed][Hkv][d]")
-        dev = _here(k) if dev is None else dev
-        return _Pool(P, PAGE, hkv, pool.num_q_heads, d, KAP_BF16, _at(k, dev), _at(v, dev), _at(ks, dev))
+        return _Pool(P, PAGE, hkv, pool.num_q_heads, d, KAP_BF16, _at(k, dev), _at(v, dev),
+                     None if ks is None else _at(ks, dev))
 
     def _c(self, dev: Optional[int] = None) -> _Packed:
-        dev = _here(self.packed) if dev is None else dev
-        return _Packed(self._base(dev), self.packed.shape[0], _at(self.packed, dev))
+        x = self.packed
+        if dev is None:
+            dev = _here(x)
+        return _Packed(self._base(dev), x.shape[0], _at(x, dev))
 
     @property
     def dtype(self):
@@ -340,7 +344,7 @@ class _RoutingPool:
         self._owner = owner
 
     def _c(self) -> _Pool:
-        p = self._owner._base()
+        p = self._owner._base(_here(self._owner.packed))
         p.num_pages += int(self._owner.packed.shape[0])
         return p
 
@@ -580,11 +584,12 @@ def kap_packed_chunk_bytes(d: int) -> int:
 
 def _pack(fn: str, pool: PackedPool, src: torch.Tensor, dst: torch.Tensor, stream):
     f = getattr(load(), fn)
-    if src.dim() != 1 or src.shape != dst.shape:
+    n = src.numel()
+    if src.dim() != 1 or dst.dim() != 1 or dst.numel() != n:
         raise ValueError("src_pages and dst_pages must be 1-D and of equal length")
     dev = _here(pool.packed)
     s, d = _at(src, dev, torch.int32, "src_pages"), _at(dst, dev, torch.int32, "dst_pages")
-    st = f(ctypes.byref(pool._c(dev)), s, d, src.shape[0], _raw_stream(stream, dev))
+    st = f(ctypes.byref(pool._c(dev)), s, d, n, _raw_stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -605,9 +610,8 @@ def kap_packed_workspace_size(R: int, hkv: int, hq: int, d: int, max_q: int = 1)
 
 def _attention_args(pool: PackedPool, rows: int, q, out, lse, workspace):
     """(device, addresses of q, out, lse, workspace, bytes of the workspace) after their checks."""
-    k = pool.pool.k_pages
-    shape = (rows, pool.pool.num_q_heads, k.shape[3])
-    if tuple(q.shape) != shape or tuple(out.shape) != shape or tuple(lse.shape) != shape[:2]:
+    shape = (rows, pool.pool.num_q_heads, pool.pool.k_pages.shape[3])
+    if q.shape != shape or out.shape != shape or lse.shape != shape[:2]:   # a torch.Size is a tuple
         raise ValueError(f"q and out must be {list(shape)} and lse {list(shape[:2])}")
     dev = _here(pool.packed)
     bf16 = torch.bfloat16
@@ -633,8 +637,8 @@ def kap_attn_propose_packed(pool: PackedPool, pmap: PageMap, view: View, q: torc
     R, i32 = pmap.block_table.shape[0], torch.int32
     dev, aq, ao, al, aw, nw = _attention_args(pool, R, q, out, lse, workspace)
     rows, cap = view.rows_per_seq, view.cap
-    if tuple(view.block_table.shape) != (R, rows, cap) or view.logical_page.shape != view.block_table.shape or \
-            tuple(view.n_entries.shape) != (R, rows) or view.n_selected.shape != view.n_entries.shape:
+    if view.block_table.shape != (R, rows, cap) or view.logical_page.shape != (R, rows, cap) or \
+            view.n_entries.shape != (R, rows) or view.n_selected.shape != (R, rows):
         raise ValueError("the view's tensors must be [R][rows_per_seq][cap] and [R][rows_per_seq]")
     v = _View(rows, cap, _at(view.block_table, dev, i32, "view.block_table"),
               _at(view.logical_page, dev, i32, "view.logical_page"), _at(view.n_entries, dev, i32, "view.n_entries"),
@@ -702,8 +706,10 @@ def kap_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: tor
 
 
 def _vector(t: torch.Tensor, n: Optional[int], dev: int, name: str, dtype=torch.int32):
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+    if t.dim() != 1 or (n is not None and t.numel() != n):
         raise ValueError(f"{name} must be 1-D" + (f" with {n} entries" if n is not None else ""))
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     return _at(t, dev, dtype, name)
 
 
