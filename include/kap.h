@@ -369,8 +369,8 @@ kap_status kap_unpack_pages(const kap_packed_pool *pool, const int32_t *src_page
 /* Attention over a pool with packed pages: kap_attn_propose and kap_attn_verify with the same arguments, visibility
  * rules and outputs, over pages of both kinds. Keys and values are those that the codes stand for (lowest + scale *
  * code, not rounded); sums and softmax statistics are fp32, probabilities enter the product with the values as fp16
- * (packed pages) or as two bf16 terms (16-bit pages). The value scales of one (request, KV head) should span less than
- * a factor of 2^20: a packed token whose probability times scale is 2^-20 of the largest scale or less loses bits.
+ * (packed pages) or as two bf16 terms (16-bit pages). Probability times value scale keeps its 11 bits down to
+ * 2^-15 of the largest scale met in a row's part, and below that an error of 2^-25 of it.
  * Every group size G in 1..8 is supported. kap_view.settled is not read. A hidden or skipped token adds nothing,
  * whatever its codes, parameters or 16-bit values hold. A query row that sees no token gets zeros and lse -infinity
  * (and, for the proposal, device error bit 4).

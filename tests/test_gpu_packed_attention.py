@@ -183,6 +183,96 @@ def test_proposal_over_a_view(kap, case):
             c.check(out, lse, q, r, head, toks)
 
 
+SHARED_OUT = [
+    # tables wider than a CTA's own rows: lens, windows, hkv, G, d, kinds, width of the table
+    ([2600, 2100, 40], [8, 3, 1], 1, 8, 128, "mixed", 170),
+    ([2300], [8], 2, 5, 128, "tail16", 170),
+    ([2300, 700], [8, 6], 1, 6, 128, "mixed", 170),
+    ([2200], [8], 1, 3, 128, "mixed", 140),
+    ([2200, 9], [4, 4], 2, 8, 128, "packed", 140),
+    ([2100, 2500], [8, 16], 1, 3, 64, "mixed", 160),
+    ([2500], [16], 1, 4, 64, "mixed", 160),
+    ([1 + (37 * r) % 60 for r in range(300)], [1] * 300, 1, 2, 64, "mixed", 131),     # more requests than threads
+    ([2 + (41 * r) % 50 for r in range(270)], [r % 3 for r in range(270)], 2, 4, 128, "mixed", 131),
+]
+
+
+@pytest.mark.parametrize("case", SHARED_OUT, ids=lambda c: f"R{len(c[0])}-{max(c[0])}-q{max(c[1])}-h{c[2]}x{c[3]}-d{c[4]}-{c[5]}")
+def test_rows_shared_out_over_ctas(kap, case):
+    lens, win, hkv, G, d, kinds, width = case
+    c = Cache(kap, lens, hkv, G, d, KINDS[kinds], seed=len(lens) + G)
+    dev, R = "cuda", len(lens)
+    bt = torch.full((R, width), -1, dtype=torch.int32)
+    bt[:, :min(width, c.mp)] = c.bt[:, :width]
+    q = c.query(sum(win) + 3)
+    off = torch.tensor([0] + list(np.cumsum(win)), dtype=torch.int32)
+    start = torch.tensor([n - w for n, w in zip(lens, win)], dtype=torch.int32)
+    ln = torch.tensor(lens, dtype=torch.int32, device=dev)
+    vp = kap.VerifyPolicy(off.to(dev), start.to(dev), max(win), sum(win) + 3)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full(q.shape[:2], 7.0, device=dev)
+    ws = kap.workspace(kap.kap_packed_workspace_size(R, hkv, hkv * G, d, max(win)), dev)
+    for _ in range(2):
+        kap.kap_attn_verify_packed(c.pool, kap.PageMap(bt.to(dev), ln, ln), vp, q.to(dev), out, lse, ws)
+        assert kap.kap_device_error() == 0
+    assert (out[sum(win):] == 7.0).all() and (lse[sum(win):] == 7.0).all()   # rows behind the last window stay
+    for r in range(0, R, max(1, R // 12)):
+        for i in sorted({0, win[r] - 1} if win[r] else set()):
+            for head in sorted({0, hkv * G - 1}):
+                toks = [c.page(int(c.bt[r, t // PAGE]), head // G)[t % PAGE] for t in range(lens[r] - win[r] + i + 1)]
+                c.check(out, lse, q, int(off[r]) + i, head, toks)
+
+
+def test_views_shared_out_over_ctas(kap):
+    """More view rows than threads, in a view wider than a CTA's own rows; some hold nothing."""
+    hkv, G, d, R, cap = 2, 3, 128, 150, 140
+    lens = [(29 * r) % 90 for r in range(R)]
+    c = Cache(kap, lens, hkv, G, d, KINDS["mixed"], seed=8)
+    dev = "cuda"
+    i32 = dict(dtype=torch.int32)
+    vbt, lp = torch.zeros(R, hkv, cap, **i32), torch.zeros(R, hkv, cap, **i32)
+    n = torch.tensor([[(x + PAGE - 1) // PAGE] * hkv for x in lens], **i32)
+    for r in range(R):
+        k = int(n[r, 0])
+        vbt[r, :, :k] = c.bt[r, :k]
+        lp[r, :, :k] = torch.arange(k, **i32)
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    q = c.query(R)
+    out, lse = torch.empty(q.shape, dtype=torch.bfloat16, device=dev), torch.empty(q.shape[:2], device=dev)
+    ws = kap.workspace(kap.kap_packed_workspace_size(R, hkv, hkv * G, d), dev)
+    kap.kap_attn_propose_packed(c.pool, kap.PageMap(c.bt.to(dev), t(lens), t(lens)),
+                                kap.View(hkv, cap, vbt.to(dev), lp.to(dev), n.to(dev), n.to(dev)), q.to(dev), out, lse, ws)
+    assert kap.kap_device_error() == 4   # the rows that hold nothing
+    for r in list(range(0, R, 13)) + [r for r in range(R) if lens[r] == 0]:
+        for head in (0, 5):
+            c.check(out, lse, q, r, head, [c.page(int(c.bt[r, x // PAGE]), head // G)[x % PAGE] for x in range(lens[r])])
+
+
+def test_value_scales_far_apart(kap):
+    """Tokens with a value scale 2^13 of the others' and nearly all of the weight, after and before large ones."""
+    dev = "cuda"
+    for order in (0, 1):
+        n = 320
+        c = Cache(kap, [n], 1, 2, 128, KINDS["packed"], seed=11)
+        q = c.query(1)
+        heavy = [3, 4] if order else [15, 16]
+        for j in range(n // PAGE):
+            pid = int(c.bt[0, j]) - c.P16
+            par = c.packed[pid, 0, 2048:].view(torch.bfloat16).view(2, 2, PAGE, 2)
+            if j in heavy:
+                par[1] *= 2.0 ** -13
+                par[0, :, :, 0] *= 0.0                  # keys along the query: all codes stand for the lowest value
+                par[0, :, :, 1] = 2.0 * q[0, 0].float().sign().view(2, 64)[:, :1].to(torch.bfloat16)
+        c.pool = kap.PackedPool(kap.KVPool(c.K.to(dev), c.V.to(dev), 2), c.packed.to(dev))
+        t = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+        out, lse = torch.empty(1, 2, 128, dtype=torch.bfloat16, device=dev), torch.empty(1, 2, device=dev)
+        ws = kap.workspace(kap.kap_packed_workspace_size(1, 1, 2, 128, 1), dev)
+        kap.kap_attn_verify_packed(c.pool, kap.PageMap(c.bt.to(dev), t([n]), t([n])),
+                                   kap.VerifyPolicy(t([0, 1]), t([n - 1]), 1, 1), q.to(dev), out, lse, ws)
+        for head in range(2):
+            c.check(out, lse, q, 0, head, [c.page(int(c.bt[0, i // PAGE]), 0)[i % PAGE] for i in range(n)])
+
+
 def test_large_and_small_magnitudes(kap):
     """Keys, values and queries far from 1: sums stay in range and keep their bits."""
     dev = "cuda"
