@@ -13,17 +13,24 @@
 // Tile. A page is 16 tokens: the M of mma.m16n8k16. Logits are S^T[16 tokens x 8 queries] = codes . q^T, and
 // O^T[16 dims x 8 queries] = codes^T . p^T; p moves from one to the other inside registers (movmatrix). Queries of one
 // KV head (G heads x window rows) are the columns, in tiles of 8. Why mma.sync and registers: a (page, head) is 2304
-// bytes, 98 SM cycles of HBM at the measured copy rate, and 65536 codes; as 16-bit operands in shared memory for
-// tcgen05 those would be 8 KiB written and read again, more than the page's time at 128 bytes a cycle. Fragments masked
-// out of the packed words cost 0.6 instructions a pair.
+// bytes, 98 SM cycles of HBM at the measured copy rate, and 4096 codes; as 16-bit operands in shared memory for tcgen05
+// those would be 8 KiB written and read again. Fragments masked out of the packed words cost 0.6 instructions a pair and
+// touch shared memory once. (A tcgen05 form with the key codes in TMEM took 117 us where this takes 63, four windows of 4
+// over 32768 tokens: its code conversion and its softmax followed one another in the eight warps that its registers allow.)
 //
-// Split. The pages of all (request, KV head) rows form one line that is cut into equal shares, one a CTA. In a share
-// the warps take pages in turn, each with its own ring of bulk copies (a whole page-head each), its own running maximum
-// and accumulators; they are joined at the end of a row's part, and the last CTA to finish a row merges the parts in
-// their order.
+// Split. Rows of up to 16 pages a warp get a CTA each. Otherwise the pages of all (request, KV head) rows form one line
+// that is cut into equal shares, one a CTA, and the last CTA to finish a row merges the parts in their order. In either
+// case the warps of a CTA take pages in turn, two at a time for independent work, each with its own ring of bulk copies (a
+// whole page-head each), its own references and accumulators; they are joined at the end of a row's part, while the next
+// part's queries, ids and first pages are on their way.
 //
 // Statistics. A warp keeps a reference per query column (at most 2^8 below the running maximum) and one for the value
 // scales (at most 2^6 below the largest), so that p s_v stays inside fp16; both move only when a page exceeds them.
+//
+// Bound by instruction issue and by the latency of dependent instructions, not by HBM. On a GB300, 8 KV heads of 128 dims:
+// 8 requests of 40960 tokens, 4 query columns: 85.5 us, 4.43 TB/s, 65% of the measured copy rate (312 instructions and 131
+// cycles a page and SM); 4 of 32768, 16 columns: 63 us, 35% (404, 217); one of 131072, 40 columns: 155 us, 14% (884, 536);
+// proposals of 8 and of 128 pages: 5.9 and 15.7 us, a chain of dependent loads.
 #include "kap_launch.h"
 #include "kap_packed.cuh"
 

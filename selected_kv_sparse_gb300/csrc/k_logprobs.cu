@@ -12,9 +12,11 @@
 // only those n tiles are read again (from L2), and the n-th tile's maximum bars nearly all of their tokens.
 //
 // Bound by HBM: one pass over the logits; at bf16 the exponential unit (16 a cycle and SM) would allow 1.36 times the
-// measured copy rate, so the loop is kept to about 7 instructions a logit with packed bf16 compares and maxima. A warp
-// streams chunks of 512 logits with the next chunk's loads in flight and its own running sums: no barriers. Rows that are
+// measured copy rate, so the loop keeps to packed bf16 compares and maxima and to pairs of fp32. A warp streams
+// chunks of 512 logits with the next chunk's loads in flight and its own running sums: no barriers. Rows that are
 // too few to fill the GPU are split over CTAs; the last one to finish a row joins the parts in their order.
+// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 132 us, 4.0 TB/s, 59% of the measured copy rate (107
+// us without alternatives; 71% of the issue slots); of fp32 182 us, 85%; 20 rows of fp32 with 5 alternatives 10.2 us.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 
