@@ -375,8 +375,9 @@ kap_status kap_unpack_pages(const kap_packed_pool *pool, const int32_t *src_page
  * whatever its codes, parameters or 16-bit values hold. A query row that sees no token gets zeros and lse -infinity
  * (and, for the proposal, device error bit 4).
  *   workspace >= kap_packed_workspace_size(R, Hkv, Hq, d, max_q) bytes (max_q = 1 for the proposal), zero-filled once
- *   before first use; the kernels leave its counters at zero. Calls that may run at the same time, captured graphs
- *   among them, need a workspace each. */
+ *   before first use; the kernels leave its counters at zero. Calls of other sizes may take the same workspace in turn
+ *   if it is large enough for each. Calls that may run at the same time, captured graphs among them, need a workspace
+ *   each. */
 kap_status kap_attn_propose_packed(const kap_packed_pool *pool, const kap_page_map *map, const kap_view *view,
                                    const void *q_dev, void *out, float *lse, void *workspace,
                                    size_t workspace_bytes, kap_stream stream);
@@ -397,7 +398,8 @@ size_t kap_packed_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
  * throughout, has no distribution: its log probabilities and entropy are NaN, ranks and ids hold. A token outside
  * [0, vocab) gets -infinity and rank vocab.
  *   workspace >= kap_logprobs_workspace_size(rows, vocab) bytes, zero-filled once before first use; the call leaves its
- *   counters at zero. Calls that may run at the same time need a workspace each.
+ *   counters at zero. Calls of other sizes may take the same workspace in turn if it is large enough for each; calls
+ *   that may run at the same time need a workspace each.
  * Errors: KAP_EINVAL for null pointers, rows < 0, vocab < 1, row_stride < vocab, top_n outside [0, min(32, vocab)];
  * KAP_EUNSUPPORTED for another dtype or vocab > 2^24; KAP_ECAPACITY for a small workspace. */
 kap_status kap_token_logprobs(const void *logits_dev, int32_t logits_dtype, int32_t vocab, int64_t row_stride,

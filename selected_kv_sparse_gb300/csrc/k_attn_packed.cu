@@ -47,6 +47,10 @@ constexpr float kMaxSlack = 8.0f;     // log2 units a logit may exceed its refer
 constexpr float kScaleSlack = 64.0f;  // factor a value scale may exceed its reference by
 
 constexpr int kMaxCtas = 320;  // records of a launch beside one per row: CTAs of the widest grid
+// The workspace begins with a counter a CTA, whatever the call's sizes, so that calls of any sizes may take one workspace
+// in turn: no call's records lie where another one's counters do.
+constexpr size_t kCounterBytes = kMaxCtas * sizeof(int);
+static_assert(kCounterBytes % 256 == 0, "records are aligned");
 
 struct AParams {
   const __nv_bfloat16 *k, *v;
@@ -61,7 +65,7 @@ struct AParams {
   const __nv_bfloat16 *q;
   __nv_bfloat16 *out;
   float *lse;
-  int *counters;  // one per row
+  int *counters;  // of the shared row that begins in a CTA's share (at most one: the next begins in a later share)
   float2 *ml;     // [slot][columns]
   float *part;    // [slot][columns][d]
   int ncol;       // columns of a record: G * max_q
@@ -967,9 +971,9 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
       __syncthreads();
       if (tid == 0) {
         const int parts = c_last - c_first + 1;
-        const int old = atom_add_acq_rel_gpu(&p.counters[done.row], 1);
+        const int old = atom_add_acq_rel_gpu(&p.counters[c_first], 1);
         s_flag = old == parts - 1;
-        if (s_flag) p.counters[done.row] = 0;  // left at zero for the next call
+        if (s_flag) p.counters[c_first] = 0;  // left at zero for the next call
       }
       __syncthreads();
       if (s_flag) {
@@ -1088,7 +1092,7 @@ AParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *out,
   const size_t rows = static_cast<size_t>(m.R) * p.hkv, slots = rows + kMaxCtas;
   unsigned char *w = static_cast<unsigned char *>(ws);
   p.counters = reinterpret_cast<int *>(w);
-  w += (rows * 4 + 255) / 256 * 256;
+  w += kCounterBytes;
   p.ml = reinterpret_cast<float2 *>(w);
   w += (slots * ncol * 8 + 255) / 256 * 256;
   p.part = reinterpret_cast<float *>(w);
@@ -1100,7 +1104,7 @@ AParams params(const PackedArgs &pa, const MapArgs &m, const void *q, void *out,
 size_t packed_workspace_bytes(int R, int hkv, int hq, int d, int max_q) {
   const size_t rows = static_cast<size_t>(R) * hkv, slots = rows + kMaxCtas;
   const size_t ncol = static_cast<size_t>(hq / hkv) * max_q;
-  return (rows * 4 + 255) / 256 * 256 + (slots * ncol * 8 + 255) / 256 * 256 + slots * ncol * d * 4;
+  return kCounterBytes + (slots * ncol * 8 + 255) / 256 * 256 + slots * ncol * d * 4;
 }
 
 cudaError_t launch_propose_packed(const PackedArgs &pa, const MapArgs &m, const ViewArgs &v, const void *q, void *out,

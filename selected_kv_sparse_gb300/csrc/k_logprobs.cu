@@ -31,6 +31,8 @@ constexpr int kChunk = 512;              // logits of a warp's step, 16 a lane
 constexpr int kMaxTiles = kLpThreads;    // tiles of a row whose maxima are kept: one a thread
 constexpr int kMaxSplit = 32;            // CTAs of a row
 constexpr int kSplitRows = 512;          // from here on there is a CTA a row
+constexpr size_t kCounterBytes = kSplitRows * sizeof(int);  // whatever the rows: calls of any sizes may take one
+                                                            // workspace in turn
 constexpr float kC = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -1e7f;         // logits are lifted to it
@@ -514,7 +516,7 @@ int tile_chunks_of(int V) { return (V / kChunk + 2 + kMaxTiles - 1) / kMaxTiles;
 size_t logprobs_workspace_bytes(int rows, int vocab) {
   (void)vocab;
   const size_t n = static_cast<size_t>(std::min(rows, kSplitRows));
-  return (n * 4 + 255) / 256 * 256 + n * kMaxSplit * 32 + n * kMaxTiles * 4;
+  return kCounterBytes + n * kMaxSplit * 32 + n * kMaxTiles * 4;
 }
 
 cudaError_t launch_logprobs(const void *logits, int dtype, int V, int64_t stride, int rows, const int32_t *tokens,
@@ -542,7 +544,7 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int V, int64_t stride
   const size_t n = static_cast<size_t>(std::min(rows, kSplitRows));
   unsigned char *w = static_cast<unsigned char *>(ws);
   p.counters = reinterpret_cast<int *>(w);
-  w += (n * 4 + 255) / 256 * 256;
+  w += kCounterBytes;
   p.parts = reinterpret_cast<float4 *>(w);
   w += n * kMaxSplit * 32;
   p.keys = reinterpret_cast<uint32_t *>(w);

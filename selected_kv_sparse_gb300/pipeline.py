@@ -124,7 +124,8 @@ class DecodeCycle:
             kb.kap_select_spans(self.map_plan, self.spans, self.span_offsets, self.policy, self.sel_ids, self.n_sel,
                                 stream)
         elif self.fused or self.packed is not None:
-            kb.kap_score_topk_view(self.pool if self.packed is None else self.packed.routing(), self.map_plan, q_route, self.policy, self.sel_ids, self.n_sel,
+            kb.kap_score_topk_view(self.pool if self.packed is None else self.packed.routing(), self.map_plan, q_route,
+                                   self.policy, self.sel_ids, self.n_sel,
                                    self.ws_score, self.horizon, self.view, self.fallback, self.s_max, self.slots_prop,
                                    self.pos_prop, stream)
         else:
