@@ -15,8 +15,8 @@
 // measured copy rate, so the loop keeps to packed bf16 compares and maxima and to pairs of fp32. A warp streams
 // chunks of 512 logits with the next chunk's loads in flight and its own running sums: no barriers. Rows that are
 // too few to fill the GPU are split over CTAs; the last one to finish a row joins the parts in their order.
-// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 132 us, 4.0 TB/s, 59% of the measured copy rate (107
-// us without alternatives; 71% of the issue slots); of fp32 182 us, 85%; 20 rows of fp32 with 5 alternatives 10.2 us.
+// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 125 us, 4.2 TB/s, 62% of the measured copy rate (107
+// us without alternatives; 78% of the issue slots); of fp32 179 us, 86%; 20 rows of fp32 with 5 alternatives 10.0 us.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 
@@ -49,7 +49,7 @@ struct LParams {
   float *top_lp;
   int *counters;
   float4 *parts;    // [row][kMaxSplit]: maximum, reference sum S, T, tokens before (bits)
-  uint32_t *keys;   // [row][kMaxTiles]
+  float *tops;      // [row][kMaxTiles] maxima of the tiles' numbers
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -60,6 +60,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Maximum of a warp's numbers; NaN when there is none.
+__device__ __forceinline__ float warp_top(float a) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(a));
   return r;
 }
 __device__ __forceinline__ unsigned long long rank_key(uint32_t k, int t) {
@@ -191,6 +197,31 @@ __device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums
   return m;
 }
 
+// Bits of the lane's values that are at least b, in one word, and the value that a bit stands for. For bf16, b is above a
+// bf16 number by less than one place (its low bits are those that a key loses), so its upper half compares alike.
+__device__ __forceinline__ unsigned reach(const Lane16<float> &c, float b) {
+  float x[16];
+  c.values(x);
+  unsigned hit = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) hit |= x[i] >= b ? 1u << i : 0u;
+  return hit;
+}
+__device__ __forceinline__ unsigned reach(const Lane16<__nv_bfloat16> &c, float b) {
+  const uint32_t w[8] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w, c.v[1].x, c.v[1].y, c.v[1].z, c.v[1].w};
+  const uint32_t u = __float_as_uint(b) >> 16, uu = u | (u << 16);
+  const __nv_bfloat162 b2 = *reinterpret_cast<const __nv_bfloat162 *>(&uu);
+  unsigned hit = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    hit |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), b2) & (0x00010001u << i);
+  return hit;
+}
+template <class T>
+__device__ __forceinline__ int bit_of(int i) { return sizeof(T) == 2 ? (i >> 1) + (i & 1) * 16 : i; }
+template <class T>
+__device__ __forceinline__ int value_of(int bit) { return sizeof(T) == 2 ? (bit & 15) * 2 + (bit >> 4) : bit; }
+
 // Keys of a warp in descending order (bitonic).
 template <class K>
 __device__ __forceinline__ K warp_sort_desc(K k, int lane) {
@@ -202,6 +233,16 @@ __device__ __forceinline__ K warp_sort_desc(K k, int lane) {
       const bool keep_max = ((lane & d) == 0) == ((lane & size) == 0);
       k = keep_max ? (o > k ? o : k) : (o > k ? k : o);
     }
+  return k;
+}
+// The 32 largest of two descending lists, descending: a, and b given backwards.
+__device__ __forceinline__ uint32_t warp_merge_desc(uint32_t a, uint32_t b_backwards, int lane) {
+  uint32_t k = max(a, b_backwards);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, k, d);
+    k = (lane & d) == 0 ? max(k, o) : min(k, o);
+  }
   return k;
 }
 // How many keys of the block's sorted warps (32 a warp, descending, distinct or 0) come before k, the lane-th of its own.
@@ -224,7 +265,7 @@ template <class T>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p) {
   __shared__ Sums s_sums[kLpWarps];
   __shared__ int s_before[kLpWarps], s_last;
-  __shared__ uint32_t s_key[kMaxTiles];
+  __shared__ float s_top[kMaxTiles];
   __shared__ int s_tile[kMaxTiles], s_ntile, s_ncand;
   __shared__ uint32_t s_sorted[kMaxTiles], s_bar;
   __shared__ unsigned long long s_list[kLpThreads];
@@ -242,7 +283,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   const int tok = p.tokens[row];
   const bool has = tok >= 0 && tok < p.V;
   const int tpos = off + tok;
-  uint32_t *keys = p.split > 1 ? p.keys + static_cast<size_t>(row) * kMaxTiles : s_key;
+  float *tops = p.split > 1 ? p.tops + static_cast<size_t>(row) * kMaxTiles : s_top;
 
   // ---- this warp's tiles: every (split * warps)-th
   Sums u;
@@ -298,8 +339,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
     if (nt != tile) {
       u.mx = fmaxf(u.mx, tmax);
       if (p.top_n > 0) {
-        const uint32_t k = __reduce_max_sync(0xffffffffu, order_key(tmax));
-        if (lane == 0) keys[tile] = k;
+        const float k = warp_top(tmax);
+        if (lane == 0) tops[tile] = k;
       }
       tmax = NAN;
     }
@@ -338,7 +379,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
     }
     __syncthreads();
     if (!s_last) return;
-    for (int i = tid; i < tiles; i += kLpThreads) s_key[i] = __ldcg(keys + i);
+    for (int i = tid; i < tiles; i += kLpThreads) s_top[i] = __ldcg(tops + i);
   }
   // ---- the row's sums
   if (warp == 0) {
@@ -417,13 +458,24 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   // have), so that a maximum and its tile make one distinct word to sort. Tiles that reach it are read again.
   const int n = p.top_n;
   {
-    uint32_t k = tid < tiles ? (s_key[tid] & ~255u) | (255u - tid) : 0u;
+    uint32_t k = tid < tiles ? (order_key(s_top[tid]) & ~255u) | (255u - tid) : 0u;
     k = warp_sort_desc(k, lane);
     const int own = k != 0u ? 255 - static_cast<int>(k & 255u) : tiles == kMaxTiles ? 255 : tiles;
     s_sorted[tid] = k;
-    if (tid == 0) s_bar = 0u, s_ntile = 0, s_ncand = 0;
+    if (tid == 0) s_ntile = 0, s_ncand = 0;
     __syncthreads();
-    if ((k != 0u || tiles == kMaxTiles) && tiles >= n && block_rank(s_sorted, k, warp, lane) == n - 1) s_bar = k & ~255u;
+    if (warp == 0) {  // the eight lists' 32 largest, pair by pair
+      uint32_t a[kLpWarps / 2];
+#pragma unroll
+      for (int i = 0; i < kLpWarps / 2; ++i)
+        a[i] = warp_merge_desc(s_sorted[2 * i * 32 + lane], s_sorted[(2 * i + 1) * 32 + 31 - lane], lane);
+#pragma unroll
+      for (int m = kLpWarps / 4; m >= 1; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < m; ++i)
+          a[i] = warp_merge_desc(a[i], __shfl_sync(0xffffffffu, a[i + m], 31 - lane), lane);
+      if (lane == n - 1) s_bar = tiles >= n ? a[0] & ~255u : 0u;
+    }
     __syncthreads();
     if (own < tiles && (k & ~255u) >= s_bar) s_tile[atomicAdd(&s_ntile, 1)] = own;
     __syncthreads();
@@ -434,27 +486,21 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   for (int z = warp; z < nt; z += kLpWarps) {
     const int c0 = s_tile[z] * p.tile_chunks, c1 = min(c0 + p.tile_chunks, chunks);
     for (int cc = c0; cc < c1; ++cc) {
-      float v[16];
-      if (whole(cc)) {
-        cur.load(base + cc * kChunk, lane);
-        cur.values(v);
-      }
       // above the key of -infinity the bar is a number and one compare decides; NaN counts only below it
       unsigned hit = 0u;
       if (whole(cc) && bar > 0x007fffffu) {
-        const float b = key_value(bar);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) hit |= v[i] >= b ? 1u << i : 0u;
+        cur.load(base + cc * kChunk, lane);
+        hit = reach(cur, key_value(bar));
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int pos = cc * kChunk + Lane16<T>::at(i, lane);
           const bool in = pos >= off && pos < end;
-          hit |= in && order_key(to_f(base[in ? pos : off])) >= bar ? 1u << i : 0u;
+          hit |= in && order_key(to_f(base[in ? pos : off])) >= bar ? 1u << bit_of<T>(i) : 0u;
         }
       }
       while (hit) {
-        const int i = __ffs(hit) - 1, pos = cc * kChunk + Lane16<T>::at(i, lane);
+        const int i = value_of<T>(__ffs(hit) - 1), pos = cc * kChunk + Lane16<T>::at(i, lane);
         hit &= hit - 1;
         const int at = atomicAdd(&s_ncand, 1);
         if (at < kLpThreads) s_list[at] = rank_key(order_key(to_f(base[pos])), pos - off);
@@ -547,7 +593,7 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int V, int64_t stride
   w += kCounterBytes;
   p.parts = reinterpret_cast<float4 *>(w);
   w += n * kMaxSplit * 32;
-  p.keys = reinterpret_cast<uint32_t *>(w);
+  p.tops = reinterpret_cast<float *>(w);
   const int64_t grid = static_cast<int64_t>(rows) * p.split;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   if (dtype == 0)
