@@ -125,6 +125,13 @@ struct Lane16 {
   }
 };
 
+// Logits before the given one, counted for two halves of a word: minus a half's count in either half, the lower one's
+// borrow taken from the upper (a warp has 2^24 / 4096 chunks at most, 8 a half each).
+__device__ __forceinline__ int halves(uint32_t acc) {
+  const uint32_t lo = (0u - acc) & 0xffffu, d = (acc + lo) >> 16;
+  return static_cast<int>(lo + ((lo - d) & 0xffffu));
+}
+
 // Two logits into the running pairs of S and T.
 __device__ __forceinline__ void add_pair(F2 x, F2 c, F2 m, F2 &s, F2 &t) {
   const F2 y = fma2(x, c, m);
@@ -143,7 +150,7 @@ __device__ __forceinline__ void close_pairs(Sums &u, F2 s, F2 t) {
 }
 
 // A whole chunk: maximum, sums, and how many logits are above xt (or at least xt when `ge`).
-__device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, float xt, bool ge, int &before) {
+__device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, float xt, bool ge, int &before, uint32_t &) {
   float x[16];
   c.values(x);
   float m = x[0];
@@ -165,7 +172,8 @@ __device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, flo
   close_pairs(u, s, t);
   return m;
 }
-__device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums &u, float xt, bool ge, int &before) {
+__device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums &u, float xt, bool ge, int &,
+                                            uint32_t &acc) {
   const uint32_t w[8] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w, c.v[1].x, c.v[1].y, c.v[1].z, c.v[1].w};
   __nv_bfloat162 h[8];
 #pragma unroll
@@ -176,15 +184,13 @@ __device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums
   u.lift(m);
   const float M = u.ref * kC;
   const __nv_bfloat162 t2 = __float2bfloat162_rn(xt), low = __float2bfloat162_rn(kLowest);  // xt is a bf16
-  __nv_bfloat162 cnt = __float2bfloat162_rn(0.0f);  // counts to 8: exact
   if (ge) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cnt = __hadd2(cnt, __hge2(h[i], t2));
+    for (int i = 0; i < 8; ++i) acc += __hge2_mask(h[i], t2);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cnt = __hadd2(cnt, __hgt2(h[i], t2));
+    for (int i = 0; i < 8; ++i) acc += __hgt2_mask(h[i], t2);
   }
-  before += static_cast<int>(__low2float(cnt) + __high2float(cnt));
   F2 s = f2(0.0f, 0.0f), t = s;
   const F2 cc = f2(kC, kC), mm = f2(-M, -M);
 #pragma unroll
@@ -288,6 +294,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   // ---- this warp's tiles: every (split * warps)-th
   Sums u;
   int before = 0;
+  uint32_t acc = 0u;
   const int w0 = part * kLpWarps + warp, ws = p.split * kLpWarps;
   // chunks [c_lo, c_hi) lie inside the row; the chunk of the given token is apart, and so is a row whose token is a NaN
   const int c_lo = off ? 1 : 0, c_hi = end / kChunk;
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
     if (whole(nc)) nxt.load(base + nc * kChunk, lane);
     float m;
     if (whole(c) && c != c_tok && !odd) {
-      m = chunk_pass(cur, u, xt, c < c_tok, before);
+      m = chunk_pass(cur, u, xt, c < c_tok, before, acc);
     } else {  // one by one
       const uint32_t kt = order_key(xt);
       float v[16];
@@ -348,6 +355,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
     tile = nt;
     c = nc;
   }
+  before += halves(acc);
   // ---- lanes, then warps, joined in a fixed order
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
