@@ -15,8 +15,8 @@
 // measured copy rate, so the loop keeps to packed bf16 compares and maxima and to pairs of fp32. A warp streams
 // chunks of 512 logits with the next chunk's loads in flight and its own running sums: no barriers. Rows that are
 // too few to fill the GPU are split over CTAs; the last one to finish a row joins the parts in their order.
-// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 125 us, 4.2 TB/s, 62% of the measured copy rate (107
-// us without alternatives; 78% of the issue slots); of fp32 179 us, 86%; 20 rows of fp32 with 5 alternatives 10.0 us.
+// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 119 us, 4.4 TB/s, 65% of the measured copy rate (101
+// us without alternatives; three quarters of the issue slots); of fp32 179 us, 87%; 20 rows of fp32 with 5 alternatives 10.2 us.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 
@@ -83,14 +83,6 @@ __device__ __forceinline__ float shift(float from, float to) {
 // Running sums of a lane: true maximum, reference (a logit), S and T.
 struct Sums {
   float mx = -INFINITY, ref = kNoRef, s = 0.0f, t = 0.0f;
-  __device__ __forceinline__ void lift(float m) {  // raises the reference to a new chunk's maximum where it must
-    if (m > ref + kSlack || (s == 0.0f && m > ref)) {
-      const float d = shift(ref, m), f = exp2_fast(d);
-      t = fmaf(t, f, s * f * d);  // sum 2^(y + d) (y + d)
-      s *= f;
-      ref = m;
-    }
-  }
 };
 // b joined to a: sums over the larger reference.
 __device__ __forceinline__ void join(Sums &a, const Sums &b) {
@@ -125,6 +117,33 @@ struct Lane16 {
   }
 };
 
+// A lane's running sums over its chunks: S and T as pairs.
+struct Run {
+  float mx = -INFINITY, ref = kNoRef;
+  F2 s = f2(0.0f, 0.0f), t = f2(0.0f, 0.0f);
+  __device__ __forceinline__ void lift(float m) {  // raises the reference to a new chunk's maximum where it must
+    float a, b;
+    split(s, a, b);
+    if (m > ref + kSlack || (a == 0.0f && m > ref)) {
+      const float d = shift(ref, m), f = exp2_fast(d);
+      const F2 ff = f2(f, f);
+      t = fma2(t, ff, mul2(s, f2(f * d, f * d)));  // sum 2^(y + d) (y + d)
+      s = mul2(s, ff);
+      ref = m;
+    }
+  }
+  __device__ __forceinline__ Sums sums() const {
+    Sums u;
+    float a, b;
+    u.mx = mx;
+    u.ref = ref;
+    split(s, a, b);
+    u.s = a + b;
+    split(t, a, b);
+    u.t = a + b;
+    return u;
+  }
+};
 // Logits before the given one, counted for two halves of a word: minus a half's count in either half, the lower one's
 // borrow taken from the upper (a warp has 2^24 / 4096 chunks at most, 8 a half each).
 __device__ __forceinline__ int halves(uint32_t acc) {
@@ -141,16 +160,8 @@ __device__ __forceinline__ void add_pair(F2 x, F2 c, F2 m, F2 &s, F2 &t) {
   s = add2(s, e);
   t = fma2(e, y, t);
 }
-__device__ __forceinline__ void close_pairs(Sums &u, F2 s, F2 t) {
-  float a, b;
-  split(s, a, b);
-  u.s += a + b;
-  split(t, a, b);
-  u.t += a + b;
-}
-
 // A whole chunk: maximum, sums, and how many logits are above xt (or at least xt when `ge`).
-__device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, float xt, bool ge, int &before, uint32_t &) {
+__device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Run &u, float xt, bool ge, int &before, uint32_t &) {
   float x[16];
   c.values(x);
   float m = x[0];
@@ -165,14 +176,12 @@ __device__ __forceinline__ float chunk_pass(const Lane16<float> &c, Sums &u, flo
 #pragma unroll
     for (int i = 0; i < 16; ++i) before += x[i] > xt ? 1 : 0;
   }
-  F2 s = f2(0.0f, 0.0f), t = s;
   const F2 cc = f2(kC, kC), mm = f2(-M, -M);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) add_pair(f2(max_nan(x[i], kLowest), max_nan(x[i + 1], kLowest)), cc, mm, s, t);
-  close_pairs(u, s, t);
+  for (int i = 0; i < 16; i += 2) add_pair(f2(max_nan(x[i], kLowest), max_nan(x[i + 1], kLowest)), cc, mm, u.s, u.t);
   return m;
 }
-__device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums &u, float xt, bool ge, int &,
+__device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Run &u, float xt, bool ge, int &,
                                             uint32_t &acc) {
   const uint32_t w[8] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w, c.v[1].x, c.v[1].y, c.v[1].z, c.v[1].w};
   __nv_bfloat162 h[8];
@@ -191,15 +200,13 @@ __device__ __forceinline__ float chunk_pass(const Lane16<__nv_bfloat16> &c, Sums
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc += __hgt2_mask(h[i], t2);
   }
-  F2 s = f2(0.0f, 0.0f), t = s;
   const F2 cc = f2(kC, kC), mm = f2(-M, -M);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const __nv_bfloat162 l = __hmax2_nan(h[i], low);
     const uint32_t b = *reinterpret_cast<const uint32_t *>(&l);
-    add_pair(f2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), cc, mm, s, t);
+    add_pair(f2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), cc, mm, u.s, u.t);
   }
-  close_pairs(u, s, t);
   return m;
 }
 
@@ -267,6 +274,47 @@ __device__ __forceinline__ int block_rank(const K *lists, K k, int warp, int lan
   return r;
 }
 
+// A chunk one by one: the given token's, a row's ends, rows whose token is a NaN. Sums s, t of the lane go on from u's.
+// A call of its own: in the loop it takes registers from the chunks that count (2048 rows 124 us against 119).
+struct Single {
+  float m, ref, s, t;
+  int before;
+};
+template <class T>
+__device__ __noinline__ Single single_chunk(const T *base, int c, int lane, int off, int end, int tpos, float xt, Sums u) {
+  const uint32_t kt = order_key(xt);
+  float v[16];
+  bool in[16];
+  Single z{NAN, u.ref, u.s, u.t, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int pos = c * kChunk + Lane16<T>::at(i, lane);
+    in[i] = pos >= off && pos < end;
+    v[i] = in[i] ? to_f(base[pos]) : NAN;
+    z.m = fmaxf(z.m, v[i]);
+    if (in[i] && tpos >= 0) {
+      const uint32_t k = order_key(v[i]);
+      z.before += k > kt || (k == kt && pos < tpos) ? 1 : 0;
+    }
+  }
+  if (z.m > z.ref + kSlack || (z.s == 0.0f && z.m > z.ref)) {
+    const float d = shift(z.ref, z.m), f = exp2_fast(d);
+    z.t = fmaf(z.t, f, z.s * f * d);
+    z.s *= f;
+    z.ref = z.m;
+  }
+  const float M = z.ref * kC;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (!in[i]) continue;
+    const float y = fmaf(max_nan(v[i], kLowest), kC, -M);
+    const float e = exp2_fast(y);
+    z.s += e;
+    z.t = fmaf(e, y, z.t);
+  }
+  return z;
+}
+
 template <class T>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p) {
   __shared__ Sums s_sums[kLpWarps];
@@ -292,7 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
   float *tops = p.split > 1 ? p.tops + static_cast<size_t>(row) * kMaxTiles : s_top;
 
   // ---- this warp's tiles: every (split * warps)-th
-  Sums u;
+  Run run;
   int before = 0;
   uint32_t acc = 0u;
   const int w0 = part * kLpWarps + warp, ws = p.split * kLpWarps;
@@ -314,37 +362,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
     if (whole(nc)) nxt.load(base + nc * kChunk, lane);
     float m;
     if (whole(c) && c != c_tok && !odd) {
-      m = chunk_pass(cur, u, xt, c < c_tok, before, acc);
-    } else {  // one by one
-      const uint32_t kt = order_key(xt);
-      float v[16];
-      bool in[16];
-      m = NAN;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int pos = c * kChunk + Lane16<T>::at(i, lane);
-        in[i] = pos >= off && pos < end;
-        v[i] = in[i] ? to_f(base[pos]) : NAN;
-        m = fmaxf(m, v[i]);
-        if (in[i] && has) {
-          const uint32_t k = order_key(v[i]);
-          before += k > kt || (k == kt && pos < tpos) ? 1 : 0;
-        }
-      }
-      u.lift(m);
-      const float M = u.ref * kC;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (!in[i]) continue;
-        const float y = fmaf(max_nan(v[i], kLowest), kC, -M);
-        const float e = exp2_fast(y);
-        u.s += e;
-        u.t = fmaf(e, y, u.t);
-      }
+      m = chunk_pass(cur, run, xt, c < c_tok, before, acc);
+    } else {
+      const Single z = single_chunk(base, c, lane, off, end, has ? tpos : -1, xt, run.sums());
+      m = z.m;
+      before += z.before;
+      run.ref = z.ref;
+      run.s = f2(z.s, 0.0f);
+      run.t = f2(z.t, 0.0f);
     }
     tmax = fmaxf(tmax, m);
     if (nt != tile) {
-      u.mx = fmaxf(u.mx, tmax);
+      run.mx = fmaxf(run.mx, tmax);
       if (p.top_n > 0) {
         const float k = warp_top(tmax);
         if (lane == 0) tops[tile] = k;
@@ -355,6 +384,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LParams p
     tile = nt;
     c = nc;
   }
+  Sums u = run.sums();
   before += halves(acc);
   // ---- lanes, then warps, joined in a fixed order
 #pragma unroll
