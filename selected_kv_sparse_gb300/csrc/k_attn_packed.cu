@@ -191,6 +191,11 @@ __device__ __forceinline__ float column_sum(float v) {
   return v;
 }
 
+// Whether a word of parameters, or either of a word's two bf16 values, is an infinity or a NaN.
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
 // Units are what has a page list of its own: a request (every head walks the same list), or a row of a per-head view.
 template <bool kView>
 struct Units {
@@ -511,10 +516,36 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     float inv_e = 1.0f;       // 1 / reference of the value scales, a power of two
     float sv_limit = -1.0f;   // largest scale that it admits; the first packed page sets both
 
+    // A token that some columns see and others do not takes part in the products of all of them, with probability 0 where it
+    // is hidden: its values have to be finite there. Those that are not are taken out of the operands and added here, to the
+    // columns that see them. value(token, block, dim of the block) is asked for these tokens only; rare.
+    auto add_not_finite = [&](int pos0, auto value) {
+#pragma unroll 1
+      for (int tok = 0; tok < kPage; ++tok) {
+        const int pos = pos0 + tok;
+        if (pos <= s.last0 || pos > s.last0 + s.nq - 1) continue;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float v = value(tok, b, g * 8 + 2 * m + i);
+              if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+              for (int j = 0; j < NTL; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  if (pos <= s.last0 + ((cg * NTL + j) * 8 + 2 * t + c) / G) acc[j][b][m][2 * i + c] += v;
+            }
+      }
+    };
+
     // Moves the references up where a page's logits (page[n][j][4]) or value scales exceed them by too much, and turns
     // the logits into probabilities over the references (pairs of columns of this lane's two tokens).
     const int last_all = s.last0 + s.nq - 1;
-    auto probabilities = [&](auto np, float (*sc)[NTL][4], float svmax, F2 (*pA)[NTL], F2 (*pB)[NTL]) {
+    // scales() is the lane's largest finite value scale, asked for where svmax is infinite.
+    auto probabilities = [&](auto np, float (*sc)[NTL][4], float svmax, auto scales, F2 (*pA)[NTL], F2 (*pB)[NTL]) {
       constexpr int NP = decltype(np)::value;
       auto distances = [&]() {
 #pragma unroll
@@ -540,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         }
       if (__any_sync(0xffffffffu, over > kMaxSlack || svmax > sv_limit)) {
         float ratio = 1.0f;
-        const float mx = column_max(svmax);  // the lanes of a column hold all tokens
+        const float mx = column_max(svmax < INFINITY ? svmax : scales());  // the lanes of a column hold all tokens
         if (mx > sv_limit) {
           const float ie = 1.0f / fmaxf(__uint_as_float(__float_as_uint(mx) & 0x7f800000u), 0x1p-100f);
           ratio = ie / inv_e;
@@ -662,6 +693,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
           }
         }
       }
+      bool odd = false;  // tokens that some columns do not see have parameters that are not finite
       if (NP == 1 && edge) {
         hide(sc[0], pos0, first);
         // a token that no column sees: its parameters may hold anything
@@ -671,6 +703,16 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
           if (hA) vpA[0][b] = 0u;
           if (hB) vpB[0][b] = 0u;
         }
+        if (!kView) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const bool oA = pos0 + tokA > s.last0 && not_finite(vpA[0][b]), oB = pos0 + tokB > s.last0 && not_finite(vpB[0][b]);
+            if (oA) vpA[0][b] = 0u;
+            if (oB) vpB[0][b] = 0u;
+            odd |= oA || oB;
+          }
+          odd = __any_sync(0xffffffffu, odd) != 0;
+        }
       }
       float svmax = 0.0f;
 #pragma unroll
@@ -678,7 +720,24 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 #pragma unroll
         for (int b = 0; b < NB; ++b) svmax = fmaxf(svmax, fmaxf(param_scale(vpA[n][b]), param_scale(vpB[n][b])));
       F2 pA[NP][NTL], pB[NP][NTL];
-      probabilities(np, sc, svmax, pA, pB);
+      auto scales = [&]() {
+        float m = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const float a = param_scale(vpA[n][b]), c = param_scale(vpB[n][b]);
+            m = fmaxf(m, fmaxf(a < INFINITY ? a : 0.0f, c < INFINITY ? c : 0.0f));
+          }
+        return m;
+      };
+      probabilities(np, sc, svmax, scales, pA, pB);
+      if (!kView && odd)
+        add_not_finite(pos0, [&](int tok, int b, int x) {
+          const uint32_t par = *reinterpret_cast<const uint32_t *>(chs[0] + L::OFF_VPAR + (b * kPage + tok) * 4);
+          const int two = chs[0][L::OFF_V + b * L::kBlock + tok * 32 + x / 2];
+          return fmaf(param_scale(par), static_cast<float>(x & 1 ? two >> 4 : two & 15), param_low(par));
+        });
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -738,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         for (int c = 0; c < 4; ++c) sc[0][j][c] *= qk;
       if (edge) hide(sc[0], pos0, first);
       F2 pA[1][NTL], pB[1][NTL];
-      probabilities(std::integral_constant<int, 1>{}, sc, -INFINITY, pA, pB);
+      probabilities(std::integral_constant<int, 1>{}, sc, -INFINITY, []() { return 0.0f; }, pA, pB);
       // p as two bf16 terms, in the accumulators' unit (2^-24 of the value over the scale reference)
       const __nv_bfloat16 *vp = p.v + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
       const float unit16 = 0x1p-24f * inv_e;
@@ -754,11 +813,12 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
           pl[j][z] = transpose8x8(pack_bf16(u0 - __uint_as_float(hi << 16), u1 - __uint_as_float(hi & 0xffff0000u)));
           ph[j][z] = transpose8x8(hi);
         }
-      bool see[4];  // rows that no column sees may hold anything
+      bool see[4], part[4], odd = false;  // rows that no column sees, or not every one, may hold anything
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
         const int pos = pos0 + t + 4 * z;
         see[z] = pos <= last_all && pos >= first;
+        part[z] = !kView && pos > s.last0;
       }
       const __nv_bfloat162 sixteen = __floats2bfloat162_rn(16.0f, 16.0f);
 #pragma unroll
@@ -767,6 +827,19 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 #pragma unroll
         for (int z = 0; z < 4; ++z)
           w[z] = see[z] ? *reinterpret_cast<const uint4 *>(vp + (t + 4 * z) * D + b * 64 + g * 8) : make_uint4(0, 0, 0, 0);
+        if (!kView && edge) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (part[z] && (not_finite(w[z].x) || not_finite(w[z].y) || not_finite(w[z].z) || not_finite(w[z].w))) {
+              odd = true;
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                uint32_t &u = (&w[z].x)[m];
+                if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+                if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
+              }
+            }
+        }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint32_t u[4] = {(&w[0].x)[m], (&w[1].x)[m], (&w[2].x)[m], (&w[3].x)[m]};
@@ -783,6 +856,8 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
           }
         }
       }
+      if (!kView && edge && __any_sync(0xffffffffu, odd))
+        add_not_finite(pos0, [&](int tok, int b, int x) { return __bfloat162float(vp[tok * D + b * 64 + x]); });
     };
 
     // Waits for the next page of the ring; false (for every lane) when the wait ran out.
