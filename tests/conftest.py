@@ -12,6 +12,16 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
 
 
+@pytest.fixture(autouse=True)
+def _decoded_pages_of_one_test():
+    """The Server of test_gpu_packed_flow keeps decoded pages under its id, in a default argument. An id comes back once its
+    owner is gone, so nothing of it is carried from one test to the next."""
+    yield
+    for name, module in list(sys.modules.items()):
+        if name.endswith("test_gpu_packed_flow"):
+            module.Server.values.__defaults__[0].clear()
+
+
 @pytest.fixture(scope="session")
 def orc():
     import oracle
