@@ -370,7 +370,10 @@ kap_status kap_unpack_pages(const kap_packed_pool *pool, const int32_t *src_page
  * rules and outputs, over pages of both kinds. Keys and values are those that the codes stand for (lowest + scale *
  * code, not rounded); sums and softmax statistics are fp32, probabilities enter the product with the values as fp16
  * (packed pages) or as two bf16 terms (16-bit pages). Probability times value scale keeps its 11 bits down to
- * 2^-15 of the largest scale met in a row's part, and below that an error of 2^-25 of it.
+ * 2^-15 of the largest scale met in a row's part (beside scales below 2^-20, 2^-40 of the largest 16-bit value counts as
+ * one), and below that an error of 2^-25 of it. Sums are divided by the probabilities' sum at the end: 2^8 times a value
+ * for each token has to fit fp32, so values of up to 2^96 in magnitude do at any length. The same goes for a logit's
+ * sums, of lowest * sum q and of scale * sum q * code.
  * Every group size G in 1..8 is supported. kap_view.settled is not read. A hidden or skipped token adds nothing,
  * whatever its codes, parameters or 16-bit values hold. A query row that sees no token gets zeros and lse -infinity
  * (and, for the proposal, device error bit 4).

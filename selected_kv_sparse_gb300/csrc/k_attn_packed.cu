@@ -573,7 +573,21 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         float ratio = 1.0f;
         const float mx = column_max(svmax < INFINITY ? svmax : scales());  // the lanes of a column hold all tokens
         if (mx > sv_limit) {
-          const float ie = 1.0f / fmaxf(__uint_as_float(__float_as_uint(mx) & 0x7f800000u), 0x1p-100f);
+          float least = 0x1p-100f;
+          if (sv_limit < 0.0f) {  // the first scale: what 16-bit pages have summed up over 1 has to stay in fp32 over it
+            float a = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NTL; ++j)
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) a = fmaxf(a, fabsf(acc[j][b][z][c]));
+            const uint32_t e = __reduce_max_sync(0xffffffffu, a < INFINITY ? __float_as_uint(a) & 0x7f800000u : 0u);
+            least = fmaxf(least, __uint_as_float(e) * 0x1p-100f);
+          }
+          const float ie = 1.0f / fmaxf(__uint_as_float(__float_as_uint(mx) & 0x7f800000u), least);
           ratio = ie / inv_e;
           inv_e = ie;
           sv_limit = kScaleSlack / ie;
@@ -796,11 +810,24 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 #pragma unroll
         for (int c = 0; c < 4; ++c) sc[0][j][c] *= qk;
       if (edge) hide(sc[0], pos0, first);
-      F2 pA[1][NTL], pB[1][NTL];
-      probabilities(std::integral_constant<int, 1>{}, sc, -INFINITY, []() { return 0.0f; }, pA, pB);
-      // p as two bf16 terms, in the accumulators' unit (2^-24 of the value over the scale reference)
       const __nv_bfloat16 *vp = p.v + (static_cast<size_t>(id) * p.hkv + s.h) * (kPage * D);
-      const float unit16 = 0x1p-24f * inv_e;
+      // Sums of values over a very small reference (of packed pages that hold next to nothing) might leave fp32: 2^-40 of
+      // the page's largest value then counts as a value scale. A packed token loses 2^-65 of that value at most.
+      float svmax = -INFINITY;
+      if (sv_limit >= 0.0f && inv_e > 0x1p20f) {
+        uint32_t m = 0u;
+#pragma unroll 1
+        for (int i = lane; i < kPage * D; i += 32) {
+          const uint32_t a = reinterpret_cast<const unsigned short *>(vp)[i] & 0x7fffu;
+          if (a < 0x7f80u && pos0 + i / D <= last_all && pos0 + i / D >= first) m = max(m, a);
+        }
+        svmax = __uint_as_float(__reduce_max_sync(0xffffffffu, m) << 16) * 0x1p-40f;
+      }
+      F2 pA[1][NTL], pB[1][NTL];
+      probabilities(std::integral_constant<int, 1>{}, sc, svmax, []() { return 0.0f; }, pA, pB);
+      // p as two bf16 terms, in the accumulators' unit (2^-24 of the value over the scale reference): a reference below 1
+      // goes into p, one above 1 into the values, so that neither leaves the normal numbers
+      const float unit16 = 0x1p-24f * fmaxf(inv_e, 1.0f), vunit = fminf(inv_e, 1.0f);
       uint32_t ph[NTL][2], pl[NTL][2];
 #pragma unroll
       for (int j = 0; j < NTL; ++j)
@@ -820,7 +847,12 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
         see[z] = pos <= last_all && pos >= first;
         part[z] = !kView && pos > s.last0;
       }
-      const __nv_bfloat162 sixteen = __floats2bfloat162_rn(16.0f, 16.0f);
+      const __nv_bfloat162 even = __floats2bfloat162_rn(vunit, vunit),
+                           high = __floats2bfloat162_rn(16.0f * vunit, 16.0f * vunit);
+      auto times = [](uint32_t w, __nv_bfloat162 f) {  // by a power of two: exact
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w), f);
+        return *reinterpret_cast<const uint32_t *>(&r);
+      };
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint4 w[4];
@@ -843,12 +875,8 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint32_t u[4] = {(&w[0].x)[m], (&w[1].x)[m], (&w[2].x)[m], (&w[3].x)[m]};
-          const uint32_t a0 = __byte_perm(u[0], u[1], 0x5410), a2 = __byte_perm(u[2], u[3], 0x5410);
-          uint32_t a1 = __byte_perm(u[0], u[1], 0x7632), a3 = __byte_perm(u[2], u[3], 0x7632);
-          const __nv_bfloat162 s1 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a1), sixteen);
-          const __nv_bfloat162 s3 = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a3), sixteen);
-          a1 = *reinterpret_cast<const uint32_t *>(&s1);
-          a3 = *reinterpret_cast<const uint32_t *>(&s3);
+          const uint32_t a0 = times(__byte_perm(u[0], u[1], 0x5410), even), a2 = times(__byte_perm(u[2], u[3], 0x5410), even);
+          const uint32_t a1 = times(__byte_perm(u[0], u[1], 0x7632), high), a3 = times(__byte_perm(u[2], u[3], 0x7632), high);
 #pragma unroll
           for (int j = 0; j < NTL; ++j) {
             mma_bf16(acc[j][b][m], a0, a1, a2, a3, ph[j][0], ph[j][1]);
@@ -920,7 +948,9 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
     }
 
     // ---- values in their own unit, columns summed over their lanes
-    const float unit_e = 0x1p24f / inv_e;
+    // 2^24 and the scale reference: in two factors, as their product may leave fp32 (and an accumulator times 2^24 where the
+    // reference is small)
+    const float unit_e = 0x1p24f / fmaxf(inv_e, 1.0f), unit_v = 1.0f / fminf(inv_e, 1.0f);
     float lr[NTL][2];
 #pragma unroll
     for (int j = 0; j < NTL; ++j) {
@@ -936,8 +966,8 @@ __global__ void __launch_bounds__(Cfg<D, NTL, CS>::kThreads, Cfg<D, NTL, CS>::kC
           l[c] = column_sum(l[c]);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            acc[j][b][m][c] = fmaf(acc[j][b][m][c], unit_e, l[c]);
-            acc[j][b][m][2 + c] = fmaf(acc[j][b][m][2 + c], unit_e * 0.0625f, l[c]);
+            acc[j][b][m][c] = fmaf(acc[j][b][m][c] * unit_e, unit_v, l[c]);
+            acc[j][b][m][2 + c] = fmaf(acc[j][b][m][2 + c] * (unit_e * 0.0625f), unit_v, l[c]);
           }
         }
       }
