@@ -42,7 +42,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;      // reference of a column that has seen nothing
+constexpr float kNoMax = -3.402823466e38f;  // reference of a column that has seen nothing: below every logit that fp32 holds
 constexpr float kMaxSlack = 8.0f;     // log2 units a logit may exceed its reference by
 constexpr float kScaleSlack = 64.0f;  // factor a value scale may exceed its reference by
 
