@@ -64,7 +64,7 @@ typedef struct {
 
 /* A pool with packed pages beside its 16-bit ones. Physical page ids below pool.num_pages name 16-bit pages (bf16),
  * ids num_pages + j name packed page j, so one block table or view mixes both and every call that only moves ids
- * (views, slot mappings, tables) takes it as it is. A packed page holds K and V in 4 bits: for nb = head_dim / 64
+ * (views, slot mappings, kap_extend_tables) takes it as it is; pages are given back by kind (kap_release_tables_packed). A packed page holds K and V in 4 bits: for nb = head_dim / 64
  * blocks of 64 dims, the chunk of one (page, KV head) is
  *   K codes [nb][16 tokens][32 bytes], V codes alike, K params [nb][16][2] bf16, V params alike,
  * kap_packed_chunk_bytes(head_dim) = 1152 * nb bytes. Byte b of a token's block holds dim 2b in its low and dim 2b + 1
@@ -428,11 +428,16 @@ size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab);
  * kap_release_tables: the pages of every request with released[r] != 0 (the first ceil(seq_len / 16) entries of its row)
  * are pushed on the stack in request and then page order; seq_len_out[r] = 0 for these and seq_len[r] for the others;
  * free_count_out = free_count plus the pages pushed. Pages past free_capacity are dropped (device error bit 2). The
- * rows themselves are left as they are.
- * Output arrays must not alias the inputs (seq_len_out, free_count_out). A negative length or count counts as 0 and a
+ * rows themselves are left as they are. The ids are pushed as they stand, so this call is for tables whose pages are
+ * all of one kind: new tokens are written to 16-bit pages, and a packed id on the stack would be granted for them.
+ * kap_release_tables_packed: the same over a pool with packed pages. Ids below num_pages are pushed on free_pages, the
+ * num_packed ids after them on free_packed (physical ids, as kap_pack_pages takes its destinations), each stack in
+ * request and then page order, with a count and a capacity of its own; any other id is dropped (device error bit 1).
+ * Output arrays must not alias the inputs (seq_len_out, free_count_out, packed_count_out), nor the stacks and counts of
+ * the two kinds one another. A negative length or count counts as 0 and a
  * free_count past free_capacity as free_capacity (device error bits 4 and 2). All arrays are int32 on the device,
- * slot_out is int64. Errors: KAP_EINVAL for null pointers, num_seqs or max_pages < 1, negative capacities or aliased
- * outputs. */
+ * slot_out is int64. Errors: KAP_EINVAL for null pointers, num_seqs or max_pages < 1, negative capacities or page counts,
+ * or aliased outputs. */
 kap_status kap_extend_tables(int32_t num_seqs, int32_t max_pages, int32_t *block_table, const int32_t *seq_len,
                              const int32_t *new_tokens, const int32_t *free_pages, int32_t free_capacity,
                              const int32_t *free_count, int32_t *free_count_out, int32_t *tok_offsets,
@@ -442,6 +447,12 @@ kap_status kap_release_tables(int32_t num_seqs, int32_t max_pages, const int32_t
                               const int32_t *seq_len, const int32_t *released, int32_t *free_pages,
                               int32_t free_capacity, const int32_t *free_count, int32_t *free_count_out,
                               int32_t *seq_len_out, kap_stream stream);
+kap_status kap_release_tables_packed(int32_t num_seqs, int32_t max_pages, const int32_t *block_table,
+                                     const int32_t *seq_len, const int32_t *released, int32_t num_pages,
+                                     int32_t *free_pages, int32_t free_capacity, const int32_t *free_count,
+                                     int32_t *free_count_out, int32_t num_packed, int32_t *free_packed,
+                                     int32_t packed_capacity, const int32_t *packed_count, int32_t *packed_count_out,
+                                     int32_t *seq_len_out, kap_stream stream);
 
 /* Check of the bounded waits. Every wait of a kernel on an mbarrier (a copy landing, a slot freed, an MMA done)
  * gives up after at most about a second, sets bit 8 of the device error word and lets the kernel return, so that a

@@ -104,6 +104,7 @@ def _declare(lib):
         "kap_token_logprobs": ([P, I, I, ctypes.c_int64, I, P, I, P, P, P, P, P, P, Z, P], I),
         "kap_extend_tables": ([I, I, P, P, P, P, I, P, P, P, P, P, I, P, P, P], I),
         "kap_release_tables": ([I, I, P, P, P, P, I, P, P, P, P], I),
+        "kap_release_tables_packed": ([I, I, P, P, P, I, P, I, P, P, I, P, I, P, P, P, P], I),
         "kap_selftest_wait_timeout": ([ctypes.c_uint32, ctypes.c_uint32, P, P], I),
     }
     for name, (args, res) in sig.items():
@@ -737,13 +738,35 @@ def kap_extend_tables(block_table: torch.Tensor, seq_len: torch.Tensor, new_toke
 
 def kap_release_tables(block_table: torch.Tensor, seq_len: torch.Tensor, released: torch.Tensor,
                        free_pages: torch.Tensor, free_count: torch.Tensor, free_count_out: torch.Tensor,
-                       seq_len_out: torch.Tensor, stream=None):
-    """Pushes the pages of the requests with released[r] != 0 on the stack free_pages and sets their length to 0."""
-    f = load().kap_release_tables
+                       seq_len_out: torch.Tensor, stream=None, pool: Optional[PackedPool] = None,
+                       free_packed: Optional[torch.Tensor] = None, packed_count: Optional[torch.Tensor] = None,
+                       packed_count_out: Optional[torch.Tensor] = None):
+    """Pushes the pages of the requests with released[r] != 0 on the stack free_pages and sets their length to 0.
+
+    Tables that name packed pages need `pool` and a second stack (kap_release_tables_packed): 16-bit ids go to free_pages,
+    from which kap_extend_tables grants pages for new tokens, packed ids to free_packed, where kap_pack_pages finds its
+    destinations. Without them every id is taken for a 16-bit page."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [R][max_pages]")
     dev = _here(block_table)
     R, mp = block_table.shape
+    both = (pool, free_packed, packed_count, packed_count_out)
+    if any(x is not None for x in both):
+        if any(x is None for x in both):
+            raise ValueError("pool, free_packed, packed_count and packed_count_out go together")
+        c = pool._c(dev)
+        st = load().kap_release_tables_packed(
+            R, mp, _at(block_table, dev, torch.int32, "block_table"), _vector(seq_len, R, dev, "seq_len"),
+            _vector(released, R, dev, "released"), c.pool.num_pages, _vector(free_pages, None, dev, "free_pages"),
+            free_pages.shape[0], _vector(free_count, 1, dev, "free_count"),
+            _vector(free_count_out, 1, dev, "free_count_out"), c.num_packed,
+            _vector(free_packed, None, dev, "free_packed"), free_packed.shape[0],
+            _vector(packed_count, 1, dev, "packed_count"), _vector(packed_count_out, 1, dev, "packed_count_out"),
+            _vector(seq_len_out, R, dev, "seq_len_out"), _raw_stream(stream, dev))
+        if st:
+            _check("kap_release_tables_packed", st)
+        return
+    f = load().kap_release_tables
     st = f(R, mp, _at(block_table, dev, torch.int32, "block_table"), _vector(seq_len, R, dev, "seq_len"),
            _vector(released, R, dev, "released"), _vector(free_pages, None, dev, "free_pages"), free_pages.shape[0],
            _vector(free_count, 1, dev, "free_count"), _vector(free_count_out, 1, dev, "free_count_out"),

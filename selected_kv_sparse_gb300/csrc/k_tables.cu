@@ -224,6 +224,78 @@ __global__ void __launch_bounds__(kTabThreads) release_kernel(
   }
 }
 
+// The same over a pool with packed pages: ids below P16 go to the stack s16, the P4 ids after them to s4. Where an id goes
+// depends on the kinds of all before it, so one CTA walks the released entries in order, kTile a turn, and scans both
+// kinds at once (a count in either half of a word), and none waits for another. On a GB300 2049 pages take 5.8 us, 16392
+// (eight requests) 22 us, 262144 310 us; the release of one kind 4.4, 17 and 24 us.
+__global__ void __launch_bounds__(kTabThreads) release_by_kind_kernel(
+    int R, int max_pages, const int32_t *__restrict__ bt, const int32_t *__restrict__ seq_len,
+    const int32_t *__restrict__ released, int P16, int P4, StackArgs s16, StackArgs s4, int32_t *__restrict__ seq_len_out,
+    int *err) {
+  __shared__ int64_t s_page[kTile];
+  __shared__ int64_t s_scr[kTabThreads / 32], s_total;
+  grid_dependency_sync();
+  int64_t n16 = clamp_count(s16.count[0], s16.cap, err), n4 = clamp_count(s4.count[0], s4.cap, err);
+  for (int base = 0; base < R; base += kTile) {
+    const int r0 = base + threadIdx.x * kPer;
+    int64_t pages[kPer], ep[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const bool in = r0 + k < R;
+      const int len = in ? seq_len[r0 + k] : 0, gone = in ? released[r0 + k] : 0;
+      int64_t n = (static_cast<int64_t>(max(len, 0)) + kPage - 1) / kPage;
+      if (len < 0 || (gone && n > max_pages)) {
+        set_error(err, kErrLength);
+        n = min(n, static_cast<int64_t>(max_pages));
+      }
+      pages[k] = gone ? n : 0;
+      if (in) seq_len_out[r0 + k] = gone ? 0 : max(len, 0);
+    }
+    int64_t psum;
+    tile_scan(pages, ep, psum, s_scr, &s_total);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) s_page[threadIdx.x * kPer + k] = ep[k];
+    __syncthreads();
+    const int n = min(kTile, R - base);
+    for (int64_t at = 0; at < psum; at += kTile) {
+      const int64_t x0 = at + threadIdx.x * kPer;
+      int i = x0 < psum ? find_last(s_page, n, x0) : 0;
+      int id[kPer];
+      int64_t v[kPer], ex[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int64_t x = x0 + k;
+        id[k] = -1;
+        v[k] = 0;
+        if (x < psum) {
+          while (i + 1 < n && s_page[i + 1] <= x) ++i;
+          id[k] = bt[static_cast<size_t>(base + i) * max_pages + (x - s_page[i])];
+          if (id[k] < 0 || id[k] >= P16 + P4) set_error(err, kErrPage);
+          else v[k] = id[k] < P16 ? 1 : int64_t(1) << 32;
+        }
+      }
+      int64_t sum;
+      tile_scan(v, ex, sum, s_scr, &s_total);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (v[k] == 0) continue;
+        const StackArgs &s = v[k] == 1 ? s16 : s4;
+        const int64_t to = v[k] == 1 ? n16 + (ex[k] & 0xffffffff) : n4 + (ex[k] >> 32);
+        if (to < s.cap) s.ids[to] = id[k];
+      }
+      n16 += sum & 0xffffffff;
+      n4 += sum >> 32;
+      __syncthreads();  // the scan's memory is used again
+    }
+    __syncthreads();  // and the tile's sums
+  }
+  if (threadIdx.x == 0) {
+    if (n16 > s16.cap || n4 > s4.cap) set_error(err, kErrCapacity);
+    s16.count_out[0] = static_cast<int32_t>(min(n16, static_cast<int64_t>(s16.cap)));
+    s4.count_out[0] = static_cast<int32_t>(min(n4, static_cast<int64_t>(s4.cap)));
+  }
+}
+
 // CTAs: enough for one stripe a thread each, at most one per SM.
 int table_grid(int64_t items) {
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, (items + kTabThreads - 1) / kTabThreads),
@@ -249,6 +321,13 @@ cudaError_t launch_release_tables(int R, int max_pages, const int32_t *bt, const
   return launch_pdl(release_kernel, dim3(table_grid(static_cast<int64_t>(R) * 8)), dim3(kTabThreads), 0, s, R,
                     max_pages, bt, seq_len, released, free_pages, free_cap, free_count, free_count_out, seq_len_out,
                     err);
+}
+
+cudaError_t launch_release_by_kind(int R, int max_pages, const int32_t *bt, const int32_t *seq_len,
+                                   const int32_t *released, int P16, int P4, const StackArgs &s16, const StackArgs &s4,
+                                   int32_t *seq_len_out, int *err, cudaStream_t s) {
+  return launch_pdl(release_by_kind_kernel, dim3(1), dim3(kTabThreads), 0, s, R, max_pages, bt, seq_len, released, P16, P4,
+                    s16, s4, seq_len_out, err);
 }
 
 }  // namespace kap

@@ -529,6 +529,28 @@ kap_status kap_release_tables(int32_t num_seqs, int32_t max_pages, const int32_t
                                            cs(stream)));
 }
 
+kap_status kap_release_tables_packed(int32_t num_seqs, int32_t max_pages, const int32_t *block_table,
+                                     const int32_t *seq_len, const int32_t *released, int32_t num_pages,
+                                     int32_t *free_pages, int32_t free_capacity, const int32_t *free_count,
+                                     int32_t *free_count_out, int32_t num_packed, int32_t *free_packed,
+                                     int32_t packed_capacity, const int32_t *packed_count, int32_t *packed_count_out,
+                                     int32_t *seq_len_out, kap_stream stream) {
+  if (num_seqs <= 0 || max_pages <= 0 || free_capacity < 0 || packed_capacity < 0 || num_pages < 0 || num_packed < 0)
+    return KAP_EINVAL;
+  if (max_pages > (1 << 26) || static_cast<int64_t>(num_pages) + num_packed > 0x7fffffff) return KAP_EUNSUPPORTED;
+  if (!block_table || !seq_len || !released || !free_count || !free_count_out || !packed_count || !packed_count_out ||
+      !seq_len_out || (free_capacity > 0 && !free_pages) || (packed_capacity > 0 && !free_packed))
+    return KAP_EINVAL;
+  if (seq_len_out == seq_len || free_count_out == free_count || packed_count_out == packed_count ||
+      free_count_out == packed_count_out || free_count_out == packed_count || packed_count_out == free_count ||
+      (free_pages && free_pages == free_packed))
+    return KAP_EINVAL;
+  const StackArgs s16{free_pages, free_capacity, free_count, free_count_out},
+      s4{free_packed, packed_capacity, packed_count, packed_count_out};
+  return cuda_status(launch_release_by_kind(num_seqs, max_pages, block_table, seq_len, released, num_pages, num_packed,
+                                            s16, s4, seq_len_out, error_word(), cs(stream)));
+}
+
 const char *kap_status_str(kap_status s) {
   switch (s) {
     case KAP_OK: return "ok";

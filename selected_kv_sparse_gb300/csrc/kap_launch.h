@@ -120,6 +120,17 @@ cudaError_t launch_release_tables(int R, int max_pages, const int32_t *bt, const
                                   const int32_t *released, int32_t *free_pages, int free_cap,
                                   const int32_t *free_count, int32_t *free_count_out, int32_t *seq_len_out, int *err,
                                   cudaStream_t s);
+// A stack of free pages: ids[0 .. *count - 1] of `cap`, its new length to *count_out.
+struct StackArgs {
+  int32_t *ids;
+  int cap;
+  const int32_t *count;
+  int32_t *count_out;
+};
+// ids below P16 to one stack, the P4 after them to the other
+cudaError_t launch_release_by_kind(int R, int max_pages, const int32_t *bt, const int32_t *seq_len,
+                                   const int32_t *released, int P16, int P4, const StackArgs &s16, const StackArgs &s4,
+                                   int32_t *seq_len_out, int *err, cudaStream_t s);
 
 // number of SMs of the current device (cached per device)
 int device_sm_count();
