@@ -15,7 +15,7 @@
 // KV head (G heads x window rows) are the columns, in tiles of 8. Why mma.sync and registers: a (page, head) is 2304
 // bytes, 98 SM cycles of HBM at the measured copy rate, and 4096 codes; as 16-bit operands in shared memory for tcgen05
 // those would be 8 KiB written and read again. Fragments masked out of the packed words cost 0.6 instructions a pair and
-// touch shared memory once. (A tcgen05 form with the key codes in TMEM took 117 us where this takes 63, four windows of 4
+// touch shared memory once. (A tcgen05 form with the key codes in TMEM took 117 us where this took 63, four windows of 4
 // over 32768 tokens: its code conversion and its softmax followed one another in the eight warps that its registers allow.)
 //
 // Split. Rows of up to 16 pages a warp get a CTA each. Otherwise the pages of all (request, KV head) rows form one line
@@ -25,12 +25,19 @@
 // part's queries, ids and first pages are on their way.
 //
 // Statistics. A warp keeps a reference per query column (at most 2^8 below the running maximum) and one for the value
-// scales (at most 2^6 below the largest), so that p s_v stays inside fp16; both move only when a page exceeds them.
+// scales (at most 2^6 below the largest), so that p s_v stays inside fp16; both move only when a page exceeds them. Values
+// of 16-bit pages count for the second one only where sums over it could leave fp32. A token that part of a window does not
+// see has probability 0 there; values of such a token that are not finite go round the products.
 //
-// Bound by instruction issue and by the latency of dependent instructions, not by HBM. On a GB300, 8 KV heads of 128 dims:
-// 8 requests of 40960 tokens, 4 query columns: 85.5 us, 4.43 TB/s, 65% of the measured copy rate (312 instructions and 131
-// cycles a page and SM); 4 of 32768, 16 columns: 63 us, 35% (404, 217); one of 131072, 40 columns: 155 us, 14% (884, 536);
-// proposals of 8 and of 128 pages: 5.9 and 15.7 us, a chain of dependent loads.
+// Bound by the latency of a warp's dependent steps (logits, maximum, exponents, transpose, products), not by HBM and not by
+// issue: with 16 warps an SM (one column tile) or 8 the waits of one are not filled by the others. On a GB300, 8 KV heads of
+// 128 dims, cycles at 2070 MHz of the whole launch a page and SM, of which HBM would take 107 at the measured copy rate:
+//   8 requests of 40960 tokens, 4 columns: 87 us, 4.35 TB/s, 64%: 167 cycles, 79 of them issue (316 instructions);
+//   4 of 32768, 16 columns: 65 us, 2.34 TB/s, 34%: 311 cycles, 98 (393);
+//   1 of 131072, 40 columns: 158 us, 0.96 TB/s, 14%: 759 cycles, 248 (992: two groups of warps);
+//   proposals of 8 and of 128 pages: 5.9 and 16.2 us, a chain of dependent loads.
+// The kernels of 16 bits a value are faster at the last two shapes (110 us, 12.7 us): packing pays for decode and for
+// windows of up to 16 columns. Heads of 128 dims spill: one column tile 64 bytes a thread, three 56, four 460 to 560.
 #include "kap_launch.h"
 #include "kap_packed.cuh"
 
@@ -42,7 +49,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -3.402823466e38f;  // reference of a column that has seen nothing: below every logit that fp32 holds
+constexpr float kNoMax = -3.402823466e38f;  // reference of a column that has seen nothing: no logit in fp32 is below it
 constexpr float kMaxSlack = 8.0f;     // log2 units a logit may exceed its reference by
 constexpr float kScaleSlack = 64.0f;  // factor a value scale may exceed its reference by
 
@@ -1152,7 +1159,11 @@ cudaError_t launch(const AParams &p, cudaStream_t s) {
   }
   // Rows of up to 16 pages a warp get a CTA each, which needs no scan, records, atomic or merge; longer ones are shared
   // out. Both sides on a GB300, proposals over 32, 256 and 2400 rows, us by row / shared out: 60 pages 10 / 15, 17 / 26,
-  // 114 / 126; 120 pages 16 / 17, 25 / 30, 161 / 175 (110 pages); 150 pages over 32 rows 18 / 16.
+  // 114 / 126; 120 pages 16 / 17, 25 / 30, 161 / 175 (110 pages); 150 pages over 32 rows 18 / 16. Windows of 16, 32 and 64
+  // columns over 8, 32 and 256 rows: 30 pages 9.4 / 18, 16 / 27, 24 / 38; 9.8 / 19, 16 / 28, 24 / 40; 19 / 28, 31 / 43,
+  // 48 / 58; 60 pages over 32 rows 13 / 21, 22 / 31, 36 / 37; 120 pages (64 for two groups of warps) over 32 rows 19 / 22, 34 /
+  // 31, over 256 rows 39 / 43, 70 / 77. The rule goes by the table's width, which the host knows, not by the lengths: short
+  // rows in a wider table are shared out.
   AParams q = p;
   const int grid = std::min(device_sm_count() * C::kCtas, C::kMaxGrid);
   const int64_t rows = static_cast<int64_t>(p.R) * p.hkv;

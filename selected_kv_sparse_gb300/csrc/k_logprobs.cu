@@ -15,8 +15,11 @@
 // measured copy rate, so the loop keeps to packed bf16 compares and maxima and to pairs of fp32. A warp streams
 // chunks of 512 logits with the next chunk's loads in flight and its own running sums: no barriers. Rows that are
 // too few to fill the GPU are split over CTAs; the last one to finish a row joins the parts in their order.
-// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 119 us, 4.4 TB/s, 65% of the measured copy rate (101
-// us without alternatives; 68% of the issue slots); of fp32 179 us, 87%; 20 rows of fp32 with 5 alternatives 9.6 us.
+// On a GB300, vocabulary 128256: 2048 rows of bf16 with 20 alternatives 118 us, 4.4 TB/s, 66% of the measured copy rate (101
+// us without alternatives): 10 instructions a logit fill 68% of the issue slots, the rest are waits; of fp32 177 us, 87%; 20
+// rows of fp32 with 5 alternatives 9.6 us. 200 and 400 rows of bf16 take 22 and 35 us (2.3 to 2.9 times the copy rate's time:
+// the CTAs come to 1.3 waves), 511 rows 42, 512 rows 39. Where a row has fewer tiles than alternatives (below 16384 tokens
+// for 32) every token is a candidate: 4096 rows of 4000 take 31 us without and 187 us with 20 alternatives.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 

@@ -9,8 +9,9 @@
 // Bound by HBM: a (page, head) of 128 dims reads 8192 and writes 2304 bytes. One warp takes one tensor of one (page,
 // head): 8 lanes share a group (16 bytes of source and one word of codes each), so source loads are 512 contiguous
 // bytes an instruction and all of them are in flight before the first is used.
-// On a GB300, 2048 pages of 8 heads: packing 42 us (65% of the issue slots, 60% of the measured copy rate), reading back 28
-// us (90%); both after one another 66.8 us, 5.15 TB/s.
+// On a GB300, 2048 pages of 8 heads: packing 42 us (60% of the measured copy rate; 65 to 72% of the issue slots, since the
+// scale, the reciprocal and the border test are worked out in all eight lanes of a group), reading back 28 us (90%); both
+// after one another 66.7 us, 5.16 TB/s.
 #include "kap_launch.h"
 #include "kap_packed.cuh"
 
