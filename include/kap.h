@@ -125,6 +125,14 @@ typedef struct {
   const int32_t *q_start_pos; /* [R] */
 } kap_verify_policy;
 
+/* Requests that share a prefix: group g owns the requests group_offsets[g] .. group_offsets[g+1]-1, whose block_table
+ * rows begin with the same prefix_pages[g] physical pages. group_offsets rises from 0 to num_seqs. */
+typedef struct {
+  int32_t num_groups;           /* 0: nothing is shared */
+  const int32_t *group_offsets; /* [num_groups+1] */
+  const int32_t *prefix_pages;  /* [num_groups] */
+} kap_prefix_groups;
+
 /* ---------------------------------------------------------------------------------------------------------
  * K-summary cache. EarlySelectKV page (routing over a K-summary cache) and the KRI page's KRI-Q row
  * (block-mean K). For every request r and prompt page j < ceil(ctx_len[r]/16), with n = min(16, ctx_len-16j)
@@ -283,6 +291,48 @@ kap_status kap_append_kv(const kap_kv_pool *pool, const void *k_new, const void 
                          const int32_t *pos_dev, const int64_t *slots_dev, int32_t num_tokens, int32_t tok_stride,
                          const float *inv_freq_dev, kap_stream stream);
 
+/* Which position axis turns each rotary pair: the table that kap_append_kv_norm takes for positions of several axes
+ * (time, height and width of images and video). Pair i of d/2 gets axis_host[i] in [0, num_axes).
+ *   interleaved 0: the first sections[0] pairs turn by axis 0, the next sections[1] by axis 1, and so on;
+ *   interleaved 1: pair i turns by axis i % num_axes where that axis a > 0 has i < num_axes * sections[a], else by axis 0.
+ * Writes HOST memory of d/2 entries owned by the caller. KAP_EINVAL for a NULL pointer, d <= 0 or odd, num_axes outside
+ * 1..8, a negative section, sections that do not add up to d/2 or that the interleaving does not give. */
+kap_status kap_rope_freq_axis(int32_t head_dim, const int32_t *sections_host, int32_t num_axes, int32_t interleaved,
+                              int32_t *axis_host);
+
+/* KV append of a model that normalises its queries and keys, or whose positions have several axes. The paper's models are
+ * of both kinds (KAP paper, setup); its executor's append is otherwise that of kap_append_kv. For token t with
+ * slot s = slots[t*tok_stride], all in fp32 with one rounding into the pool dtype at the end:
+ *   y = x * (mean of x^2 over the head's d dims + eps)^(-1/2) * weight   (y = x where the weight is NULL)
+ *   pairs (i, i + d/2) of y turn by pos[axis(i)*axis_stride + t*tok_stride] * inv_freq[i], axis(i) = freq_axis[i]
+ *   (0 where freq_axis is NULL; a pair whose axis lies outside [0, num_axes) keeps its y)
+ * for the rows of k_new into K[s] and of q into q_out; v_new goes to V[s] unchanged. With s < 0 the token's K and V are
+ * not written (q_out is). The angle is not rounded to fp32 before its sine and cosine, as kap_append_kv and
+ * kap_append_propose do: at position 131072 theirs may be off by 1/128 rad. The keys of one cache are to be written by
+ * calls of one kind. The mean of squares is formed in fp32: it takes |x| up to 2^60.
+ *   Rows: token t's heads start t*stride elements after the pointer and are contiguous [heads][d], so the parts of one
+ *   fused projection are taken as they are. Pointers 16-byte aligned, strides multiples of 16 bytes and at least
+ *   heads*d. q may be NULL (then q_out is not used); q_out may be q with the same stride (in place) and must not overlap an
+ *   input otherwise. Slots >= 0 must be distinct.
+ * Errors: KAP_EINVAL for null or misaligned pointers, sizes or strides out of range, eps < 0 or not finite, num_axes
+ * outside 1..8. A slot past the pool is skipped and sets device error bit 1. */
+typedef struct {
+  const void *k_new, *v_new;  /* [T][Hkv][d] pool dtype */
+  const void *q;              /* [T][Hq][d], or NULL */
+  void *q_out;                /* [T][Hq][d] */
+  int64_t k_stride, v_stride, q_stride, q_out_stride; /* elements between tokens */
+  const float *q_weight, *k_weight; /* [d] fp32, or NULL: not normalised */
+  float eps;
+  int32_t num_axes;
+  const int32_t *pos;         /* [num_axes][axis_stride] */
+  int64_t axis_stride;
+  const int32_t *freq_axis;   /* [d/2], or NULL */
+  const int64_t *slots;
+  const float *inv_freq;      /* [d/2] */
+  int32_t num_tokens, tok_stride;
+} kap_norm_append;
+kap_status kap_append_kv_norm(const kap_kv_pool *pool, const kap_norm_append *args, kap_stream stream);
+
 /* Selected-KV proposal attention, q = 1 per request. KAP paper, executor (proposal: a decode-like step with
  * q_prop = 1 over the compact view; only prompt-side KV is restricted) and EarlySelectKV (sparse attention with
  * the real query on precomputed page indices).
@@ -322,6 +372,26 @@ kap_status kap_attn_verify(const kap_kv_pool *pool, const kap_page_map *map, con
                            kap_stream stream);
 size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
                                  int32_t max_q);
+
+/* Verification attention of requests that share prefixes: several questions on one document, or several answers to one
+ * question (KAP paper: the knowledge that requests share is prompt KV). The same arguments, visibility and outputs as
+ * kap_attn_verify (windows of one row are decode), over the whole table, but the pages that a group shares are read once
+ * for all its requests, through the row of the group's first request. A group of one request, and a request whose
+ * window starts inside its group's shared pages, are taken as sharing nothing. The results are those of kap_attn_verify
+ * up to rounding: sums and statistics are fp32; over a bf16 pool probabilities enter the product with the values as bf16.
+ * A token that a row does not see adds nothing to it, whatever its K and V hold. A row that sees no token gets zeros
+ * and lse -infinity. Tokens on a page id outside the pool, or past the table's end, are skipped (device error bit 1).
+ *   groups: see kap_prefix_groups; group_offsets that do not rise from 0 to num_seqs set device error bit 4 (the results of
+ *   the requests concerned are then undefined).
+ *   workspace >= kap_shared_workspace_size(R, Hkv, Hq, d, total_q, num_groups) bytes; it needs no clearing. Calls that may
+ *   run at the same time, captured graphs among them, need a workspace each.
+ * Errors: those of kap_attn_verify; KAP_EINVAL for num_groups < 0 or null group arrays; KAP_EUNSUPPORTED for more than 2^26
+ * table columns, 2^20 groups or 2^31 - 1 query rows (total_q * Hq). */
+kap_status kap_attn_verify_shared(const kap_kv_pool *pool, const kap_page_map *map, const kap_verify_policy *vp,
+                                  const kap_prefix_groups *groups, const void *q_dev, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, kap_stream stream);
+size_t kap_shared_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
+                                 int32_t total_q, int32_t num_groups);
 
 /* Proposal attention without a caller workspace, for callers that cannot allocate device memory (a serving host
  * that fixes its device memory budget at start-up and owns the only allocator, a plug-in without access to that
@@ -410,6 +480,30 @@ kap_status kap_token_logprobs(const void *logits_dev, int32_t logits_dtype, int3
                               float *entropy_out, int32_t *rank_out, int32_t *top_ids, float *top_logprobs,
                               void *workspace, size_t workspace_bytes, kap_stream stream);
 size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab);
+
+/* Sampling of one token a row from given random numbers: the proposal's and the carry's tokens where decoding is not
+ * greedy. Row r has logits x over the vocabulary, the largest m, and settings of its own, each optional (NULL: off):
+ *   temperature  T (1 where NULL): weight w = exp((x - m) / T). T that is not above 0 takes the first token.
+ *   top_k        keeps the first k of the rank order of kap_accept_commit (logit descending, lower id first); off when
+ *                k < 1 or k is not below the number of tokens.
+ *   min_p        keeps tokens with w >= min_p; off when not above 0.
+ *   top_p        of the tokens that both keep, the shortest run of the rank order whose weight reaches top_p times their
+ *                weight; off when not below 1. The first token is always kept.
+ *   uniform      u in [0, 1): the token drawn is the first in id order at which the running sum of the kept weights passes
+ *                u times their sum. Values outside [0, 1) are taken to its nearest end, NaN to 0.
+ * tokens_out [rows]; logprob_out [rows] (may be NULL) = log of the drawn token's share of the kept weight; kept_out [rows]
+ * (may be NULL) = how many tokens were kept. Weights are held to 2^-44 of the largest (fewer bits past 2^18 tokens):
+ * one that rounds to nothing is never drawn. Sums are whole numbers, so a row's result does not depend on the other rows,
+ * on their number or on the order of any addition. A logit of -infinity is never kept. A row with a NaN or +infinity, or
+ * with -infinity throughout, has no distribution: it gets the first token of the rank order, NaN and 0.
+ *   logits_dev [rows] rows of `vocab` values (KAP_BF16 or KAP_F32), row_stride elements apart, at any element alignment;
+ *   the others [rows] on the device, fp32 but for top_k (int32). No workspace.
+ * Errors: KAP_EINVAL for null pointers, rows < 0, vocab < 1, row_stride < vocab; KAP_EUNSUPPORTED for another dtype,
+ * vocab > 2^24 or rows > 2^26. */
+kap_status kap_sample_tokens(const void *logits_dev, int32_t logits_dtype, int32_t vocab, int64_t row_stride, int32_t rows,
+                             const float *uniform_dev, const float *temperature_dev, const int32_t *top_k_dev,
+                             const float *top_p_dev, const float *min_p_dev, int32_t *tokens_out, float *logprob_out,
+                             int32_t *kept_out, kap_stream stream);
 
 /* Block tables and slot maps from request lengths. KAP paper, compiler and executor (block tables and slot mappings
  * are plan objects of fixed shape): the tables grow and the slots of a step are found on the device, from the lengths

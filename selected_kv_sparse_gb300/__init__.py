@@ -19,4 +19,8 @@ from ._binding import (  # noqa: F401
     kap_pack_pages, kap_packed_chunk_bytes, kap_packed_workspace_size, kap_release_tables, kap_token_logprobs,
     kap_unpack_pages,
 )
+from ._binding import (  # noqa: F401
+    PrefixGroups, kap_append_kv_norm, kap_attn_verify_shared, kap_sample_tokens, kap_shared_workspace_size,
+    rope_freq_axis,
+)
 from .pipeline import DecodeCycle, DecodeLoop, SideFlowDecode  # noqa: F401

@@ -66,6 +66,18 @@ class _Packed(ctypes.Structure):
     _fields_ = [("pool", _Pool), ("num_packed", ctypes.c_int32), ("packed", ctypes.c_void_p)]
 
 
+class _Groups(ctypes.Structure):
+    _fields_ = [("num_groups", ctypes.c_int32), ("group_offsets", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p)]
+
+
+class _NormAppend(ctypes.Structure):
+    _P, _L, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    _fields_ = [("k_new", _P), ("v_new", _P), ("q", _P), ("q_out", _P), ("k_stride", _L), ("v_stride", _L),
+                ("q_stride", _L), ("q_out_stride", _L), ("q_weight", _P), ("k_weight", _P), ("eps", ctypes.c_float),
+                ("num_axes", _I), ("pos", _P), ("axis_stride", _L), ("freq_axis", _P), ("slots", _P), ("inv_freq", _P),
+                ("num_tokens", _I), ("tok_stride", _I)]
+
+
 def _declare(lib):
     P, I, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     F = ctypes.c_float
@@ -105,6 +117,11 @@ def _declare(lib):
         "kap_extend_tables": ([I, I, P, P, P, P, I, P, P, P, P, P, I, P, P, P], I),
         "kap_release_tables": ([I, I, P, P, P, P, I, P, P, P, P], I),
         "kap_release_tables_packed": ([I, I, P, P, P, I, P, I, P, P, I, P, I, P, P, P, P], I),
+        "kap_rope_freq_axis": ([I, P, I, I, P], I),
+        "kap_append_kv_norm": ([P, P, P], I),
+        "kap_shared_workspace_size": ([I, I, I, I, I, I], Z),
+        "kap_attn_verify_shared": ([P, P, P, P, P, P, P, P, Z, P], I),
+        "kap_sample_tokens": ([P, I, I, ctypes.c_int64, I, P, P, P, P, P, P, P, P, P], I),
         "kap_selftest_wait_timeout": ([ctypes.c_uint32, ctypes.c_uint32, P, P], I),
     }
     for name, (args, res) in sig.items():
@@ -287,6 +304,14 @@ class VerifyPolicy:
 
     def _c(self) -> _Verify:
         return _Verify(self.max_q, self.total_q, _i32(self.q_offsets, "q_offsets"), _i32(self.q_start_pos, "q_start_pos"))
+
+
+@dataclass
+class PrefixGroups:
+    """Requests that share prefixes: group g owns requests group_offsets[g] .. group_offsets[g+1]-1 (offsets rise from 0 to
+    R), whose block_table rows begin with the same prefix_pages[g] pages. int32, device."""
+    group_offsets: torch.Tensor   # [num_groups + 1]
+    prefix_pages: torch.Tensor    # [num_groups]
 
 
 @dataclass
@@ -512,6 +537,66 @@ def kap_append_kv(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, q_inou
                                               _stream(stream)))
 
 
+def _rows_of(t: torch.Tensor, T: int, heads: int, d: int, dt, dev: int, name: str):
+    """(address, token stride) of [T][heads][d] rows that are contiguous within a token."""
+    if t.shape != (T, heads, d):
+        raise ValueError(f"{name} must be {[T, heads, d]}")
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must have the pool dtype")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device {dev}, got one on {t.device}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"{name}: a token's [heads][d] must be contiguous")
+    return t.data_ptr(), st[0] if T > 1 else heads * d
+
+
+def kap_append_kv_norm(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, q: Optional[torch.Tensor],
+                       q_out: Optional[torch.Tensor], pos: torch.Tensor, slots: torch.Tensor, inv_freq: torch.Tensor,
+                       q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, freq_axis: Optional[torch.Tensor] = None, num_tokens: Optional[int] = None,
+                       tok_stride: int = 1, stream=None):
+    """KV append with norms of queries and keys and positions of several axes: k_new, v_new [T][Hkv][d] and q [T][Hq][d]
+    (tokens any stride apart, so the parts of one fused projection go in as they are), q_out [T][Hq][d] (q itself for in
+    place), pos [axes][T] or [T] int32, slots [T] int64, weights [d] fp32, freq_axis [d/2] int32 (rope_freq_axis). Token t
+    reads pos[..., t * tok_stride] and slots[t * tok_stride]."""
+    f = load().kap_append_kv_norm
+    kp, vp = pool.k_pages, pool.v_pages
+    shape, dt, i32, f32 = kp.shape, kp.dtype, torch.int32, torch.float32
+    if len(shape) != 4 or shape != vp.shape or shape[2] != PAGE or vp.dtype is not dt:
+        raise ValueError("k_pages/v_pages must both be [num_pages][Hkv][16][d] of one dtype")
+    if dt is not torch.bfloat16 and dt is not f32:
+        raise TypeError("pool dtype must be bfloat16 or float32")
+    dev = _here(kp)
+    P, hkv, _, d = shape
+    hq = pool.num_q_heads
+    T = k_new.shape[0] if num_tokens is None else int(num_tokens)
+    k, ks = _rows_of(k_new, T, hkv, d, dt, dev, "k_new")
+    v, vs = _rows_of(v_new, T, hkv, d, dt, dev, "v_new")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    qa = qs = oa = os_ = 0
+    if q is not None:
+        qa, qs = _rows_of(q, T, hq, d, dt, dev, "q")
+        oa, os_ = _rows_of(q_out, T, hq, d, dt, dev, "q_out")
+    need = (T - 1) * tok_stride + 1 if T > 0 else 0
+    if pos.dim() not in (1, 2) or pos.shape[-1] < need or slots.dim() != 1 or slots.shape[0] < need or tok_stride < 1:
+        raise ValueError("pos must be [axes][T] or [T] and slots [T], with room for every token")
+    axes, wide = (pos.shape[0], pos.shape[1]) if pos.dim() == 2 else (1, pos.shape[0])
+    for t, n, name in ((q_weight, d, "q_weight"), (k_weight, d, "k_weight"), (inv_freq, d // 2, "inv_freq"),
+                       (freq_axis, d // 2, "freq_axis")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries")
+    a = _NormAppend(k, v, qa, oa, ks, vs, qs, os_, _at(q_weight, dev, f32, "q_weight"), _at(k_weight, dev, f32, "k_weight"),
+                    eps, axes, _at(pos, dev, i32, "pos"), wide, _at(freq_axis, dev, i32, "freq_axis"),
+                    _at(slots, dev, torch.int64, "slots"), _at(inv_freq, dev, f32, "inv_freq"), T, tok_stride)
+    p = _Pool(P, PAGE, hkv, hq, d, KAP_BF16 if dt is torch.bfloat16 else KAP_F32, _at(kp, dev, None, "k_pages"),
+              _at(vp, dev, None, "v_pages"), None)
+    st = f(ctypes.byref(p), ctypes.byref(a), _raw_stream(stream, dev))
+    if st:
+        _check("kap_append_kv_norm", st)
+
+
 def kap_propose_workspace_size(R: int, hkv: int, hq: int, d: int) -> int:
     return int(load().kap_propose_workspace_size(R, hkv, hq, d))
 
@@ -576,6 +661,43 @@ def kap_attn_verify(pool: KVPool, pmap: PageMap, vp: VerifyPolicy, q: torch.Tens
     _check("kap_attn_verify", lib.kap_attn_verify(ctypes.byref(p), ctypes.byref(m), ctypes.byref(v), _ptr(q),
                                                   _ptr(out), _ptr(lse), _ptr(workspace),
                                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kap_shared_workspace_size(R: int, hkv: int, hq: int, d: int, total_q: int, num_groups: int) -> int:
+    return int(load().kap_shared_workspace_size(R, hkv, hq, d, total_q, num_groups))
+
+
+def kap_attn_verify_shared(pool: KVPool, pmap: PageMap, vp: VerifyPolicy, groups: PrefixGroups, q: torch.Tensor,
+                           out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """kap_attn_verify over requests that share prefixes: a group's shared pages are read once for all its requests
+    (workspace: kap_shared_workspace_size)."""
+    f = load().kap_attn_verify_shared
+    kp, va = pool.k_pages, pool.v_pages
+    shape, dt, i32 = kp.shape, kp.dtype, torch.int32
+    if len(shape) != 4 or shape != va.shape or shape[2] != PAGE or va.dtype is not dt:
+        raise ValueError("k_pages/v_pages must both be [num_pages][Hkv][16][d] of one dtype")
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError("pool dtype must be bfloat16 or float32")
+    dev = _here(kp)
+    P, hkv, _, d = shape
+    hq, R, tq = pool.num_q_heads, pmap.block_table.shape[0], vp.total_q
+    if q.shape != (tq, hq, d) or out.shape != (tq, hq, d) or lse.shape != (tq, hq):
+        raise ValueError(f"q and out must be {[tq, hq, d]} and lse {[tq, hq]}")
+    if vp.q_offsets.numel() != R + 1 or vp.q_start_pos.numel() != R:
+        raise ValueError("q_offsets must have R + 1 and q_start_pos R entries")
+    go, pp = groups.group_offsets, groups.prefix_pages
+    ng = pp.numel()
+    if go.numel() != ng + 1:
+        raise ValueError("group_offsets must have one entry more than prefix_pages")
+    p = _Pool(P, PAGE, hkv, hq, d, KAP_BF16 if dt is torch.bfloat16 else KAP_F32, _at(kp, dev, None, "k_pages"),
+              _at(va, dev, None, "v_pages"), None)
+    v = _Verify(vp.max_q, tq, _at(vp.q_offsets, dev, i32, "q_offsets"), _at(vp.q_start_pos, dev, i32, "q_start_pos"))
+    g = _Groups(ng, _at(go, dev, i32, "group_offsets"), _at(pp, dev, i32, "prefix_pages"))
+    st = f(ctypes.byref(p), ctypes.byref(_map_c(pmap, dev)), ctypes.byref(v), ctypes.byref(g), _at(q, dev, dt, "q"),
+           _at(out, dev, dt, "out"), _at(lse, dev, torch.float32, "lse"), _at(workspace, dev, None, "workspace"),
+           workspace.nbytes, _raw_stream(stream, dev))
+    if st:
+        _check("kap_attn_verify_shared", st)
 
 
 def kap_packed_chunk_bytes(d: int) -> int:
@@ -706,6 +828,35 @@ def kap_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: tor
         _check("kap_token_logprobs", st)
 
 
+def kap_sample_tokens(logits: torch.Tensor, uniform: torch.Tensor, tokens: torch.Tensor,
+                      temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                      top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+                      logprob: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None, stream=None):
+    """One token a row of logits [rows][vocab] (bf16 or fp32, rows any stride apart) from uniform [rows] in [0, 1), into
+    tokens [rows] (int32). temperature, top_p, min_p [rows] fp32 and top_k [rows] int32 are each row's own; None: off.
+    logprob [rows] fp32: the token's log probability among the kept_out[r] kept ones (kept [rows] int32)."""
+    f = load().kap_sample_tokens
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda:
+        raise TypeError("logits must be a [rows][vocab] bf16 or fp32 CUDA tensor")
+    dev = _here(logits)
+    rows, vocab = logits.shape
+    stride, step = logits.stride()
+    if rows <= 1:
+        stride = vocab
+    if (vocab > 1 and step != 1) or stride < vocab:
+        raise ValueError("a row of logits must be contiguous and rows must not overlap")
+    i32, f32 = torch.int32, torch.float32
+    for t in (uniform, tokens, temperature, top_k, top_p, min_p, logprob, kept):
+        if t is not None and (t.dim() != 1 or t.shape[0] != rows):
+            raise ValueError("every array beside the logits must be [rows]")
+    st = f(logits.data_ptr(), KAP_BF16 if logits.dtype == torch.bfloat16 else KAP_F32, vocab, stride, rows,
+           _at(uniform, dev, f32, "uniform"), _at(temperature, dev, f32, "temperature"), _at(top_k, dev, i32, "top_k"),
+           _at(top_p, dev, f32, "top_p"), _at(min_p, dev, f32, "min_p"), _at(tokens, dev, i32, "tokens"),
+           _at(logprob, dev, f32, "logprob"), _at(kept, dev, i32, "kept"), _raw_stream(stream, dev))
+    if st:
+        _check("kap_sample_tokens", st)
+
+
 def _vector(t: torch.Tensor, n: Optional[int], dev: int, name: str, dtype=torch.int32):
     if t.dim() != 1 or (n is not None and t.numel() != n):
         raise ValueError(f"{name} must be 1-D" + (f" with {n} entries" if n is not None else ""))
@@ -801,4 +952,13 @@ def rope_inv_freq(d: int, theta: float = 1.0e4, device="cpu") -> torch.Tensor:
     fp32), as a tensor on `device`."""
     out = torch.empty(d // 2, dtype=torch.float32)
     _check("kap_rope_inv_freq", load().kap_rope_inv_freq(int(d), float(theta), ctypes.c_void_p(out.data_ptr())))
+    return out.to(device)
+
+
+def rope_freq_axis(d: int, sections, interleaved: bool = False, device="cpu") -> torch.Tensor:
+    """The position axis of each of the d/2 rotary pairs (kap_rope_freq_axis), as an int32 tensor on `device`."""
+    sec = torch.tensor([int(x) for x in sections], dtype=torch.int32)
+    out = torch.empty(max(d, 2) // 2, dtype=torch.int32)
+    _check("kap_rope_freq_axis", load().kap_rope_freq_axis(int(d), ctypes.c_void_p(sec.data_ptr()), sec.numel(),
+                                                           int(bool(interleaved)), ctypes.c_void_p(out.data_ptr())))
     return out.to(device)

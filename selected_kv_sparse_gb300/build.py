@@ -18,7 +18,7 @@ OUT = os.path.join(HERE, "libkap.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["kap_api.cu", "k_select.cu", "k_append.cu", "k_propose.cu", "k_verify.cu", "k_accept.cu",
            "k_materialize.cu", "k_packed.cu", "k_attn_packed.cu", "k_logprobs.cu", "k_tables.cu", "kap_noalloc.cu",
-           "k_selftest.cu"]
+           "k_append_norm.cu", "k_attn_shared.cu", "k_sample.cu", "k_selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -474,6 +474,100 @@ kap_status kap_attn_verify_packed(const kap_packed_pool *pool, const kap_page_ma
                                           vp->q_start_pos, q_dev, out, lse, workspace, error_word(), cs(stream)));
 }
 
+kap_status kap_rope_freq_axis(int32_t head_dim, const int32_t *sections_host, int32_t num_axes, int32_t interleaved,
+                              int32_t *axis_host) {
+  if (!sections_host || !axis_host || head_dim <= 0 || (head_dim & 1) || num_axes < 1 || num_axes > 8) return KAP_EINVAL;
+  const int32_t half = head_dim / 2;
+  int64_t sum = 0;
+  for (int32_t a = 0; a < num_axes; ++a) {
+    if (sections_host[a] < 0) return KAP_EINVAL;
+    sum += sections_host[a];
+  }
+  if (sum != half) return KAP_EINVAL;
+  int32_t count[8] = {0};
+  auto axis_of = [&](int32_t i) {
+    if (interleaved) {
+      const int32_t a = i % num_axes;
+      return i < static_cast<int64_t>(num_axes) * sections_host[a] ? a : 0;
+    }
+    int32_t a = 0, end = sections_host[0];
+    while (i >= end) end += sections_host[++a];
+    return a;
+  };
+  for (int32_t i = 0; i < half; ++i) ++count[axis_of(i)];
+  for (int32_t a = 0; a < num_axes; ++a)
+    if (count[a] != sections_host[a]) return KAP_EINVAL;
+  for (int32_t i = 0; i < half; ++i) axis_host[i] = axis_of(i);
+  return KAP_OK;
+}
+
+kap_status kap_append_kv_norm(const kap_kv_pool *pool, const kap_norm_append *a, kap_stream stream) {
+  kap_status st = check_pool(pool, false);
+  if (st != KAP_OK) return st;
+  if (!a || a->num_tokens < 0) return KAP_EINVAL;
+  if (a->num_axes < 1 || a->num_axes > 8 || a->tok_stride < 1 || a->axis_stride < 0) return KAP_EINVAL;
+  if (!std::isfinite(a->eps) || a->eps < 0.0f) return KAP_EINVAL;
+  if (a->num_tokens == 0) return KAP_OK;
+  if (!a->k_new || !a->v_new || !a->pos || !a->slots || !a->inv_freq || (a->q && !a->q_out)) return KAP_EINVAL;
+  if (!aligned16(a->k_new) || !aligned16(a->v_new) || !aligned16(a->q) || (a->q && !aligned16(a->q_out)))
+    return KAP_EINVAL;
+  const int64_t kv = static_cast<int64_t>(pool->num_kv_heads) * pool->head_dim,
+                qw = static_cast<int64_t>(pool->num_q_heads) * pool->head_dim;
+  const int64_t unit = pool->dtype == KAP_BF16 ? 8 : 4;   // elements of 16 bytes
+  auto bad = [&](int64_t stride, int64_t width) { return stride < width || stride % unit != 0; };
+  if (bad(a->k_stride, kv) || bad(a->v_stride, kv) || (a->q && (bad(a->q_stride, qw) || bad(a->q_out_stride, qw))))
+    return KAP_EINVAL;
+  if (a->q && a->q == a->q_out && a->q_stride != a->q_out_stride) return KAP_EINVAL;
+  const NormAppendArgs n{a->k_new, a->v_new, a->q, a->q_out, a->k_stride, a->v_stride, a->q_stride, a->q_out_stride,
+                         a->q_weight, a->k_weight, a->eps, a->pos, a->freq_axis, a->slots, a->inv_freq, a->num_axes,
+                         a->num_tokens, a->tok_stride, a->axis_stride};
+  return cuda_status(launch_append_norm(pool_args(pool), n, error_word(), cs(stream)));
+}
+
+size_t kap_shared_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
+                                 int32_t total_q, int32_t num_groups) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || total_q < 0 || num_groups < 0) return 0;
+  return shared_workspace_bytes(num_seqs, num_kv_heads, num_q_heads, head_dim, total_q, num_groups);
+}
+
+kap_status kap_attn_verify_shared(const kap_kv_pool *pool, const kap_page_map *map, const kap_verify_policy *vp,
+                                  const kap_prefix_groups *groups, const void *q_dev, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, kap_stream stream) {
+  kap_status st = check_pool(pool, false);
+  if (st != KAP_OK) return st;
+  if ((st = check_map(map, false)) != KAP_OK) return st;
+  if (!vp || !groups) return KAP_EINVAL;
+  if (vp->max_q <= 0 || vp->total_q < 0 || groups->num_groups < 0) return KAP_EINVAL;
+  if (groups->num_groups > 0 && (!groups->group_offsets || !groups->prefix_pages)) return KAP_EINVAL;
+  if (pool->num_q_heads / pool->num_kv_heads * static_cast<int64_t>(vp->max_q) > 64) return KAP_EUNSUPPORTED;
+  if (map->max_pages > (1 << 26) || groups->num_groups > (1 << 20) ||
+      static_cast<int64_t>(vp->total_q) * pool->num_q_heads > 0x7fffffff)
+    return KAP_EUNSUPPORTED;
+  if (vp->total_q == 0) return KAP_OK;
+  if (!q_dev || !out || !lse || !workspace || !vp->q_offsets || !vp->q_start_pos) return KAP_EINVAL;
+  if (!aligned16(q_dev) || !aligned16(out) || !aligned16(workspace)) return KAP_EINVAL;
+  if (workspace_bytes < shared_workspace_bytes(map->num_seqs, pool->num_kv_heads, pool->num_q_heads, pool->head_dim,
+                                               vp->total_q, groups->num_groups))
+    return KAP_ECAPACITY;
+  return cuda_status(launch_verify_shared(pool_args(pool), map_args(map), vp->total_q, vp->q_offsets, vp->q_start_pos,
+                                          groups->num_groups, groups->group_offsets, groups->prefix_pages, q_dev, out,
+                                          lse, workspace, error_word(), cs(stream)));
+}
+
+kap_status kap_sample_tokens(const void *logits_dev, int32_t logits_dtype, int32_t vocab, int64_t row_stride, int32_t rows,
+                             const float *uniform_dev, const float *temperature_dev, const int32_t *top_k_dev,
+                             const float *top_p_dev, const float *min_p_dev, int32_t *tokens_out, float *logprob_out,
+                             int32_t *kept_out, kap_stream stream) {
+  if (logits_dtype != KAP_BF16 && logits_dtype != KAP_F32) return KAP_EUNSUPPORTED;
+  if (rows < 0 || vocab <= 0 || row_stride < vocab) return KAP_EINVAL;
+  if (vocab > (1 << 24) || rows > (1 << 26)) return KAP_EUNSUPPORTED;
+  if (rows == 0) return KAP_OK;
+  if (!logits_dev || !uniform_dev || !tokens_out) return KAP_EINVAL;
+  if (reinterpret_cast<uintptr_t>(logits_dev) & (logits_dtype == KAP_BF16 ? 1u : 3u)) return KAP_EINVAL;
+  return cuda_status(launch_sample(logits_dev, logits_dtype, vocab, row_stride, rows, uniform_dev, temperature_dev,
+                                   top_k_dev, top_p_dev, min_p_dev, tokens_out, logprob_out, kept_out, cs(stream)));
+}
+
 size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab) {
   if (rows <= 0 || vocab <= 0) return 0;
   return logprobs_workspace_bytes(rows, vocab);

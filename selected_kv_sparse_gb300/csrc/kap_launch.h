@@ -74,6 +74,22 @@ cudaError_t launch_append(const PoolArgs &p, const void *k_new, const void *v_ne
                           const int32_t *pos, const int64_t *slots, int T, int tok_stride, const float *inv_freq,
                           int *err, cudaStream_t s);
 
+// KV append with norms of queries and keys and positions on several axes (k_append_norm.cu); strides in elements
+struct NormAppendArgs {
+  const void *k, *v, *q;  // rows [T][heads][d]; q may be null
+  void *q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  const float *q_weight, *k_weight;  // [d] or null
+  float eps;
+  const int32_t *pos;       // [num_axes][axis_stride]
+  const int32_t *freq_axis; // [d/2] or null
+  const int64_t *slots;
+  const float *inv_freq;
+  int num_axes, num_tokens, tok_stride;
+  int64_t axis_stride;
+};
+cudaError_t launch_append_norm(const PoolArgs &p, const NormAppendArgs &a, int *err, cudaStream_t s);
+
 // proposal attention (k_propose.cu)
 size_t propose_workspace_bytes(int R, int hkv, int hq, int d);
 // k_new/v_new/inv_freq non-null: fused append of the step token at seq_len-1 (q is then taken before RoPE)
@@ -104,11 +120,23 @@ cudaError_t launch_verify_packed(const PackedArgs &p, const MapArgs &m, int max_
                                  const int32_t *q_offsets, const int32_t *q_start, const void *q, void *out,
                                  float *lse, void *ws, int *err, cudaStream_t s);
 
+// verification attention of requests that share prefixes (k_attn_shared.cu)
+size_t shared_workspace_bytes(int R, int hkv, int hq, int d, int total_q, int num_groups);
+cudaError_t launch_verify_shared(const PoolArgs &p, const MapArgs &m, int total_q, const int32_t *q_offsets,
+                                 const int32_t *q_start, int num_groups, const int32_t *group_off,
+                                 const int32_t *prefix_pages, const void *q, void *out, float *lse, void *ws, int *err,
+                                 cudaStream_t s);
+
 // log probabilities of given tokens (k_logprobs.cu)
 size_t logprobs_workspace_bytes(int rows, int vocab);
 cudaError_t launch_logprobs(const void *logits, int dtype, int V, int64_t stride, int rows, const int32_t *tokens,
                             int top_n, float *lp, float *ent, int32_t *rank, int32_t *top_ids, float *top_lp, void *ws,
                             cudaStream_t s);
+
+// token sampling (k_sample.cu)
+cudaError_t launch_sample(const void *logits, int dtype, int V, int64_t stride, int rows, const float *u,
+                          const float *temp, const int32_t *top_k, const float *top_p, const float *min_p,
+                          int32_t *tokens, float *logprob, int32_t *kept, cudaStream_t s);
 
 // block tables and slot maps from request lengths (k_tables.cu)
 cudaError_t launch_extend_tables(int R, int max_pages, int32_t *bt, const int32_t *seq_len, const int32_t *new_tokens,
