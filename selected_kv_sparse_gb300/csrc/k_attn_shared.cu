@@ -15,6 +15,7 @@
 // others do not.
 #include "kap_device.cuh"
 #include "kap_launch.h"
+#include "kap_tma.h"
 
 #include <algorithm>
 
@@ -287,6 +288,549 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
   }
 }
 
+// ------------------------------------------------------------------------------------------------- tensor cores
+// bf16 pools. S[128 rows x 128 tokens] = Q . K^T (tcgen05.mma, M = 128, both operands K-major in shared memory), softmax with
+// a thread a row, P back into the tensor memory that S had, as bf16, O[128 rows x d] += P . V (A from tensor memory, V read
+// MN-major from shared memory). Two streams of softmax warps, each with an S and an O, take turns at the tensor core:
+// an item's block of up to 128 rows gives its even tiles to one and its odd tiles to the other and joins the two at the
+// end; a block of up to 256 rows gives each stream 128 of them, and both read every tile.
+// Warps: 0-3 and 4-7 the streams' softmax (thread = row), 8 K pages and tile records, 9 tcgen05 issuer, 10 V pages,
+// 11 queries. K and V tiles share a ring. Every wait is bounded, and no role waits on a block-wide barrier.
+constexpr int kTcThreads = 384;
+constexpr int kTcBlock = 256;
+constexpr float kRescale = 8.0f;  // log2: the reference of a row's weights follows its maximum when 2^8 behind
+
+// A tile's record, 32 bytes: tiles of 128 dims leave little shared memory beside the ring.
+struct TileInfo {
+  int flags, idx, n, tp;   // tile idx of the segment's n; tp: tokens, and from bit 8 on which of its pages are in the pool
+  int h, n0, rows, q0;     // rows of the block, from row n0 of the item on
+};
+constexpr int kValid = 1, kFirst = 2, kLast = 4, kTwo = 8, kQbuf = 16, kQpar = 32, kKind = 128, kLater = 256;  // kQpar: 2 bits
+
+template <int D>
+struct Tc {
+  static constexpr int ATOM = 128 * 128;               // 64 columns of a 128-row bf16 operand
+  static constexpr int UNIT = 128 * D * 2;             // a K or V tile, or 128 query rows
+  static constexpr int NU = D == 128 ? 5 : 10;         // ring of tiles
+  static constexpr int kMeta = D == 128 ? 4 : 8;       // tile records in flight
+  static constexpr int OFF_RING = 0;
+  static constexpr int OFF_Q = NU * UNIT;
+  static constexpr int OFF_INFO = OFF_Q + 2 * UNIT;
+  static constexpr int OFF_X = OFF_INFO + kMeta * static_cast<int>(sizeof(TileInfo));  // m [2][128], l of stream 1 [128]
+  // full, empty [NU]; mfull, mfree [kMeta]; qfull, qempty, sfull, pfull, ofull [2]; xready, xdone
+  static constexpr int NBAR = 2 * NU + 2 * kMeta + 10 + 2;
+  static constexpr int OFF_BAR = OFF_X + 3 * 128 * 4;
+  static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+  static constexpr int ALLOC = OFF_TMEM + 16 + 1024;   // room to align the base to 1024 bytes
+  static_assert(ALLOC <= 227 * 1024 - 64, "shared memory per CTA");
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {  // relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// The segments of a CTA's tiles, in order: runs of tiles of one (item, block of rows).
+struct Segment {
+  Entry x;
+  int e, h, n0, rows, t0, n;  // tiles [t0, t0 + n) of the block's
+};
+struct Walker {
+  const HParams &p;
+  const Groups gr;
+  int64_t at, end, es;
+  int e, have;
+  Entry x;
+  __device__ __forceinline__ Walker(const HParams &p_, const Plan &pl)
+      : p(p_), gr{p_.group_off}, at(pl.begin), end(pl.end), es(pl.entry_start), e(pl.entry), have(-1) {}
+  __device__ __forceinline__ bool next(Segment &s) {
+    if (at >= end) return false;
+    while (true) {
+      if (have != e) {
+        x = entry(p, gr, e);
+        have = e;
+      }
+      const int64_t size = static_cast<int64_t>(x.tiles) * x.blocks * p.hkv;
+      if (at < es + size) break;
+      es += size;
+      ++e;
+    }
+    const int sub = static_cast<int>((at - es) / x.tiles);
+    s.x = x;
+    s.e = e;
+    s.t0 = static_cast<int>(at - es - static_cast<int64_t>(sub) * x.tiles);
+    s.n = static_cast<int>(min(static_cast<int64_t>(x.tiles - s.t0), end - at));
+    s.h = sub / x.blocks;
+    s.n0 = (sub - s.h * x.blocks) * p.block;
+    s.rows = min(x.rows - s.n0, p.block);
+    at += s.n;
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    shared_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const HParams p) {
+  using L = Tc<D>;
+  constexpr int NU = L::NU, kMeta = L::kMeta;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  unsigned char *sm = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  unsigned char *ring = sm + L::OFF_RING, *Qs = sm + L::OFF_Q;
+  TileInfo *info = reinterpret_cast<TileInfo *>(sm + L::OFF_INFO);
+  float *xm = reinterpret_cast<float *>(sm + L::OFF_X);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
+  uint64_t *full = bars, *empty = full + NU, *mfull = empty + NU, *mfree = mfull + kMeta, *qfull = mfree + kMeta;
+  uint64_t *qempty = qfull + 2, *sfull = qempty + 2, *pfull = sfull + 2, *ofull = pfull + 2, *xready = ofull + 2;
+  uint64_t *xdone = xready + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_TMEM);
+  __shared__ int s_abort;
+  volatile int *abort_flag = &s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_sync();
+
+  // the plan's scratch lies where the ring will be
+  int64_t *scratch = reinterpret_cast<int64_t *>(ring);
+  const Groups gs = load_groups(p, reinterpret_cast<int32_t *>(ring + 512));
+  check_groups(p, gs);
+  const Plan pl = make_plan(p, gs, scratch, scratch + 40);
+  if (pl.begin >= pl.end) return;   // the whole CTA
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < L::NBAR; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < kMeta; ++i) mbar_init(&mfree[i], 9);  // 8 softmax warps and the issuer
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qempty[i], 2);
+      mbar_init(&pfull[i], 4);
+    }
+    mbar_init(xready, 8);
+    mbar_init(xdone, 8);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;   // S of stream s at column 128 s, O at 256 + 128 s
+
+  auto wait = [&](uint64_t *bar, int phase) -> bool {   // the whole warp
+    const bool ok = *abort_flag == 0 && mbar_wait(bar, phase & 1, p.err);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    *abort_flag = 1;
+    return false;
+  };
+
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------------------------------------------------------------ pages
+    const bool keys = warp == 8;
+    Walker walk(p, pl);
+    Segment s{};
+    int u = 0, i = 0, seg = -1, uses[2] = {0, 0}, qflags = 0;
+    bool more = walk.next(s);
+    int page = -1;
+    auto fetch = [&](const Segment &g, int k) {   // this lane's page of tile k of the segment
+      const int j = g.x.page0 + (g.t0 + k) * kTilePages + lane;
+      page = lane < kTilePages && j < p.max_pages && j * kPage < g.x.tok1
+                 ? p.bt[static_cast<size_t>(g.x.req) * p.max_pages + j] : -1;
+    };
+    if (more) fetch(s, 0);
+    for (;; ++u) {
+      const int un = 2 * u + (keys ? 0 : 1), st = un % NU, mi = u % kMeta;
+      if (un >= NU && !wait(&empty[st], un / NU - 1)) break;
+      if (keys && u >= kMeta && !wait(&mfree[mi], u / kMeta - 1)) break;
+      if (!more) {
+        if (keys && lane == 0) {
+          info[mi].flags = 0;
+          mbar_arrive(&mfull[mi]);
+        }
+        break;
+      }
+      const int tok = s.x.tok0 + (s.t0 + i) * kTileTok, ntok = min(kTileTok, s.x.tok1 - tok);
+      const int npg = (ntok + kPage - 1) / kPage;
+      const bool in = lane < npg, ok = in && page >= 0 && page < p.num_pages;
+      if (in && !ok) set_error(p.err, kErrPage);
+      const uint32_t pages = __ballot_sync(0xffffffffu, ok);
+      unsigned char *dst = ring + st * L::UNIT;
+      if (!keys) {   // values that no copy brings must be finite: their weights are zero
+        for (int j = 0; j < kTilePages; ++j)
+          if (!((pages >> j) & 1))
+            for (int c = lane; c < kPage * D / 8; c += 32) {
+              const int half = c / (kPage * 8), w = c % (kPage * 8);
+              *reinterpret_cast<uint4 *>(dst + half * L::ATOM + j * 2048 + w * 16) = make_uint4(0, 0, 0, 0);
+            }
+        if (pages != 0xff) fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (keys && i == 0) {
+        ++seg;
+        const bool two = s.rows > 128;
+        const int qbuf = two ? 0 : (seg & 1);
+        qflags = (two ? kTwo : 0) | (qbuf ? kQbuf : 0) | ((uses[0] & 1) ? kQpar : 0) | ((uses[1] & 1) ? 2 * kQpar : 0) |
+                 (s.e < p.num_groups ? 0 : kKind) | (s.t0 > 0 ? kLater : 0);
+        if (two || qbuf == 0) ++uses[0];
+        if (two || qbuf == 1) ++uses[1];
+      }
+      if (lane == 0) {
+        if (keys)
+          info[mi] = TileInfo{kValid | qflags | (i == 0 ? kFirst : 0) | (i == s.n - 1 ? kLast : 0), i, s.n,
+                              ntok | (static_cast<int>(pages) << 8), s.h, s.n0, s.rows, s.x.q0};
+        if (keys) mbar_arrive(&mfull[mi]);
+        mbar_arrive_expect_tx(&full[st], __popc(pages) * kPage * D * 2);
+      }
+      __syncwarp();
+      if (ok) {
+        const int row0 = (page * p.hkv + s.h) * kPage;
+        const CUtensorMap *tm = keys ? &tmK : &tmV;
+        tma_load_2d(dst + lane * 2048, tm, 0, row0, &full[st]);
+        if (D == 128) tma_load_2d(dst + L::ATOM + lane * 2048, tm, 64, row0, &full[st]);
+      }
+      if (++i == s.n) {
+        more = walk.next(s);
+        i = 0;
+      }
+      if (more) fetch(s, i);
+    }
+    // after an abort, copies in flight are waited for (bounded) before the CTA leaves
+    if (*abort_flag)
+      for (int k = max(0, u - NU); k < u; ++k) {
+        const int un = 2 * k + (keys ? 0 : 1);
+        mbar_wait(&full[un % NU], (un / NU) & 1, nullptr);
+      }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------------------------------------------ queries
+    Walker walk(p, pl);
+    Segment s;
+    int uses[2] = {0, 0};
+    for (int seg = 0; walk.next(s); ++seg) {
+      const bool two = s.rows > 128;
+      const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(p.q);
+      bool stop = false;
+      for (int b = 0; b < 2 && !stop; ++b) {
+        if (!two && b != (seg & 1)) continue;
+        if (uses[b] > 0 && !wait(&qempty[b], uses[b] - 1)) {
+          stop = true;
+          break;
+        }
+        ++uses[b];
+        const int first = two ? 128 * b : 0, rows = min(s.rows - first, 128);
+        constexpr int CH = D / 8;   // 16-byte pieces of a row
+        for (int c = lane; c < rows * CH; c += 32) {
+          const int row = c / CH, k = c % CH, n = s.n0 + first + row;
+          const int t = n / p.G, g = n - t * p.G;
+          cp_async16(Qs + b * L::UNIT + (k >> 3) * L::ATOM + (row >> 3) * 1024 + (row & 7) * 128 +
+                         (((k & 7) ^ (row & 7)) << 4),
+                     qg + (static_cast<size_t>(s.x.q0 + t) * p.hq + s.h * p.G + g) * D + k * 8);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[b]);
+      }
+      if (stop) break;
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------------------------------------- issuer
+    // Whichever product of either stream has its operands: S of a stream's next tile once its P . V is issued
+    // (they share tensor memory, and the tensor core works in order), P . V once P is written.
+    if (lane == 0) {
+      int t[2] = {0, 0}, done[2] = {0, 0}, released = 0;   // tile, products finished; tiles given back
+      bool pv[2] = {false, false}, over[2] = {false, false}, looked[2] = {false, false};
+      TileInfo cur[2];
+      const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
+      uint32_t idle = 0;
+      while (!(over[0] && over[1])) {
+        if (*abort_flag) break;
+        bool progressed = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (over[s]) continue;
+          const int o = 1 - s;
+          if (!looked[s]) {
+            if (!mbar_test(&mfull[t[s] % kMeta], (t[s] / kMeta) & 1)) continue;
+            cur[s] = info[t[s] % kMeta];
+            looked[s] = true;
+            progressed = true;
+            if (!(cur[s].flags & kValid)) {
+              over[s] = true;
+              continue;
+            }
+          }
+          const TileInfo &m = cur[s];
+          const bool two = (m.flags & kTwo) != 0;
+          const int ku = 2 * t[s], vu = ku + 1;
+          if (!two && (m.idx & 1) != s) {   // the other stream's
+            ++t[s];
+            looked[s] = false;
+            progressed = true;
+          } else if (!pv[s]) {
+            const int b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
+            if (mbar_test(&qfull[b], (m.flags / kQpar >> b) & 1) && mbar_test(&full[ku % NU], (ku / NU) & 1)) {
+              tc_fence_after();
+              const uint32_t qa = smem_u32(Qs + b * L::UNIT), ka = smem_u32(ring + (ku % NU) * L::UNIT);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * L::ATOM + (kk & 3) * 32;
+                umma_bf16(tmem + 128 * s, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka + off, 16, 1024, 2), idesc_s,
+                          kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&sfull[s]);
+              if (!two || t[o] > t[s] || (t[o] == t[s] && pv[o])) umma_commit(&empty[ku % NU]);
+              // this stream's last use of its queries; a buffer counts two
+              if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {
+                umma_commit(&qempty[b]);
+                if (two || m.n == 1) umma_commit(&qempty[b]);
+              }
+              pv[s] = true;
+              progressed = true;
+            }
+          } else if (mbar_test(&pfull[s], done[s] & 1) && mbar_test(&full[vu % NU], (vu / NU) & 1)) {
+            tc_fence_after();
+            const uint32_t va = smem_u32(ring + (vu % NU) * L::UNIT);
+            const bool fresh = two ? m.idx == 0 : m.idx < 2;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, smem_desc(va + kk * 2048, L::ATOM, 1024, 2),
+                           idesc_o, (kk > 0 || !fresh) ? 1u : 0u);
+            umma_commit(&ofull[s]);
+            if (!two || t[o] > t[s]) umma_commit(&empty[vu % NU]);
+            ++done[s];
+            pv[s] = false;
+            looked[s] = false;
+            ++t[s];
+            progressed = true;
+          }
+        }
+        while (released < min(t[0], t[1])) {
+          mbar_arrive(&mfree[released % kMeta]);
+          ++released;
+        }
+        if (progressed) {
+          idle = 0;
+        } else if (++idle > kSpinPolls) {
+          set_error(p.err, kErrTimeout);
+          *abort_flag = 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------------------------------------ softmax
+    const int s = warp >> 2, wq = warp & 3;
+    const int trow = wq * 32 + lane;   // row of the stream's 128
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lanes + 128 * s;
+    const float scale2 = rsqrtf(static_cast<float>(D)) * kLog2e;
+    float m = -INFINITY, l = 0.0f;
+    int cnt = 0, had = 0, joins = 0;
+    for (int ti = 0;; ++ti) {
+      const int mi = ti % kMeta;
+      if (!wait(&mfull[mi], ti / kMeta)) break;
+      const TileInfo f = info[mi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mfree[mi]);
+      if (!(f.flags & kValid)) break;
+      if (f.flags & kFirst) {
+        m = -INFINITY;
+        l = 0.0f;
+        had = 0;
+      }
+      const bool two = (f.flags & kTwo) != 0;
+      const int ntok = f.tp & 0xff, pages = f.tp >> 8;
+      const int base = two ? 128 * s : 0;
+      const bool active = base + wq * 32 < f.rows;
+      if (two || (f.idx & 1) == s) {
+        if (!wait(&sfull[s], cnt)) break;
+        tc_fence_after();
+        if (active) {
+          const bool whole = ntok == kTileTok && pages == 0xff;
+          auto hide = [&](float *x, int c) {   // columns c .. c + 31: tokens past the end or on no page
+            if (whole) return;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i >= ntok || !((pages >> ((c + i) / kPage)) & 1)) x[i] = -INFINITY;
+          };
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            float x[32];
+            tmem_ld32(tS + c, x);
+            tmem_wait_ld();
+            hide(x, c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
+          }
+          mx *= scale2;
+          if (had == 0) {
+            m = mx;
+          } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
+            const float mn = fmaxf(m, mx);
+            const float a = m == -INFINITY ? 0.0f : exp2f(m - mn);
+            l *= a;
+            m = mn;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float x[32];
+              tmem_ld32(tmem + lanes + 256 + 128 * s + c, x);
+              tmem_wait_ld();
+              uint32_t y[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[i] * a);
+              tmem_st16(tmem + lanes + 256 + 128 * s + c, y);
+              tmem_st16(tmem + lanes + 256 + 128 * s + c + 16, y + 16);
+            }
+          }
+          const float ms = m == -INFINITY ? 0.0f : m;
+          float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            float x[32];
+            tmem_ld32(tS + c, x);
+            tmem_wait_ld();
+            hide(x, c);
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float a = fast_exp2(fmaf(x[2 * i], scale2, -ms)), b = fast_exp2(fmaf(x[2 * i + 1], scale2, -ms));
+              l0 += a;
+              l1 += b;
+              const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
+              y[i] = *reinterpret_cast<const uint32_t *>(&q);
+            }
+            tmem_st16(tS + c / 2, y);
+          }
+          l += l0 + l1;
+          tmem_wait_st();
+        }
+        if (ntok % kPage) {   // rows of the last page past the end: their weights are zero, their values may be anything
+          const int vu = 2 * ti + 1;
+          if (!wait(&full[vu % NU], vu / NU)) break;
+          unsigned char *v = ring + (vu % NU) * L::UNIT;
+          const int rows = kPage - ntok % kPage;
+          for (int c = wq * 32 + lane; c < rows * (D / 8); c += 128) {
+            const int row = ntok + c / (D / 8), k = c % (D / 8);
+            *reinterpret_cast<uint4 *>(v + (k >> 3) * L::ATOM + row * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[s]);
+        ++cnt;
+        had = 1;
+      }
+      if (!(f.flags & kLast)) continue;
+      const int kind = (f.flags & kKind) ? 1 : 0;
+      const bool later = (f.flags & kLater) != 0;
+      if (had && !wait(&ofull[s], cnt - 1)) break;
+      tc_fence_after();
+      Entry x;
+      x.q0 = f.q0;
+      if (two) {
+        const int row = base + trow;
+        const bool mine = row < f.rows;
+        const Place pp = place<D>(p, x, kind, f.h, f.n0 + min(row, f.rows - 1), later, blockIdx.x);
+        if (mine) *pp.ml = make_float2(m, l);
+        if (active) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tmem + lanes + 256 + 128 * s + c, o);
+            tmem_wait_ld();
+            if (mine)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(pp.o + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        tc_fence_before();
+      } else {
+        // the two streams' sums of the same rows: each joins half of the columns
+        xm[s * 128 + trow] = m;
+        if (s == 1) xm[256 + trow] = l;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xready);
+        if (!wait(xready, joins)) break;
+        tc_fence_after();
+        const float m0 = xm[trow], m1 = xm[128 + trow], l1 = xm[256 + trow];
+        const float M = fmaxf(m0, m1);
+        // a stream that saw no token adds nothing (one that saw only NaN has no maximum either, but a sum)
+        const bool none0 = m0 == -INFINITY, none1 = m1 == -INFINITY;
+        const float w0 = none0 ? 0.0f : exp2f(m0 - M), w1 = none1 ? 0.0f : exp2f(m1 - M);
+        const bool mine = trow < f.rows;
+        const Place pp = place<D>(p, x, kind, f.h, f.n0 + min(trow, f.rows - 1), later, blockIdx.x);
+        if (mine && s == 0) *pp.ml = make_float2(M, l * w0 + l1 * w1);
+        if (active) {
+#pragma unroll 1
+          for (int c = s * (D / 2); c < (s + 1) * (D / 2); c += 32) {
+            float o0[32], o1[32];
+            tmem_ld32(tmem + lanes + 256 + c, o0);
+            tmem_ld32(tmem + lanes + 384 + c, o1);
+            tmem_wait_ld();
+            if (mine)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[k] = (none0 ? 0.0f : o0[i + k] * w0) + (none1 ? 0.0f : o1[i + k] * w1);
+                *reinterpret_cast<float4 *>(pp.o + c + i) = make_float4(r[0], r[1], r[2], r[3]);
+              }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xdone);
+        if (!wait(xdone, joins)) break;
+        tc_fence_after();
+        ++joins;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
 // --------------------------------------------------------------------------------------------- joining the records
 // One warp a query row: its records of the prefix and of the own context, and the window's tokens up to itself.
 template <class T, int D>
@@ -312,7 +856,7 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.0f;
   auto join = [&](float2 ml, const float *rec) {
-    if (!(ml.y > 0.0f) && ml.x == -INFINITY) return;
+    if (ml.y == 0.0f && ml.x == -INFINITY) return;
     const float mn = fmaxf(m, ml.x);
     const float a = m == -INFINITY ? 0.0f : exp2f(m - mn), b = exp2f(ml.x - mn);
     l = fmaf(l, a, ml.y * b);
@@ -376,6 +920,30 @@ template <class T, int D> cudaError_t launch_join(const HParams &p, cudaStream_t
   return launch_pdl(shared_join_kernel<T, D>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, s, p);
 }
 
+template <class T, int D> cudaError_t launch_plain(HParams p, cudaStream_t s) {
+  p.block = kPlainRows;
+  const cudaError_t e = launch_pdl(shared_plain_kernel<T, D>, dim3(p.nb), dim3(kPlainThreads), 0, s, p);
+  return e == cudaSuccess ? launch_join<T, D>(p, s) : e;
+}
+
+template <int D> cudaError_t launch_tc(const PoolArgs &pa, HParams p, cudaStream_t s) {
+  p.block = kTcBlock;
+  CUtensorMap tmK, tmV;
+  if (!make_pool_map(&tmK, pa.k, pa.num_pages, pa.hkv, D) || !make_pool_map(&tmV, pa.v, pa.num_pages, pa.hkv, D))
+    return cudaErrorInvalidValue;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!attr_set[dev & 63]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(shared_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::ALLOC);
+    if (e != cudaSuccess) return e;
+    attr_set[dev & 63] = true;
+  }
+  const cudaError_t e = launch_pdl(shared_tc_kernel<D>, dim3(p.nb), dim3(kTcThreads), Tc<D>::ALLOC, s, tmK, tmV, p);
+  return e == cudaSuccess ? launch_join<__nv_bfloat16, D>(p, s) : e;
+}
+
 }  // namespace
 
 size_t shared_workspace_bytes(int R, int hkv, int hq, int d, int total_q, int num_groups) {
@@ -422,19 +990,8 @@ cudaError_t launch_verify_shared(const PoolArgs &pa, const MapArgs &ma, int tota
   p.xml = reinterpret_cast<float2 *>(take(static_cast<size_t>(kMaxCtas) * kMaxBlock * 8));
   p.xo = reinterpret_cast<float *>(take(static_cast<size_t>(kMaxCtas) * kMaxBlock * pa.d * 4));
   p.nb = std::min(device_sm_count(), kMaxCtas);
-  p.block = kPlainRows;
-  cudaError_t e;
-#define KAP_SHARED(T, D)                                                                                     \
-  do {                                                                                                       \
-    e = launch_pdl(shared_plain_kernel<T, D>, dim3(p.nb), dim3(kPlainThreads), 0, s, p);                     \
-    if (e == cudaSuccess) e = launch_join<T, D>(p, s);                                                       \
-  } while (0)
-  if (pa.dtype == 0 && pa.d == 128) KAP_SHARED(__nv_bfloat16, 128);
-  else if (pa.dtype == 0) KAP_SHARED(__nv_bfloat16, 64);
-  else if (pa.d == 128) KAP_SHARED(float, 128);
-  else KAP_SHARED(float, 64);
-#undef KAP_SHARED
-  return e;
+  if (pa.dtype == 0) return pa.d == 128 ? launch_tc<128>(pa, p, s) : launch_tc<64>(pa, p, s);
+  return pa.d == 128 ? launch_plain<float, 128>(p, s) : launch_plain<float, 64>(p, s);
 }
 
 }  // namespace kap

@@ -15,8 +15,8 @@
 // Other shapes (fp32 pools, head_dim 64) use a plain FFMA kernel, one warp per (query row, query head).
 #include "kap_device.cuh"
 #include "kap_launch.h"
+#include "kap_tma.h"
 
-#include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -919,12 +919,13 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
-// 2-D view [num_pages * Hkv * 16 rows][128 columns] of a bf16 pool; boxes of 64 columns x 16 rows, 128B swizzle.
-bool make_pool_map(CUtensorMap *map, const void *base, int num_pages, int hkv) {
+}  // namespace
+
+bool make_pool_map(CUtensorMap *map, const void *base, int num_pages, int hkv, int d) {
   auto enc = get_encode();
   if (!enc) return false;
-  cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(num_pages) * hkv * kPage};
-  cuuint64_t strides[1] = {128 * 2};
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(num_pages) * hkv * kPage};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
   cuuint32_t box[2] = {64, 16};
   cuuint32_t estr[2] = {1, 1};
   CUresult rc = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
@@ -933,12 +934,14 @@ bool make_pool_map(CUtensorMap *map, const void *base, int num_pages, int hkv) {
   return rc == CUDA_SUCCESS;
 }
 
+namespace {
+
 template <int NPMAX>
 cudaError_t launch_tc(const PoolArgs &pa, const VParams &prm, cudaStream_t s) {
   using L = TcSmem<NPMAX>;
   static_assert(L::ALLOC <= 227 * 1024, "shared memory over the per-CTA limit");
   CUtensorMap tmK, tmV;
-  if (!make_pool_map(&tmK, pa.k, pa.num_pages, pa.hkv) || !make_pool_map(&tmV, pa.v, pa.num_pages, pa.hkv))
+  if (!make_pool_map(&tmK, pa.k, pa.num_pages, pa.hkv, 128) || !make_pool_map(&tmV, pa.v, pa.num_pages, pa.hkv, 128))
     return cudaErrorInvalidValue;
   static bool attr_set[64] = {false};
   int dev = 0;

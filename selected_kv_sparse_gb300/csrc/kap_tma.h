@@ -1,0 +1,11 @@
+// kap_tma.h - tensor maps of the KV pool for tiled TMA loads (internal to the library).
+#pragma once
+
+#include <cuda.h>
+
+namespace kap {
+
+// 2-D view [num_pages * Hkv * 16 rows][d columns] of a bf16 pool; boxes of 64 columns x 16 rows, 128-byte swizzle.
+bool make_pool_map(CUtensorMap *map, const void *base, int num_pages, int hkv, int d);
+
+}  // namespace kap
