@@ -28,6 +28,7 @@ constexpr int kTilePages = 8, kTileTok = kTilePages * kPage;
 constexpr int kMaxCtas = 192;      // CTAs of the first kernel at most
 constexpr int kMaxBlock = 256;     // rows of an item's block at most
 constexpr int kSmemGroups = 1024;  // group offsets kept in shared memory
+constexpr int kItemCost = 2;       // what starting and ending an item costs, in tiles: counted when work is shared out
 constexpr int kPlainThreads = 256, kPlainRows = 32;
 
 struct HParams {
@@ -54,6 +55,8 @@ struct Entry {
   int req;            // the request whose table row names the pages
   int page0, tok0, tok1;  // first page, and the tokens [tok0, tok1) (tok0 = 16 page0)
   int tiles, blocks;  // 128-token tiles; blocks of rows
+  int span;           // a block's length in the line that is shared out: kItemCost and then its tiles
+  __device__ __forceinline__ int64_t length(int hkv) const { return static_cast<int64_t>(span) * blocks * hkv; }
 };
 
 struct Groups {
@@ -103,6 +106,7 @@ __device__ __forceinline__ Entry entry(const HParams &p, const Groups &gr, int e
   x.tok0 = x.page0 * kPage;
   x.tiles = x.rows > 0 && x.tok1 > x.tok0 ? (x.tok1 - x.tok0 + kTileTok - 1) / kTileTok : 0;
   x.blocks = (x.rows + p.block - 1) / p.block;
+  x.span = x.tiles > 0 ? x.tiles + kItemCost : 0;
   return x;
 }
 
@@ -111,28 +115,35 @@ __device__ __forceinline__ int owner_cta(int64_t x, int64_t E, int nb) {
 }
 
 struct Plan {
-  int64_t total, begin, end;  // tiles in all, and this CTA's
-  int nb;                     // CTAs with tiles
-  int entry;                  // the entry that `begin` lies in, and its first tile
+  int64_t total, begin, end;  // the line's length, and this CTA's part of it
+  int nb;                     // CTAs with a part
+  int entry;                  // the entry that `begin` lies in, and where it starts
   int64_t entry_start;
+  Entry x;                    // that entry
+};
+struct PlanSlots {
+  int64_t total, base, entry, first;
+  Entry x;
 };
 
 // Every thread of the block takes part; the block has at most 32 warps.
-__device__ inline Plan make_plan(const HParams &p, const Groups &gr, int64_t *scratch, int64_t *slot) {
+__device__ inline Plan make_plan(const HParams &p, const Groups &gr, int64_t *scratch, PlanSlots *slot) {
   const int n = p.num_groups + p.R, tid = threadIdx.x, nt = blockDim.x;
+  Entry x{};
   auto count = [&](int e) -> int64_t {
     if (e >= n) return 0;
-    const Entry x = entry(p, gr, e);
-    return static_cast<int64_t>(x.tiles) * x.blocks * p.hkv;
+    x = entry(p, gr, e);
+    return x.length(p.hkv);
   };
   const int64_t mine = count(tid);
+  const Entry x0 = x;
   int64_t sum = mine;
   for (int e = tid + nt; e < n; e += nt) sum += count(e);
   const int64_t incl = block_inclusive_scan(sum, scratch);
-  if (tid == nt - 1) slot[0] = incl;
+  if (tid == nt - 1) slot->total = incl;
   __syncthreads();
   Plan pl;
-  pl.total = slot[0];
+  pl.total = slot->total;
   pl.nb = static_cast<int>(min(pl.total, static_cast<int64_t>(p.nb)));
   pl.begin = pl.end = 0;
   pl.entry = 0;
@@ -150,19 +161,21 @@ __device__ inline Plan make_plan(const HParams &p, const Groups &gr, int64_t *sc
     const int64_t inc = block_inclusive_scan(c, scratch);
     const int64_t first = base + inc - c;
     if (works && first <= pl.begin && pl.begin < first + c) {
-      slot[1] = e;
-      slot[2] = first;
+      slot->entry = e;
+      slot->first = first;
+      slot->x = e0 == 0 ? x0 : x;
     }
     if (writer && e < n) p.start[e] = first;
-    if (tid == nt - 1) slot[3] = base + inc;
+    if (tid == nt - 1) slot->base = base + inc;
     __syncthreads();
-    base = slot[3];
+    base = slot->base;
     __syncthreads();
   }
   if (writer && tid == 0) p.start[n] = pl.total;
   if (works) {
-    pl.entry = static_cast<int>(slot[1]);
-    pl.entry_start = slot[2];
+    pl.entry = static_cast<int>(slot->entry);
+    pl.entry_start = slot->first;
+    pl.x = slot->x;
   }
   return pl;
 }
@@ -198,38 +211,68 @@ __device__ __forceinline__ Place place(const HParams &p, const Entry &x, int kin
   return Place{p.ml[kind] + i, p.o[kind] + i * D};
 }
 
+// The segments of a CTA's part, in order: runs of tiles of one (item, block of rows).
+struct Segment {
+  Entry x;
+  int e, h, n0, rows, t0, n;  // tiles [t0, t0 + n) of the block's
+};
+struct Walker {
+  const HParams &p;
+  const Groups gr;
+  int64_t at, end, es;
+  int e, have;
+  Entry x;
+  __device__ __forceinline__ Walker(const HParams &p_, const Plan &pl)
+      : p(p_), gr{p_.group_off}, at(pl.begin), end(pl.end), es(pl.entry_start), e(pl.entry), have(pl.entry), x(pl.x) {}
+  __device__ __forceinline__ bool next(Segment &s) {
+    while (at < end) {
+      if (have != e) {
+        x = entry(p, gr, e);
+        have = e;
+      }
+      const int64_t size = x.length(p.hkv);
+      if (at >= es + size) {
+        es += size;
+        ++e;
+        continue;
+      }
+      const int sub = static_cast<int>((at - es) / x.span);
+      const int from = static_cast<int>(at - es - static_cast<int64_t>(sub) * x.span);
+      const int to = static_cast<int>(min(static_cast<int64_t>(x.span), from + (end - at)));
+      at += to - from;
+      s.t0 = max(from - kItemCost, 0);
+      s.n = to - kItemCost - s.t0;
+      if (s.n <= 0) continue;   // no more than the item's start
+      s.x = x;
+      s.e = e;
+      s.h = sub / x.blocks;
+      s.n0 = (sub - s.h * x.blocks) * p.block;
+      s.rows = min(x.rows - s.n0, p.block);
+      return true;
+    }
+    return false;
+  }
+};
+
 // ------------------------------------------------------------------------------------------------- plain arithmetic
 // fp32 pools: a warp takes every eighth row of a block of 32 and all tokens of a tile, a lane every 32nd dim.
 template <class T, int D>
 __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HParams p) {
   constexpr int PL = D / 32, RW = kPlainRows / (kPlainThreads / 32);
   __shared__ int32_t s_off[kSmemGroups + 1];
-  __shared__ int64_t s_scratch[32], s_slot[4];
+  __shared__ int64_t s_scratch[32];
+  __shared__ PlanSlots s_slot;
   grid_dependency_sync();
   const Groups gr = load_groups(p, s_off);
   check_groups(p, gr);
-  const Plan pl = make_plan(p, gr, s_scratch, s_slot);
+  const Plan pl = make_plan(p, gr, s_scratch, &s_slot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float scale = rsqrtf(static_cast<float>(D)) * kLog2e;
-  int e = pl.entry;
-  int64_t es = pl.entry_start;
-  Entry x{};
-  int have = -1;
-  for (int64_t at = pl.begin; at < pl.end;) {
-    if (have != e) {
-      x = entry(p, gr, e);
-      have = e;
-    }
-    const int64_t size = static_cast<int64_t>(x.tiles) * x.blocks * p.hkv;
-    if (at >= es + size) {
-      es += size;
-      ++e;
-      continue;
-    }
-    const int sub = static_cast<int>((at - es) / x.tiles);
-    const int t0 = static_cast<int>(at - es - static_cast<int64_t>(sub) * x.tiles);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(x.tiles), t0 + pl.end - at));
-    const int h = sub / x.blocks, n0 = (sub - h * x.blocks) * p.block;
+  Walker walk(p, pl);
+  Segment sg;
+  while (walk.next(sg)) {
+    const Entry &x = sg.x;
+    const int h = sg.h, n0 = sg.n0, t0 = sg.t0, t1 = sg.t0 + sg.n;
     float qv[RW][PL], ov[RW][PL], m[RW], l[RW];
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
@@ -278,13 +321,12 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
     for (int i = 0; i < RW; ++i) {
       const int n = n0 + warp + i * (kPlainThreads / 32);
       if (n < min(x.rows, n0 + p.block)) {
-        const Place pp = place<D>(p, x, e < p.num_groups ? 0 : 1, h, n, t0 > 0, blockIdx.x);
+        const Place pp = place<D>(p, x, sg.e < p.num_groups ? 0 : 1, h, n, t0 > 0, blockIdx.x);
         if (lane == 0) *pp.ml = make_float2(m[i], l[i]);
 #pragma unroll
         for (int k = 0; k < PL; ++k) pp.o[lane + 32 * k] = ov[i][k];
       }
     }
-    at += t1 - t0;
   }
 }
 
@@ -294,8 +336,8 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
 // MN-major from shared memory). Two streams of softmax warps, each with an S and an O, take turns at the tensor core:
 // an item's block of up to 128 rows gives its even tiles to one and its odd tiles to the other and joins the two at the
 // end; a block of up to 256 rows gives each stream 128 of them, and both read every tile.
-// Warps: 0-3 and 4-7 the streams' softmax (thread = row), 8 K pages and tile records, 9 tcgen05 issuer, 10 V pages,
-// 11 queries. K and V tiles share a ring. Every wait is bounded, and no role waits on a block-wide barrier.
+// Warps: 0-3 and 4-7 the streams' softmax (thread = row), 8 K and V pages and tile records, 9 queries, 10 and 11 the
+// streams' tcgen05 issuers. K and V tiles share a ring. Every wait is bounded, and no role waits on a block-wide barrier.
 constexpr int kTcThreads = 384;
 constexpr int kTcBlock = 256;
 constexpr float kRescale = 8.0f;  // log2: the reference of a row's weights follows its maximum when 2^8 behind
@@ -329,6 +371,11 @@ __device__ __forceinline__ float fast_exp2(float x) {  // relative error about 2
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
   uint32_t r[32];
@@ -366,44 +413,6 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// The segments of a CTA's tiles, in order: runs of tiles of one (item, block of rows).
-struct Segment {
-  Entry x;
-  int e, h, n0, rows, t0, n;  // tiles [t0, t0 + n) of the block's
-};
-struct Walker {
-  const HParams &p;
-  const Groups gr;
-  int64_t at, end, es;
-  int e, have;
-  Entry x;
-  __device__ __forceinline__ Walker(const HParams &p_, const Plan &pl)
-      : p(p_), gr{p_.group_off}, at(pl.begin), end(pl.end), es(pl.entry_start), e(pl.entry), have(-1) {}
-  __device__ __forceinline__ bool next(Segment &s) {
-    if (at >= end) return false;
-    while (true) {
-      if (have != e) {
-        x = entry(p, gr, e);
-        have = e;
-      }
-      const int64_t size = static_cast<int64_t>(x.tiles) * x.blocks * p.hkv;
-      if (at < es + size) break;
-      es += size;
-      ++e;
-    }
-    const int sub = static_cast<int>((at - es) / x.tiles);
-    s.x = x;
-    s.e = e;
-    s.t0 = static_cast<int>(at - es - static_cast<int64_t>(sub) * x.tiles);
-    s.n = static_cast<int>(min(static_cast<int64_t>(x.tiles - s.t0), end - at));
-    s.h = sub / x.blocks;
-    s.n0 = (sub - s.h * x.blocks) * p.block;
-    s.rows = min(x.rows - s.n0, p.block);
-    at += s.n;
-    return true;
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const HParams p) {
@@ -423,18 +432,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ int s_abort;
   volatile int *abort_flag = &s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dependency_sync();
-
-  // the plan's scratch lies where the ring will be
-  int64_t *scratch = reinterpret_cast<int64_t *>(ring);
-  const Groups gs = load_groups(p, reinterpret_cast<int32_t *>(ring + 512));
-  check_groups(p, gs);
-  const Plan pl = make_plan(p, gs, scratch, scratch + 40);
-  if (pl.begin >= pl.end) return;   // the whole CTA
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < L::NBAR; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < kMeta; ++i) mbar_init(&mfree[i], 9);  // 8 softmax warps and the issuer
+    for (int i = 0; i < kMeta; ++i) mbar_init(&mfree[i], 10);  // 8 softmax warps and the issuers
+    for (int i = 0; i < NU; ++i) mbar_init(&empty[i], 2);      // one of each stream, or two of the stream that used it
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qempty[i], 2);
       mbar_init(&pfull[i], 4);
@@ -442,15 +444,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(xready, 8);
     mbar_init(xdone, 8);
     fence_barrier_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_sync();
+
+  // the plan's scratch lies where the ring will be
+  const Groups gs = load_groups(p, reinterpret_cast<int32_t *>(ring + 512));
+  check_groups(p, gs);
+  const Plan pl = make_plan(p, gs, reinterpret_cast<int64_t *>(ring), reinterpret_cast<PlanSlots *>(ring + 256));
+  fence_proxy_async_smem();
+  __syncthreads();
   const uint32_t tmem = *tmem_slot;   // S of stream s at column 128 s, O at 256 + 128 s
 
   auto wait = [&](uint64_t *bar, int phase) -> bool {   // the whole warp
@@ -460,45 +471,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return false;
   };
 
-  if (warp == 8 || warp == 10) {
+  if (warp == 8) {
     // ------------------------------------------------------------------------------------------------ pages
-    const bool keys = warp == 8;
     Walker walk(p, pl);
     Segment s{};
-    int u = 0, i = 0, seg = -1, uses[2] = {0, 0}, qflags = 0;
+    int u = 0, i = 0, seg = -1, uses[2] = {0, 0}, qflags = 0;   // u: the unit of the ring, tile u / 2's keys or values
     bool more = walk.next(s);
-    int page = -1;
+    int page = -1, next_page = -1;
     auto fetch = [&](const Segment &g, int k) {   // this lane's page of tile k of the segment
       const int j = g.x.page0 + (g.t0 + k) * kTilePages + lane;
-      page = lane < kTilePages && j < p.max_pages && j * kPage < g.x.tok1
-                 ? p.bt[static_cast<size_t>(g.x.req) * p.max_pages + j] : -1;
+      next_page = lane < kTilePages && j < p.max_pages && j * kPage < g.x.tok1
+                      ? p.bt[static_cast<size_t>(g.x.req) * p.max_pages + j] : -1;
     };
     if (more) fetch(s, 0);
     for (;; ++u) {
-      const int un = 2 * u + (keys ? 0 : 1), st = un % NU, mi = u % kMeta;
-      if (un >= NU && !wait(&empty[st], un / NU - 1)) break;
-      if (keys && u >= kMeta && !wait(&mfree[mi], u / kMeta - 1)) break;
+      const int st = u % NU, mi = (u >> 1) % kMeta;
+      const bool keys = (u & 1) == 0;
+      if (keys && u >= 2 * kMeta && !wait(&mfree[mi], (u >> 1) / kMeta - 1)) break;
       if (!more) {
-        if (keys && lane == 0) {
+        if (lane == 0) {
           info[mi].flags = 0;
           mbar_arrive(&mfull[mi]);
         }
         break;
       }
+      if (u >= NU && !wait(&empty[st], u / NU - 1)) break;
+      if (keys) page = next_page;
       const int tok = s.x.tok0 + (s.t0 + i) * kTileTok, ntok = min(kTileTok, s.x.tok1 - tok);
       const int npg = (ntok + kPage - 1) / kPage;
       const bool in = lane < npg, ok = in && page >= 0 && page < p.num_pages;
       if (in && !ok) set_error(p.err, kErrPage);
       const uint32_t pages = __ballot_sync(0xffffffffu, ok);
       unsigned char *dst = ring + st * L::UNIT;
-      if (!keys) {   // values that no copy brings must be finite: their weights are zero
+      if (!keys && pages != 0xff) {   // values that no copy brings must be finite: their weights are zero
         for (int j = 0; j < kTilePages; ++j)
           if (!((pages >> j) & 1))
             for (int c = lane; c < kPage * D / 8; c += 32) {
               const int half = c / (kPage * 8), w = c % (kPage * 8);
               *reinterpret_cast<uint4 *>(dst + half * L::ATOM + j * 2048 + w * 16) = make_uint4(0, 0, 0, 0);
             }
-        if (pages != 0xff) fence_proxy_async_smem();
+        fence_proxy_async_smem();
         __syncwarp();
       }
       if (keys && i == 0) {
@@ -511,10 +523,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (two || qbuf == 1) ++uses[1];
       }
       if (lane == 0) {
-        if (keys)
+        if (keys) {
           info[mi] = TileInfo{kValid | qflags | (i == 0 ? kFirst : 0) | (i == s.n - 1 ? kLast : 0), i, s.n,
                               ntok | (static_cast<int>(pages) << 8), s.h, s.n0, s.rows, s.x.q0};
-        if (keys) mbar_arrive(&mfull[mi]);
+          mbar_arrive(&mfull[mi]);
+        }
         mbar_arrive_expect_tx(&full[st], __popc(pages) * kPage * D * 2);
       }
       __syncwarp();
@@ -524,19 +537,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tma_load_2d(dst + lane * 2048, tm, 0, row0, &full[st]);
         if (D == 128) tma_load_2d(dst + L::ATOM + lane * 2048, tm, 64, row0, &full[st]);
       }
-      if (++i == s.n) {
+      if (keys) {   // the next tile's page ids are on their way while the values' turn comes
+        if (i + 1 < s.n) fetch(s, i + 1);
+      } else if (++i == s.n) {
         more = walk.next(s);
         i = 0;
+        if (more) fetch(s, 0);
       }
-      if (more) fetch(s, i);
     }
     // after an abort, copies in flight are waited for (bounded) before the CTA leaves
     if (*abort_flag)
-      for (int k = max(0, u - NU); k < u; ++k) {
-        const int un = 2 * k + (keys ? 0 : 1);
-        mbar_wait(&full[un % NU], (un / NU) & 1, nullptr);
-      }
-  } else if (warp == 11) {
+      for (int k = max(0, u - NU); k < u; ++k) mbar_wait(&full[k % NU], (k / NU) & 1, nullptr);
+  } else if (warp == 9) {
     // ------------------------------------------------------------------------------------------------ queries
     Walker walk(p, pl);
     Segment s;
@@ -568,91 +580,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (stop) break;
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------------------------------------- issuer
-    // Whichever product of either stream has its operands: S of a stream's next tile once its P . V is issued
-    // (they share tensor memory, and the tensor core works in order), P . V once P is written.
-    if (lane == 0) {
-      int t[2] = {0, 0}, done[2] = {0, 0}, released = 0;   // tile, products finished; tiles given back
-      bool pv[2] = {false, false}, over[2] = {false, false}, looked[2] = {false, false};
-      TileInfo cur[2];
-      const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
-      uint32_t idle = 0;
-      while (!(over[0] && over[1])) {
-        if (*abort_flag) break;
-        bool progressed = false;
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------------------------------------------ issuers
+    // S of the stream's next tile right behind P . V of its last (they share tensor memory, and what a thread issues
+    // is carried out in order), P . V once P is written. The whole warp waits, one lane issues.
+    const int s = warp - 10;
+    const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
+    int done = 0;
+    for (int t = 0;; ++t) {
+      const int mi = t % kMeta;
+      if (!wait(&mfull[mi], t / kMeta)) break;
+      const TileInfo m = info[mi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mfree[mi]);
+      if (!(m.flags & kValid)) break;
+      const bool two = (m.flags & kTwo) != 0;
+      if (!two && (m.idx & 1) != s) continue;   // the other stream's
+      const int ku = 2 * t, vu = ku + 1;
+      const int b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
+      if (!wait(&qfull[b], m.flags / kQpar >> b) || !wait(&full[ku % NU], ku / NU)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t qa = smem_u32(Qs + b * L::UNIT), ka = smem_u32(ring + (ku % NU) * L::UNIT);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (over[s]) continue;
-          const int o = 1 - s;
-          if (!looked[s]) {
-            if (!mbar_test(&mfull[t[s] % kMeta], (t[s] / kMeta) & 1)) continue;
-            cur[s] = info[t[s] % kMeta];
-            looked[s] = true;
-            progressed = true;
-            if (!(cur[s].flags & kValid)) {
-              over[s] = true;
-              continue;
-            }
-          }
-          const TileInfo &m = cur[s];
-          const bool two = (m.flags & kTwo) != 0;
-          const int ku = 2 * t[s], vu = ku + 1;
-          if (!two && (m.idx & 1) != s) {   // the other stream's
-            ++t[s];
-            looked[s] = false;
-            progressed = true;
-          } else if (!pv[s]) {
-            const int b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
-            if (mbar_test(&qfull[b], (m.flags / kQpar >> b) & 1) && mbar_test(&full[ku % NU], (ku / NU) & 1)) {
-              tc_fence_after();
-              const uint32_t qa = smem_u32(Qs + b * L::UNIT), ka = smem_u32(ring + (ku % NU) * L::UNIT);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * L::ATOM + (kk & 3) * 32;
-                umma_bf16(tmem + 128 * s, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka + off, 16, 1024, 2), idesc_s,
-                          kk > 0 ? 1u : 0u);
-              }
-              umma_commit(&sfull[s]);
-              if (!two || t[o] > t[s] || (t[o] == t[s] && pv[o])) umma_commit(&empty[ku % NU]);
-              // this stream's last use of its queries; a buffer counts two
-              if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {
-                umma_commit(&qempty[b]);
-                if (two || m.n == 1) umma_commit(&qempty[b]);
-              }
-              pv[s] = true;
-              progressed = true;
-            }
-          } else if (mbar_test(&pfull[s], done[s] & 1) && mbar_test(&full[vu % NU], (vu / NU) & 1)) {
-            tc_fence_after();
-            const uint32_t va = smem_u32(ring + (vu % NU) * L::UNIT);
-            const bool fresh = two ? m.idx == 0 : m.idx < 2;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, smem_desc(va + kk * 2048, L::ATOM, 1024, 2),
-                           idesc_o, (kk > 0 || !fresh) ? 1u : 0u);
-            umma_commit(&ofull[s]);
-            if (!two || t[o] > t[s]) umma_commit(&empty[vu % NU]);
-            ++done[s];
-            pv[s] = false;
-            looked[s] = false;
-            ++t[s];
-            progressed = true;
-          }
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * L::ATOM + (kk & 3) * 32;
+          umma_bf16(tmem + 128 * s, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka + off, 16, 1024, 2), idesc_s,
+                    kk > 0 ? 1u : 0u);
         }
-        while (released < min(t[0], t[1])) {
-          mbar_arrive(&mfree[released % kMeta]);
-          ++released;
-        }
-        if (progressed) {
-          idle = 0;
-        } else if (++idle > kSpinPolls) {
-          set_error(p.err, kErrTimeout);
-          *abort_flag = 1;
+        umma_commit(&sfull[s]);
+        umma_commit(&empty[ku % NU]);
+        if (!two) umma_commit(&empty[ku % NU]);
+        // this stream's last use of its queries; a buffer counts two
+        if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {
+          umma_commit(&qempty[b]);
+          if (two || m.n == 1) umma_commit(&qempty[b]);
         }
       }
+      __syncwarp();
+      if (!wait(&full[vu % NU], vu / NU) || !wait(&pfull[s], done)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t va = smem_u32(ring + (vu % NU) * L::UNIT);
+        const bool fresh = two ? m.idx == 0 : m.idx < 2;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, smem_desc(va + kk * 2048, L::ATOM, 1024, 2),
+                       idesc_o, (kk > 0 || !fresh) ? 1u : 0u);
+        umma_commit(&ofull[s]);
+        umma_commit(&empty[vu % NU]);
+        if (!two) umma_commit(&empty[vu % NU]);
+      }
+      __syncwarp();
+      ++done;
     }
-    __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------------------------------------------ softmax
     const int s = warp >> 2, wq = warp & 3;
@@ -690,14 +671,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (c + i >= ntok || !((pages >> ((c + i) / kPage)) & 1)) x[i] = -INFINITY;
           };
           float mx = -INFINITY;
+          {
+            float x[2][32];   // the next 32 columns are on their way while these are looked at
+            tmem_ld32(tS, x[0]);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            float x[32];
-            tmem_ld32(tS + c, x);
-            tmem_wait_ld();
-            hide(x, c);
+            for (int c = 0; c < 4; ++c) {
+              tmem_wait_ld();
+              if (c < 3) tmem_ld32(tS + 32 * c + 32, x[(c + 1) & 1]);
+              hide(x[c & 1], 32 * c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
+              for (int i = 0; i < 32; i += 2) mx = max3(mx, x[c & 1][i], x[c & 1][i + 1]);
+            }
           }
           mx *= scale2;
           if (had == 0) {
@@ -720,24 +704,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           const float ms = m == -INFINITY ? 0.0f : m;
-          float l0 = 0.0f, l1 = 0.0f;
+          F2 sum = f2(0.0f, 0.0f);
+          const F2 sc = f2(scale2, scale2), sub = f2(-ms, -ms);
+          float x[2][32];
+          tmem_ld32(tS, x[0]);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            float x[32];
-            tmem_ld32(tS + c, x);
+          for (int c = 0; c < 4; ++c) {
             tmem_wait_ld();
-            hide(x, c);
+            if (c < 3) tmem_ld32(tS + 32 * c + 32, x[(c + 1) & 1]);
+            hide(x[c & 1], 32 * c);
             uint32_t y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float a = fast_exp2(fmaf(x[2 * i], scale2, -ms)), b = fast_exp2(fmaf(x[2 * i + 1], scale2, -ms));
-              l0 += a;
-              l1 += b;
+              float a, b;
+              split(fma2(f2(x[c & 1][2 * i], x[c & 1][2 * i + 1]), sc, sub), a, b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              sum = add2(sum, f2(a, b));
               const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
               y[i] = *reinterpret_cast<const uint32_t *>(&q);
             }
-            tmem_st16(tS + c / 2, y);
+            tmem_st16(tS + 16 * c, y);
           }
+          float l0, l1;
+          split(sum, l0, l1);
           l += l0 + l1;
           tmem_wait_st();
         }
@@ -832,79 +822,132 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // --------------------------------------------------------------------------------------------- joining the records
-// One warp a query row: its records of the prefix and of the own context, and the window's tokens up to itself.
+// The last i in [0, n) with a[i] <= key (0 if there is none), by the whole warp: 32 places at a time.
+__device__ __forceinline__ int find_last(const int32_t *a, int n, int key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;   // the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && a[min(at, hi - 1)] <= key);
+    const int k = le ? 31 - __clz(le) : 0;   // rising entries: the lanes up to k
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// One warp a query row: the window's tokens up to itself, and its records of the prefix and of the own context. All but
+// the records is older than the first kernel, so it is done before that kernel's end is waited for.
 template <class T, int D>
 __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
   constexpr int PL = D / 32;  // consecutive dims of a lane
-  grid_dependency_sync();
+  constexpr int CH = 8;       // records whose loads are in flight together
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (wid >= static_cast<int64_t>(p.total_q) * p.hq) return;
-  const int t = static_cast<int>(wid / p.hq), hq = static_cast<int>(wid - static_cast<int64_t>(t) * p.hq);
-  const int h = hq / p.G;
-  int lo = 0, hi = p.R;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_offsets[mid] <= t) lo = mid; else hi = mid;
-  }
-  const int r = lo;
-  const Groups gr{p.group_off};
-  const int n = p.num_groups + p.R;
-  const int64_t total = p.start[n];
-  const int nb = static_cast<int>(min(total, static_cast<int64_t>(p.nb)));
+  const bool live = wid < static_cast<int64_t>(p.total_q) * p.hq;
   float m = -INFINITY, l = 0.0f, o[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.0f;
-  auto join = [&](float2 ml, const float *rec) {
-    if (ml.y == 0.0f && ml.x == -INFINITY) return;
-    const float mn = fmaxf(m, ml.x);
-    const float a = m == -INFINITY ? 0.0f : exp2f(m - mn), b = exp2f(ml.x - mn);
-    l = fmaf(l, a, ml.y * b);
+  int t = 0, hq = 0, h = 0, ent[2] = {-1, -1}, row[2] = {0, 0}, blocks[2] = {0, 0}, tiles[2] = {0, 0};
+  int q0[2] = {0, 0};
+  if (live) {
+    t = static_cast<int>(wid / p.hq);
+    hq = static_cast<int>(wid - static_cast<int64_t>(t) * p.hq);
+    h = hq / p.G;
+    const T *qr = static_cast<const T *>(p.q) + (static_cast<size_t>(t) * p.hq + hq) * D + lane * PL;
+    const float scale = rsqrtf(static_cast<float>(D)) * kLog2e;
+    float qv[PL];
 #pragma unroll
-    for (int k = 0; k < PL; ++k) o[k] = fmaf(rec[lane * PL + k], b, o[k] * a);
-    m = mn;
-  };
-  const bool shares = taken_pages(p, gr, r) > 0;
-  for (int kind = 0; kind < 2; ++kind) {
-    if (kind == 0 && !shares) continue;
-    const int e = kind == 0 ? gr.of(p, r) : p.num_groups + r;
-    const Entry x = entry(p, gr, e);
-    if (x.tiles == 0) continue;
-    const int row = (t - x.q0) * p.G + hq - h * p.G;
-    const int64_t first = p.start[e] + (static_cast<int64_t>(h) * x.blocks + row / p.block) * x.tiles;
-    const int b0 = owner_cta(first, total, nb), b1 = owner_cta(first + x.tiles - 1, total, nb);
-    for (int b = b0; b <= b1; ++b) {
-      const Place pp = place<D>(p, x, kind, h, row, b > b0, b);
-      join(*pp.ml, pp.o);
+    for (int k = 0; k < PL; ++k) qv[k] = to_f(qr[k]) * scale;
+    const int r = find_last(p.q_offsets, p.R, t);
+    const int start = p.q_start[r];
+    if (start > p.max_pages * kPage && lane == 0) set_error(p.err, kErrPage);   // context past the table's end
+    const int pos1 = start > p.max_pages * kPage ? -1 : start + (t - p.q_offsets[r]);
+    for (int pos = max(start, 0); pos <= pos1; ++pos) {
+      const int pg = pos / kPage < p.max_pages ? p.bt[static_cast<size_t>(r) * p.max_pages + pos / kPage] : -1;
+      if (pg < 0 || pg >= p.num_pages) {
+        if (lane == 0) set_error(p.err, kErrPage);
+        continue;
+      }
+      const size_t off = ((static_cast<size_t>(pg) * p.hkv + h) * kPage + pos % kPage) * D + lane * PL;
+      const T *kr = static_cast<const T *>(p.K) + off, *vr = static_cast<const T *>(p.V) + off;
+      float s = 0.0f, v[PL];
+#pragma unroll
+      for (int k = 0; k < PL; ++k) {
+        s = fmaf(qv[k], to_f(kr[k]), s);
+        v[k] = to_f(vr[k]);
+      }
+      s = warp_sum(s);
+      const float mn = fmaxf(m, s);
+      const float a = m == -INFINITY ? 0.0f : exp2f(m - mn), w = s == -INFINITY ? 0.0f : exp2f(s - mn);
+      l = fmaf(l, a, w);
+#pragma unroll
+      for (int k = 0; k < PL; ++k) o[k] = fmaf(w, v[k], o[k] * a);
+      m = mn;
     }
+    const Groups gr{p.group_off};
+    const int g = p.num_groups > 0 ? find_last(p.group_off, p.num_groups, r) : -1;
+    const bool in = g >= 0 && gr.off[g] <= r && r < gr.off[g + 1];
+    const int shared = in ? shared_pages(p, gr.off, g) : 0;
+    if (shared > 0 && shared * kPage <= start) ent[0] = g;
+    ent[1] = p.num_groups + r;
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+      if (ent[kind] >= 0) {
+        const Entry x = entry(p, gr, ent[kind]);
+        tiles[kind] = x.tiles;
+        blocks[kind] = x.blocks;
+        q0[kind] = x.q0;
+        row[kind] = (t - x.q0) * p.G + hq - h * p.G;
+      }
   }
-  // the window's tokens
-  const T *qr = static_cast<const T *>(p.q) + (static_cast<size_t>(t) * p.hq + hq) * D + lane * PL;
-  const float scale = rsqrtf(static_cast<float>(D)) * kLog2e;
-  float qv[PL];
+  grid_dependency_sync();
+  if (!live) return;
+  const int64_t total = p.start[p.num_groups + p.R];
+  const int nb = static_cast<int>(min(total, static_cast<int64_t>(p.nb)));
 #pragma unroll
-  for (int k = 0; k < PL; ++k) qv[k] = to_f(qr[k]) * scale;
-  const int start = p.q_start[r];
-  if (start > p.max_pages * kPage && lane == 0) set_error(p.err, kErrPage);   // context past the table's end
-  const int pos1 = start > p.max_pages * kPage ? -1 : start + (t - p.q_offsets[r]);
-  for (int pos = max(start, 0); pos <= pos1; ++pos) {
-    const int pg = pos / kPage < p.max_pages ? p.bt[static_cast<size_t>(r) * p.max_pages + pos / kPage] : -1;
-    if (pg < 0 || pg >= p.num_pages) {
-      if (lane == 0) set_error(p.err, kErrPage);
-      continue;
+  for (int kind = 0; kind < 2; ++kind) {
+    if (ent[kind] < 0 || tiles[kind] == 0) continue;
+    const int64_t first = p.start[ent[kind]] + kItemCost +
+                          (static_cast<int64_t>(h) * blocks[kind] + row[kind] / p.block) * (tiles[kind] + kItemCost);
+    const int b0 = owner_cta(first, total, nb), b1 = owner_cta(first + tiles[kind] - 1, total, nb);
+    Entry x;
+    x.q0 = q0[kind];
+    for (int c0 = b0; c0 <= b1; c0 += CH) {   // a chunk's records: all loads first, then one step for all
+      float2 ml[CH];
+      float rec[CH][PL];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int b = min(c0 + c, b1);
+        const Place pp = place<D>(p, x, kind, h, row[kind], b > b0, b);
+        ml[c] = __ldcg(pp.ml);
+#pragma unroll
+        for (int k = 0; k < PL; k += 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(pp.o + lane * PL + k));
+          rec[c][k] = v.x;
+          rec[c][k + 1] = v.y;
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (c0 + c <= b1) mn = fmaxf(mn, ml[c].x);
+      const float a = m == -INFINITY ? 0.0f : exp2f(m - mn);
+      l *= a;
+#pragma unroll
+      for (int k = 0; k < PL; ++k) o[k] *= a;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        // a record that saw nothing is (-infinity, 0); one that saw only NaN has a sum
+        if (c0 + c > b1 || (ml[c].x == -INFINITY && ml[c].y == 0.0f)) continue;
+        const float w = exp2f(ml[c].x - mn);
+        l = fmaf(ml[c].y, w, l);
+#pragma unroll
+        for (int k = 0; k < PL; ++k) o[k] = fmaf(rec[c][k], w, o[k]);
+      }
+      m = mn;
     }
-    const size_t off = ((static_cast<size_t>(pg) * p.hkv + h) * kPage + pos % kPage) * D + lane * PL;
-    const T *kr = static_cast<const T *>(p.K) + off, *vr = static_cast<const T *>(p.V) + off;
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < PL; ++k) s = fmaf(qv[k], to_f(kr[k]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    const float a = m == -INFINITY ? 0.0f : exp2f(m - mn), w = s == -INFINITY ? 0.0f : exp2f(s - mn);
-    l = fmaf(l, a, w);
-#pragma unroll
-    for (int k = 0; k < PL; ++k) o[k] = fmaf(w, to_f(vr[k]), o[k] * a);
-    m = mn;
   }
   T *op = static_cast<T *>(p.out) + (static_cast<size_t>(t) * p.hq + hq) * D + lane * PL;
   const bool none = l == 0.0f && m == -INFINITY;
