@@ -336,8 +336,12 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
 // MN-major from shared memory). Two streams of softmax warps, each with an S and an O, take turns at the tensor core:
 // an item's block of up to 128 rows gives its even tiles to one and its odd tiles to the other and joins the two at the
 // end; a block of up to 256 rows gives each stream 128 of them, and both read every tile.
-// Warps: 0-3 and 4-7 the streams' softmax (thread = row), 8 K and V pages and tile records, 9 queries, 10 and 11 the
-// streams' tcgen05 issuers. K and V tiles share a ring. Every wait is bounded, and no role waits on a block-wide barrier.
+// Warps: 0-3 and 4-7 the streams' softmax (thread = row; they also bring the first segment's queries), 8 and 9 the pages,
+// four of each tile, 8 the tile records, 10 the tcgen05 issuer, 11 the later segments' queries. A page of a head is one TMA request (about 50 ns of its issuing warp each).
+// In shared memory 8 rows of 64 columns are one swizzled block of 1 KB; a K or V tile holds, for each group of 8
+// tokens, the blocks of its d / 64 column halves. K and V tiles share a ring.
+// A barrier's parity tells a phase from its neighbours only to a thread that has seen every phase before it, so the page
+// warps and the issuer watch the ring's places in order and miss none. Every wait is bounded, and no role waits on a block-wide barrier.
 constexpr int kTcThreads = 384;
 constexpr int kTcBlock = 256;
 constexpr float kRescale = 8.0f;  // log2: the reference of a row's weights follows its maximum when 2^8 behind
@@ -347,11 +351,13 @@ struct TileInfo {
   int flags, idx, n, tp;   // tile idx of the segment's n; tp: tokens, and from bit 8 on which of its pages are in the pool
   int h, n0, rows, q0;     // rows of the block, from row n0 of the item on
 };
-constexpr int kValid = 1, kFirst = 2, kLast = 4, kTwo = 8, kQbuf = 16, kQpar = 32, kKind = 128, kLater = 256;  // kQpar: 2 bits
+constexpr int kValid = 1, kFirst = 2, kLast = 4, kTwo = 8, kQbuf = 16, kKind = 32, kLater = 64;
+constexpr int kQuse = 8;  // from this bit on, 2 bits each: how often the two query buffers were filled before, modulo 4
 
 template <int D>
 struct Tc {
-  static constexpr int ATOM = 128 * 128;               // 64 columns of a 128-row bf16 operand
+  static constexpr int ATOM = 128 * 128;               // 64 columns of 128 query rows
+  static constexpr int GROUP = 16 * D;                 // 8 tokens of a K or V tile
   static constexpr int UNIT = 128 * D * 2;             // a K or V tile, or 128 query rows
   static constexpr int NU = D == 128 ? 5 : 10;         // ring of tiles
   static constexpr int kMeta = D == 128 ? 4 : 8;       // tile records in flight
@@ -359,12 +365,12 @@ struct Tc {
   static constexpr int OFF_Q = NU * UNIT;
   static constexpr int OFF_INFO = OFF_Q + 2 * UNIT;
   static constexpr int OFF_X = OFF_INFO + kMeta * static_cast<int>(sizeof(TileInfo));  // m [2][128], l of stream 1 [128]
-  // full, empty [NU]; mfull, mfree [kMeta]; qfull, qempty, sfull, pfull, ofull [2]; xready, xdone
-  static constexpr int NBAR = 2 * NU + 2 * kMeta + 10 + 2;
+  // full, empty [NU]; mfull, mfree [kMeta]; qfull, qempty, sfull, pfull, ofull [2]; xready, xdone, drain
+  static constexpr int NBAR = 2 * NU + 2 * kMeta + 10 + 3;
   static constexpr int OFF_BAR = OFF_X + 3 * 128 * 4;
-  static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
-  static constexpr int ALLOC = OFF_TMEM + 16 + 1024;   // room to align the base to 1024 bytes
-  static_assert(ALLOC <= 227 * 1024 - 64, "shared memory per CTA");
+  static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;  // the tensor memory's address and the abort flag
+  static constexpr int ALLOC = OFF_TMEM + 16;          // leaves the SM 1 KB: a CTA of the joining kernel fits beside
+  static_assert(ALLOC <= 226 * 1024, "shared memory per CTA");
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {  // relative error about 2^-22
@@ -409,8 +415,42 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// One page of a head through the 4-D map of make_page_map: 2 groups of 8 tokens, with their column halves.
+__device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, int group, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::
+          "r"(smem_u32(dst_smem)),
+      "l"(tmap), "r"(0), "r"(group), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void store32(float *p, const float *v) {   // 32 bytes, aligned
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void touch(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.ca.s32 %0, [%1];" : "=r"(v) : "l"(p));
+}
+__device__ __forceinline__ void mbar_arrive8(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], 8;" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// A block's query rows [first, first + rows) into a buffer of 128, by threads i of n. Not waited for.
+template <int D>
+__device__ __forceinline__ void load_queries(const HParams &p, const Segment &s, int first, int rows, unsigned char *dst,
+                                             int i, int n) {
+  constexpr int CH = D / 8;   // 16-byte pieces of a row
+  const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(p.q);
+  for (int c = i; c < rows * CH; c += n) {
+    const int row = c / CH, k = c % CH, r = s.n0 + first + row;
+    const int t = r / p.G, g = r - t * p.G;
+    cp_async16(dst + (k >> 3) * Tc<D>::ATOM + (row >> 3) * 1024 + (row & 7) * 128 + (((k & 7) ^ (row & 7)) << 4),
+               qg + (static_cast<size_t>(s.x.q0 + t) * p.hq + s.h * p.G + g) * D + k * 8);
+  }
 }
 
 template <int D>
@@ -418,26 +458,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const HParams p) {
   using L = Tc<D>;
   constexpr int NU = L::NU, kMeta = L::kMeta;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  unsigned char *sm = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  // The only shared memory of the kernel, so its base is where the SM's own first KB ends.
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if (smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) set_error(p.err, kErrTimeout);
+    return;
+  }
   unsigned char *ring = sm + L::OFF_RING, *Qs = sm + L::OFF_Q;
   TileInfo *info = reinterpret_cast<TileInfo *>(sm + L::OFF_INFO);
   float *xm = reinterpret_cast<float *>(sm + L::OFF_X);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
   uint64_t *full = bars, *empty = full + NU, *mfull = empty + NU, *mfree = mfull + kMeta, *qfull = mfree + kMeta;
   uint64_t *qempty = qfull + 2, *sfull = qempty + 2, *pfull = sfull + 2, *ofull = pfull + 2, *xready = ofull + 2;
-  uint64_t *xdone = xready + 1;
+  uint64_t *xdone = xready + 1, *drain = xready + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_TMEM);
-  __shared__ int s_abort;
-  volatile int *abort_flag = &s_abort;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    s_abort = 0;
+    *abort_flag = 0;
     for (int i = 0; i < L::NBAR; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < kMeta; ++i) mbar_init(&mfree[i], 10);  // 8 softmax warps and the issuers
-    for (int i = 0; i < NU; ++i) mbar_init(&empty[i], 2);      // one of each stream, or two of the stream that used it
+    for (int i = 0; i < kMeta; ++i) mbar_init(&mfree[i], 9);  // 8 softmax warps and the issuer
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(&full[i], 2);    // the two page warps
+      mbar_init(&empty[i], 2);   // one of each stream, or two of the stream that used it
+    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 8);
       mbar_init(&qempty[i], 2);
       mbar_init(&pfull[i], 4);
     }
@@ -456,6 +502,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   grid_dependency_sync();
 
+  // what the plan reads is asked for at once; its own loads then find it near
+  for (int i = tid; i <= p.R; i += kTcThreads) {
+    touch(p.q_offsets + i);
+    if (i < p.R) touch(p.q_start + i);
+  }
+  for (int i = tid; i < p.num_groups; i += kTcThreads) touch(p.prefix_pages + i);
   // the plan's scratch lies where the ring will be
   const Groups gs = load_groups(p, reinterpret_cast<int32_t *>(ring + 512));
   check_groups(p, gs);
@@ -471,169 +523,207 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return false;
   };
 
-  if (warp == 8) {
-    // ------------------------------------------------------------------------------------------------ pages
+  if (warp == 8 || warp == 9) {
+    // ------------------------------------------------------------------------------------------------- pages
+    const int part = (warp - 8) * (kTilePages / 2);   // this warp's pages of a tile: part .. part + 3
     Walker walk(p, pl);
     Segment s{};
-    int u = 0, i = 0, seg = -1, uses[2] = {0, 0}, qflags = 0;   // u: the unit of the ring, tile u / 2's keys or values
+    int u = 0, i = 0, seg = 0, uses[2] = {0, 0}, qflags = 0, freed = 0, issued = 0;
+    int page = -1;
     bool more = walk.next(s);
-    int page = -1, next_page = -1;
-    auto fetch = [&](const Segment &g, int k) {   // this lane's page of tile k of the segment
-      const int j = g.x.page0 + (g.t0 + k) * kTilePages + lane;
-      next_page = lane < kTilePages && j < p.max_pages && j * kPage < g.x.tok1
-                      ? p.bt[static_cast<size_t>(g.x.req) * p.max_pages + j] : -1;
+    auto fetch = [&]() {   // page lane of tile i of the segment
+      const int j = s.x.page0 + (s.t0 + i) * kTilePages + lane;
+      page = lane < kTilePages && j < p.max_pages && j * kPage < s.x.tok1
+                 ? p.bt[static_cast<size_t>(s.x.req) * p.max_pages + j] : -1;
     };
-    if (more) fetch(s, 0);
-    for (;; ++u) {
-      const int st = u % NU, mi = (u >> 1) % kMeta;
-      const bool keys = (u & 1) == 0;
-      if (keys && u >= 2 * kMeta && !wait(&mfree[mi], (u >> 1) / kMeta - 1)) break;
+    if (more) fetch();
+    bool stop = false;
+    for (; !stop; ++u) {
+      const int mi = u % kMeta;
+      if (part == 0 && u >= kMeta && !wait(&mfree[mi], u / kMeta - 1)) break;
       if (!more) {
-        if (lane == 0) {
+        if (part == 0 && lane == 0) {
           info[mi].flags = 0;
           mbar_arrive(&mfull[mi]);
         }
         break;
       }
-      if (u >= NU && !wait(&empty[st], u / NU - 1)) break;
-      if (keys) page = next_page;
       const int tok = s.x.tok0 + (s.t0 + i) * kTileTok, ntok = min(kTileTok, s.x.tok1 - tok);
       const int npg = (ntok + kPage - 1) / kPage;
       const bool in = lane < npg, ok = in && page >= 0 && page < p.num_pages;
       if (in && !ok) set_error(p.err, kErrPage);
       const uint32_t pages = __ballot_sync(0xffffffffu, ok);
-      unsigned char *dst = ring + st * L::UNIT;
-      if (!keys && pages != 0xff) {   // values that no copy brings must be finite: their weights are zero
-        for (int j = 0; j < kTilePages; ++j)
-          if (!((pages >> j) & 1))
-            for (int c = lane; c < kPage * D / 8; c += 32) {
-              const int half = c / (kPage * 8), w = c % (kPage * 8);
-              *reinterpret_cast<uint4 *>(dst + half * L::ATOM + j * 2048 + w * 16) = make_uint4(0, 0, 0, 0);
-            }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (keys && i == 0) {
-        ++seg;
-        const bool two = s.rows > 128;
-        const int qbuf = two ? 0 : (seg & 1);
-        qflags = (two ? kTwo : 0) | (qbuf ? kQbuf : 0) | ((uses[0] & 1) ? kQpar : 0) | ((uses[1] & 1) ? 2 * kQpar : 0) |
-                 (s.e < p.num_groups ? 0 : kKind) | (s.t0 > 0 ? kLater : 0);
-        if (two || qbuf == 0) ++uses[0];
-        if (two || qbuf == 1) ++uses[1];
-      }
-      if (lane == 0) {
-        if (keys) {
+      const int group0 = (page * p.hkv + s.h) * (kPage / 8);
+      if (part == 0) {
+        if (i == 0) {   // a new segment: its query buffers
+          const bool two = s.rows > 128;
+          const int qbuf = two ? 0 : (seg & 1);
+          qflags = (two ? kTwo : 0) | (qbuf ? kQbuf : 0) | ((uses[0] & 3) << kQuse) | ((uses[1] & 3) << (kQuse + 2)) |
+                   (s.e < p.num_groups ? 0 : kKind) | (s.t0 > 0 ? kLater : 0);
+          if (two || qbuf == 0) ++uses[0];
+          if (two || qbuf == 1) ++uses[1];
+          ++seg;
+        }
+        if (lane == 0) {
           info[mi] = TileInfo{kValid | qflags | (i == 0 ? kFirst : 0) | (i == s.n - 1 ? kLast : 0), i, s.n,
                               ntok | (static_cast<int>(pages) << 8), s.h, s.n0, s.rows, s.x.q0};
           mbar_arrive(&mfull[mi]);
         }
-        mbar_arrive_expect_tx(&full[st], __popc(pages) * kPage * D * 2);
       }
-      __syncwarp();
-      if (ok) {
-        const int row0 = (page * p.hkv + s.h) * kPage;
-        const CUtensorMap *tm = keys ? &tmK : &tmV;
-        tma_load_2d(dst + lane * 2048, tm, 0, row0, &full[st]);
-        if (D == 128) tma_load_2d(dst + L::ATOM + lane * 2048, tm, 64, row0, &full[st]);
-      }
-      if (keys) {   // the next tile's page ids are on their way while the values' turn comes
-        if (i + 1 < s.n) fetch(s, i + 1);
-      } else if (++i == s.n) {
-        more = walk.next(s);
-        i = 0;
-        if (more) fetch(s, 0);
-      }
-    }
-    // after an abort, copies in flight are waited for (bounded) before the CTA leaves
-    if (*abort_flag)
-      for (int k = max(0, u - NU); k < u; ++k) mbar_wait(&full[k % NU], (k / NU) & 1, nullptr);
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------------------------------------ queries
-    Walker walk(p, pl);
-    Segment s;
-    int uses[2] = {0, 0};
-    for (int seg = 0; walk.next(s); ++seg) {
-      const bool two = s.rows > 128;
-      const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(p.q);
-      bool stop = false;
-      for (int b = 0; b < 2 && !stop; ++b) {
-        if (!two && b != (seg & 1)) continue;
-        if (uses[b] > 0 && !wait(&qempty[b], uses[b] - 1)) {
+      const uint32_t mine = (pages >> part) & 0xf;
+#pragma unroll 1
+      for (int v = 0; v < 2 && !stop; ++v) {   // keys, then values
+        const int un = 2 * u + v, st = un % NU;
+        while (freed <= un - NU && wait(&empty[freed % NU], freed / NU)) ++freed;
+        if (freed <= un - NU) {
           stop = true;
           break;
         }
-        ++uses[b];
-        const int first = two ? 128 * b : 0, rows = min(s.rows - first, 128);
-        constexpr int CH = D / 8;   // 16-byte pieces of a row
-        for (int c = lane; c < rows * CH; c += 32) {
-          const int row = c / CH, k = c % CH, n = s.n0 + first + row;
-          const int t = n / p.G, g = n - t * p.G;
-          cp_async16(Qs + b * L::UNIT + (k >> 3) * L::ATOM + (row >> 3) * 1024 + (row & 7) * 128 +
-                         (((k & 7) ^ (row & 7)) << 4),
-                     qg + (static_cast<size_t>(s.x.q0 + t) * p.hq + s.h * p.G + g) * D + k * 8);
+        unsigned char *dst = ring + st * L::UNIT;
+        if (v == 1 && mine != 0xf) {   // values that no copy brings must be finite: their weights are zero
+          for (int j = part; j < part + 4; ++j)
+            if (!((pages >> j) & 1))
+              for (int c = lane; c < kPage * D / 8; c += 32)
+                *reinterpret_cast<uint4 *>(dst + j * 2 * L::GROUP + c * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(mine) * kPage * D * 2);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[b]);
+        if (ok && (lane & ~3) == part) tma_load_4d(dst + lane * 2 * L::GROUP, v == 0 ? &tmK : &tmV, group0, &full[st]);
+        issued = un + 1;
       }
       if (stop) break;
+      if (++i == s.n) {
+        more = walk.next(s);
+        i = 0;
+      }
+      if (more) fetch();
     }
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------------------------------------------ issuers
-    // S of the stream's next tile right behind P . V of its last (they share tensor memory, and what a thread issues
-    // is carried out in order), P . V once P is written. The whole warp waits, one lane issues.
-    const int s = warp - 10;
-    const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
-    int done = 0;
-    for (int t = 0;; ++t) {
-      const int mi = t % kMeta;
-      if (!wait(&mfull[mi], t / kMeta)) break;
-      const TileInfo m = info[mi];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&mfree[mi]);
-      if (!(m.flags & kValid)) break;
-      const bool two = (m.flags & kTwo) != 0;
-      if (!two && (m.idx & 1) != s) continue;   // the other stream's
-      const int ku = 2 * t, vu = ku + 1;
-      const int b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
-      if (!wait(&qfull[b], m.flags / kQpar >> b) || !wait(&full[ku % NU], ku / NU)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t qa = smem_u32(Qs + b * L::UNIT), ka = smem_u32(ring + (ku % NU) * L::UNIT);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * L::ATOM + (kk & 3) * 32;
-          umma_bf16(tmem + 128 * s, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka + off, 16, 1024, 2), idesc_s,
-                    kk > 0 ? 1u : 0u);
+    // after an abort, copies in flight are waited for (bounded) before the CTA leaves
+    if (*abort_flag)
+      for (int un = max(0, issued - NU); un < issued; ++un) mbar_wait(&full[un % NU], (un / NU) & 1, nullptr);
+  } else if (warp == 11) {
+    // ----------------------------------------------------------------------------------------------- queries
+    Walker walk(p, pl);
+    Segment s;
+    int uses[2] = {0, 0};
+    bool stop = false;
+    for (int seg = 0; !stop && walk.next(s); ++seg) {
+      const bool two = s.rows > 128;
+      for (int b = 0; b < 2; ++b) {
+        if (!two && b != (seg & 1)) continue;
+        if (seg > 0) {
+          if (uses[b] > 0 && !wait(&qempty[b], uses[b] - 1)) {
+            stop = true;
+            break;
+          }
+          const int first = two ? 128 * b : 0;
+          load_queries<D>(p, s, first, min(s.rows - first, 128), Qs + b * L::UNIT, lane, 32);
         }
-        umma_commit(&sfull[s]);
-        umma_commit(&empty[ku % NU]);
-        if (!two) umma_commit(&empty[ku % NU]);
-        // this stream's last use of its queries; a buffer counts two
-        if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {
-          umma_commit(&qempty[b]);
-          if (two || m.n == 1) umma_commit(&qempty[b]);
+        ++uses[b];
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (seg > 0 && !stop) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (two || (seg & 1) == 0) mbar_arrive8(&qfull[0]);
+          if (two || (seg & 1) == 1) mbar_arrive8(&qfull[1]);
         }
       }
-      __syncwarp();
-      if (!wait(&full[vu % NU], vu / NU) || !wait(&pfull[s], done)) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t va = smem_u32(ring + (vu % NU) * L::UNIT);
-        const bool fresh = two ? m.idx == 0 : m.idx < 2;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, smem_desc(va + kk * 2048, L::ATOM, 1024, 2),
-                       idesc_o, (kk > 0 || !fresh) ? 1u : 0u);
-        umma_commit(&ofull[s]);
-        umma_commit(&empty[vu % NU]);
-        if (!two) umma_commit(&empty[vu % NU]);
-      }
-      __syncwarp();
-      ++done;
     }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------------------------------------- issuer
+    // Whichever stream has its operands: P . V once P is written and, right behind it, S of the stream's next tile (they
+    // share tensor memory, and what one thread issues is carried out in order). So the streams fall out of step, and one's
+    // products run under the other's softmax.
+    if (lane == 0) {
+      constexpr int kLook = 0, kS = 1, kPV = 2, kOver = 3;
+      int t[2] = {0, 0}, done[2] = {0, 0}, state[2] = {kLook, kLook}, released = 0;
+      int landed = 0, qseen[2] = {0, 0};   // units of the ring and fillings of the query buffers seen
+      TileInfo cur[2];
+      const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
+      uint32_t idle = 0;
+      while (state[0] != kOver || state[1] != kOver) {
+        if (*abort_flag) break;
+        bool progressed = false;
+        while (mbar_test(&full[landed % NU], (landed / NU) & 1)) ++landed;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          while (mbar_test(&qfull[b], qseen[b] & 1)) ++qseen[b];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (state[s] == kPV) {
+            const int vu = 2 * t[s] + 1;
+            if (vu < landed && mbar_test(&pfull[s], done[s] & 1)) {
+              tc_fence_after();
+              const bool two = (cur[s].flags & kTwo) != 0;
+              const uint32_t va = smem_u32(ring + (vu % NU) * L::UNIT);
+              const bool fresh = two ? cur[s].idx == 0 : cur[s].idx < 2;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8,
+                             smem_desc(va + kk * 2 * L::GROUP, 1024, L::GROUP, 2), idesc_o, (kk > 0 || !fresh) ? 1u : 0u);
+              umma_commit(&ofull[s]);
+              umma_commit(&empty[vu % NU]);
+              if (!two) umma_commit(&empty[vu % NU]);
+              ++done[s];
+              ++t[s];
+              state[s] = kLook;
+              progressed = true;
+            }
+          }
+          while (state[s] == kLook && mbar_test(&mfull[t[s] % kMeta], (t[s] / kMeta) & 1)) {
+            cur[s] = info[t[s] % kMeta];
+            progressed = true;
+            if (!(cur[s].flags & kValid)) state[s] = kOver;
+            else if ((cur[s].flags & kTwo) || (cur[s].idx & 1) == s) state[s] = kS;
+            else ++t[s];   // the other stream's
+          }
+          if (state[s] == kS) {
+            const TileInfo &m = cur[s];
+            const bool two = (m.flags & kTwo) != 0;
+            const int ku = 2 * t[s], b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
+            if (ku < landed && (((b ? qseen[1] : qseen[0]) - (m.flags >> (kQuse + 2 * b))) & 3) == 1) {
+              tc_fence_after();
+              const uint32_t qa = smem_u32(Qs + b * L::UNIT), ka = smem_u32(ring + (ku % NU) * L::UNIT);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t qd = smem_desc(qa + (kk >> 2) * L::ATOM + (kk & 3) * 32, 16, 1024, 2);
+                const uint64_t kd = smem_desc(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16, L::GROUP, 2);
+                umma_bf16(tmem + 128 * s, qd, kd, idesc_s, kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&sfull[s]);
+              umma_commit(&empty[ku % NU]);
+              if (!two) umma_commit(&empty[ku % NU]);
+              // this stream's last use of its queries; a buffer counts two
+              if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {
+                umma_commit(&qempty[b]);
+                if (two || m.n == 1) umma_commit(&qempty[b]);
+              }
+              state[s] = kPV;
+              progressed = true;
+            }
+          }
+        }
+        while (released < min(t[0], t[1])) {
+          mbar_arrive(&mfree[released % kMeta]);
+          ++released;
+        }
+        if (progressed) {
+          idle = 0;
+        } else if (++idle > kSpinPolls) {
+          set_error(p.err, kErrTimeout);
+          *abort_flag = 1;
+        }
+      }
+      if (landed > 0) {   // products and arrivals in flight end before the CTA does
+        umma_commit(drain);
+        mbar_wait(drain, 0, p.err);
+      }
+    }
+    __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------------------------------------------ softmax
     const int s = warp >> 2, wq = warp & 3;
@@ -641,6 +731,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lanes + 128 * s;
     const float scale2 = rsqrtf(static_cast<float>(D)) * kLog2e;
+    {   // the first segment's queries, while its pages are on their way
+      Walker walk(p, pl);
+      Segment f;
+      if (walk.next(f)) {
+        load_queries<D>(p, f, 0, min(f.rows, 128), Qs, tid, 256);
+        if (f.rows > 128) load_queries<D>(p, f, 128, f.rows - 128, Qs + L::UNIT, tid, 256);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&qfull[0]);
+          if (f.rows > 128) mbar_arrive(&qfull[1]);
+        }
+      }
+    }
     float m = -INFINITY, l = 0.0f;
     int cnt = 0, had = 0, joins = 0;
     for (int ti = 0;; ++ti) {
@@ -664,24 +769,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         if (active) {
           const bool whole = ntok == kTileTok && pages == 0xff;
-          auto hide = [&](float *x, int c) {   // columns c .. c + 31: tokens past the end or on no page
+          auto hide = [&](float *x, int c) {   // columns 32 c .. 32 c + 31: tokens past the end or on no page
             if (whole) return;
+            const int n = ntok - 32 * c;
+            uint32_t see = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u;
+            see &= (((pages >> (2 * c)) & 1) ? 0xffffu : 0u) | (((pages >> (2 * c + 1)) & 1) ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i >= ntok || !((pages >> ((c + i) / kPage)) & 1)) x[i] = -INFINITY;
+            for (int i = 0; i < 32; ++i) x[i] = (see >> i) & 1 ? x[i] : -INFINITY;
           };
           float mx = -INFINITY;
-          {
-            float x[2][32];   // the next 32 columns are on their way while these are looked at
-            tmem_ld32(tS, x[0]);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            tmem_ld32(tS + 32 * c, x);
+            tmem_wait_ld();
+            hide(x, c);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_wait_ld();
-              if (c < 3) tmem_ld32(tS + 32 * c + 32, x[(c + 1) & 1]);
-              hide(x[c & 1], 32 * c);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) mx = max3(mx, x[c & 1][i], x[c & 1][i + 1]);
-            }
+            for (int i = 0; i < 32; i += 2) mx = max3(mx, x[i], x[i + 1]);
           }
           mx *= scale2;
           if (had == 0) {
@@ -706,18 +810,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float ms = m == -INFINITY ? 0.0f : m;
           F2 sum = f2(0.0f, 0.0f);
           const F2 sc = f2(scale2, scale2), sub = f2(-ms, -ms);
-          float x[2][32];
-          tmem_ld32(tS, x[0]);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            float x[32];
+            tmem_ld32(tS + 32 * c, x);
             tmem_wait_ld();
-            if (c < 3) tmem_ld32(tS + 32 * c + 32, x[(c + 1) & 1]);
-            hide(x[c & 1], 32 * c);
+            hide(x, c);
             uint32_t y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float a, b;
-              split(fma2(f2(x[c & 1][2 * i], x[c & 1][2 * i + 1]), sc, sub), a, b);
+              split(fma2(f2(x[2 * i], x[2 * i + 1]), sc, sub), a, b);
               a = fast_exp2(a);
               b = fast_exp2(b);
               sum = add2(sum, f2(a, b));
@@ -738,7 +841,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int rows = kPage - ntok % kPage;
           for (int c = wq * 32 + lane; c < rows * (D / 8); c += 128) {
             const int row = ntok + c / (D / 8), k = c % (D / 8);
-            *reinterpret_cast<uint4 *>(v + (k >> 3) * L::ATOM + row * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(v + (row >> 3) * L::GROUP + (k >> 3) * 1024 + (row & 7) * 128 + (k & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -768,8 +872,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_wait_ld();
             if (mine)
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(pp.o + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              for (int i = 0; i < 32; i += 8) store32(pp.o + c + i, o + i);
           }
         }
         tc_fence_before();
@@ -799,11 +902,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_wait_ld();
             if (mine)
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float r[4];
+              for (int i = 0; i < 32; i += 8) {
+                float r[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r[k] = (none0 ? 0.0f : o0[i + k] * w0) + (none1 ? 0.0f : o1[i + k] * w1);
-                *reinterpret_cast<float4 *>(pp.o + c + i) = make_float4(r[0], r[1], r[2], r[3]);
+                for (int k = 0; k < 8; ++k) r[k] = (none0 ? 0.0f : o0[i + k] * w0) + (none1 ? 0.0f : o1[i + k] * w1);
+                store32(pp.o + c + i, r);
               }
           }
         }
@@ -972,7 +1075,7 @@ template <class T, int D> cudaError_t launch_plain(HParams p, cudaStream_t s) {
 template <int D> cudaError_t launch_tc(const PoolArgs &pa, HParams p, cudaStream_t s) {
   p.block = kTcBlock;
   CUtensorMap tmK, tmV;
-  if (!make_pool_map(&tmK, pa.k, pa.num_pages, pa.hkv, D) || !make_pool_map(&tmV, pa.v, pa.num_pages, pa.hkv, D))
+  if (!make_page_map(&tmK, pa.k, pa.num_pages, pa.hkv, D) || !make_page_map(&tmV, pa.v, pa.num_pages, pa.hkv, D))
     return cudaErrorInvalidValue;
   static bool attr_set[64] = {false};
   int dev = 0;

@@ -921,14 +921,28 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 
 }  // namespace
 
-bool make_pool_map(CUtensorMap *map, const void *base, int num_pages, int hkv, int d) {
+bool make_pool_map(CUtensorMap *map, const void *base, int num_pages, int hkv) {
   auto enc = get_encode();
   if (!enc) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(num_pages) * hkv * kPage};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
+  cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(num_pages) * hkv * kPage};
+  cuuint64_t strides[1] = {128 * 2};
   cuuint32_t box[2] = {64, 16};
   cuuint32_t estr[2] = {1, 1};
   CUresult rc = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return rc == CUDA_SUCCESS;
+}
+
+bool make_page_map(CUtensorMap *map, const void *base, int num_pages, int hkv, int d) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2, halves = static_cast<cuuint64_t>(d / 64);
+  cuuint64_t dims[4] = {64, 8, halves, static_cast<cuuint64_t>(num_pages) * hkv * (kPage / 8)};
+  cuuint64_t strides[3] = {row, 128, 8 * row};
+  cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(halves), kPage / 8};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult rc = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS;
@@ -941,7 +955,7 @@ cudaError_t launch_tc(const PoolArgs &pa, const VParams &prm, cudaStream_t s) {
   using L = TcSmem<NPMAX>;
   static_assert(L::ALLOC <= 227 * 1024, "shared memory over the per-CTA limit");
   CUtensorMap tmK, tmV;
-  if (!make_pool_map(&tmK, pa.k, pa.num_pages, pa.hkv, 128) || !make_pool_map(&tmV, pa.v, pa.num_pages, pa.hkv, 128))
+  if (!make_pool_map(&tmK, pa.k, pa.num_pages, pa.hkv) || !make_pool_map(&tmV, pa.v, pa.num_pages, pa.hkv))
     return cudaErrorInvalidValue;
   static bool attr_set[64] = {false};
   int dev = 0;
