@@ -478,10 +478,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < L::NBAR; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < kMeta; ++i) mbar_init(&mfree[i], 9);  // 8 softmax warps and the issuer
-    for (int i = 0; i < NU; ++i) {
-      mbar_init(&full[i], 2);    // the two page warps
-      mbar_init(&empty[i], 2);   // one of each stream, or two of the stream that used it
-    }
+    for (int i = 0; i < NU; ++i) mbar_init(&full[i], 2);  // the two page warps
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 8);
       mbar_init(&qempty[i], 2);
@@ -639,83 +636,97 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // share tensor memory, and what one thread issues is carried out in order). So the streams fall out of step, and one's
     // products run under the other's softmax.
     if (lane == 0) {
-      constexpr int kLook = 0, kS = 1, kPV = 2, kOver = 3;
-      int t[2] = {0, 0}, done[2] = {0, 0}, state[2] = {kLook, kLook}, released = 0;
+      // A stream: `cur` is the tile whose S is issued and whose P . V is not (busy), `next` the one after it (known).
+      int tn[2] = {0, 0}, tc[2] = {-1, -1}, done[2] = {0, 0}, released = 0;
+      bool busy[2] = {false, false}, known[2] = {false, false}, over[2] = {false, false};
       int landed = 0, qseen[2] = {0, 0};   // units of the ring and fillings of the query buffers seen
-      TileInfo cur[2];
+      TileInfo cur[2], next[2];
       const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
+      auto has_landed = [&](int un) {
+        while (landed <= un && mbar_test(&full[landed % NU], (landed / NU) & 1)) ++landed;
+        return landed > un;
+      };
       uint32_t idle = 0;
-      while (state[0] != kOver || state[1] != kOver) {
-        if (*abort_flag) break;
+      while (true) {
         bool progressed = false;
-        while (mbar_test(&full[landed % NU], (landed / NU) & 1)) ++landed;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          while (mbar_test(&qfull[b], qseen[b] & 1)) ++qseen[b];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (state[s] == kPV) {
-            const int vu = 2 * t[s] + 1;
-            if (vu < landed && mbar_test(&pfull[s], done[s] & 1)) {
-              tc_fence_after();
-              const bool two = (cur[s].flags & kTwo) != 0;
-              const uint32_t va = smem_u32(ring + (vu % NU) * L::UNIT);
-              const bool fresh = two ? cur[s].idx == 0 : cur[s].idx < 2;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8,
-                             smem_desc(va + kk * 2 * L::GROUP, 1024, L::GROUP, 2), idesc_o, (kk > 0 || !fresh) ? 1u : 0u);
-              umma_commit(&ofull[s]);
-              umma_commit(&empty[vu % NU]);
-              if (!two) umma_commit(&empty[vu % NU]);
-              ++done[s];
-              ++t[s];
-              state[s] = kLook;
-              progressed = true;
-            }
-          }
-          while (state[s] == kLook && mbar_test(&mfull[t[s] % kMeta], (t[s] / kMeta) & 1)) {
-            cur[s] = info[t[s] % kMeta];
+          const int o = 1 - s;
+          if (!known[s] && !over[s] && mbar_test(&mfull[tn[s] % kMeta], (tn[s] / kMeta) & 1)) {
+            next[s] = info[tn[s] % kMeta];
             progressed = true;
-            if (!(cur[s].flags & kValid)) state[s] = kOver;
-            else if ((cur[s].flags & kTwo) || (cur[s].idx & 1) == s) state[s] = kS;
-            else ++t[s];   // the other stream's
+            if (!(next[s].flags & kValid)) over[s] = true;
+            else if ((next[s].flags & kTwo) || (next[s].idx & 1) == s) known[s] = true;
+            else ++tn[s];   // the other stream's
           }
-          if (state[s] == kS) {
-            const TileInfo &m = cur[s];
-            const bool two = (m.flags & kTwo) != 0;
-            const int ku = 2 * t[s], b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
-            if (ku < landed && (((b ? qseen[1] : qseen[0]) - (m.flags >> (kQuse + 2 * b))) & 3) == 1) {
-              tc_fence_after();
-              const uint32_t qa = smem_u32(Qs + b * L::UNIT), ka = smem_u32(ring + (ku % NU) * L::UNIT);
+          bool gave_v = false, gave_k = false, last = false;
+          int vu = 0;
+          if (busy[s]) {
+            vu = 2 * tc[s] + 1;
+            if (!has_landed(vu) || !mbar_test(&pfull[s], done[s] & 1)) continue;
+            tc_fence_after();
+            const bool two = (cur[s].flags & kTwo) != 0;
+            const uint64_t vd = smem_desc(smem_u32(ring + (vu % NU) * L::UNIT), 1024, L::GROUP, 2);
+            const bool fresh = two ? cur[s].idx == 0 : cur[s].idx < 2;
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t qd = smem_desc(qa + (kk >> 2) * L::ATOM + (kk & 3) * 32, 16, 1024, 2);
-                const uint64_t kd = smem_desc(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16, L::GROUP, 2);
-                umma_bf16(tmem + 128 * s, qd, kd, idesc_s, kk > 0 ? 1u : 0u);
-              }
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, vd + (kk * 2 * L::GROUP >> 4), idesc_o,
+                           (kk > 0 || !fresh) ? 1u : 0u);
+            // who uses a tile last gives it back
+            gave_v = !two || tc[o] > tc[s] || (tc[o] == tc[s] && !busy[o]);
+            last = two ? (cur[s].flags & kLast) != 0 : cur[s].idx + 2 >= cur[s].n;
+            if (last) umma_commit(&ofull[s]);
+            ++done[s];
+            busy[s] = false;
+            progressed = true;
+          }
+          int ku = 0;
+          if (known[s]) {
+            const TileInfo &m = next[s];
+            const bool two = (m.flags & kTwo) != 0;
+            const int b = two ? s : ((m.flags & kQbuf) ? 1 : 0);
+            ku = 2 * tn[s];
+            bool ready = has_landed(ku);
+            if (ready && (two ? m.idx == 0 : m.idx < 2)) {   // the stream's first use of its queries
+              while (mbar_test(&qfull[b], (b ? qseen[1] : qseen[0]) & 1)) b ? ++qseen[1] : ++qseen[0];
+              ready = (((b ? qseen[1] : qseen[0]) - (m.flags >> (kQuse + 2 * b))) & 3) == 1;
+            }
+            if (ready) {
+              tc_fence_after();
+              // a descriptor counts its address in 16 bytes, and no sum here carries out of that field
+              const uint64_t qd = smem_desc(smem_u32(Qs + b * L::UNIT), 16, 1024, 2);
+              const uint64_t kd = smem_desc(smem_u32(ring + (ku % NU) * L::UNIT), 16, L::GROUP, 2);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16(tmem + 128 * s, qd + (((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4),
+                          kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
               umma_commit(&sfull[s]);
-              umma_commit(&empty[ku % NU]);
-              if (!two) umma_commit(&empty[ku % NU]);
-              // this stream's last use of its queries; a buffer counts two
-              if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {
+              gave_k = !two || tn[o] > tn[s];
+              if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {   // its last use of them; a buffer counts two
                 umma_commit(&qempty[b]);
                 if (two || m.n == 1) umma_commit(&qempty[b]);
               }
-              state[s] = kPV;
+              cur[s] = m;
+              tc[s] = tn[s]++;
+              busy[s] = true;
+              known[s] = false;
               progressed = true;
             }
           }
+          if (gave_v) umma_commit(&empty[vu % NU]);
+          if (gave_k) umma_commit(&empty[ku % NU]);
         }
-        while (released < min(t[0], t[1])) {
-          mbar_arrive(&mfree[released % kMeta]);
-          ++released;
-        }
+        if (over[0] && over[1] && !busy[0] && !busy[1]) break;
+        const int passed = min(tn[0], tn[1]);   // both streams know what they need of the tiles before
+        for (; released < passed; ++released) mbar_arrive(&mfree[released % kMeta]);
         if (progressed) {
           idle = 0;
-        } else if (++idle > kSpinPolls) {
-          set_error(p.err, kErrTimeout);
-          *abort_flag = 1;
+        } else if ((++idle & 0xff) == 0) {
+          if (idle > kSpinPolls) {
+            set_error(p.err, kErrTimeout);
+            *abort_flag = 1;
+          }
+          if (*abort_flag) break;
         }
       }
       if (landed > 0) {   // products and arrivals in flight end before the CTA does
@@ -747,7 +758,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     float m = -INFINITY, l = 0.0f;
-    int cnt = 0, had = 0, joins = 0;
+    int cnt = 0, had = 0, joins = 0, ends = 0;
     for (int ti = 0;; ++ti) {
       const int mi = ti % kMeta;
       if (!wait(&mfull[mi], ti / kMeta)) break;
@@ -855,7 +866,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!(f.flags & kLast)) continue;
       const int kind = (f.flags & kKind) ? 1 : 0;
       const bool later = (f.flags & kLater) != 0;
-      if (had && !wait(&ofull[s], cnt - 1)) break;
+      if (had && !wait(&ofull[s], ends++)) break;
       tc_fence_after();
       Entry x;
       x.q0 = f.q0;
