@@ -405,14 +405,41 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The issuing warp stays together and one elected lane acts: descriptors then live in uniform registers, and a product
+// takes 15 to 20 cycles to issue where a branch for one lane takes 52 (128 x 128 x 16 itself takes 64).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p;
+}
+// D[tmem] (+)= A[smem] * B[smem], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 // One page of a head through the 4-D map of make_page_map: 2 groups of 8 tokens, with their column halves.
@@ -635,7 +662,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Whichever stream has its operands: P . V once P is written and, right behind it, S of the stream's next tile (they
     // share tensor memory, and what one thread issues is carried out in order). So the streams fall out of step, and one's
     // products run under the other's softmax.
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_lane();
+      auto test = [&](uint64_t *bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0; };
       // A stream: `cur` is the tile whose S is issued and whose P . V is not (busy), `next` the one after it (known).
       int tn[2] = {0, 0}, tc[2] = {-1, -1}, done[2] = {0, 0}, released = 0;
       bool busy[2] = {false, false}, known[2] = {false, false}, over[2] = {false, false};
@@ -643,7 +672,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       TileInfo cur[2], next[2];
       const uint32_t idesc_s = idesc_bf16(128, 128, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
       auto has_landed = [&](int un) {
-        while (landed <= un && mbar_test(&full[landed % NU], (landed / NU) & 1)) ++landed;
+        while (landed <= un && test(&full[landed % NU], landed / NU)) ++landed;
         return landed > un;
       };
       uint32_t idle = 0;
@@ -652,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int o = 1 - s;
-          if (!known[s] && !over[s] && mbar_test(&mfull[tn[s] % kMeta], (tn[s] / kMeta) & 1)) {
+          if (!known[s] && !over[s] && test(&mfull[tn[s] % kMeta], tn[s] / kMeta)) {
             next[s] = info[tn[s] % kMeta];
             progressed = true;
             if (!(next[s].flags & kValid)) over[s] = true;
@@ -663,19 +692,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           int vu = 0;
           if (busy[s]) {
             vu = 2 * tc[s] + 1;
-            if (!has_landed(vu) || !mbar_test(&pfull[s], done[s] & 1)) continue;
+            if (!has_landed(vu) || !test(&pfull[s], done[s])) continue;
             tc_fence_after();
             const bool two = (cur[s].flags & kTwo) != 0;
             const uint64_t vd = smem_desc(smem_u32(ring + (vu % NU) * L::UNIT), 1024, L::GROUP, 2);
             const bool fresh = two ? cur[s].idx == 0 : cur[s].idx < 2;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, vd + (kk * 2 * L::GROUP >> 4), idesc_o,
+              umma_ts(lead, tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, vd + (kk * 2 * L::GROUP >> 4), idesc_o,
                            (kk > 0 || !fresh) ? 1u : 0u);
             // who uses a tile last gives it back
             gave_v = !two || tc[o] > tc[s] || (tc[o] == tc[s] && !busy[o]);
             last = two ? (cur[s].flags & kLast) != 0 : cur[s].idx + 2 >= cur[s].n;
-            if (last) umma_commit(&ofull[s]);
+            if (last) commit_by(lead, &ofull[s]);
             ++done[s];
             busy[s] = false;
             progressed = true;
@@ -688,7 +717,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ku = 2 * tn[s];
             bool ready = has_landed(ku);
             if (ready && (two ? m.idx == 0 : m.idx < 2)) {   // the stream's first use of its queries
-              while (mbar_test(&qfull[b], (b ? qseen[1] : qseen[0]) & 1)) b ? ++qseen[1] : ++qseen[0];
+              while (test(&qfull[b], b ? qseen[1] : qseen[0])) b ? ++qseen[1] : ++qseen[0];
               ready = (((b ? qseen[1] : qseen[0]) - (m.flags >> (kQuse + 2 * b))) & 3) == 1;
             }
             if (ready) {
@@ -698,13 +727,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const uint64_t kd = smem_desc(smem_u32(ring + (ku % NU) * L::UNIT), 16, L::GROUP, 2);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                umma_bf16(tmem + 128 * s, qd + (((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4),
+                umma_ss(lead, tmem + 128 * s, qd + (((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4),
                           kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-              umma_commit(&sfull[s]);
+              commit_by(lead, &sfull[s]);
               gave_k = !two || tn[o] > tn[s];
               if (two ? (m.flags & kLast) != 0 : m.idx + 2 >= m.n) {   // its last use of them; a buffer counts two
-                umma_commit(&qempty[b]);
-                if (two || m.n == 1) umma_commit(&qempty[b]);
+                commit_by(lead, &qempty[b]);
+                if (two || m.n == 1) commit_by(lead, &qempty[b]);
               }
               cur[s] = m;
               tc[s] = tn[s]++;
@@ -713,12 +742,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               progressed = true;
             }
           }
-          if (gave_v) umma_commit(&empty[vu % NU]);
-          if (gave_k) umma_commit(&empty[ku % NU]);
+          if (gave_v) commit_by(lead, &empty[vu % NU]);
+          if (gave_k) commit_by(lead, &empty[ku % NU]);
         }
         if (over[0] && over[1] && !busy[0] && !busy[1]) break;
         const int passed = min(tn[0], tn[1]);   // both streams know what they need of the tiles before
-        for (; released < passed; ++released) mbar_arrive(&mfree[released % kMeta]);
+        if (released < passed) {
+          __syncwarp();   // every lane has read them
+          for (; released < passed; ++released)
+            if (lane == 0) mbar_arrive(&mfree[released % kMeta]);
+        }
         if (progressed) {
           idle = 0;
         } else if ((++idle & 0xff) == 0) {
@@ -726,11 +759,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             set_error(p.err, kErrTimeout);
             *abort_flag = 1;
           }
-          if (*abort_flag) break;
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         }
       }
       if (landed > 0) {   // products and arrivals in flight end before the CTA does
-        umma_commit(drain);
+        commit_by(lead, drain);
         mbar_wait(drain, 0, p.err);
       }
     }
