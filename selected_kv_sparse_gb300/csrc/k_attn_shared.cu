@@ -28,7 +28,10 @@ constexpr int kTilePages = 8, kTileTok = kTilePages * kPage;
 constexpr int kMaxCtas = 192;      // CTAs of the first kernel at most
 constexpr int kMaxBlock = 256;     // rows of an item's block at most
 constexpr int kSmemGroups = 1024;  // group offsets kept in shared memory
-constexpr int kItemCost = 2;       // what starting and ending an item costs, in tiles: counted when work is shared out
+// Lengths on the line that is shared out, about 0.7 us each: a tile under up to 128 rows takes 2 (what its 64 KB take to
+// come at an SM's share of the measured copy rate), under more 3 (four products and two softmaxes); starting and ending an
+// item takes 4.
+constexpr int kTileCost = 2, kWideCost = 3, kItemCost = 4;
 constexpr int kPlainThreads = 256, kPlainRows = 32;
 
 struct HParams {
@@ -55,9 +58,23 @@ struct Entry {
   int req;            // the request whose table row names the pages
   int page0, tok0, tok1;  // first page, and the tokens [tok0, tok1) (tok0 = 16 page0)
   int tiles, blocks;  // 128-token tiles; blocks of rows
-  int span;           // a block's length in the line that is shared out: kItemCost and then its tiles
-  __device__ __forceinline__ int64_t length(int hkv) const { return static_cast<int64_t>(span) * blocks * hkv; }
+  // A block's length on the line is its start's and then its tiles'. All blocks but the last are whole.
+  __device__ __forceinline__ int cost(const HParams &p, int block) const {
+    return p.block > 128 && rows - block * p.block > 128 ? kWideCost : kTileCost;
+  }
+  __device__ __forceinline__ int64_t span(int w) const { return static_cast<int64_t>(tiles) * w + kItemCost; }
+  __device__ __forceinline__ int64_t of_head(const HParams &p) const {
+    return tiles == 0 ? 0 : (blocks - 1) * span(cost(p, 0)) + span(cost(p, blocks - 1));
+  }
+  __device__ __forceinline__ int64_t length(const HParams &p) const { return of_head(p) * p.hkv; }
+  // Where the tiles of (head, block) start, from the entry's own start on.
+  __device__ __forceinline__ int64_t first_tile(const HParams &p, int h, int block) const {
+    return h * of_head(p) + block * span(cost(p, 0)) + kItemCost;
+  }
 };
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {   // of numbers >= 0; 32 bits where they do
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 
 struct Groups {
   const int32_t *off;  // in shared memory where they fit
@@ -106,78 +123,82 @@ __device__ __forceinline__ Entry entry(const HParams &p, const Groups &gr, int e
   x.tok0 = x.page0 * kPage;
   x.tiles = x.rows > 0 && x.tok1 > x.tok0 ? (x.tok1 - x.tok0 + kTileTok - 1) / kTileTok : 0;
   x.blocks = (x.rows + p.block - 1) / p.block;
-  x.span = x.tiles > 0 ? x.tiles + kItemCost : 0;
   return x;
 }
 
 __device__ __forceinline__ int owner_cta(int64_t x, int64_t E, int nb) {
-  return static_cast<int>(((x + 1) * nb - 1) / E);
+  return static_cast<int>(quotient((x + 1) * nb - 1, E));
+}
+// CTAs that take part: every part holds a tile's start at least, so every CTA between an item's first and last has a record.
+__device__ __forceinline__ int parts(const HParams &p, int64_t total) {
+  return static_cast<int>(max(int64_t(total > 0), min(total / kWideCost, static_cast<int64_t>(p.nb))));
 }
 
+// Where a CTA's part of the line starts: an entry, a head and block of it, and units into that block.
 struct Plan {
-  int64_t total, begin, end;  // the line's length, and this CTA's part of it
-  int nb;                     // CTAs with a part
-  int entry;                  // the entry that `begin` lies in, and where it starts
-  int64_t entry_start;
-  Entry x;                    // that entry
+  Entry x;
+  int entry, h, block, from;
+  int64_t left;        // the part's length
 };
 struct PlanSlots {
-  int64_t total, base, entry, first;
-  Entry x;
+  int64_t total, base;
+  Plan plan;
 };
 
 // Every thread of the block takes part; the block has at most 32 warps.
 __device__ inline Plan make_plan(const HParams &p, const Groups &gr, int64_t *scratch, PlanSlots *slot) {
   const int n = p.num_groups + p.R, tid = threadIdx.x, nt = blockDim.x;
-  Entry x{};
-  auto count = [&](int e) -> int64_t {
-    if (e >= n) return 0;
-    x = entry(p, gr, e);
-    return x.length(p.hkv);
-  };
-  const int64_t mine = count(tid);
-  const Entry x0 = x;
-  int64_t sum = mine;
-  for (int e = tid + nt; e < n; e += nt) sum += count(e);
-  const int64_t incl = block_inclusive_scan(sum, scratch);
-  if (tid == nt - 1) slot->total = incl;
-  __syncthreads();
-  Plan pl;
-  pl.total = slot->total;
-  pl.nb = static_cast<int>(min(pl.total, static_cast<int64_t>(p.nb)));
-  pl.begin = pl.end = 0;
-  pl.entry = 0;
-  pl.entry_start = 0;
-  const bool works = static_cast<int>(blockIdx.x) < pl.nb;
-  if (works) {
-    pl.begin = static_cast<int64_t>(blockIdx.x) * pl.total / pl.nb;
-    pl.end = static_cast<int64_t>(blockIdx.x + 1) * pl.total / pl.nb;
-  }
   const bool writer = blockIdx.x == 0;
-  int64_t base = 0;
-  for (int e0 = 0; e0 < n; e0 += nt) {
-    const int e = e0 + tid;
-    const int64_t c = e0 == 0 ? mine : count(e);
-    const int64_t inc = block_inclusive_scan(c, scratch);
-    const int64_t first = base + inc - c;
-    if (works && first <= pl.begin && pl.begin < first + c) {
-      slot->entry = e;
-      slot->first = first;
-      slot->x = e0 == 0 ? x0 : x;
+  Entry x{};
+  int64_t c = 0, sum = 0, base = 0, begin = 0, end = 0;
+  if (tid == 0) slot->plan.left = 0;
+  for (int pass = 0; pass < 2; ++pass) {   // the sum of all lengths; then where each entry starts
+    for (int e0 = 0; e0 < n; e0 += nt) {
+      const int e = e0 + tid;
+      if (pass == 0 || n > nt) {
+        c = 0;
+        if (e < n) {
+          x = entry(p, gr, e);
+          c = x.length(p);
+        }
+      }
+      if (pass == 0) {
+        sum += c;
+        continue;
+      }
+      const int64_t incl = block_inclusive_scan(c, scratch), first = base + incl - c;
+      if (first <= begin && begin < first + c && begin < end) {
+        const int64_t in = begin - first, per_head = x.of_head(p), whole = x.span(x.cost(p, 0));
+        Plan pl;
+        pl.x = x;
+        pl.entry = e;
+        pl.h = static_cast<int>(quotient(in, per_head));
+        const int64_t in_head = in - pl.h * per_head;
+        pl.block = min(static_cast<int>(quotient(in_head, whole)), x.blocks - 1);
+        pl.from = static_cast<int>(in_head - pl.block * whole);
+        pl.left = end - begin;
+        slot->plan = pl;
+      }
+      if (writer && e < n) p.start[e] = first;
+      if (tid == nt - 1) slot->base = base + incl;
+      __syncthreads();
+      base = slot->base;
+      __syncthreads();
     }
-    if (writer && e < n) p.start[e] = first;
-    if (tid == nt - 1) slot->base = base + inc;
-    __syncthreads();
-    base = slot->base;
-    __syncthreads();
+    if (pass == 0) {
+      const int64_t incl = block_inclusive_scan(sum, scratch);
+      if (tid == nt - 1) slot->total = incl;
+      __syncthreads();
+      const int64_t total = slot->total;
+      const int nb = parts(p, total), cta = static_cast<int>(blockIdx.x);
+      if (cta < nb) {
+        begin = quotient(cta * total, nb);
+        end = quotient((cta + 1) * total, nb);
+      }
+      if (writer && tid == 0) p.start[n] = total;
+    }
   }
-  if (writer && tid == 0) p.start[n] = pl.total;
-  if (works) {
-    pl.entry = static_cast<int>(slot->entry);
-    pl.entry_start = slot->first;
-    pl.x = slot->x;
-  }
-  return pl;
+  return slot->plan;
 }
 
 __device__ __forceinline__ Groups load_groups(const HParams &p, int32_t *s_off) {
@@ -219,40 +240,43 @@ struct Segment {
 struct Walker {
   const HParams &p;
   const Groups gr;
-  int64_t at, end, es;
-  int e, have;
-  Entry x;
-  __device__ __forceinline__ Walker(const HParams &p_, const Plan &pl)
-      : p(p_), gr{p_.group_off}, at(pl.begin), end(pl.end), es(pl.entry_start), e(pl.entry), have(pl.entry), x(pl.x) {}
+  Plan w;
+  __device__ __forceinline__ Walker(const HParams &p_, const Plan &pl) : p(p_), gr{p_.group_off}, w(pl) {}
   __device__ __forceinline__ bool next(Segment &s) {
-    while (at < end) {
-      if (have != e) {
-        x = entry(p, gr, e);
-        have = e;
-      }
-      const int64_t size = x.length(p.hkv);
-      if (at >= es + size) {
-        es += size;
-        ++e;
+    while (w.left > 0) {
+      if (w.x.tiles == 0) {
+        if (++w.entry >= p.num_groups + p.R) return false;
+        w.x = entry(p, gr, w.entry);
         continue;
       }
-      const int sub = static_cast<int>((at - es) / x.span);
-      const int from = static_cast<int>(at - es - static_cast<int64_t>(sub) * x.span);
-      const int to = static_cast<int>(min(static_cast<int64_t>(x.span), from + (end - at)));
-      at += to - from;
-      s.t0 = max(from - kItemCost, 0);
-      s.n = to - kItemCost - s.t0;
-      if (s.n <= 0) continue;   // no more than the item's start
-      s.x = x;
-      s.e = e;
-      s.h = sub / x.blocks;
-      s.n0 = (sub - s.h * x.blocks) * p.block;
-      s.rows = min(x.rows - s.n0, p.block);
-      return true;
+      const int cost = w.x.cost(p, w.block), span = static_cast<int>(w.x.span(cost));
+      const int to = static_cast<int>(min(static_cast<int64_t>(span), w.from + w.left));
+      auto tiles_before = [&](int at) {   // tiles that start before unit `at`
+        const int u = max(at - kItemCost, 0) + cost - 1;
+        return cost == 2 ? u >> 1 : u / 3;
+      };
+      s.t0 = tiles_before(w.from);
+      s.n = tiles_before(to) - s.t0;
+      s.x = w.x;
+      s.e = w.entry;
+      s.h = w.h;
+      s.n0 = w.block * p.block;
+      s.rows = min(w.x.rows - s.n0, p.block);
+      w.left -= to - w.from;
+      w.from = 0;
+      if (++w.block == w.x.blocks) {
+        w.block = 0;
+        if (++w.h == p.hkv) {
+          w.h = 0;
+          w.x.tiles = 0;   // on to the next entry
+        }
+      }
+      if (s.n > 0) return true;   // else no more than the item's start, or the rest of a tile
     }
     return false;
   }
 };
+static_assert(kTileCost == 2 && kWideCost == 3, "Walker divides by these");
 
 // ------------------------------------------------------------------------------------------------- plain arithmetic
 // fp32 pools: a warp takes every eighth row of a block of 32 and all tokens of a tile, a lane every 32nd dim.
@@ -984,53 +1008,101 @@ __device__ __forceinline__ int find_last(const int32_t *a, int n, int key) {
   return lo;
 }
 
+// The N consecutive elements of a lane, as one load.
+template <int N> __device__ __forceinline__ void lane_load(const __nv_bfloat16 *p, float *v) {
+  uint32_t w[N / 2];
+  if (N == 4) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    w[0] = u.x;
+    w[N / 2 - 1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <int N> __device__ __forceinline__ void lane_load(const float *p, float *v) {
+  if (N == 4) {
+    const float4 u = *reinterpret_cast<const float4 *>(p);
+    v[0] = u.x, v[1] = u.y, v[N - 2] = u.z, v[N - 1] = u.w;
+  } else {
+    const float2 u = *reinterpret_cast<const float2 *>(p);
+    v[0] = u.x, v[1] = u.y;
+  }
+}
+
 // One warp a query row: the window's tokens up to itself, and its records of the prefix and of the own context. All but
 // the records is older than the first kernel, so it is done before that kernel's end is waited for.
 template <class T, int D>
 __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
   constexpr int PL = D / 32;  // consecutive dims of a lane
-  constexpr int CH = 8;       // records whose loads are in flight together
+  constexpr int CH = 8;       // records, and WT window tokens, whose loads are in flight together
+  constexpr int WT = 4;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const bool live = wid < static_cast<int64_t>(p.total_q) * p.hq;
   float m = -INFINITY, l = 0.0f, o[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.0f;
-  int t = 0, hq = 0, h = 0, ent[2] = {-1, -1}, row[2] = {0, 0}, blocks[2] = {0, 0}, tiles[2] = {0, 0};
-  int q0[2] = {0, 0};
+  int t = 0, hq = 0, h = 0, ent[2] = {-1, -1};
+  int64_t at[2] = {0, 0}, end[2] = {0, 0};   // from the entry's start: the item's first tile and its last one's start
+  int q0[2] = {0, 0}, row[2] = {0, 0};
   if (live) {
-    t = static_cast<int>(wid / p.hq);
+    t = static_cast<int>(quotient(wid, p.hq));
     hq = static_cast<int>(wid - static_cast<int64_t>(t) * p.hq);
     h = hq / p.G;
-    const T *qr = static_cast<const T *>(p.q) + (static_cast<size_t>(t) * p.hq + hq) * D + lane * PL;
-    const float scale = rsqrtf(static_cast<float>(D)) * kLog2e;
     float qv[PL];
+    lane_load<PL>(static_cast<const T *>(p.q) + (static_cast<size_t>(t) * p.hq + hq) * D + lane * PL, qv);
+    const float scale = rsqrtf(static_cast<float>(D)) * kLog2e;
 #pragma unroll
-    for (int k = 0; k < PL; ++k) qv[k] = to_f(qr[k]) * scale;
+    for (int k = 0; k < PL; ++k) qv[k] *= scale;
     const int r = find_last(p.q_offsets, p.R, t);
-    const int start = p.q_start[r];
-    if (start > p.max_pages * kPage && lane == 0) set_error(p.err, kErrPage);   // context past the table's end
-    const int pos1 = start > p.max_pages * kPage ? -1 : start + (t - p.q_offsets[r]);
-    for (int pos = max(start, 0); pos <= pos1; ++pos) {
-      const int pg = pos / kPage < p.max_pages ? p.bt[static_cast<size_t>(r) * p.max_pages + pos / kPage] : -1;
-      if (pg < 0 || pg >= p.num_pages) {
-        if (lane == 0) set_error(p.err, kErrPage);
-        continue;
-      }
-      const size_t off = ((static_cast<size_t>(pg) * p.hkv + h) * kPage + pos % kPage) * D + lane * PL;
-      const T *kr = static_cast<const T *>(p.K) + off, *vr = static_cast<const T *>(p.V) + off;
-      float s = 0.0f, v[PL];
+    const int start = p.q_start[r], past = p.max_pages * kPage;
+    if (start > past && lane == 0) set_error(p.err, kErrPage);   // context past the table's end
+    const int pos0 = max(start, 0), pos1 = start > past ? -1 : start + (t - p.q_offsets[r]);
+    // the window's pages: 64 tokens lie on no more than 5
+    const int page0 = pos0 / kPage;
+    int my_page = -1;
+    if (lane <= pos1 / kPage - page0 && page0 + lane < p.max_pages)
+      my_page = p.bt[static_cast<size_t>(r) * p.max_pages + page0 + lane];
+    for (int base = pos0; base <= pos1; base += WT) {
+      float kv[WT][PL], vv[WT][PL], s[WT];
 #pragma unroll
-      for (int k = 0; k < PL; ++k) {
-        s = fmaf(qv[k], to_f(kr[k]), s);
-        v[k] = to_f(vr[k]);
+      for (int c = 0; c < WT; ++c) {
+        const int pos = min(base + c, pos1);
+        const int pg = __shfl_sync(0xffffffffu, my_page, pos / kPage - page0);
+        const bool ok = pg >= 0 && pg < p.num_pages;
+        s[c] = ok && base + c <= pos1 ? 0.0f : -INFINITY;
+        if (!ok && lane == 0) set_error(p.err, kErrPage);
+        const size_t off = ((static_cast<size_t>(ok ? pg : 0) * p.hkv + h) * kPage + pos % kPage) * D + lane * PL;
+        lane_load<PL>(static_cast<const T *>(p.K) + off, kv[c]);
+        lane_load<PL>(static_cast<const T *>(p.V) + off, vv[c]);
       }
-      s = warp_sum(s);
-      const float mn = fmaxf(m, s);
-      const float a = m == -INFINITY ? 0.0f : exp2f(m - mn), w = s == -INFINITY ? 0.0f : exp2f(s - mn);
-      l = fmaf(l, a, w);
+      float mn = m;
 #pragma unroll
-      for (int k = 0; k < PL; ++k) o[k] = fmaf(w, v[k], o[k] * a);
+      for (int c = 0; c < WT; ++c) {
+        float x = 0.0f;
+#pragma unroll
+        for (int k = 0; k < PL; ++k) x = fmaf(qv[k], kv[c][k], x);
+        x = warp_sum(x);
+        if (s[c] == 0.0f) s[c] = x;
+        mn = fmaxf(mn, s[c]);
+      }
+      const float a = m == -INFINITY ? 0.0f : exp2f(m - mn);
+      l *= a;
+#pragma unroll
+      for (int k = 0; k < PL; ++k) o[k] *= a;
+#pragma unroll
+      for (int c = 0; c < WT; ++c) {
+        if (s[c] == -INFINITY) continue;   // no token, or of weight zero
+        const float w = exp2f(s[c] - mn);
+        l += w;
+#pragma unroll
+        for (int k = 0; k < PL; ++k) o[k] = fmaf(w, vv[c][k], o[k]);
+      }
       m = mn;
     }
     const Groups gr{p.group_off};
@@ -1043,22 +1115,26 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
     for (int kind = 0; kind < 2; ++kind)
       if (ent[kind] >= 0) {
         const Entry x = entry(p, gr, ent[kind]);
-        tiles[kind] = x.tiles;
-        blocks[kind] = x.blocks;
+        if (x.tiles == 0) {
+          ent[kind] = -1;
+          continue;
+        }
         q0[kind] = x.q0;
         row[kind] = (t - x.q0) * p.G + hq - h * p.G;
+        const int block = row[kind] / p.block;
+        at[kind] = x.first_tile(p, h, block);
+        end[kind] = at[kind] + static_cast<int64_t>(x.tiles - 1) * x.cost(p, block);
       }
   }
   grid_dependency_sync();
   if (!live) return;
   const int64_t total = p.start[p.num_groups + p.R];
-  const int nb = static_cast<int>(min(total, static_cast<int64_t>(p.nb)));
+  const int nb = parts(p, total);
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
-    if (ent[kind] < 0 || tiles[kind] == 0) continue;
-    const int64_t first = p.start[ent[kind]] + kItemCost +
-                          (static_cast<int64_t>(h) * blocks[kind] + row[kind] / p.block) * (tiles[kind] + kItemCost);
-    const int b0 = owner_cta(first, total, nb), b1 = owner_cta(first + tiles[kind] - 1, total, nb);
+    if (ent[kind] < 0) continue;
+    const int64_t es = p.start[ent[kind]];
+    const int b0 = owner_cta(es + at[kind], total, nb), b1 = owner_cta(es + end[kind], total, nb);
     Entry x;
     x.q0 = q0[kind];
     for (int c0 = b0; c0 <= b1; c0 += CH) {   // a chunk's records: all loads first, then one step for all
@@ -1069,11 +1145,12 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
         const int b = min(c0 + c, b1);
         const Place pp = place<D>(p, x, kind, h, row[kind], b > b0, b);
         ml[c] = __ldcg(pp.ml);
-#pragma unroll
-        for (int k = 0; k < PL; k += 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2 *>(pp.o + lane * PL + k));
-          rec[c][k] = v.x;
-          rec[c][k + 1] = v.y;
+        if (PL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(pp.o + lane * PL));
+          rec[c][0] = v.x, rec[c][1] = v.y, rec[c][PL - 2] = v.z, rec[c][PL - 1] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(pp.o + lane * PL));
+          rec[c][0] = v.x, rec[c][1] = v.y;
         }
       }
       float mn = m;
