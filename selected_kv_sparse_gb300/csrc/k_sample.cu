@@ -77,13 +77,72 @@ __device__ __forceinline__ void st_remote32(uint32_t a, uint32_t v) {
 __device__ __forceinline__ float key_value(uint32_t k) {  // inverse of order_key
   return k == 0u ? NAN : __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
+// 2^(-j/64) for j < 64: as a sum of two fp32 and times 2^44, from the exponential series.
+struct Powers {
+  float2 f[64];
+  u64 q[64];
+};
+constexpr double power_series(int j) {
+  const double x = -0.69314718055994530942 * j / 64.0;
+  double t = 1.0, s = 1.0;
+  for (int n = 1; n < 30; ++n) {
+    t *= x / n;
+    s += t;
+  }
+  return s;
+}
+constexpr Powers make_powers() {
+  Powers t{};
+  for (int j = 0; j < 64; ++j) {
+    const double v = power_series(j);
+    t.f[j].x = static_cast<float>(v);
+    t.f[j].y = static_cast<float>(v - static_cast<double>(t.f[j].x));
+    t.q[j] = static_cast<u64>(v * 17592186044416.0 + 0.5);
+  }
+  return t;
+}
+__device__ const Powers kPowers = make_powers();
+
+// exp((x - m) / T) as a whole number of 2^-qb, right to about 2^-40 of itself and a half unit, for x <= m that is no NaN:
+// with y = (m - x) log2 e / T as a sum of two fp32, k the nearest whole number to 64 y and r = y - k / 64,
+//   2^-y = 2^(-k/64) (1 - t + t^2/2 - t^3/6 + t^4/24),  t = r ln 2 <= 0.0055, t's leading term again as two fp32.
+// From y = 22 on (weights below 2^-22, units 2^-44) the exponential unit's 2^-22 of the value is below a unit.
 struct Weigh {
-  double c, m;   // log2 e / T, the largest logit
-  int qb;
+  float m, ch, cl;   // largest logit; log2 e / T
+  int down;          // 44 - qb
+  const Powers *tab;
   __device__ __forceinline__ u64 operator()(float x) const {
-    const double y = (m - static_cast<double>(x)) * c;
-    if (!(y < 64.0)) return 0;
-    return static_cast<u64>(__double2ll_rn(ldexp(exp2(-y), qb)));
+    // m - x, exactly (two-sum)
+    const float dh = m - x, bb = m - dh, dl = (m - (dh + bb)) + (bb - x);
+    const float yh = dh * ch;
+    const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
+    if (!(yh < 62.0f)) return 0;   // also an infinite distance
+    constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
+    u64 w;
+    int e;
+    if (yh >= 22.0f) {
+      float v;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(44.0f - yh));   // the difference is exact
+      v = fmaf(v, -yl * kLn2h, v);
+      return (static_cast<u64>(__float_as_uint(v + 12582912.0f) - 0x4b400000u) + ((1u << down) >> 1)) >> down;
+    }
+    const float kf = fmaf(yh, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
+    const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
+    const float r = fmaf(kf - 12582912.0f, -0.015625f, yh);
+    const float th = r * kLn2h, tl = fmaf(r, kLn2h, -th) + fmaf(r, kLn2l, yl * kLn2h);
+    const float q = th * th * fmaf(th, fmaf(th, 0.0416666679f, -0.166666672f), 0.5f) - tl;
+    const float2 f = tab->f[k & 63];
+    const float ph = f.x * -th;
+    const float pl = fmaf(f.x, -th, -ph) + fmaf(f.x, q, f.y * -th);
+    // ph + pl in units of 2^-44, through the low bits of sums at 3 (unit 2^-22) and at 3 * 2^-22
+    const float u = ph + pl, ub = u - ph, ul = (ph - (u - ub)) + (pl - ub);
+    const float s1 = u + 3.0f;
+    const int i1 = static_cast<int>(__float_as_uint(s1) - 0x40400000u);
+    const float rest = (u - (s1 - 3.0f)) + ul;
+    const int i2 = static_cast<int>(__float_as_uint(rest + 7.152557373046875e-7f) - 0x35400000u);
+    w = tab->q[k & 63] + static_cast<u64>(static_cast<int64_t>(i1) * (1 << 22) + i2);
+    e = (k >> 6) + down;
+    return (w + ((u64(1) << e) >> 1)) >> e;
   }
 };
 
@@ -130,22 +189,52 @@ struct Row {
   // The N logits of vector j; -infinity outside the row.
   __device__ __forceinline__ void load(int j, float *x) const {
     const int id = j * N - sh;
-    if (id >= 0 && id + N <= V) {
-      Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(base + static_cast<int64_t>(j) * N), x);
+    if (inside(j)) {
+      Vec16<T>::unpack(at(j), x);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
         x[i] = (id + i >= 0 && id + i < V) ? to_f(base[static_cast<int64_t>(j) * N + i]) : -INFINITY;
     }
   }
-  // f(x, id) for this thread's logits, which are in its warp's range; ids outside the row come with -infinity.
+  // f(x, id) for this thread's logits, which are in its warp's range; ids outside the row come with -infinity. The next
+  // vector is on its way while f sees this one.
   template <class F> __device__ __forceinline__ void each(F &&f) const {
-    for (int j = v0 + (threadIdx.x & 31); j < v1; j += 32) {
+    int j = v0 + (threadIdx.x & 31);
+    uint4 raw{};
+    if (j < v1 && inside(j)) raw = at(j);
+#pragma unroll 1
+    for (; j < v1; j += 32) {
       float x[N];
-      load(j, x);
+      if (inside(j)) Vec16<T>::unpack(raw, x);
+      else load(j, x);
+      if (j + 32 < v1 && inside(j + 32)) raw = at(j + 32);
 #pragma unroll
       for (int i = 0; i < N; ++i) f(x[i], j * N - sh + i);
     }
+  }
+  // f(x) for the same logits in light passes: four vectors on their way together.
+  template <class F> __device__ __forceinline__ void each_light(F &&f) const {
+#pragma unroll 1
+    for (int j = v0 + (threadIdx.x & 31); j < v1; j += 128) {
+      uint4 raw[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + 32 * k < v1 && inside(j + 32 * k)) raw[k] = at(j + 32 * k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (j + 32 * k >= v1) break;
+        float x[N];
+        if (inside(j + 32 * k)) Vec16<T>::unpack(raw[k], x);
+        else load(j + 32 * k, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f(x[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ bool inside(int j) const { return j * N - sh >= 0 && (j + 1) * N - sh <= V; }
+  __device__ __forceinline__ uint4 at(int j) const {
+    return *reinterpret_cast<const uint4 *>(base + static_cast<int64_t>(j) * N);
   }
 };
 
@@ -209,57 +298,101 @@ struct Sampler {
     return b;
   }
 
-  // The least logit of the shortest run of the rank order, among logits whose key is `floor` or more, that holds `target`
-  // tokens (by_weight false) or that much weight. Out: its key, how many tokens at it and above it there are, and the
-  // weight above (by_weight). The run has to exist.
-  __device__ void find(bool by_weight, u64 target, uint32_t floor, uint32_t top, uint32_t &key, u64 &at, u64 &above,
-                       u64 &above_w) {
-    const float m = static_cast<float>(weigh.m);
-    const float c = static_cast<float>(fmin(weigh.c, 3.0e38));
+  // Histogram of the distances to the maximum, 1/16 octave of weight a bin, of the logits from `least` on: their number,
+  // and their weight (of those at `least`, only `ties` count where they are fewer). s.total holds the bins.
+  struct Mass {
+    u64 count, weight;
+  };
+  __device__ Mass histogram(float least, bool weights) {
     for (int i = threadIdx.x; i < kBins; i += kSaThreads) s.hist[i] = 0;
     __syncthreads();
-    row.each([&](float x, int) {
-      if (order_key(x) >= floor && x > -INFINITY) {
-        const float y = (m - x) * c * kBinsPerOctave;
-        atomicAdd(&s.hist[y < kBins - 1 ? static_cast<int>(y) : kBins - 1], 1u);
-      }
-    });
-    join_hist();
-    // the roundings of y widen each bin by less than 2^-20 of its distance
-    auto edge = [&](double b, double slack) {
-      const double y = b / kBinsPerOctave * (1.0 + slack);
-      return y < 64.0 ? ldexp(exp2(-y), weigh.qb) : 0.0;
+    const float m = weigh.m, c = weigh.ch * kBinsPerOctave;
+    u64 n = 0, w = 0;
+    auto count = [&](float x) {
+      ++n;
+      const float y = (m - x) * c;
+      atomicAdd(&s.hist[y < kBins - 1 ? static_cast<int>(y) : kBins - 1], 1u);
     };
+    if (weights) {
+      row.each([&](float x, int) {
+        if (x >= least) {
+          count(x);
+          w += weigh(x);
+        }
+      });
+    } else {
+      row.each_light([&](float x) {
+        if (x >= least) count(x);
+      });
+    }
+    Mass r;
+    r.count = cluster_sum(n);
+    r.weight = weights ? cluster_sum(w) : 0;
+    join_hist();
+    return r;
+  }
+  // A logit at or above (up) or at or below all of the logits b bins from the maximum: rounding of the bin's number, of
+  // the distance and of the sum widen it.
+  __device__ float bin_edge(float b, bool up) const {
+    const float d = fmaxf(b + (up ? -0.05f : 0.05f), 0.0f) / (weigh.ch * kBinsPerOctave);
+    if (!(d < 1e38f)) return up ? weigh.m : -INFINITY;
+    const float slack = (fabsf(weigh.m) + d) * 9.5e-7f;
+    return up ? fminf(weigh.m, weigh.m - d + slack) : weigh.m - d - slack;
+  }
+
+  // After histogram(key_value(floor)): the least logit of the shortest run of the rank order, among logits whose key is
+  // `floor` or more, that holds `target` tokens (by_weight false) or that much weight. Out: its key, how many tokens at it
+  // and above it there are, and the weight above (by_weight). The run has to exist.
+  __device__ void find(bool by_weight, u64 target, uint32_t floor, uint32_t top, uint32_t &key, u64 &at, u64 &above,
+                       u64 &above_w) {
     int b0, b1;
     if (by_weight) {
-      b0 = first_bin(0, target, [&](int b) { return s.total[b] * static_cast<u64>(ceil(edge(b, -1e-6)) + 1.0); });
+      // the weight at a bin's edge, b / 16 octaves down; a logit's bin may be off by 2^-19 of its distance (2^-12 of a weight)
+      auto edge = [&](int b) {
+        const int e = (b >> 4) + weigh.down;
+        return e < 64 ? weigh.tab->q[(b & 15) * 4] >> e : u64(0);
+      };
+      b0 = first_bin(0, target, [&](int b) {
+        const u64 w = edge(b);
+        return s.total[b] * (w + (w >> 12) + 4);
+      });
       b1 = first_bin(0, target, [&](int b) {
-        return b == kBins - 1 ? 0 : s.total[b] * static_cast<u64>(fmax(edge(b + 1, 1e-6) - 1.0, 0.0));
+        const u64 w = edge(b + 1);
+        return b == kBins - 1 || w < 8 ? u64(0) : s.total[b] * (w - (w >> 12) - 4);
       });
     } else {
       b0 = b1 = first_bin(0, target, [&](int b) { return static_cast<u64>(s.total[b]); });
     }
-    // the interval of keys that the bins b0 .. b1 can hold, widened by a part of a bin
+    // the interval of keys that the bins b0 .. b1 can hold
     uint32_t khi = top, klo = floor;
-    const double bin = 1.0 / (static_cast<double>(c) * kBinsPerOctave);
-    if (b0 > 0) khi = min(top, order_key(__double2float_ru(weigh.m - (b0 - 0.01) * (1.0 - 1e-6) * bin)));
-    if (b1 < kBins - 1) klo = max(floor, order_key(__double2float_rd(weigh.m - (b1 + 1.01) * (1.0 + 1e-6) * bin)));
+    if (b0 > 0) khi = min(top, order_key(bin_edge(static_cast<float>(b0), true)));
+    if (b1 < kBins - 1) klo = max(floor, order_key(bin_edge(static_cast<float>(b1 + 1), false)));
     khi = max(khi, klo);
     while (true) {
       const uint32_t range = khi - klo;
       const int sh = max(0, 32 - __clz(range) - 11);
+      const float vhi = key_value(khi), vlo = key_value(klo);
       for (int i = threadIdx.x; i < kBins; i += kSaThreads) s.hist[i] = 0;
       __syncthreads();
       u64 n = 0, w = 0;
-      row.each([&](float x, int) {
-        const uint32_t k = order_key(x);
-        if (k > khi) {
-          ++n;
-          if (by_weight) w += weigh(x);
-        } else if (k >= klo && x > -INFINITY) {
-          atomicAdd(&s.hist[(khi - k) >> sh], 1u);
-        }
-      });
+      auto place = [&](float x) {
+        if (x >= vlo) atomicAdd(&s.hist[(khi - order_key(x)) >> sh], 1u);
+      };
+      if (by_weight) {
+        row.each([&](float x, int) {
+          if (x > vhi) {
+            ++n;
+            w += weigh(x);
+          } else {
+            place(x);
+          }
+        });
+      } else {
+        row.each_light([&](float x) {
+          if (x > vhi) ++n;
+          else place(x);
+        });
+      }
       above = cluster_sum(n);
       above_w = by_weight ? cluster_sum(w) : 0;
       join_hist();
@@ -269,12 +402,13 @@ struct Sampler {
         return d > range ? klo : khi - static_cast<uint32_t>(d);
       };
       auto weight_of = [&](uint32_t k) { return weigh(key_value(k)); };
-      auto used = [&](int b) { return (static_cast<u64>(b) << sh) <= range; };
+      auto used = [&](int b) { return s.total[b] != 0 && (static_cast<u64>(b) << sh) <= range; };
       if (by_weight) {
-        b0 = first_bin(above_w, target,
-                       [&](int b) { return used(b) && s.total[b] ? s.total[b] * weight_of(hi_key(b)) : u64(0); });
+        const u64 more = sh == 0 ? 0 : 4;   // neighbours' weights may be out of order by their rounding
+        b0 = first_bin(above_w, target, [&](int b) { return used(b) ? s.total[b] * (weight_of(hi_key(b)) + more) : u64(0); });
         b1 = sh == 0 ? b0 : first_bin(above_w, target, [&](int b) {
-          return used(b) && s.total[b] ? s.total[b] * weight_of(lo_key(b)) : u64(0);
+          const u64 lw = used(b) ? weight_of(lo_key(b)) : 0;
+          return lw > more ? s.total[b] * (lw - more) : u64(0);
         });
       } else {
         b0 = b1 = first_bin(above, target, [&](int b) { return static_cast<u64>(s.total[b]); });
@@ -303,11 +437,13 @@ struct Sampler {
         continue;
       }
       // the bounds leave more than half of the interval (weights far apart within a part): one halving by the exact sum
-      const uint32_t mid = klo + range / 2;
+      const float mid = key_value(klo + range / 2);
       w = 0;
-      row.each([&](float x, int) { w += order_key(x) > mid ? weigh(x) : u64(0); });
-      if (cluster_sum(w) >= target) klo = mid + 1;
-      else khi = mid;
+      row.each([&](float x, int) {
+        if (x > mid) w += weigh(x);
+      });
+      if (cluster_sum(w) >= target) klo += range / 2 + 1;
+      else khi = klo + range / 2;
     }
   }
 
@@ -399,7 +535,7 @@ __device__ __forceinline__ u64 part_of(u64 x, float f, bool up) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(kSaThreads) sample_kernel(const SParams p) {
+__global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) {
   __shared__ Shared s;
   grid_dependency_sync();
   const int nc = cluster_size(), rank = cluster_rank();
@@ -411,12 +547,13 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SParams p) {
   Sampler<T> a{row, s, rank, nc, 0, {}};
 
   // ---- the largest logit, and whether the row is a distribution
-  uint32_t best = 0;   // key: 0 stands for no number
+  float mx = -INFINITY;
   bool nan = false;
-  row.each([&](float x, int) {
+  row.each_light([&](float x) {
     nan |= x != x;
-    best = max(best, order_key(x));
+    mx = fmaxf(mx, x);
   });
+  uint32_t best = order_key(mx);
   best = __reduce_max_sync(0xffffffffu, best);
   nan = __any_sync(0xffffffffu, nan);
   if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = (static_cast<u64>(best) << 1) | (nan ? 1 : 0);
@@ -440,72 +577,90 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SParams p) {
   const bool sound = !nan && fabsf(m) < INFINITY;
   float x_tok = m;
   int token;
-  float lp;
-  u64 count;
+  float lp = 0.0f;
+  u64 count = 0;
   if (!sound || !(temp > 0.0f)) {   // the first of the rank order
-    token = a.locate(0, [&](float x, int id) -> u64 { return id >= 0 && id < p.V && order_key(x) == best ? 1 : 0; }, x_tok);
+    // (in a row of -infinity and NaN the first -infinity, of NaN alone token 0)
+    token = a.locate(0, [&](float x, int id) -> u64 { return id >= 0 && id < p.V && x == m ? 1 : 0; }, x_tok);
     lp = sound ? 0.0f : NAN;
     count = sound ? 1 : 0;
   } else {
-    a.weigh = Weigh{1.4426950408889634 / static_cast<double>(temp), static_cast<double>(m), p.qb};
-    uint32_t floor = order_key(-INFINITY) + 1;
+    const double cd = 1.4426950408889634 / static_cast<double>(temp);
+    const float ch = static_cast<float>(cd);
+    a.weigh = Weigh{m, ch, static_cast<float>(cd - static_cast<double>(ch)), 44 - p.qb, &kPowers};
+    float least = -3.402823466e38f;
     if (mp > 0.0f) {
-      const double least = static_cast<double>(m) + static_cast<double>(temp) * log(fmin(static_cast<double>(mp), 1.0));
-      floor = max(floor, order_key(fmaxf(__double2float_ru(least), -3.402823466e38f)));
-      floor = min(floor, best);
+      if (threadIdx.x == 0)
+        s.pick[1] = __float_as_uint(__double2float_ru(
+            static_cast<double>(m) + static_cast<double>(temp) * log(fmin(static_cast<double>(mp), 1.0))));
+      __syncthreads();
+      least = fminf(m, fmaxf(least, __uint_as_float(static_cast<uint32_t>(s.pick[1]))));
     }
-    // the tokens from `floor` on; at it the first `ties` in id order
-    u64 ties = ~u64(0);
+    // kept: the logits above `least`, and of those at it the first `ties` in id order
+    uint32_t floor = order_key(least);
+    constexpr u64 kAll = ~u64(0);
+    u64 ties = kAll, total = 0;
     int id_cut = 0x7fffffff;
-    u64 n = 0;
-    row.each([&](float x, int) { n += order_key(x) >= floor && x > -INFINITY ? 1 : 0; });
-    count = a.cluster_sum(n);
-    if (k > 0 && static_cast<u64>(k) < count) {
-      uint32_t key;
-      u64 at, above, unused;
-      a.find(false, k, floor, best, key, at, above, unused);
-      floor = key;
-      ties = min(at, static_cast<u64>(k) - above);
-      if (ties == at) ties = ~u64(0);
-      count = k;
+    bool counted = false, summed = false;
+    const bool by_p = tp < 1.0f;
+    if (k > 0 && k < p.V) {
+      const auto mass = a.histogram(least, false);
+      count = mass.count;
+      counted = true;
+      if (static_cast<u64>(k) < count) {
+        uint32_t key;
+        u64 at, above, unused;
+        a.find(false, k, floor, best, key, at, above, unused);
+        floor = key;
+        least = key_value(key);
+        ties = static_cast<u64>(k) - above < at ? static_cast<u64>(k) - above : kAll;
+        count = k;
+      }
     }
-    u64 total = 0;
-    bool have_total = false;
-    if (tp < 1.0f) {
-      const float fl = key_value(floor);
-      u64 w = 0;
-      row.each([&](float x, int) { w += order_key(x) > floor || (ties == ~u64(0) && x == fl) ? a.weigh(x) : u64(0); });
-      total = a.cluster_sum(w) + (ties == ~u64(0) ? 0 : ties * a.weigh(fl));
-      const u64 target = max(u64(1), part_of(total, tp, true));
+    if (by_p) {
+      auto mass = a.histogram(least, true);
+      const u64 w_least = a.weigh(least);
+      u64 n_all = mass.count;
+      if (ties != kAll) {   // tokens at the least logit that top_k does not keep
+        const u64 dropped = mass.count - count;
+        mass.weight -= dropped * w_least;
+        n_all = count;
+      }
+      const u64 target = max(u64(1), part_of(mass.weight, tp, true));
       uint32_t key;
       u64 at, above, above_w;
       a.find(true, target, floor, best, key, at, above, above_w);
       const u64 each = a.weigh(key_value(key));
-      if (key == floor && ties != ~u64(0)) at = ties;
+      if (key == floor) at = min(at, n_all - above);
       const u64 need = each ? min(at, (target - above_w + each - 1) / each) : at;
       count = above + need;
       total = above_w + need * each;
-      have_total = true;
-      if (key != floor || ties == ~u64(0)) ties = need < at ? need : ~u64(0);
-      else ties = need;
+      counted = summed = true;
+      ties = need < at || (key == floor && ties != kAll) ? need : kAll;
       floor = key;
+      least = key_value(key);
     }
-    if (ties != ~u64(0)) {
+    if (ties != kAll) {
       float unused;
-      id_cut = a.locate(ties - 1, [&](float x, int) -> u64 { return order_key(x) == floor ? 1 : 0; }, unused);
+      id_cut = a.locate(ties - 1, [&](float x, int) -> u64 { return x == least ? 1 : 0; }, unused);
     }
     auto weight = [&](float x, int id) -> u64 {
-      const uint32_t key = order_key(x);
-      return (key > floor || (key == floor && id <= id_cut)) && x > -INFINITY ? a.weigh(x) : u64(0);
+      return x > least || (x == least && id <= id_cut) ? a.weigh(x) : u64(0);
     };
-    if (!have_total) {
+    if (!counted) {   // the kept tokens' number and weight come with the sums of the draw below
+      u64 n = 0;
+      row.each_light([&](float x) { n += x >= least ? 1 : 0; });
+      count = a.cluster_sum(n);
+    }
+    if (!summed) {
       u64 w = 0;
       row.each([&](float x, int id) { w += weight(x, id); });
       total = a.cluster_sum(w);
     }
     const float u = p.u[r];
     token = a.locate(part_of(total, u == u ? fminf(u, 0.99999994f) : 0.0f, false), weight, x_tok);
-    lp = static_cast<float>((static_cast<double>(x_tok) - m) / temp - log(ldexp(static_cast<double>(total), -p.qb)));
+    if (rank == 0 && threadIdx.x == 0)
+      lp = static_cast<float>((static_cast<double>(x_tok) - m) / temp - log(ldexp(static_cast<double>(total), -p.qb)));
   }
   if (rank == 0 && threadIdx.x == 0) {
     p.tokens[r] = max(token, 0);
