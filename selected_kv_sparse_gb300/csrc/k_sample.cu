@@ -146,14 +146,53 @@ struct Weigh {
   }
 };
 
+constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept
+constexpr int kFew = kSaThreads;   // candidates that are sorted and drawn from directly
+constexpr int kMaxFewK = 256;      // top_k up to which the candidates are gathered
+constexpr int kFewBar = 64;        // candidates to gather, about, where top_k does not say
+// Logits of 16 bits from 2^-10 to 2^10 in magnitude, counted by value: 2560 of either sign, the largest first.
+constexpr int kValues = 5120, kHalfValues = kValues / 2;
+constexpr uint32_t kFirstValue = 0x3A80, kEndValue = 0x4480;   // bits of 2^-10 and 2^10
+constexpr int kOdd = 512;          // logits of other magnitudes that a CTA keeps aside
+
 struct Shared {
-  uint32_t hist[kBins], total[kBins];
+  uint32_t hist[kValues], total[kValues];
+  union {
+    u64 weight[kValues];   // of each counted value
+    struct {
+      u64 list[kFew], sorted[kFew], w[kFew];   // candidates: key and inverted id; their weights
+      float tile[kSaWarps * kTiles];
+    } few;
+  };
+  Powers powers;
+  float odd[kOdd];
   u64 scan[kSaWarps];
   u64 sums[2][2];   // values for the other CTAs, in turn: a slot is written again two exchanges later
   u64 pick[6];
+  float fscan[kSaWarps];
+  uint32_t few_count, few_done, odd_count;
 };
 
 __device__ __forceinline__ u64 shfl_up64(u64 v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_top(float a) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_remote32(uint32_t a, uint32_t v) {
+  uint32_t o;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(o) : "r"(a), "r"(v) : "memory");
+  return o;
+}
+__device__ __forceinline__ void st_remote64(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
 
 // Sum over the block, to every thread.
 __device__ __forceinline__ u64 block_sum(u64 v, u64 *scratch) {
@@ -238,6 +277,19 @@ struct Row {
   }
 };
 
+// x * f for a fraction f in [0, 1): rounded down, or up.
+__device__ __forceinline__ u64 part_of(u64 x, float f, bool up) {
+  if (!(f > 0.0f)) return 0;
+  const uint32_t b = __float_as_uint(f);
+  const int e = static_cast<int>(b >> 23);
+  const uint32_t man = e ? ((b & 0x7fffffu) | 0x800000u) : (b & 0x7fffffu);
+  const int sh = 150 - (e ? e : 1);
+  const unsigned __int128 p = static_cast<unsigned __int128>(x) * man;
+  if (sh >= 127) return up ? 1 : 0;
+  const u64 q = static_cast<u64>(p >> sh);
+  return q + ((up && (static_cast<unsigned __int128>(q) << sh) != p) ? 1 : 0);
+}
+
 template <class T>
 struct Sampler {
   const Row<T> &row;
@@ -257,18 +309,18 @@ struct Sampler {
     return t;
   }
   // The cluster's histogram: s.hist of every CTA added up into s.total of every CTA.
-  __device__ void join_hist() {
+  __device__ void join_hist(int bins = kBins) {
     __syncthreads();
     if (nc == 1) {
-      for (int i = threadIdx.x; i < kBins; i += kSaThreads) s.total[i] = s.hist[i];
+      for (int i = threadIdx.x; i < bins; i += kSaThreads) s.total[i] = s.hist[i];
       __syncthreads();
       return;
     }
     cluster_sync();
-    const int per = (kBins + nc - 1) / nc;
+    const int per = (bins + nc - 1) / nc;
     for (int i = threadIdx.x; i < per; i += kSaThreads) {
       const int b = rank * per + i;
-      if (b < kBins) {
+      if (b < bins) {
         uint32_t t = 0;
         for (int r = 0; r < nc; ++r) t += ld_remote32(remote(&s.hist[b], r));
         for (int r = 0; r < nc; ++r) st_remote32(remote(&s.total[b], r), t);
@@ -447,9 +499,185 @@ struct Sampler {
     }
   }
 
-  // The id at which the running sum in id order of amount(x, id) first passes `target`, and that logit; -1 if it never
-  // does. Every thread of the cluster gets them.
-  template <class F> __device__ int locate(u64 target, F &&amount, float &value) {
+  // One pass: this lane's largest logit, the sum of 2^((x - ref) c) with ref the larger of that and -1e30 (NaN where a
+  // logit is), and the maxima of tiles of the warp's range.
+  int tile_iters;
+  __device__ void first_pass(float c, float &mx, float &ref, float &sum) {
+    constexpr int N = Row<T>::N;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int iters = (row.v1 - row.v0 + 31) / 32;
+    tile_iters = max(1, (iters + kTiles - 1) / kTiles);
+    mx = -INFINITY;
+    ref = -1e30f;
+    sum = 0.0f;
+#pragma unroll 1
+    for (int it = 0; it < iters; it += 4) {
+      const int j0 = row.v0 + it * 32 + lane;
+      uint4 raw[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j0 + 32 * k < row.v1 && row.inside(j0 + 32 * k)) raw[k] = row.at(j0 + 32 * k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (it + k >= iters) break;
+        const int j = j0 + 32 * k;
+        float x[N];
+        if (j >= row.v1) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] = -INFINITY;
+        } else if (row.inside(j)) {
+          Vec16<T>::unpack(raw[k], x);
+        } else {
+          row.load(j, x);
+        }
+        float v = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        if (N == 8) v = fmaxf(v, fmaxf(fmaxf(x[N - 4], x[N - 3]), fmaxf(x[N - 2], x[N - 1])));
+        mx = fmaxf(mx, v);
+        const float r = fmaxf(ref, v);
+        const F2 sub = f2(-r, -r), mul = f2(c, c);
+        F2 t[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          float a, b;
+          split(mul2(add2(f2(x[2 * i], x[2 * i + 1]), sub), mul), a, b);
+          t[i] = f2(exp2_fast(a), exp2_fast(b));
+        }
+        F2 u = add2(t[0], t[1]);
+        if (N == 8) u = add2(u, add2(t[N / 2 - 2], t[N / 2 - 1]));
+        float a, b;
+        split(u, a, b);
+        sum = fmaf(sum, exp2_fast((ref - r) * c), a + b);
+        ref = r;
+        const float top = warp_top(v);
+        if (lane == 0) {
+          const int q = it + k, slot_ = warp * kTiles + q / tile_iters;
+          s.few.tile[slot_] = q % tile_iters == 0 ? top : fmaxf(s.few.tile[slot_], top);
+        }
+      }
+    }
+  }
+
+  // The draw from few candidates: all logits at or above a bar that at least `n_bar` logits reach, gathered in the first CTA
+  // and sorted there. It decides the row unless there are too many of them, or a border lies past them or within the error of
+  // the row's approximate weight `mass` (2^-17 of it: sums of 32 terms a lane and their joins at 2^-24 each, exponentials
+  // 2^-22). True when the row is done. All of the cluster takes part.
+  __device__ bool few(float mx, int n_bar, int k, bool greedy, float least, float tp, float u, float mass, float temp,
+                      const SParams &p, int r) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
+    // the bar: of the lanes' largest logits about the n_bar-th, by the upper 16 bits of its key
+    const uint32_t mine = order_key(mx) >> 16;
+    uint32_t bar = 0;
+    if (t == 0) s.few_count = 0;
+    const int share = (n_bar + nc - 1) / nc;   // every CTA brings its share
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t b = bar | (1u << bit);
+      if (__syncthreads_count(mine >= b) >= share) bar = b;
+    }
+    if (nc > 1) {
+      if (t == 0) s.sums[0][slot] = bar;
+      cluster_sync();
+      for (int c = 0; c < nc; ++c) bar = min(bar, static_cast<uint32_t>(ld_remote64(remote(&s.sums[0][slot], c))));
+      slot ^= 1;
+    }
+    float low = bar > 0x00800000u >> 16 ? key_value(bar << 16) : -INFINITY;   // the keys below are -infinity's and NaN's
+    if (row.V <= kFew) low = -3.402823466e38f;   // all of them
+    else if (!(low > -1e30f)) return false;
+    const uint32_t count_at = remote(&s.few_count, 0);
+    const int iters = (row.v1 - row.v0 + 31) / 32;
+    for (int q = 0; q * tile_iters < iters; ++q) {
+      if (!(s.few.tile[warp * kTiles + q] >= low)) continue;
+      for (int it = q * tile_iters; it < min(iters, (q + 1) * tile_iters); ++it) {
+        const int j = row.v0 + it * 32 + lane;
+        if (j >= row.v1) continue;
+        float x[Row<T>::N];
+        row.load(j, x);
+#pragma unroll
+        for (int i = 0; i < Row<T>::N; ++i)
+          if (x[i] >= low) {
+            const uint32_t at = add_remote32(count_at, 1);
+            if (at < kFew)
+              st_remote64(remote(&s.few.list[at], 0), (static_cast<u64>(order_key(x[i])) << 32) |
+                                                          (0xffffffffu - static_cast<uint32_t>(j * Row<T>::N - row.sh + i)));
+          }
+      }
+    }
+    if (nc > 1) cluster_sync();
+    else __syncthreads();
+    bool done = false;
+    if (rank == 0) {
+      const int n = s.few_count;
+      if (n <= kFew) {
+        const u64 v = t < n ? s.few.list[t] : 0;
+        int place = 0;
+        for (int i = 0; i < n; ++i) place += s.few.list[i] > v ? 1 : 0;
+        if (t < n) s.few.sorted[place] = v;
+        __syncthreads();
+        const u64 e = t < n ? s.few.sorted[t] : 0;
+        const float x = t < n ? key_value(static_cast<uint32_t>(e >> 32)) : -INFINITY;
+        const bool in = t < n && x >= least;
+        const u64 w = in ? weigh(x) : 0;
+        s.few.w[t] = w;
+        const u64 cum = block_inclusive_scan(w, s.scan);
+        if (t == 0) s.pick[2] = s.pick[3] = kFew;
+        const int survive = __syncthreads_count(in);   // a run from the first on
+        const int most = k > 0 ? min(k, survive) : survive;
+        // whether the candidates hold all that top_p is a share of
+        const bool whole = k > 0 || least >= low;
+        if (t == most - 1) s.pick[4] = cum;
+        __syncthreads();
+        const u64 sum = whole ? s.pick[4] : static_cast<u64>(mass * static_cast<float>(u64(1) << (44 - weigh.down)));
+        int keep = most;
+        // (the row's weight is not the survivors' where min_p drops some)
+        bool sure = whole || (tp < 1.0f && least <= -3.402823466e38f);
+        if (tp < 1.0f) {
+          const u64 off = whole ? 0 : (sum >> 17) + 1;
+          const u64 lo = max(u64(1), part_of(sum - off, tp, true)), hi = max(u64(1), part_of(sum + off, tp, true));
+          if (t < most && cum >= lo && cum - w < lo) s.pick[2] = t;
+          if (t < most && cum >= hi && cum - w < hi) s.pick[3] = t;
+          __syncthreads();
+          sure = sure && s.pick[2] == s.pick[3] && s.pick[2] < kFew;
+          keep = static_cast<int>(s.pick[2]) + 1;
+        }
+        if (greedy) {
+          sure = true;
+          keep = 1;
+        }
+        if (sure) {
+          done = true;
+          if (t == keep - 1) s.pick[5] = cum;
+          __syncthreads();
+          const u64 kept = s.pick[5], target = part_of(kept, u, false);
+          if (t < keep) {
+            u64 before = 0;   // kept weight of lower ids
+            for (int i = 0; i < keep; ++i)
+              before += static_cast<uint32_t>(s.few.sorted[i]) > static_cast<uint32_t>(e) ? s.few.w[i] : 0;
+            if (greedy ? t == 0 : before <= target && target < before + w) {
+              p.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(e));
+              if (p.logprob) p.logprob[r] = greedy ? 0.0f : log_share(x, kept, temp);
+              if (p.kept) p.kept[r] = keep;
+            }
+          }
+        }
+      }
+      if (t == 0) s.few_done = done ? 1 : 0;
+    }
+    if (nc > 1) {
+      cluster_sync();
+      done = ld_remote32(remote(&s.few_done, 0)) != 0;
+    }
+    return done;
+  }
+
+  __device__ float log_share(float x, u64 kept, float temp) const {
+    return static_cast<float>((static_cast<double>(x) - weigh.m) / temp -
+                              log(ldexp(static_cast<double>(kept), weigh.down - 44)));
+  }
+
+  // Sums of amount(x, id) in id order: this warp's range, what lies before it in the cluster, and all.
+  struct Sums {
+    u64 mine, before, all;
+  };
+  template <class F> __device__ Sums sums(F &&amount) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u64 w = 0;
     row.each([&](float x, int id) { w += amount(x, id); });
@@ -458,54 +686,88 @@ struct Sampler {
     __syncthreads();
     if (lane == 0) s.scan[warp] = w;
     __syncthreads();
-    u64 mine = 0, all = 0;
+    Sums r{w, 0, 0};
     for (int i = 0; i < kSaWarps; ++i) {
-      mine += i < warp ? s.scan[i] : 0;
-      all += s.scan[i];
-    }
-    const int sl = slot;
-    slot ^= 1;
-    if (threadIdx.x == 0) {
-      s.sums[0][sl] = all;
-      s.sums[1][sl] = ~u64(0);
+      r.before += i < warp ? s.scan[i] : 0;
+      r.all += s.scan[i];
     }
     if (nc > 1) {
+      if (threadIdx.x == 0) s.sums[0][slot] = r.all;
       cluster_sync();
-      for (int r = 0; r < rank; ++r) mine += ld_remote64(remote(&s.sums[0][sl], r));
-    } else {
-      __syncthreads();
+      r.all = 0;
+      for (int c = 0; c < nc; ++c) {
+        const u64 v = ld_remote64(remote(&s.sums[0][slot], c));
+        r.before += c < rank ? v : 0;
+        r.all += v;
+      }
+      slot ^= 1;
     }
-    if (mine <= target && target < mine + w) {   // one warp of the cluster
-      u64 run = mine;
-      for (int j0 = row.v0; j0 < row.v1; j0 += 32) {
-        const int j = j0 + lane;
-        float x[Row<T>::N];
-        u64 a = 0;
-        if (j < row.v1) {
+    return r;
+  }
+  // The id at which the running sum first passes `target`, and its logit; -1 if it never does. Every thread of the cluster
+  // gets them.
+  template <class F> __device__ int pick(const Sums &sm, u64 target, F &&amount, float &value) {
+    constexpr int N = Row<T>::N;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sl = slot;
+    slot ^= 1;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s.sums[1][sl] = ~u64(0);
+      s.pick[0] = 0;
+    }
+    __syncthreads();
+    if (lane == 0 && sm.before <= target && target < sm.before + sm.mine) {   // one warp of the cluster
+      s.pick[0] = (static_cast<u64>(static_cast<uint32_t>(row.v0)) << 32) | static_cast<uint32_t>(row.v1);
+      s.pick[1] = sm.before;
+    }
+    __syncthreads();
+    const int a0 = static_cast<int>(s.pick[0] >> 32), a1 = static_cast<int>(s.pick[0] & 0xffffffffu);
+    if (a1 > a0) {   // its CTA: the warps share its range
+      const int per = (a1 - a0 + kSaWarps - 1) / kSaWarps;
+      const int w0 = min(a0 + warp * per, a1), w1 = min(w0 + per, a1);
+      auto of_vector = [&](int j, float *x) {
+        u64 t = 0;
+        if (j < w1) {
           row.load(j, x);
 #pragma unroll
-          for (int i = 0; i < Row<T>::N; ++i) a += amount(x[i], j * Row<T>::N - row.sh + i);
+          for (int i = 0; i < N; ++i) t += amount(x[i], j * N - row.sh + i);
         }
-        u64 incl = a;
+        return t;
+      };
+      float x[N];
+      u64 w = 0;
+      for (int j = w0 + lane; j < w1; j += 32) w += of_vector(j, x);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 v = shfl_up64(incl, o);
-          if (lane >= o) incl += v;
-        }
-        if (run + incl - a <= target && target < run + incl) {   // one lane
-          u64 r = run + incl - a;
-          u64 hit = ~u64(0);
+      for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      if (lane == 0) s.scan[warp] = w;
+      __syncthreads();
+      u64 run = s.pick[1];
+      for (int i = 0; i < warp; ++i) run += s.scan[i];
+      if (run <= target && target < run + w) {   // one warp
+        for (int j0 = w0; j0 < w1; j0 += 32) {
+          const int j = j0 + lane;
+          const u64 t = of_vector(j, x);
+          u64 incl = t;
 #pragma unroll
-          for (int i = 0; i < Row<T>::N; ++i) {
-            const int id = j * Row<T>::N - row.sh + i;
-            r += amount(x[i], id);
-            if (r > target && hit == ~u64(0))
-              hit = (static_cast<u64>(static_cast<uint32_t>(id)) << 32) | __float_as_uint(x[i]);
+          for (int o = 1; o < 32; o <<= 1) {
+            const u64 v = shfl_up64(incl, o);
+            if (lane >= o) incl += v;
           }
-          s.sums[1][sl] = hit;
+          if (run + incl - t <= target && target < run + incl) {   // one lane
+            u64 r = run + incl - t, hit = ~u64(0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const int id = j * N - row.sh + i;
+              r += amount(x[i], id);
+              if (r > target && hit == ~u64(0))
+                hit = (static_cast<u64>(static_cast<uint32_t>(id)) << 32) | __float_as_uint(x[i]);
+            }
+            s.sums[1][sl] = hit;
+          }
+          run += __shfl_sync(0xffffffffu, incl, 31);
+          if (run > target) break;
         }
-        run += __shfl_sync(0xffffffffu, incl, 31);
-        if (run > target) break;
       }
     }
     u64 got = ~u64(0);
@@ -519,24 +781,124 @@ struct Sampler {
     value = __uint_as_float(static_cast<uint32_t>(got));
     return got == ~u64(0) ? -1 : static_cast<int>(got >> 32);
   }
-};
 
-// x * f for a fraction f in [0, 1): rounded down, or up.
-__device__ __forceinline__ u64 part_of(u64 x, float f, bool up) {
-  if (!(f > 0.0f)) return 0;
-  const uint32_t b = __float_as_uint(f);
-  const int e = static_cast<int>(b >> 23);
-  const uint32_t man = e ? ((b & 0x7fffffu) | 0x800000u) : (b & 0x7fffffu);
-  const int sh = 150 - (e ? e : 1);
-  const unsigned __int128 p = static_cast<unsigned __int128>(x) * man;
-  if (sh >= 127) return up ? 1 : 0;
-  const u64 q = static_cast<u64>(p >> sh);
-  return q + ((up && (static_cast<unsigned __int128>(q) << sh) != p) ? 1 : 0);
-}
+  // ---- 16-bit logits, counted by value: all sums from counts, each value weighed once
+  static __device__ __forceinline__ int value_index(float x) {   // -1: another magnitude
+    const uint32_t u = __float_as_uint(x) >> 16, i = (u & 0x7fffu) - kFirstValue;
+    return i >= kEndValue - kFirstValue ? -1 : static_cast<int>(u & 0x8000u ? kHalfValues + i : kHalfValues - 1 - i);
+  }
+  static __device__ __forceinline__ float value_of(int b) {
+    const uint32_t u = b < kHalfValues ? kFirstValue + (kHalfValues - 1 - b) : 0x8000u | (kFirstValue + (b - kHalfValues));
+    return __uint_as_float(u << 16);
+  }
+  __device__ __forceinline__ u64 value_weight(float x) const {
+    const int b = value_index(x);
+    return b >= 0 ? s.weight[b] : weigh(x);
+  }
+  // Before the running sums of a thread's values; those between the signs, kept aside, count before the negative ones.
+  static constexpr int kPer = kValues / kSaThreads;
+  static_assert(kValues % kSaThreads == 0 && kHalfValues % kPer == 0, "a thread's values have one sign");
+  struct Counted {
+    u64 count, weight;             // before this thread's values
+    u64 all_count, all_weight;
+    u64 pos_count, pos_weight;     // of the positive values
+    u64 odd_count, odd_weight;
+  };
+  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^10 on.
+  __device__ bool count_values(float least, Counted &c) {
+    const int t = threadIdx.x;
+    __syncthreads();
+    for (int i = t; i < kValues; i += kSaThreads) s.hist[i] = 0;
+    if (t == 0) s.odd_count = 0;
+    __syncthreads();
+    row.each_light([&](float x) {
+      if (x >= least) {
+        const int b = value_index(x);
+        if (b >= 0) {
+          atomicAdd(&s.hist[b], 1u);
+        } else {
+          const uint32_t at = atomicAdd(&s.odd_count, 1u);
+          if (at < kOdd) s.odd[at] = x;
+        }
+      }
+    });
+    __syncthreads();
+    const uint32_t n = s.odd_count;
+    const float x = t < min(n, static_cast<uint32_t>(kOdd)) ? s.odd[t] : 0.0f;
+    // one word: the odd ones' number, and above 2^32 whether this CTA cannot go on
+    const u64 odd = cluster_sum(t == 0 ? n + (n > kOdd ? u64(1) << 32 : 0) : 0) +
+                    cluster_sum(fabsf(x) >= 1024.0f ? u64(1) << 32 : 0);
+    if (odd >> 32) return false;
+    c.odd_count = odd;
+    c.odd_weight = odd ? cluster_sum(t < n ? weigh(x) : 0) : 0;
+    join_hist(kValues);
+    u64 cn = 0, cw = 0;
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) {
+      const int b = t * kPer + i;
+      const u64 k = s.total[b], w = k ? weigh(value_of(b)) : 0;
+      s.weight[b] = w;
+      cn += k;
+      cw += k * w;
+    }
+    c.count = block_inclusive_scan(cn, s.scan) - cn;
+    c.weight = block_inclusive_scan(cw, s.scan) - cw;
+    if (t * kPer == kHalfValues) {
+      s.pick[2] = c.count;
+      s.pick[3] = c.weight;
+    }
+    if (t == kSaThreads - 1) {
+      s.pick[4] = c.count + cn;
+      s.pick[5] = c.weight + cw;
+    }
+    __syncthreads();
+    c.pos_count = s.pick[2];
+    c.pos_weight = s.pick[3];
+    c.all_count = s.pick[4] + c.odd_count;
+    c.all_weight = s.pick[5] + c.odd_weight;
+    if (t * kPer >= kHalfValues) {
+      c.count += c.odd_count;
+      c.weight += c.odd_weight;
+    }
+    __syncthreads();
+    return true;
+  }
+  // find() over counted values. False: the border lies among those kept aside.
+  __device__ bool find_value(const Counted &c, bool by_weight, u64 target, uint32_t &key, u64 &at, u64 &above,
+                             u64 &above_w) {
+    u64 n = c.count, w = c.weight;
+    if (threadIdx.x == 0) s.pick[0] = ~u64(0);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) {
+      const int b = threadIdx.x * kPer + i;
+      const u64 k = s.total[b], kw = k * s.weight[b];
+      if (by_weight ? w < target && w + kw >= target : n < target && n + k >= target) {
+        s.pick[0] = b;
+        s.pick[1] = n;
+        s.pick[2] = w;
+      }
+      n += k;
+      w += kw;
+    }
+    __syncthreads();
+    const u64 b = s.pick[0];
+    above = s.pick[1];
+    above_w = s.pick[2];
+    const bool found = b < kValues;
+    if (found) {
+      key = order_key(value_of(static_cast<int>(b)));
+      at = s.total[b];
+    }
+    __syncthreads();
+    return found;
+  }
+};
 
 template <class T>
 __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) {
-  __shared__ Shared s;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared &s = *reinterpret_cast<Shared *>(smem);
   grid_dependency_sync();
   const int nc = cluster_size(), rank = cluster_rank();
   const int r = blockIdx.x / nc;
@@ -544,125 +906,173 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
   const float temp = p.temp ? (p.temp[r] > 0.0f ? fmaxf(p.temp[r], 1e-36f) : 0.0f) : 1.0f;
   const int k = p.top_k ? p.top_k[r] : 0;
   const float tp = p.top_p ? p.top_p[r] : 1.0f, mp = p.min_p ? p.min_p[r] : 0.0f;
-  Sampler<T> a{row, s, rank, nc, 0, {}};
+  const float ur = p.u[r], u = ur == ur ? fminf(ur, 0.99999994f) : 0.0f;
+  Sampler<T> a{row, s, rank, nc, 0, {}, 0};
+  const double cd = 1.4426950408889634 / static_cast<double>(temp > 0.0f ? temp : 1.0f);
+  const float ch = static_cast<float>(cd);
 
-  // ---- the largest logit, and whether the row is a distribution
-  float mx = -INFINITY;
-  bool nan = false;
-  row.each_light([&](float x) {
-    nan |= x != x;
-    mx = fmaxf(mx, x);
-  });
-  uint32_t best = order_key(mx);
-  best = __reduce_max_sync(0xffffffffu, best);
-  nan = __any_sync(0xffffffffu, nan);
-  if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = (static_cast<u64>(best) << 1) | (nan ? 1 : 0);
-  __syncthreads();
-  best = 0;
-  for (int w = 0; w < kSaWarps; ++w) {
-    best = max(best, static_cast<uint32_t>(s.scan[w] >> 1));
-    nan |= (s.scan[w] & 1) != 0;
+  if (threadIdx.x < 64) {
+    s.powers.f[threadIdx.x] = kPowers.f[threadIdx.x];
+    s.powers.q[threadIdx.x] = kPowers.q[threadIdx.x];
   }
+  // ---- the largest logit, whether the row is a distribution, and its weight to about 2^-17
+  float mx, ref, mass;
+  a.first_pass(fmaxf(ch, 1e-30f), mx, ref, mass);
+  const int warp = threadIdx.x >> 5;
+  float m = warp_top(mx);
+  if ((threadIdx.x & 31) == 0) s.fscan[warp] = m;
+  __syncthreads();
+  for (int w = 0; w < kSaWarps; ++w) m = fmaxf(m, s.fscan[w]);
   if (nc > 1) {
-    if (threadIdx.x == 0) s.sums[0][a.slot] = (static_cast<u64>(best) << 1) | (nan ? 1 : 0);
+    if (threadIdx.x == 0) s.sums[0][a.slot] = __float_as_uint(m);
     cluster_sync();
-    for (int c = 0; c < nc; ++c) {
-      const u64 v = ld_remote64(remote(&s.sums[0][a.slot], c));
-      best = max(best, static_cast<uint32_t>(v >> 1));
-      nan |= (v & 1) != 0;
-    }
+    for (int c = 0; c < nc; ++c) m = fmaxf(m, __uint_as_float(static_cast<uint32_t>(ld_remote64(remote(&s.sums[0][a.slot], c)))));
     a.slot ^= 1;
   }
-  const float m = key_value(best);
-  const bool sound = !nan && fabsf(m) < INFINITY;
+  mass = warp_sum(mass * exp2f((ref - fmaxf(m, -1e30f)) * fmaxf(ch, 1e-30f)));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s.fscan[warp] = mass;
+  __syncthreads();
+  mass = 0.0f;
+  for (int w = 0; w < kSaWarps; ++w) mass += s.fscan[w];
+  if (nc > 1) {
+    if (threadIdx.x == 0) s.sums[0][a.slot] = __float_as_uint(mass);
+    cluster_sync();
+    mass = 0.0f;
+    for (int c = 0; c < nc; ++c) mass += __uint_as_float(static_cast<uint32_t>(ld_remote64(remote(&s.sums[0][a.slot], c))));
+    a.slot ^= 1;
+  }
+  const uint32_t best = order_key(m);
+  const bool sound = mass == mass && fabsf(m) < INFINITY;
   float x_tok = m;
-  int token;
+  int token = 0;
   float lp = 0.0f;
   u64 count = 0;
-  if (!sound || !(temp > 0.0f)) {   // the first of the rank order
-    // (in a row of -infinity and NaN the first -infinity, of NaN alone token 0)
-    token = a.locate(0, [&](float x, int id) -> u64 { return id >= 0 && id < p.V && x == m ? 1 : 0; }, x_tok);
-    lp = sound ? 0.0f : NAN;
-    count = sound ? 1 : 0;
-  } else {
-    const double cd = 1.4426950408889634 / static_cast<double>(temp);
-    const float ch = static_cast<float>(cd);
-    a.weigh = Weigh{m, ch, static_cast<float>(cd - static_cast<double>(ch)), 44 - p.qb, &kPowers};
-    float least = -3.402823466e38f;
-    if (mp > 0.0f) {
+  bool done = false;
+  const bool greedy = !(temp > 0.0f);
+  float least = -3.402823466e38f;
+  if (sound) {
+    a.weigh = Weigh{m, ch, static_cast<float>(cd - static_cast<double>(ch)), 44 - p.qb, &s.powers};
+    if (mp > 0.0f && !greedy) {
       if (threadIdx.x == 0)
         s.pick[1] = __float_as_uint(__double2float_ru(
             static_cast<double>(m) + static_cast<double>(temp) * log(fmin(static_cast<double>(mp), 1.0))));
       __syncthreads();
       least = fminf(m, fmaxf(least, __uint_as_float(static_cast<uint32_t>(s.pick[1]))));
     }
+    const bool by_k = k > 0 && k < p.V;
+    if (greedy || p.V <= kFew || (by_k ? k <= kMaxFewK : (tp < 1.0f || mp > 0.0f)))
+      done = a.few(mx, greedy ? 1 : by_k ? k : kFewBar, by_k ? k : 0, greedy, least, tp, u, mass, temp, p, r);
+  }
+  if (done) {
+  } else if (!sound || greedy) {   // the first of the rank order
+    // (in a row of -infinity and NaN the first -infinity, of NaN alone token 0)
+    auto first = [&](float x, int id) -> u64 { return id >= 0 && id < p.V && x == m ? 1 : 0; };
+    token = a.pick(a.sums(first), 0, first, x_tok);
+    lp = sound ? 0.0f : NAN;
+    count = sound ? 1 : 0;
+  } else {
     // kept: the logits above `least`, and of those at it the first `ties` in id order
-    uint32_t floor = order_key(least);
     constexpr u64 kAll = ~u64(0);
     u64 ties = kAll, total = 0;
     int id_cut = 0x7fffffff;
-    bool counted = false, summed = false;
+    bool counted = false, settled = false;
     const bool by_p = tp < 1.0f;
-    if (k > 0 && k < p.V) {
-      const auto mass = a.histogram(least, false);
-      count = mass.count;
-      counted = true;
-      if (static_cast<u64>(k) < count) {
-        uint32_t key;
-        u64 at, above, unused;
-        a.find(false, k, floor, best, key, at, above, unused);
-        floor = key;
-        least = key_value(key);
-        ties = static_cast<u64>(k) - above < at ? static_cast<u64>(k) - above : kAll;
-        count = k;
-      }
-    }
-    if (by_p) {
-      auto mass = a.histogram(least, true);
-      const u64 w_least = a.weigh(least);
-      u64 n_all = mass.count;
-      if (ties != kAll) {   // tokens at the least logit that top_k does not keep
-        const u64 dropped = mass.count - count;
-        mass.weight -= dropped * w_least;
-        n_all = count;
-      }
-      const u64 target = max(u64(1), part_of(mass.weight, tp, true));
-      uint32_t key;
-      u64 at, above, above_w;
-      a.find(true, target, floor, best, key, at, above, above_w);
+    const float least0 = least;
+    // the steps on any way of counting: top_k's cut of `all` tokens, then top_p's
+    auto cut_k = [&](uint32_t key, u64 at, u64 above) {
+      least = key_value(key);
+      ties = static_cast<u64>(k) - above < at ? static_cast<u64>(k) - above : kAll;
+      count = k;
+    };
+    auto cut_p = [&](uint32_t key, u64 at, u64 above, u64 above_w, u64 target, u64 n_all) {
       const u64 each = a.weigh(key_value(key));
-      if (key == floor) at = min(at, n_all - above);
+      const bool last = key_value(key) == least;   // the least logit that top_k left
+      if (last) at = min(at, n_all - above);
       const u64 need = each ? min(at, (target - above_w + each - 1) / each) : at;
       count = above + need;
-      total = above_w + need * each;
-      counted = summed = true;
-      ties = need < at || (key == floor && ties != kAll) ? need : kAll;
-      floor = key;
+      ties = need < at || (last && ties != kAll) ? need : kAll;
       least = key_value(key);
+    };
+    typename Sampler<T>::Counted c;
+    if (sizeof(T) == 2 && a.count_values(least, c)) {
+      counted = settled = true;
+      uint32_t key;
+      u64 at, above, above_w, weight = c.all_weight;
+      count = c.all_count;
+      if (k > 0 && static_cast<u64>(k) < count) {
+        settled = a.find_value(c, false, k, key, at, above, above_w);
+        if (settled) {
+          cut_k(key, at, above);
+          weight = above_w + (static_cast<u64>(k) - above) * a.weigh(least);
+        }
+      }
+      if (settled && by_p) {
+        const u64 target = max(u64(1), part_of(weight, tp, true)), n_all = count;
+        settled = a.find_value(c, true, target, key, at, above, above_w);
+        if (settled) cut_p(key, at, above, above_w, target, n_all);
+      }
+      if (!settled) {
+        least = least0;
+        ties = kAll;
+      }
+    }
+    const bool by_value = settled;
+    if (!settled) {
+      counted = false;
+      if (k > 0 && k < p.V) {
+        count = a.histogram(least, false).count;
+        counted = true;
+        if (static_cast<u64>(k) < count) {
+          uint32_t key;
+          u64 at, above, unused;
+          a.find(false, k, order_key(least), best, key, at, above, unused);
+          cut_k(key, at, above);
+        }
+      }
+      if (by_p) {
+        auto mass = a.histogram(least, true);
+        u64 n_all = mass.count;
+        if (ties != kAll) {   // tokens at the least logit that top_k does not keep
+          mass.weight -= (mass.count - count) * a.weigh(least);
+          n_all = count;
+        }
+        const u64 target = max(u64(1), part_of(mass.weight, tp, true));
+        uint32_t key;
+        u64 at, above, above_w;
+        a.find(true, target, order_key(least), best, key, at, above, above_w);
+        cut_p(key, at, above, above_w, target, n_all);
+        counted = true;
+      }
     }
     if (ties != kAll) {
       float unused;
-      id_cut = a.locate(ties - 1, [&](float x, int) -> u64 { return x == least ? 1 : 0; }, unused);
+      auto tie = [&](float x, int) -> u64 { return x == least ? 1 : 0; };
+      id_cut = a.pick(a.sums(tie), ties - 1, tie, unused);
     }
-    auto weight = [&](float x, int id) -> u64 {
-      return x > least || (x == least && id <= id_cut) ? a.weigh(x) : u64(0);
-    };
-    if (!counted) {   // the kept tokens' number and weight come with the sums of the draw below
+    if (!counted) {
       u64 n = 0;
       row.each_light([&](float x) { n += x >= least ? 1 : 0; });
       count = a.cluster_sum(n);
     }
-    if (!summed) {
-      u64 w = 0;
-      row.each([&](float x, int id) { w += weight(x, id); });
-      total = a.cluster_sum(w);
+    if (by_value) {
+      auto weight = [&](float x, int id) -> u64 {
+        return x > least || (x == least && id <= id_cut) ? a.value_weight(x) : u64(0);
+      };
+      const auto sm = a.sums(weight);
+      total = sm.all;
+      token = a.pick(sm, part_of(total, u, false), weight, x_tok);
+    } else {
+      auto weight = [&](float x, int id) -> u64 {
+        return x > least || (x == least && id <= id_cut) ? a.weigh(x) : u64(0);
+      };
+      const auto sm = a.sums(weight);
+      total = sm.all;
+      token = a.pick(sm, part_of(total, u, false), weight, x_tok);
     }
-    const float u = p.u[r];
-    token = a.locate(part_of(total, u == u ? fminf(u, 0.99999994f) : 0.0f, false), weight, x_tok);
-    if (rank == 0 && threadIdx.x == 0)
-      lp = static_cast<float>((static_cast<double>(x_tok) - m) / temp - log(ldexp(static_cast<double>(total), -p.qb)));
+    if (rank == 0 && threadIdx.x == 0) lp = a.log_share(x_tok, total, temp);
   }
-  if (rank == 0 && threadIdx.x == 0) {
+  if (!done && rank == 0 && threadIdx.x == 0) {
     p.tokens[r] = max(token, 0);
     if (p.logprob) p.logprob[r] = lp;
     if (p.kept) p.kept[r] = static_cast<int32_t>(count);
@@ -675,13 +1085,16 @@ template <class T> cudaError_t launch(const SParams &p, int nc, cudaStream_t s) 
   int dev = 0;
   cudaGetDevice(&dev);
   if (!attr_set[dev & 63]) {
-    const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
     if (e != cudaSuccess) return e;
     attr_set[dev & 63] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.rows * nc);
   cfg.blockDim = dim3(kSaThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -705,7 +1118,8 @@ cudaError_t launch_sample(const void *logits, int dtype, int V, int64_t stride, 
   const SParams p{logits, V, rows, std::min(44, 62 - bits), stride, u, temp, top_p, min_p, top_k, tokens, logprob, kept};
   // CTAs of a row: as many as fill the GPU twice, but no slice below 2048 logits
   int nc = 1;
-  while (nc < kMaxCluster && rows * nc * 2 <= 2 * device_sm_count() && V / (nc * 2) >= 2048) nc *= 2;
+  nc = std::max(1, std::min({kMaxCluster, 2 * device_sm_count() / rows, V / 2048}));
+  if (nc > 8 && nc < kMaxCluster) nc = 8;   // past 8, a cluster of 16 or none
   return dtype == 0 ? launch<__nv_bfloat16>(p, nc, s) : launch<float>(p, nc, s);
 }
 
