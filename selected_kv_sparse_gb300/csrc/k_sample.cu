@@ -21,7 +21,8 @@
 namespace kap {
 namespace {
 
-constexpr int kSaThreads = 512;
+constexpr int kSaThreads = 256;
+constexpr int kSaCtas = 4;         // CTAs of an SM: one's joins and draws run under the others' passes
 constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinsPerThread = kBins / kSaThreads;
@@ -107,56 +108,58 @@ __device__ const Powers kPowers = make_powers();
 // with y = (m - x) log2 e / T as a sum of two fp32, k the nearest whole number to 64 y and r = y - k / 64,
 //   2^-y = 2^(-k/64) (1 - t + t^2/2 - t^3/6 + t^4/24),  t = r ln 2 <= 0.0055, t's leading term again as two fp32.
 // From y = 22 on (weights below 2^-22, units 2^-44) the exponential unit's 2^-22 of the value is below a unit.
+// Out of line: passes that weigh logits in several places would not stay in the instruction cache.
+__device__ __noinline__ u64 weight_of(float x, float m, float ch, float cl, int down, const Powers *tab) {
+  // m - x, exactly (two-sum)
+  const float dh = m - x, bb = m - dh, dl = (m - (dh + bb)) + (bb - x);
+  const float yh = dh * ch;
+  const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
+  if (!(yh < 62.0f)) return 0;   // also an infinite distance
+  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
+  u64 w;
+  int e;
+  if (yh >= 22.0f) {
+    float v;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(44.0f - yh));   // the difference is exact
+    v = fmaf(v, -yl * kLn2h, v);
+    return (static_cast<u64>(__float_as_uint(v + 12582912.0f) - 0x4b400000u) + ((1u << down) >> 1)) >> down;
+  }
+  const float kf = fmaf(yh, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
+  const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
+  const float r = fmaf(kf - 12582912.0f, -0.015625f, yh);
+  const float th = r * kLn2h, tl = fmaf(r, kLn2h, -th) + fmaf(r, kLn2l, yl * kLn2h);
+  const float q = th * th * fmaf(th, fmaf(th, 0.0416666679f, -0.166666672f), 0.5f) - tl;
+  const float2 f = tab->f[k & 63];
+  const float ph = f.x * -th;
+  const float pl = fmaf(f.x, -th, -ph) + fmaf(f.x, q, f.y * -th);
+  // ph + pl in units of 2^-44, through the low bits of sums at 3 (unit 2^-22) and at 3 * 2^-22
+  const float u = ph + pl, ub = u - ph, ul = (ph - (u - ub)) + (pl - ub);
+  const float s1 = u + 3.0f;
+  const int i1 = static_cast<int>(__float_as_uint(s1) - 0x40400000u);
+  const float rest = (u - (s1 - 3.0f)) + ul;
+  const int i2 = static_cast<int>(__float_as_uint(rest + 7.152557373046875e-7f) - 0x35400000u);
+  w = tab->q[k & 63] + static_cast<u64>(static_cast<int64_t>(i1) * (1 << 22) + i2);
+  e = (k >> 6) + down;
+  return (w + ((u64(1) << e) >> 1)) >> e;
+}
 struct Weigh {
   float m, ch, cl;   // largest logit; log2 e / T
   int down;          // 44 - qb
   const Powers *tab;
-  __device__ __forceinline__ u64 operator()(float x) const {
-    // m - x, exactly (two-sum)
-    const float dh = m - x, bb = m - dh, dl = (m - (dh + bb)) + (bb - x);
-    const float yh = dh * ch;
-    const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
-    if (!(yh < 62.0f)) return 0;   // also an infinite distance
-    constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
-    u64 w;
-    int e;
-    if (yh >= 22.0f) {
-      float v;
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(44.0f - yh));   // the difference is exact
-      v = fmaf(v, -yl * kLn2h, v);
-      return (static_cast<u64>(__float_as_uint(v + 12582912.0f) - 0x4b400000u) + ((1u << down) >> 1)) >> down;
-    }
-    const float kf = fmaf(yh, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
-    const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
-    const float r = fmaf(kf - 12582912.0f, -0.015625f, yh);
-    const float th = r * kLn2h, tl = fmaf(r, kLn2h, -th) + fmaf(r, kLn2l, yl * kLn2h);
-    const float q = th * th * fmaf(th, fmaf(th, 0.0416666679f, -0.166666672f), 0.5f) - tl;
-    const float2 f = tab->f[k & 63];
-    const float ph = f.x * -th;
-    const float pl = fmaf(f.x, -th, -ph) + fmaf(f.x, q, f.y * -th);
-    // ph + pl in units of 2^-44, through the low bits of sums at 3 (unit 2^-22) and at 3 * 2^-22
-    const float u = ph + pl, ub = u - ph, ul = (ph - (u - ub)) + (pl - ub);
-    const float s1 = u + 3.0f;
-    const int i1 = static_cast<int>(__float_as_uint(s1) - 0x40400000u);
-    const float rest = (u - (s1 - 3.0f)) + ul;
-    const int i2 = static_cast<int>(__float_as_uint(rest + 7.152557373046875e-7f) - 0x35400000u);
-    w = tab->q[k & 63] + static_cast<u64>(static_cast<int64_t>(i1) * (1 << 22) + i2);
-    e = (k >> 6) + down;
-    return (w + ((u64(1) << e) >> 1)) >> e;
-  }
+  __device__ __forceinline__ u64 operator()(float x) const { return weight_of(x, m, ch, cl, down, tab); }
 };
 
-constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept
-constexpr int kFew = kSaThreads;   // candidates that are sorted and drawn from directly
-constexpr int kMaxFewK = 256;      // top_k up to which the candidates are gathered
+constexpr int kTiles = 128;        // tiles of a warp's range whose maxima are kept
+constexpr int kFew = 2 * kSaThreads;   // candidates that are sorted and drawn from directly
+constexpr int kMaxFewK = 128;      // top_k up to which the candidates are gathered: half of the lanes
 constexpr int kFewBar = 64;        // candidates to gather, about, where top_k does not say
-// Logits of 16 bits from 2^-10 to 2^10 in magnitude, counted by value: 2560 of either sign, the largest first.
-constexpr int kValues = 5120, kHalfValues = kValues / 2;
-constexpr uint32_t kFirstValue = 0x3A80, kEndValue = 0x4480;   // bits of 2^-10 and 2^10
-constexpr int kOdd = 512;          // logits of other magnitudes that a CTA keeps aside
+// Logits of 16 bits from 2^-8 to 2^6 in magnitude, counted by value: 1792 of either sign, the largest first.
+constexpr int kValues = 3584, kHalfValues = kValues / 2;
+constexpr uint32_t kFirstValue = 0x3B80, kEndValue = 0x4280;   // bits of 2^-8 and 2^6
+constexpr int kOdd = 1024;         // logits of other magnitudes that a CTA keeps aside
 
 struct Shared {
-  uint32_t hist[kValues], total[kValues];
+  uint32_t hist[kValues];
   union {
     u64 weight[kValues];   // of each counted value
     struct {
@@ -166,11 +169,12 @@ struct Shared {
   };
   Powers powers;
   float odd[kOdd];
-  u64 scan[kSaWarps];
-  u64 sums[2][2];   // values for the other CTAs, in turn: a slot is written again two exchanges later
+  u64 scan[kSaWarps], scan2[kSaWarps];
+  u64 sums[3][2];   // values for the other CTAs, in turn: a slot is written again two exchanges later
   u64 pick[6];
   float fscan[kSaWarps];
   uint32_t few_count, few_done, odd_count;
+  uint32_t joined[];   // [kValues] the cluster's histogram, where it has more than one CTA
 };
 
 __device__ __forceinline__ u64 shfl_up64(u64 v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
@@ -225,55 +229,101 @@ struct Row {
     v0 = min(c0 + w * pw, c1);
     v1 = min(v0 + pw, c1);
   }
-  // The N logits of vector j; -infinity outside the row.
-  __device__ __forceinline__ void load(int j, float *x) const {
-    const int id = j * N - sh;
-    if (inside(j)) {
-      Vec16<T>::unpack(at(j), x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        x[i] = (id + i >= 0 && id + i < V) ? to_f(base[static_cast<int64_t>(j) * N + i]) : -INFINITY;
-    }
+  static constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -infinity
+  // Vector j; -infinity outside the row and the warp's range.
+  __device__ __forceinline__ uint4 get(int j) const {
+    return j < v1 ? vector(j) : make_uint4(kNone, kNone, kNone, kNone);
   }
-  // f(x, id) for this thread's logits, which are in its warp's range; ids outside the row come with -infinity. The next
-  // vector is on its way while f sees this one.
-  template <class F> __device__ __forceinline__ void each(F &&f) const {
-    int j = v0 + (threadIdx.x & 31);
-    uint4 raw{};
-    if (j < v1 && inside(j)) raw = at(j);
-#pragma unroll 1
-    for (; j < v1; j += 32) {
-      float x[N];
-      if (inside(j)) Vec16<T>::unpack(raw, x);
-      else load(j, x);
-      if (j + 32 < v1 && inside(j + 32)) raw = at(j + 32);
-#pragma unroll
-      for (int i = 0; i < N; ++i) f(x[i], j * N - sh + i);
-    }
+  __device__ __forceinline__ uint4 vector(int j) const {   // of any warp's range
+    return j * N - sh >= 0 && (j + 1) * N - sh <= V
+               ? *reinterpret_cast<const uint4 *>(base + static_cast<int64_t>(j) * N)
+               : edge(base + static_cast<int64_t>(j) * N, j * N - sh, V);
   }
-  // f(x) for the same logits in light passes: four vectors on their way together.
-  template <class F> __device__ __forceinline__ void each_light(F &&f) const {
-#pragma unroll 1
-    for (int j = v0 + (threadIdx.x & 31); j < v1; j += 128) {
-      uint4 raw[4];
+  static __device__ __noinline__ uint4 edge(const T *p, int id, int V) {
+    uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (j + 32 * k < v1 && inside(j + 32 * k)) raw[k] = at(j + 32 * k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (j + 32 * k >= v1) break;
-        float x[N];
-        if (inside(j + 32 * k)) Vec16<T>::unpack(raw[k], x);
-        else load(j + 32 * k, x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) f(x[i]);
+    for (int i = 0; i < 4; ++i) {
+      w[i] = kNone;
+      if (sizeof(T) == 2) {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+        const uint32_t lo = id + 2 * i >= 0 && id + 2 * i < V ? h[2 * i] : 0xff80u;
+        const uint32_t hi = id + 2 * i + 1 >= 0 && id + 2 * i + 1 < V ? h[2 * i + 1] : 0xff80u;
+        w[i] = lo | hi << 16;
+      } else if (id + i >= 0 && id + i < V) {
+        w[i] = reinterpret_cast<const uint32_t *>(p)[i];
       }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ bool inside(int j) const { return j * N - sh >= 0 && (j + 1) * N - sh <= V; }
-  __device__ __forceinline__ uint4 at(int j) const {
-    return *reinterpret_cast<const uint4 *>(base + static_cast<int64_t>(j) * N);
+  static __device__ __forceinline__ bool reaches(const uint4 &v, float low) {   // one of its logits is at or above `low`
+    float x[N];
+    Vec16<T>::unpack(v, x);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) any |= x[i] >= low;
+    return any;
+  }
+  // f(x, id) for the logits of vector j, in order; a loop, so that f's code stands there once or twice.
+  template <class F> __device__ __forceinline__ void elements(uint4 v, int j, F &&f) const {
+    int id = j * N - sh;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(T) == 2) {
+        f(__uint_as_float(v.x << 16), id);
+        f(__uint_as_float(v.x & 0xffff0000u), id + 1);
+        id += 2;
+      } else {
+        f(__uint_as_float(v.x), id++);
+      }
+      v.x = v.y;
+      v.y = v.z;
+      v.z = v.w;
+    }
+  }
+  // f(vector, j) for this lane's vectors of the warp's range, DEPTH of them on their way: loads go straight to the registers
+  // they are used from (a copy from one to another would wait for them). The warp's iterations are those that have all their
+  // vectors inside the row, and at most two others, at the row's ends.
+  template <int DEPTH, class F> __device__ __forceinline__ void stream(F &&f) const {
+    const int lane = threadIdx.x & 31;
+    const int first = v0 == 0 && sh != 0 ? 1 : 0;                       // iteration 0 holds the row's first, partial vector
+    const int full = max(first, (min(v1, (V + sh) / N) - v0) / 32);     // iterations [first, full) lie inside
+    const T *p = base + static_cast<int64_t>(v0 + lane) * N;
+    if (full > first) {
+      uint4 r[DEPTH];
+      auto fetch = [&](int it) {
+        return *reinterpret_cast<const uint4 *>(p + static_cast<int64_t>(min(it, full - 1)) * (32 * N));
+      };
+#pragma unroll
+      for (int k = 0; k < DEPTH; ++k) r[k] = fetch(first + k);
+#pragma unroll 1
+      for (int it = first; it < full; it += DEPTH) {
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k)
+          if (it + k < full) {
+            const uint4 v = r[k];
+            r[k] = fetch(it + k + DEPTH);
+            f(v, v0 + (it + k) * 32 + lane);
+          }
+      }
+    }
+    const int iters = (v1 - v0 + 31) / 32;
+#pragma unroll 1
+    for (int it = first ? 0 : full; it < iters; it = it == 0 && first ? full : it + 1) f(get(v0 + it * 32 + lane), v0 + it * 32 + lane);
+  }
+  // g(x, id) for this lane's logits; ids outside the row come with -infinity.
+  template <class G> __device__ __forceinline__ void each(G &&g) const {
+    stream<2>([&](const uint4 &v, int j) {
+      if (j < v1) elements(v, j, g);
+    });
+  }
+  // g(x) in light passes.
+  template <class G> __device__ __forceinline__ void each_light(G &&g) const {
+    stream<4>([&](const uint4 &v, int) {
+      float x[N];
+      Vec16<T>::unpack(v, x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) g(x[i]);
+    });
   }
 };
 
@@ -296,6 +346,7 @@ struct Sampler {
   Shared &s;
   int rank, nc, slot = 0;
   Weigh weigh;
+  uint32_t *total;   // the cluster's histogram
 
   // Sums over the cluster, to every thread.
   __device__ u64 cluster_sum(u64 v) {
@@ -308,14 +359,23 @@ struct Sampler {
     slot ^= 1;
     return t;
   }
-  // The cluster's histogram: s.hist of every CTA added up into s.total of every CTA.
+  __device__ uint32_t cluster_max(uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = v;
+    __syncthreads();
+    for (int w = 0; w < kSaWarps; ++w) v = max(v, static_cast<uint32_t>(s.scan[w]));
+    if (nc == 1) return v;
+    if (threadIdx.x == 0) s.sums[0][slot] = v;
+    cluster_sync();
+    for (int r = 0; r < nc; ++r) v = max(v, static_cast<uint32_t>(ld_remote64(remote(&s.sums[0][slot], r))));
+    slot ^= 1;
+    return v;
+  }
+  // The cluster's histogram: s.hist of every CTA added up for every CTA.
   __device__ void join_hist(int bins = kBins) {
     __syncthreads();
-    if (nc == 1) {
-      for (int i = threadIdx.x; i < bins; i += kSaThreads) s.total[i] = s.hist[i];
-      __syncthreads();
-      return;
-    }
+    if (nc == 1) return;
     cluster_sync();
     const int per = (bins + nc - 1) / nc;
     for (int i = threadIdx.x; i < per; i += kSaThreads) {
@@ -323,7 +383,7 @@ struct Sampler {
       if (b < bins) {
         uint32_t t = 0;
         for (int r = 0; r < nc; ++r) t += ld_remote32(remote(&s.hist[b], r));
-        for (int r = 0; r < nc; ++r) st_remote32(remote(&s.total[b], r), t);
+        for (int r = 0; r < nc; ++r) st_remote32(remote(&s.joined[b], r), t);
       }
     }
     cluster_sync();
@@ -351,7 +411,7 @@ struct Sampler {
   }
 
   // Histogram of the distances to the maximum, 1/16 octave of weight a bin, of the logits from `least` on: their number,
-  // and their weight (of those at `least`, only `ties` count where they are fewer). s.total holds the bins.
+  // and their weight (of those at `least`, only `ties` count where they are fewer). `total` holds the bins.
   struct Mass {
     u64 count, weight;
   };
@@ -406,14 +466,14 @@ struct Sampler {
       };
       b0 = first_bin(0, target, [&](int b) {
         const u64 w = edge(b);
-        return s.total[b] * (w + (w >> 12) + 4);
+        return total[b] * (w + (w >> 12) + 4);
       });
       b1 = first_bin(0, target, [&](int b) {
         const u64 w = edge(b + 1);
-        return b == kBins - 1 || w < 8 ? u64(0) : s.total[b] * (w - (w >> 12) - 4);
+        return b == kBins - 1 || w < 8 ? u64(0) : total[b] * (w - (w >> 12) - 4);
       });
     } else {
-      b0 = b1 = first_bin(0, target, [&](int b) { return static_cast<u64>(s.total[b]); });
+      b0 = b1 = first_bin(0, target, [&](int b) { return static_cast<u64>(total[b]); });
     }
     // the interval of keys that the bins b0 .. b1 can hold
     uint32_t khi = top, klo = floor;
@@ -453,17 +513,17 @@ struct Sampler {
         const u64 d = ((static_cast<u64>(b) + 1) << sh) - 1;
         return d > range ? klo : khi - static_cast<uint32_t>(d);
       };
-      auto weight_of = [&](uint32_t k) { return weigh(key_value(k)); };
-      auto used = [&](int b) { return s.total[b] != 0 && (static_cast<u64>(b) << sh) <= range; };
+      auto weight_at = [&](uint32_t k) { return weigh(key_value(k)); };
+      auto used = [&](int b) { return total[b] != 0 && (static_cast<u64>(b) << sh) <= range; };
       if (by_weight) {
         const u64 more = sh == 0 ? 0 : 4;   // neighbours' weights may be out of order by their rounding
-        b0 = first_bin(above_w, target, [&](int b) { return used(b) ? s.total[b] * (weight_of(hi_key(b)) + more) : u64(0); });
+        b0 = first_bin(above_w, target, [&](int b) { return used(b) ? total[b] * (weight_at(hi_key(b)) + more) : u64(0); });
         b1 = sh == 0 ? b0 : first_bin(above_w, target, [&](int b) {
-          const u64 lw = used(b) ? weight_of(lo_key(b)) : 0;
-          return lw > more ? s.total[b] * (lw - more) : u64(0);
+          const u64 lw = used(b) ? weight_at(lo_key(b)) : 0;
+          return lw > more ? total[b] * (lw - more) : u64(0);
         });
       } else {
-        b0 = b1 = first_bin(above, target, [&](int b) { return static_cast<u64>(s.total[b]); });
+        b0 = b1 = first_bin(above, target, [&](int b) { return static_cast<u64>(total[b]); });
       }
       const int last = static_cast<int>(range >> sh);
       b0 = min(b0, last);
@@ -471,13 +531,13 @@ struct Sampler {
       if (sh == 0) {
         u64 n_before = 0, w_before = 0;
         for (int b = threadIdx.x; b < b0; b += kSaThreads) {
-          n_before += s.total[b];
-          if (by_weight && s.total[b]) w_before += s.total[b] * weight_of(hi_key(b));
+          n_before += total[b];
+          if (by_weight && total[b]) w_before += total[b] * weight_at(hi_key(b));
         }
         above += block_sum(n_before, s.scan);
         if (by_weight) above_w += block_sum(w_before, s.scan);
         key = hi_key(b0);
-        at = s.total[b0];
+        at = total[b0];
         __syncthreads();
         return;
       }
@@ -510,26 +570,15 @@ struct Sampler {
     mx = -INFINITY;
     ref = -1e30f;
     sum = 0.0f;
-#pragma unroll 1
-    for (int it = 0; it < iters; it += 4) {
-      const int j0 = row.v0 + it * 32 + lane;
-      uint4 raw[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (j0 + 32 * k < row.v1 && row.inside(j0 + 32 * k)) raw[k] = row.at(j0 + 32 * k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (it + k >= iters) break;
-        const int j = j0 + 32 * k;
+    if (tile_iters > 1) {
+      for (int i = lane; i < kTiles; i += 32) s.few.tile[warp * kTiles + i] = -INFINITY;
+      __syncwarp();
+    }
+    row.template stream<4>([&](const uint4 &raw, int j) {
+      {
+        const int it = (j - lane - row.v0) >> 5;
         float x[N];
-        if (j >= row.v1) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) x[i] = -INFINITY;
-        } else if (row.inside(j)) {
-          Vec16<T>::unpack(raw[k], x);
-        } else {
-          row.load(j, x);
-        }
+        Vec16<T>::unpack(raw, x);
         float v = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         if (N == 8) v = fmaxf(v, fmaxf(fmaxf(x[N - 4], x[N - 3]), fmaxf(x[N - 2], x[N - 1])));
         mx = fmaxf(mx, v);
@@ -550,11 +599,12 @@ struct Sampler {
         ref = r;
         const float top = warp_top(v);
         if (lane == 0) {
-          const int q = it + k, slot_ = warp * kTiles + q / tile_iters;
-          s.few.tile[slot_] = q % tile_iters == 0 ? top : fmaxf(s.few.tile[slot_], top);
+          const int at = warp * kTiles + (tile_iters == 1 ? it : it / tile_iters);
+          // (iterations at the row's ends come last)
+          s.few.tile[at] = tile_iters == 1 ? top : fmaxf(s.few.tile[at], top);
         }
       }
-    }
+    });
   }
 
   // The draw from few candidates: all logits at or above a bar that at least `n_bar` logits reach, gathered in the first CTA
@@ -584,21 +634,33 @@ struct Sampler {
     else if (!(low > -1e30f)) return false;
     const uint32_t count_at = remote(&s.few_count, 0);
     const int iters = (row.v1 - row.v0 + 31) / 32;
-    for (int q = 0; q * tile_iters < iters; ++q) {
-      if (!(s.few.tile[warp * kTiles + q] >= low)) continue;
-      for (int it = q * tile_iters; it < min(iters, (q + 1) * tile_iters); ++it) {
-        const int j = row.v0 + it * 32 + lane;
-        if (j >= row.v1) continue;
-        float x[Row<T>::N];
-        row.load(j, x);
+    auto push = [&](float x, int id) {
+      if (x >= low) {
+        const uint32_t at = add_remote32(count_at, 1);
+        if (at < kFew)
+          st_remote64(remote(&s.few.list[at], 0),
+                      (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id)));
+      }
+    };
+    const int tiles = (iters + tile_iters - 1) / tile_iters;
+    for (int q0 = 0; q0 < tiles; q0 += 32) {
+      uint32_t mask = __ballot_sync(0xffffffffu, q0 + lane < tiles && s.few.tile[warp * kTiles + q0 + lane] >= low);
+      while (mask) {   // four tiles together
+        int j[4];
 #pragma unroll
-        for (int i = 0; i < Row<T>::N; ++i)
-          if (x[i] >= low) {
-            const uint32_t at = add_remote32(count_at, 1);
-            if (at < kFew)
-              st_remote64(remote(&s.few.list[at], 0), (static_cast<u64>(order_key(x[i])) << 32) |
-                                                          (0xffffffffu - static_cast<uint32_t>(j * Row<T>::N - row.sh + i)));
-          }
+        for (int c = 0; c < 4; ++c) {
+          j[c] = mask ? row.v0 + (q0 + __ffs(mask) - 1) * tile_iters * 32 + lane : row.v1;
+          mask &= mask - 1;
+        }
+#pragma unroll 1
+        for (int i = 0; i < tile_iters; ++i) {
+          uint4 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = row.get(j[c] + 32 * i);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (Row<T>::reaches(v[c], low)) row.elements(v[c], j[c] + 32 * i, push);
+        }
       }
     }
     if (nc > 1) cluster_sync();
@@ -607,23 +669,34 @@ struct Sampler {
     if (rank == 0) {
       const int n = s.few_count;
       if (n <= kFew) {
-        const u64 v = t < n ? s.few.list[t] : 0;
-        int place = 0;
-        for (int i = 0; i < n; ++i) place += s.few.list[i] > v ? 1 : 0;
-        if (t < n) s.few.sorted[place] = v;
+        for (int i = t; i < n; i += kSaThreads) {
+          const u64 v = s.few.list[i];
+          int place = 0;
+          for (int q = 0; q < n; ++q) place += s.few.list[q] > v ? 1 : 0;
+          s.few.sorted[place] = v;
+        }
         __syncthreads();
-        const u64 e = t < n ? s.few.sorted[t] : 0;
-        const float x = t < n ? key_value(static_cast<uint32_t>(e >> 32)) : -INFINITY;
-        const bool in = t < n && x >= least;
-        const u64 w = in ? weigh(x) : 0;
-        s.few.w[t] = w;
-        const u64 cum = block_inclusive_scan(w, s.scan);
+        // thread t looks at places 2 t and 2 t + 1
+        u64 e[2], w[2], cum[2];
+        int in = 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int i = 2 * t + q;
+          e[q] = i < n ? s.few.sorted[i] : 0;
+          const float x = key_value(static_cast<uint32_t>(e[q] >> 32));
+          const bool is = i < n && x >= least;
+          w[q] = is ? weigh(x) : 0;
+          in += is ? 1 : 0;
+          s.few.w[i] = w[q];
+        }
+        cum[1] = block_inclusive_scan(w[0] + w[1], s.scan);
+        cum[0] = cum[1] - w[1];
         if (t == 0) s.pick[2] = s.pick[3] = kFew;
-        const int survive = __syncthreads_count(in);   // a run from the first on
+        const int survive = static_cast<int>(block_sum(in, s.scan));   // a run from the first on
         const int most = k > 0 ? min(k, survive) : survive;
         // whether the candidates hold all that top_p is a share of
         const bool whole = k > 0 || least >= low;
-        if (t == most - 1) s.pick[4] = cum;
+        if ((most - 1) / 2 == t) s.pick[4] = (most - 1) & 1 ? cum[1] : cum[0];
         __syncthreads();
         const u64 sum = whole ? s.pick[4] : static_cast<u64>(mass * static_cast<float>(u64(1) << (44 - weigh.down)));
         int keep = most;
@@ -632,8 +705,12 @@ struct Sampler {
         if (tp < 1.0f) {
           const u64 off = whole ? 0 : (sum >> 17) + 1;
           const u64 lo = max(u64(1), part_of(sum - off, tp, true)), hi = max(u64(1), part_of(sum + off, tp, true));
-          if (t < most && cum >= lo && cum - w < lo) s.pick[2] = t;
-          if (t < most && cum >= hi && cum - w < hi) s.pick[3] = t;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int i = 2 * t + q;
+            if (i < most && cum[q] >= lo && cum[q] - w[q] < lo) s.pick[2] = i;
+            if (i < most && cum[q] >= hi && cum[q] - w[q] < hi) s.pick[3] = i;
+          }
           __syncthreads();
           sure = sure && s.pick[2] == s.pick[3] && s.pick[2] < kFew;
           keep = static_cast<int>(s.pick[2]) + 1;
@@ -644,16 +721,21 @@ struct Sampler {
         }
         if (sure) {
           done = true;
-          if (t == keep - 1) s.pick[5] = cum;
+          if ((keep - 1) / 2 == t) s.pick[5] = (keep - 1) & 1 ? cum[1] : cum[0];
           __syncthreads();
           const u64 kept = s.pick[5], target = part_of(kept, u, false);
-          if (t < keep) {
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            const int i = 2 * t + q;
+            if (i >= keep) break;
+            const u64 eq = q ? e[1] : e[0], wq = q ? w[1] : w[0];
+            const uint32_t inv = static_cast<uint32_t>(eq);
             u64 before = 0;   // kept weight of lower ids
-            for (int i = 0; i < keep; ++i)
-              before += static_cast<uint32_t>(s.few.sorted[i]) > static_cast<uint32_t>(e) ? s.few.w[i] : 0;
-            if (greedy ? t == 0 : before <= target && target < before + w) {
-              p.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(e));
-              if (p.logprob) p.logprob[r] = greedy ? 0.0f : log_share(x, kept, temp);
+            for (int o = 0; o < keep; ++o) before += static_cast<uint32_t>(s.few.sorted[o]) > inv ? s.few.w[o] : 0;
+            if (greedy ? i == 0 : before <= target && target < before + wq) {
+              p.tokens[r] = static_cast<int32_t>(0xffffffffu - inv);
+              if (p.logprob)
+                p.logprob[r] = greedy ? 0.0f : log_share(key_value(static_cast<uint32_t>(eq >> 32)), kept, temp);
               if (p.kept) p.kept[r] = keep;
             }
           }
@@ -673,41 +755,77 @@ struct Sampler {
                               log(ldexp(static_cast<double>(kept), weigh.down - 44)));
   }
 
-  // Sums of amount(x, id) in id order: this warp's range, what lies before it in the cluster, and all.
-  struct Sums {
-    u64 mine, before, all;
+  // What is kept: the logits above `least`, and of those at it (of weight w_least each) the first `ties` in id order.
+  struct Kept {
+    float least;
+    u64 ties, w_least;
+    // weight of `some` of the logits at `least`, `before` of which lie ahead
+    __device__ __forceinline__ u64 of_ties(u64 before, u64 some) const {
+      return before < ties ? min(some, ties - before) * w_least : 0;
+    }
   };
-  template <class F> __device__ Sums sums(F &&amount) {
+  // Kept weight of this warp's range, what lies before it in the cluster, and all; logits at `least` in the range and
+  // before it; the kept tokens' number.
+  struct Sums {
+    u64 mine, before, all, t_before, count;
+  };
+  template <class W> __device__ Sums sums(const Kept &kp, W &&weight) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u64 w = 0;
-    row.each([&](float x, int id) { w += amount(x, id); });
+    uint32_t n = 0, e = 0;
+    row.each([&](float x, int) {
+      if (x > kp.least) {
+        w += weight(x);
+        ++n;
+      } else if (x == kp.least) {
+        ++e;
+      }
+    });
+    n = __reduce_add_sync(0xffffffffu, n);
+    e = __reduce_add_sync(0xffffffffu, e);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
     __syncthreads();
-    if (lane == 0) s.scan[warp] = w;
+    if (lane == 0) {
+      s.scan[warp] = w;
+      s.scan2[warp] = (static_cast<u64>(n) << 32) | e;
+    }
     __syncthreads();
-    Sums r{w, 0, 0};
+    u64 w_all = 0, c_all = 0, w_before = 0, c_before = 0;
     for (int i = 0; i < kSaWarps; ++i) {
-      r.before += i < warp ? s.scan[i] : 0;
-      r.all += s.scan[i];
+      w_before += i < warp ? s.scan[i] : 0;
+      c_before += i < warp ? s.scan2[i] : 0;
+      w_all += s.scan[i];
+      c_all += s.scan2[i];
     }
     if (nc > 1) {
-      if (threadIdx.x == 0) s.sums[0][slot] = r.all;
+      if (threadIdx.x == 0) {
+        s.sums[0][slot] = w_all;
+        s.sums[2][slot] = c_all;
+      }
       cluster_sync();
-      r.all = 0;
+      w_all = c_all = 0;
       for (int c = 0; c < nc; ++c) {
-        const u64 v = ld_remote64(remote(&s.sums[0][slot], c));
-        r.before += c < rank ? v : 0;
-        r.all += v;
+        const u64 v = ld_remote64(remote(&s.sums[0][slot], c)), k = ld_remote64(remote(&s.sums[2][slot], c));
+        w_before += c < rank ? v : 0;
+        c_before += c < rank ? k : 0;
+        w_all += v;
+        c_all += k;
       }
       slot ^= 1;
     }
+    constexpr u64 kLow = 0xffffffffu;
+    Sums r;
+    r.t_before = c_before & kLow;
+    r.before = w_before + kp.of_ties(0, r.t_before);
+    r.mine = w + kp.of_ties(r.t_before, e);
+    r.all = w_all + kp.of_ties(0, c_all & kLow);
+    r.count = (c_all >> 32) + min(c_all & kLow, kp.ties);
     return r;
   }
-  // The id at which the running sum first passes `target`, and its logit; -1 if it never does. Every thread of the cluster
-  // gets them.
-  template <class F> __device__ int pick(const Sums &sm, u64 target, F &&amount, float &value) {
-    constexpr int N = Row<T>::N;
+  // The id at which the running kept weight in id order first passes `target`, and its logit; -1 if it never does. Every
+  // thread of the cluster gets them.
+  template <class W> __device__ int pick(const Sums &sm, const Kept &kp, u64 target, W &&weight, float &value) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sl = slot;
     slot ^= 1;
@@ -720,52 +838,73 @@ struct Sampler {
     if (lane == 0 && sm.before <= target && target < sm.before + sm.mine) {   // one warp of the cluster
       s.pick[0] = (static_cast<u64>(static_cast<uint32_t>(row.v0)) << 32) | static_cast<uint32_t>(row.v1);
       s.pick[1] = sm.before;
+      s.pick[2] = sm.t_before;
     }
     __syncthreads();
     const int a0 = static_cast<int>(s.pick[0] >> 32), a1 = static_cast<int>(s.pick[0] & 0xffffffffu);
     if (a1 > a0) {   // its CTA: the warps share its range
       const int per = (a1 - a0 + kSaWarps - 1) / kSaWarps;
       const int w0 = min(a0 + warp * per, a1), w1 = min(w0 + per, a1);
-      auto of_vector = [&](int j, float *x) {
-        u64 t = 0;
-        if (j < w1) {
-          row.load(j, x);
-#pragma unroll
-          for (int i = 0; i < N; ++i) t += amount(x[i], j * N - row.sh + i);
-        }
-        return t;
+      auto of_vector = [&](int j, u64 &w, uint32_t &e) {   // a lane's vector: weight above `least`, logits at it
+        if (j < w1)
+          row.elements(row.vector(j), j, [&](float x, int) {
+            if (x > kp.least) w += weight(x);
+            else if (x == kp.least) ++e;
+          });
       };
-      float x[N];
       u64 w = 0;
-      for (int j = w0 + lane; j < w1; j += 32) w += of_vector(j, x);
+      uint32_t e = 0;
+#pragma unroll 1
+      for (int j = w0 + lane; j < w1; j += 32) of_vector(j, w, e);
+      e = __reduce_add_sync(0xffffffffu, e);
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      if (lane == 0) s.scan[warp] = w;
+      if (lane == 0) {
+        s.scan[warp] = w;
+        s.scan2[warp] = e;
+      }
       __syncthreads();
-      u64 run = s.pick[1];
-      for (int i = 0; i < warp; ++i) run += s.scan[i];
-      if (run <= target && target < run + w) {   // one warp
+      u64 run = s.pick[1], ties = s.pick[2];
+      for (int i = 0; i < warp; ++i) {
+        run += s.scan[i] + kp.of_ties(ties, s.scan2[i]);
+        ties += s.scan2[i];
+      }
+      if (run <= target && target < run + w + kp.of_ties(ties, e)) {   // one warp
+#pragma unroll 1
         for (int j0 = w0; j0 < w1; j0 += 32) {
-          const int j = j0 + lane;
-          const u64 t = of_vector(j, x);
-          u64 incl = t;
+          u64 lw = 0;
+          uint32_t le = 0;
+          of_vector(j0 + lane, lw, le);
+          u64 wi = lw;
+          uint32_t ei = le;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const u64 v = shfl_up64(incl, o);
-            if (lane >= o) incl += v;
-          }
-          if (run + incl - t <= target && target < run + incl) {   // one lane
-            u64 r = run + incl - t, hit = ~u64(0);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int id = j * N - row.sh + i;
-              r += amount(x[i], id);
-              if (r > target && hit == ~u64(0))
-                hit = (static_cast<u64>(static_cast<uint32_t>(id)) << 32) | __float_as_uint(x[i]);
+            const u64 v = shfl_up64(wi, o);
+            const uint32_t c = __shfl_up_sync(0xffffffffu, ei, o);
+            if (lane >= o) {
+              wi += v;
+              ei += c;
             }
+          }
+          // before this lane's vector
+          u64 r = run + (wi - lw) + kp.of_ties(ties, ei - le), tb = ties + (ei - le);
+          if (r <= target && target < r + lw + kp.of_ties(tb, le)) {   // one lane
+            u64 hit = ~u64(0);
+            row.elements(row.vector(j0 + lane), j0 + lane, [&](float x, int id) {
+              if (x > kp.least) {
+                r += weight(x);
+              } else if (x == kp.least) {
+                r += kp.of_ties(tb, 1);
+                ++tb;
+              }
+              if (r > target && hit == ~u64(0))
+                hit = (static_cast<u64>(static_cast<uint32_t>(id)) << 32) | __float_as_uint(x);
+            });
             s.sums[1][sl] = hit;
           }
-          run += __shfl_sync(0xffffffffu, incl, 31);
+          const uint32_t ea = __shfl_sync(0xffffffffu, ei, 31);
+          run += __shfl_sync(0xffffffffu, wi, 31) + kp.of_ties(ties, ea);
+          ties += ea;
           if (run > target) break;
         }
       }
@@ -804,7 +943,7 @@ struct Sampler {
     u64 pos_count, pos_weight;     // of the positive values
     u64 odd_count, odd_weight;
   };
-  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^10 on.
+  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^6 on.
   __device__ bool count_values(float least, Counted &c) {
     const int t = threadIdx.x;
     __syncthreads();
@@ -824,19 +963,22 @@ struct Sampler {
     });
     __syncthreads();
     const uint32_t n = s.odd_count;
-    const float x = t < min(n, static_cast<uint32_t>(kOdd)) ? s.odd[t] : 0.0f;
-    // one word: the odd ones' number, and above 2^32 whether this CTA cannot go on
-    const u64 odd = cluster_sum(t == 0 ? n + (n > kOdd ? u64(1) << 32 : 0) : 0) +
-                    cluster_sum(fabsf(x) >= 1024.0f ? u64(1) << 32 : 0);
-    if (odd >> 32) return false;
-    c.odd_count = odd;
-    c.odd_weight = odd ? cluster_sum(t < n ? weigh(x) : 0) : 0;
+    // one word: the odd ones' number, and from 2^32 on whether this CTA cannot go on
+    u64 word = t == 0 ? n + (n > kOdd ? u64(1) << 32 : 0) : 0, ow = 0;
+    for (uint32_t i = t; i < min(n, static_cast<uint32_t>(kOdd)); i += kSaThreads) {
+      const float x = s.odd[i];
+      if (fabsf(x) >= 64.0f) word += u64(1) << 32;
+      ow += weigh(x);
+    }
+    c.odd_count = cluster_sum(word);
+    if (c.odd_count >> 32) return false;
+    c.odd_weight = c.odd_count ? cluster_sum(ow) : 0;
     join_hist(kValues);
     u64 cn = 0, cw = 0;
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
       const int b = t * kPer + i;
-      const u64 k = s.total[b], w = k ? weigh(value_of(b)) : 0;
+      const u64 k = total[b], w = k ? weigh(value_of(b)) : 0;
       s.weight[b] = w;
       cn += k;
       cw += k * w;
@@ -872,7 +1014,7 @@ struct Sampler {
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
       const int b = threadIdx.x * kPer + i;
-      const u64 k = s.total[b], kw = k * s.weight[b];
+      const u64 k = total[b], kw = k * s.weight[b];
       if (by_weight ? w < target && w + kw >= target : n < target && n + k >= target) {
         s.pick[0] = b;
         s.pick[1] = n;
@@ -888,7 +1030,7 @@ struct Sampler {
     const bool found = b < kValues;
     if (found) {
       key = order_key(value_of(static_cast<int>(b)));
-      at = s.total[b];
+      at = total[b];
     }
     __syncthreads();
     return found;
@@ -896,7 +1038,7 @@ struct Sampler {
 };
 
 template <class T>
-__global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) {
+__global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared &s = *reinterpret_cast<Shared *>(smem);
   grid_dependency_sync();
@@ -907,7 +1049,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
   const int k = p.top_k ? p.top_k[r] : 0;
   const float tp = p.top_p ? p.top_p[r] : 1.0f, mp = p.min_p ? p.min_p[r] : 0.0f;
   const float ur = p.u[r], u = ur == ur ? fminf(ur, 0.99999994f) : 0.0f;
-  Sampler<T> a{row, s, rank, nc, 0, {}, 0};
+  Sampler<T> a{row, s, rank, nc, 0, {}, nc > 1 ? s.joined : s.hist, 0};
   const double cd = 1.4426950408889634 / static_cast<double>(temp > 0.0f ? temp : 1.0f);
   const float ch = static_cast<float>(cd);
 
@@ -967,16 +1109,27 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
   if (done) {
   } else if (!sound || greedy) {   // the first of the rank order
     // (in a row of -infinity and NaN the first -infinity, of NaN alone token 0)
-    auto first = [&](float x, int id) -> u64 { return id >= 0 && id < p.V && x == m ? 1 : 0; };
-    token = a.pick(a.sums(first), 0, first, x_tok);
+    // padding is -infinity as well, but its ids come after those of the row's first one, or before 0: where the maximum is
+    // -infinity, ids are looked at one by one
+    if (m > -INFINITY) {
+      const typename Sampler<T>::Kept kp{m, 1, 1};
+      auto none = [](float) { return u64(0); };
+      token = a.pick(a.sums(kp, none), kp, 0, none, x_tok);
+    } else {
+      int lowest = 0x7fffffff;
+      row.each([&](float x, int id) {
+        if (id >= 0 && id < p.V && x == -INFINITY) lowest = min(lowest, id);
+      });
+      lowest = static_cast<int>(0x7fffffffu - a.cluster_max(0x7fffffffu - static_cast<uint32_t>(lowest)));
+      token = lowest < p.V ? lowest : 0;
+    }
     lp = sound ? 0.0f : NAN;
     count = sound ? 1 : 0;
   } else {
     // kept: the logits above `least`, and of those at it the first `ties` in id order
     constexpr u64 kAll = ~u64(0);
     u64 ties = kAll, total = 0;
-    int id_cut = 0x7fffffff;
-    bool counted = false, settled = false;
+    bool settled = false;
     const bool by_p = tp < 1.0f;
     const float least0 = least;
     // the steps on any way of counting: top_k's cut of `all` tokens, then top_p's
@@ -996,7 +1149,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
     };
     typename Sampler<T>::Counted c;
     if (sizeof(T) == 2 && a.count_values(least, c)) {
-      counted = settled = true;
+      settled = true;
       uint32_t key;
       u64 at, above, above_w, weight = c.all_weight;
       count = c.all_count;
@@ -1019,10 +1172,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
     }
     const bool by_value = settled;
     if (!settled) {
-      counted = false;
       if (k > 0 && k < p.V) {
         count = a.histogram(least, false).count;
-        counted = true;
         if (static_cast<u64>(k) < count) {
           uint32_t key;
           u64 at, above, unused;
@@ -1042,34 +1193,17 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
         u64 at, above, above_w;
         a.find(true, target, order_key(least), best, key, at, above, above_w);
         cut_p(key, at, above, above_w, target, n_all);
-        counted = true;
       }
     }
-    if (ties != kAll) {
-      float unused;
-      auto tie = [&](float x, int) -> u64 { return x == least ? 1 : 0; };
-      id_cut = a.pick(a.sums(tie), ties - 1, tie, unused);
-    }
-    if (!counted) {
-      u64 n = 0;
-      row.each_light([&](float x) { n += x >= least ? 1 : 0; });
-      count = a.cluster_sum(n);
-    }
-    if (by_value) {
-      auto weight = [&](float x, int id) -> u64 {
-        return x > least || (x == least && id <= id_cut) ? a.value_weight(x) : u64(0);
-      };
-      const auto sm = a.sums(weight);
+    const typename Sampler<T>::Kept kp{least, ties, a.weigh(least)};
+    auto draw = [&](auto &&weight) {
+      const auto sm = a.sums(kp, weight);
+      count = sm.count;
       total = sm.all;
-      token = a.pick(sm, part_of(total, u, false), weight, x_tok);
-    } else {
-      auto weight = [&](float x, int id) -> u64 {
-        return x > least || (x == least && id <= id_cut) ? a.weigh(x) : u64(0);
-      };
-      const auto sm = a.sums(weight);
-      total = sm.all;
-      token = a.pick(sm, part_of(total, u, false), weight, x_tok);
-    }
+      token = a.pick(sm, kp, part_of(total, u, false), weight, x_tok);
+    };
+    if (by_value) draw([&](float x) { return a.value_weight(x); });
+    else draw([&](float x) { return a.weigh(x); });
     if (rank == 0 && threadIdx.x == 0) lp = a.log_share(x_tok, total, temp);
   }
   if (!done && rank == 0 && threadIdx.x == 0) {
@@ -1080,6 +1214,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SParams p) 
   if (nc > 1) cluster_sync();   // the others may still read this CTA's shared memory
 }
 
+constexpr int kSharedAll = sizeof(Shared) + kValues * sizeof(uint32_t);
+
 template <class T> cudaError_t launch(const SParams &p, int nc, cudaStream_t s) {
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -1087,14 +1223,14 @@ template <class T> cudaError_t launch(const SParams &p, int nc, cudaStream_t s) 
   if (!attr_set[dev & 63]) {
     cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+      e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedAll);
     if (e != cudaSuccess) return e;
     attr_set[dev & 63] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.rows * nc);
   cfg.blockDim = dim3(kSaThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.dynamicSmemBytes = nc > 1 ? kSharedAll : sizeof(Shared);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1116,9 +1252,9 @@ cudaError_t launch_sample(const void *logits, int dtype, int V, int64_t stride, 
   int bits = 0;
   while ((int64_t(1) << bits) < V) ++bits;
   const SParams p{logits, V, rows, std::min(44, 62 - bits), stride, u, temp, top_p, min_p, top_k, tokens, logprob, kept};
-  // CTAs of a row: as many as fill the GPU twice, but no slice below 2048 logits
+  // CTAs of a row: as many as fill the GPU (three an SM, with the cluster's histogram), but no slice below 2048 logits
   int nc = 1;
-  nc = std::max(1, std::min({kMaxCluster, 2 * device_sm_count() / rows, V / 2048}));
+  nc = std::max(1, std::min({kMaxCluster, (kSaCtas - 1) * device_sm_count() / rows, V / 2048}));
   if (nc > 8 && nc < kMaxCluster) nc = 8;   // past 8, a cluster of 16 or none
   return dtype == 0 ? launch<__nv_bfloat16>(p, nc, s) : launch<float>(p, nc, s);
 }
