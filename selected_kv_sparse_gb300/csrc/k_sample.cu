@@ -21,8 +21,9 @@
 namespace kap {
 namespace {
 
-constexpr int kSaThreads = 256;
-constexpr int kSaCtas = 4;         // CTAs of an SM: one's joins and draws run under the others' passes
+constexpr int kSaThreads = 512;
+constexpr int kSaCtas = 2;         // CTAs of an SM: one's joins and draws run under the other's passes, and the rows of all
+                                   // (80 MB of 16-bit logits) stay in L2 between their passes
 constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinsPerThread = kBins / kSaThreads;
@@ -149,13 +150,13 @@ struct Weigh {
   __device__ __forceinline__ u64 operator()(float x) const { return weight_of(x, m, ch, cl, down, tab); }
 };
 
-constexpr int kTiles = 128;        // tiles of a warp's range whose maxima are kept
+constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept
 constexpr int kFew = 2 * kSaThreads;   // candidates that are sorted and drawn from directly
-constexpr int kMaxFewK = 128;      // top_k up to which the candidates are gathered: half of the lanes
+constexpr int kMaxFewK = 256;      // top_k up to which the candidates are gathered: half of the lanes
 constexpr int kFewBar = 64;        // candidates to gather, about, where top_k does not say
-// Logits of 16 bits from 2^-8 to 2^6 in magnitude, counted by value: 1792 of either sign, the largest first.
-constexpr int kValues = 3584, kHalfValues = kValues / 2;
-constexpr uint32_t kFirstValue = 0x3B80, kEndValue = 0x4280;   // bits of 2^-8 and 2^6
+// Logits of 16 bits from 2^-10 to 2^10 in magnitude, counted by value: 2560 of either sign, the largest first.
+constexpr int kValues = 5120, kHalfValues = kValues / 2;
+constexpr uint32_t kFirstValue = 0x3A80, kEndValue = 0x4480;   // bits of 2^-10 and 2^10
 constexpr int kOdd = 1024;         // logits of other magnitudes that a CTA keeps aside
 
 struct Shared {
@@ -309,6 +310,49 @@ struct Row {
     const int iters = (v1 - v0 + 31) / 32;
 #pragma unroll 1
     for (int it = first ? 0 : full; it < iters; it = it == 0 && first ? full : it + 1) f(get(v0 + it * 32 + lane), v0 + it * 32 + lane);
+  }
+  // above(x) for the logits of a vector above `least`, and the number of those at it. Of 16-bit logits packed compares give
+  // a mask first, and only its bits are looked at.
+  template <class A> static __device__ __forceinline__ uint32_t kept(const uint4 &v, float least, A &&above) {
+    if (sizeof(T) == 2) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
+      // `least` is a logit or one of these limits, rounded up: a logit above it is above its rounding or equal to it
+      const bool exact = __bfloat162float(__low2bfloat16(l2)) == least;
+      uint32_t m = 0, e = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+        const uint32_t g = __hgt2_mask(x, l2), q = __heq2_mask(x, l2);
+        m |= ((g & 1u) | ((g >> 15) & 2u)) << (2 * i);
+        e |= ((q & 1u) | ((q >> 15) & 2u)) << (2 * i);
+      }
+      if (!exact) {
+        if (__bfloat162float(__low2bfloat16(l2)) > least) m |= e;
+        e = 0;
+      }
+      const uint32_t ties = __popc(e);
+      while (m) {
+        const int b = __ffs(m) - 1;
+        m &= m - 1;
+        const uint32_t lo = b & 2 ? v.y : v.x, hi = b & 2 ? v.w : v.z, word = b & 4 ? hi : lo;
+        above(__uint_as_float(b & 1 ? word & 0xffff0000u : word << 16));
+      }
+      return ties;
+    } else {
+      uint32_t ties = 0;
+      uint4 u = v;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const float x = __uint_as_float(u.x);
+        u.x = u.y;
+        u.y = u.z;
+        u.z = u.w;
+        if (x > least) above(x);
+        else if (x == least) ++ties;
+      }
+      return ties;
+    }
   }
   // g(x, id) for this lane's logits; ids outside the row come with -infinity.
   template <class G> __device__ __forceinline__ void each(G &&g) const {
@@ -773,13 +817,11 @@ struct Sampler {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u64 w = 0;
     uint32_t n = 0, e = 0;
-    row.each([&](float x, int) {
-      if (x > kp.least) {
+    row.template stream<2>([&](const uint4 &v, int) {
+      e += Row<T>::kept(v, kp.least, [&](float x) {
         w += weight(x);
         ++n;
-      } else if (x == kp.least) {
-        ++e;
-      }
+      });
     });
     n = __reduce_add_sync(0xffffffffu, n);
     e = __reduce_add_sync(0xffffffffu, e);
@@ -841,21 +883,19 @@ struct Sampler {
       s.pick[2] = sm.t_before;
     }
     __syncthreads();
-    const int a0 = static_cast<int>(s.pick[0] >> 32), a1 = static_cast<int>(s.pick[0] & 0xffffffffu);
-    if (a1 > a0) {   // its CTA: the warps share its range
-      const int per = (a1 - a0 + kSaWarps - 1) / kSaWarps;
+    auto of_vector = [&](int j, int end, u64 &w, uint32_t &e) {   // a lane's vector: weight above `least`, logits at it
+      if (j < end) e += Row<T>::kept(row.vector(j), kp.least, [&](float x) { w += weight(x); });
+    };
+    int a0 = static_cast<int>(s.pick[0] >> 32), a1 = static_cast<int>(s.pick[0] & 0xffffffffu);
+    // its CTA: the warps share the range, then the part that the target lies in, until that is 32 vectors
+    for (int step = 0; step < 10 && a1 - a0 > 32; ++step) {   // an eighth each time
+      const u64 run0 = s.pick[1], ties0 = s.pick[2];
+      const int per = ((a1 - a0 + kSaWarps - 1) / kSaWarps + 31) & ~31;
       const int w0 = min(a0 + warp * per, a1), w1 = min(w0 + per, a1);
-      auto of_vector = [&](int j, u64 &w, uint32_t &e) {   // a lane's vector: weight above `least`, logits at it
-        if (j < w1)
-          row.elements(row.vector(j), j, [&](float x, int) {
-            if (x > kp.least) w += weight(x);
-            else if (x == kp.least) ++e;
-          });
-      };
       u64 w = 0;
       uint32_t e = 0;
 #pragma unroll 1
-      for (int j = w0 + lane; j < w1; j += 32) of_vector(j, w, e);
+      for (int j = w0 + lane; j < w1; j += 32) of_vector(j, w1, w, e);
       e = __reduce_add_sync(0xffffffffu, e);
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -864,49 +904,52 @@ struct Sampler {
         s.scan2[warp] = e;
       }
       __syncthreads();
-      u64 run = s.pick[1], ties = s.pick[2];
+      u64 run = run0, ties = ties0;
       for (int i = 0; i < warp; ++i) {
         run += s.scan[i] + kp.of_ties(ties, s.scan2[i]);
         ties += s.scan2[i];
       }
-      if (run <= target && target < run + w + kp.of_ties(ties, e)) {   // one warp
-#pragma unroll 1
-        for (int j0 = w0; j0 < w1; j0 += 32) {
-          u64 lw = 0;
-          uint32_t le = 0;
-          of_vector(j0 + lane, lw, le);
-          u64 wi = lw;
-          uint32_t ei = le;
+      __syncthreads();
+      if (lane == 0 && run <= target && target < run + w + kp.of_ties(ties, e)) {   // one warp
+        s.pick[0] = (static_cast<u64>(static_cast<uint32_t>(w0)) << 32) | static_cast<uint32_t>(w1);
+        s.pick[1] = run;
+        s.pick[2] = ties;
+      }
+      __syncthreads();
+      a0 = static_cast<int>(s.pick[0] >> 32);
+      a1 = static_cast<int>(s.pick[0] & 0xffffffffu);
+    }
+    if (a1 > a0 && warp == 0) {
+      const u64 run = s.pick[1], ties = s.pick[2];
+      u64 lw = 0;
+      uint32_t le = 0;
+      of_vector(a0 + lane, a1, lw, le);
+      u64 wi = lw;
+      uint32_t ei = le;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const u64 v = shfl_up64(wi, o);
-            const uint32_t c = __shfl_up_sync(0xffffffffu, ei, o);
-            if (lane >= o) {
-              wi += v;
-              ei += c;
-            }
-          }
-          // before this lane's vector
-          u64 r = run + (wi - lw) + kp.of_ties(ties, ei - le), tb = ties + (ei - le);
-          if (r <= target && target < r + lw + kp.of_ties(tb, le)) {   // one lane
-            u64 hit = ~u64(0);
-            row.elements(row.vector(j0 + lane), j0 + lane, [&](float x, int id) {
-              if (x > kp.least) {
-                r += weight(x);
-              } else if (x == kp.least) {
-                r += kp.of_ties(tb, 1);
-                ++tb;
-              }
-              if (r > target && hit == ~u64(0))
-                hit = (static_cast<u64>(static_cast<uint32_t>(id)) << 32) | __float_as_uint(x);
-            });
-            s.sums[1][sl] = hit;
-          }
-          const uint32_t ea = __shfl_sync(0xffffffffu, ei, 31);
-          run += __shfl_sync(0xffffffffu, wi, 31) + kp.of_ties(ties, ea);
-          ties += ea;
-          if (run > target) break;
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 v = shfl_up64(wi, o);
+        const uint32_t c = __shfl_up_sync(0xffffffffu, ei, o);
+        if (lane >= o) {
+          wi += v;
+          ei += c;
         }
+      }
+      // before this lane's vector
+      u64 r = run + (wi - lw) + kp.of_ties(ties, ei - le), tb = ties + (ei - le);
+      if (r <= target && target < r + lw + kp.of_ties(tb, le)) {   // one lane
+        u64 hit = ~u64(0);
+        row.elements(row.vector(a0 + lane), a0 + lane, [&](float x, int id) {
+          if (x > kp.least) {
+            r += weight(x);
+          } else if (x == kp.least) {
+            r += kp.of_ties(tb, 1);
+            ++tb;
+          }
+          if (r > target && hit == ~u64(0))
+            hit = (static_cast<u64>(static_cast<uint32_t>(id)) << 32) | __float_as_uint(x);
+        });
+        s.sums[1][sl] = hit;
       }
     }
     u64 got = ~u64(0);
@@ -943,7 +986,7 @@ struct Sampler {
     u64 pos_count, pos_weight;     // of the positive values
     u64 odd_count, odd_weight;
   };
-  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^6 on.
+  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^10 on.
   __device__ bool count_values(float least, Counted &c) {
     const int t = threadIdx.x;
     __syncthreads();
@@ -967,7 +1010,7 @@ struct Sampler {
     u64 word = t == 0 ? n + (n > kOdd ? u64(1) << 32 : 0) : 0, ow = 0;
     for (uint32_t i = t; i < min(n, static_cast<uint32_t>(kOdd)); i += kSaThreads) {
       const float x = s.odd[i];
-      if (fabsf(x) >= 64.0f) word += u64(1) << 32;
+      if (fabsf(x) >= 1024.0f) word += u64(1) << 32;
       ow += weigh(x);
     }
     c.odd_count = cluster_sum(word);
@@ -1252,9 +1295,9 @@ cudaError_t launch_sample(const void *logits, int dtype, int V, int64_t stride, 
   int bits = 0;
   while ((int64_t(1) << bits) < V) ++bits;
   const SParams p{logits, V, rows, std::min(44, 62 - bits), stride, u, temp, top_p, min_p, top_k, tokens, logprob, kept};
-  // CTAs of a row: as many as fill the GPU (three an SM, with the cluster's histogram), but no slice below 2048 logits
+  // CTAs of a row: as many as fill the GPU, but no slice below 2048 logits
   int nc = 1;
-  nc = std::max(1, std::min({kMaxCluster, (kSaCtas - 1) * device_sm_count() / rows, V / 2048}));
+  nc = std::max(1, std::min({kMaxCluster, kSaCtas * device_sm_count() / rows, V / 2048}));
   if (nc > 8 && nc < kMaxCluster) nc = 8;   // past 8, a cluster of 16 or none
   return dtype == 0 ? launch<__nv_bfloat16>(p, nc, s) : launch<float>(p, nc, s);
 }
