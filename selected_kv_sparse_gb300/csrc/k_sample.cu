@@ -150,11 +150,11 @@ struct Weigh {
   __device__ __forceinline__ u64 operator()(float x) const { return weight_of(x, m, ch, cl, down, tab); }
 };
 
-constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept
+constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept, two a lane
 constexpr int kFew = 2 * kSaThreads;   // candidates that are sorted and drawn from directly
 constexpr int kMaxFewK = 256;      // top_k up to which the candidates are gathered: half of the lanes
 constexpr int kFewBar = 64;        // candidates to gather, about, where top_k does not say
-// Logits of 16 bits from 2^-10 to 2^10 in magnitude, counted by value: 2560 of either sign, the largest first.
+// Logits of 16 bits from 2^-10 to 2^10 in magnitude, counted by value: 2560 of either sign, by their bits.
 constexpr int kValues = 5120, kHalfValues = kValues / 2;
 constexpr uint32_t kFirstValue = 0x3A80, kEndValue = 0x4480;   // bits of 2^-10 and 2^10
 constexpr int kOdd = 1024;         // logits of other magnitudes that a CTA keeps aside
@@ -165,7 +165,6 @@ struct Shared {
     u64 weight[kValues];   // of each counted value
     struct {
       u64 list[kFew], sorted[kFew], w[kFew];   // candidates: key and inverted id; their weights
-      float tile[kSaWarps * kTiles];
     } few;
   };
   Powers powers;
@@ -216,7 +215,8 @@ struct Row {
   static constexpr int N = Vec16<T>::N;
   const T *base;      // 16-byte aligned address at or below the row's first logit
   int sh, V;          // logits of the first vector that lie before the row
-  int v0, v1;         // this warp's vectors
+  int c0, c1;         // this CTA's vectors
+  int v0, v1;         // this warp's, where the order of ids counts
 
   __device__ __forceinline__ Row(const T *row, int V_, int rank, int nc) : V(V_) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(row);
@@ -224,18 +224,16 @@ struct Row {
     base = row - sh;
     const int nvec = (V + sh + N - 1) / N;
     const int per = (nvec + nc - 1) / nc;
-    const int c0 = min(rank * per, nvec), c1 = min(c0 + per, nvec);
+    c0 = min(rank * per, nvec);
+    c1 = min(c0 + per, nvec);
     const int pw = (c1 - c0 + kSaWarps - 1) / kSaWarps;
     const int w = threadIdx.x >> 5;
     v0 = min(c0 + w * pw, c1);
     v1 = min(v0 + pw, c1);
   }
   static constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -infinity
-  // Vector j; -infinity outside the row and the warp's range.
-  __device__ __forceinline__ uint4 get(int j) const {
-    return j < v1 ? vector(j) : make_uint4(kNone, kNone, kNone, kNone);
-  }
-  __device__ __forceinline__ uint4 vector(int j) const {   // of any warp's range
+  // Vector j of the row.
+  __device__ __forceinline__ uint4 vector(int j) const {
     return j * N - sh >= 0 && (j + 1) * N - sh <= V
                ? *reinterpret_cast<const uint4 *>(base + static_cast<int64_t>(j) * N)
                : edge(base + static_cast<int64_t>(j) * N, j * N - sh, V);
@@ -281,36 +279,51 @@ struct Row {
       v.z = v.w;
     }
   }
-  // f(vector, j) for this lane's vectors of the warp's range, DEPTH of them on their way: loads go straight to the registers
-  // they are used from (a copy from one to another would wait for them). The warp's iterations are those that have all their
-  // vectors inside the row, and at most two others, at the row's ends.
-  template <int DEPTH, class F> __device__ __forceinline__ void stream(F &&f) const {
+  // Vector j; -infinity outside the CTA's range.
+  __device__ __forceinline__ uint4 get_any(int j) const {
+    return j < c1 ? vector(j) : make_uint4(kNone, kNone, kNone, kNone);
+  }
+  // Step g of 32 vectors from a0 on is a warp's whenever g is `me` modulo `of`; f(vector, j, i) for its i-th one, DEPTH of them
+  // on their way: loads go straight to the registers they are used from (a copy from one to another would wait for them).
+  // Steps that do not lie inside the row and before a1 (at most three) come after the others.
+  template <int DEPTH, class F>
+  __device__ __forceinline__ void steps(int a0, int a1, int me, int of, F &&f) const {
     const int lane = threadIdx.x & 31;
-    const int first = v0 == 0 && sh != 0 ? 1 : 0;                       // iteration 0 holds the row's first, partial vector
-    const int full = max(first, (min(v1, (V + sh) / N) - v0) / 32);     // iterations [first, full) lie inside
-    const T *p = base + static_cast<int64_t>(v0 + lane) * N;
-    if (full > first) {
+    const int first = a0 == 0 && sh != 0 ? 1 : 0;                     // step 0 holds the row's first, partial vector
+    const int full = max(first, (min(a1, (V + sh) / N) - a0) / 32);   // steps [first, full) lie inside
+    const int i0 = me < first ? 1 : 0, i1 = full > me ? (full - me + of - 1) / of : 0;
+    const T *p = base + (static_cast<int64_t>(a0) + me * 32 + lane) * N;
+    if (i1 > i0) {
       uint4 r[DEPTH];
-      auto fetch = [&](int it) {
-        return *reinterpret_cast<const uint4 *>(p + static_cast<int64_t>(min(it, full - 1)) * (32 * N));
+      auto fetch = [&](int i) {
+        return *reinterpret_cast<const uint4 *>(p + static_cast<int64_t>(min(i, i1 - 1)) * (of * 32 * N));
       };
 #pragma unroll
-      for (int k = 0; k < DEPTH; ++k) r[k] = fetch(first + k);
+      for (int k = 0; k < DEPTH; ++k) r[k] = fetch(i0 + k);
 #pragma unroll 1
-      for (int it = first; it < full; it += DEPTH) {
+      for (int i = i0; i < i1; i += DEPTH) {
 #pragma unroll
         for (int k = 0; k < DEPTH; ++k)
-          if (it + k < full) {
+          if (i + k < i1) {
             const uint4 v = r[k];
-            r[k] = fetch(it + k + DEPTH);
-            f(v, v0 + (it + k) * 32 + lane);
+            r[k] = fetch(i + k + DEPTH);
+            f(v, a0 + ((i + k) * of + me) * 32 + lane, i + k);
           }
       }
     }
-    const int iters = (v1 - v0 + 31) / 32;
+    const int all = (a1 - a0 + 31) / 32;
 #pragma unroll 1
-    for (int it = first ? 0 : full; it < iters; it = it == 0 && first ? full : it + 1) f(get(v0 + it * 32 + lane), v0 + it * 32 + lane);
+    for (int i = i0 ? 0 : max(i1, 0); i * of + me < all; i = i0 && i == 0 ? max(i1, 1) : i + 1) {
+      const int j = a0 + (i * of + me) * 32 + lane;
+      f(j < a1 ? vector(j) : make_uint4(kNone, kNone, kNone, kNone), j, i);
+    }
   }
+  // The warps take a CTA's steps in turn, so that they read on side by side.
+  template <int DEPTH, class F> __device__ __forceinline__ void stream(F &&f) const {
+    steps<DEPTH>(c0, c1, threadIdx.x >> 5, kSaWarps, f);
+  }
+  // Each warp its own range, in the order of ids.
+  template <int DEPTH, class F> __device__ __forceinline__ void in_order(F &&f) const { steps<DEPTH>(v0, v1, 0, 1, f); }
   // above(x) for the logits of a vector above `least`, and the number of those at it. Of 16-bit logits packed compares give
   // a mask first, and only its bits are looked at.
   template <class A> static __device__ __forceinline__ uint32_t kept(const uint4 &v, float least, A &&above) {
@@ -356,13 +369,13 @@ struct Row {
   }
   // g(x, id) for this lane's logits; ids outside the row come with -infinity.
   template <class G> __device__ __forceinline__ void each(G &&g) const {
-    stream<2>([&](const uint4 &v, int j) {
-      if (j < v1) elements(v, j, g);
+    stream<2>([&](const uint4 &v, int j, int) {
+      if (j < c1) elements(v, j, g);
     });
   }
   // g(x) in light passes.
   template <class G> __device__ __forceinline__ void each_light(G &&g) const {
-    stream<4>([&](const uint4 &v, int) {
+    stream<4>([&](const uint4 &v, int, int) {
       float x[N];
       Vec16<T>::unpack(v, x);
 #pragma unroll
@@ -603,50 +616,54 @@ struct Sampler {
     }
   }
 
-  // One pass: this lane's largest logit, the sum of 2^((x - ref) c) with ref the larger of that and -1e30 (NaN where a
-  // logit is), and the maxima of tiles of the warp's range.
+  // One pass: this lane's largest logit, and the sum of 2^(x c - ref) with ref its running largest x c, rounded up, or -1e30 (ref
+  // is a number of its own, so the exponents have one rounding; NaN where a logit is). Lane l keeps the maxima of the
+  // warp's tiles l and l + 32: tile_iters iterations each.
   int tile_iters;
+  float tile[2];
   __device__ void first_pass(float c, float &mx, float &ref, float &sum) {
-    constexpr int N = Row<T>::N;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int iters = (row.v1 - row.v0 + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    const int iters = ((row.c1 - row.c0 + 31) / 32 + kSaWarps - 1) / kSaWarps;
     tile_iters = max(1, (iters + kTiles - 1) / kTiles);
     mx = -INFINITY;
     ref = -1e30f;
     sum = 0.0f;
-    if (tile_iters > 1) {
-      for (int i = lane; i < kTiles; i += 32) s.few.tile[warp * kTiles + i] = -INFINITY;
-      __syncwarp();
-    }
-    row.template stream<4>([&](const uint4 &raw, int j) {
-      {
-        const int it = (j - lane - row.v0) >> 5;
-        float x[N];
-        Vec16<T>::unpack(raw, x);
-        float v = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        if (N == 8) v = fmaxf(v, fmaxf(fmaxf(x[N - 4], x[N - 3]), fmaxf(x[N - 2], x[N - 1])));
-        mx = fmaxf(mx, v);
-        const float r = fmaxf(ref, v);
-        const F2 sub = f2(-r, -r), mul = f2(c, c);
-        F2 t[N / 2];
+    tile[0] = tile[1] = -INFINITY;
+    const F2 cc = f2(c, c);
+    row.template stream<4>([&](const uint4 &raw, int, int q) {
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      float v, s0, s1;
+      F2 t[4];
+      if (sizeof(T) == 2) {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(w);
+        const __nv_bfloat162 top = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(&top);
+        v = fmaxf(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+      } else {
+        v = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+      }
+      mx = fmaxf(mx, v);
+      const float r = fmaxf(ref, __fmul_ru(v, c));   // upwards: no exponent is above 0
+      const F2 nr = f2(-r, -r);
+      constexpr int PAIRS = Row<T>::N / 2;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          float a, b;
-          split(mul2(add2(f2(x[2 * i], x[2 * i + 1]), sub), mul), a, b);
-          t[i] = f2(exp2_fast(a), exp2_fast(b));
-        }
-        F2 u = add2(t[0], t[1]);
-        if (N == 8) u = add2(u, add2(t[N / 2 - 2], t[N / 2 - 1]));
+      for (int i = 0; i < PAIRS; ++i) {
         float a, b;
-        split(u, a, b);
-        sum = fmaf(sum, exp2_fast((ref - r) * c), a + b);
-        ref = r;
-        const float top = warp_top(v);
-        if (lane == 0) {
-          const int at = warp * kTiles + (tile_iters == 1 ? it : it / tile_iters);
-          // (iterations at the row's ends come last)
-          s.few.tile[at] = tile_iters == 1 ? top : fmaxf(s.few.tile[at], top);
-        }
+        split(fma2(sizeof(T) == 2 ? f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u))
+                                  : f2(__uint_as_float(w[2 * i & 3]), __uint_as_float(w[(2 * i + 1) & 3])),
+                   cc, nr), a, b);
+        t[i] = f2(exp2_fast(a), exp2_fast(b));
+      }
+      F2 u = add2(t[0], t[1]);
+      if (PAIRS == 4) u = add2(u, add2(t[2], t[3]));
+      split(u, s0, s1);
+      sum = fmaf(sum, exp2_fast(ref - r), s0 + s1);
+      ref = r;
+      const float top = warp_top(v);
+      if (tile_iters > 1) q /= tile_iters;
+      if (lane == (q & 31)) {
+        if (q < 32) tile[0] = fmaxf(tile[0], top);
+        else tile[1] = fmaxf(tile[1], top);
       }
     });
   }
@@ -657,7 +674,7 @@ struct Sampler {
   // 2^-22). True when the row is done. All of the cluster takes part.
   __device__ bool few(float mx, int n_bar, int k, bool greedy, float least, float tp, float u, float mass, float temp,
                       const SParams &p, int r) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
+    const int lane = threadIdx.x & 31, t = threadIdx.x;
     // the bar: of the lanes' largest logits about the n_bar-th, by the upper 16 bits of its key
     const uint32_t mine = order_key(mx) >> 16;
     uint32_t bar = 0;
@@ -677,7 +694,6 @@ struct Sampler {
     if (row.V <= kFew) low = -3.402823466e38f;   // all of them
     else if (!(low > -1e30f)) return false;
     const uint32_t count_at = remote(&s.few_count, 0);
-    const int iters = (row.v1 - row.v0 + 31) / 32;
     auto push = [&](float x, int id) {
       if (x >= low) {
         const uint32_t at = add_remote32(count_at, 1);
@@ -686,24 +702,24 @@ struct Sampler {
                       (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id)));
       }
     };
-    const int tiles = (iters + tile_iters - 1) / tile_iters;
-    for (int q0 = 0; q0 < tiles; q0 += 32) {
-      uint32_t mask = __ballot_sync(0xffffffffu, q0 + lane < tiles && s.few.tile[warp * kTiles + q0 + lane] >= low);
+#pragma unroll 1
+    for (int q0 = 0; q0 < kTiles; q0 += 32) {
+      uint32_t mask = __ballot_sync(0xffffffffu, (q0 ? tile[1] : tile[0]) >= low);
       while (mask) {   // four tiles together
         int j[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          j[c] = mask ? row.v0 + (q0 + __ffs(mask) - 1) * tile_iters * 32 + lane : row.v1;
+          j[c] = mask ? row.c0 + ((q0 + __ffs(mask) - 1) * tile_iters * kSaWarps + (t >> 5)) * 32 + lane : row.c1;
           mask &= mask - 1;
         }
 #pragma unroll 1
         for (int i = 0; i < tile_iters; ++i) {
           uint4 v[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = row.get(j[c] + 32 * i);
+          for (int c = 0; c < 4; ++c) v[c] = row.get_any(j[c] + 32 * kSaWarps * i);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (Row<T>::reaches(v[c], low)) row.elements(v[c], j[c] + 32 * i, push);
+            if (Row<T>::reaches(v[c], low)) row.elements(v[c], j[c] + 32 * kSaWarps * i, push);
         }
       }
     }
@@ -745,7 +761,7 @@ struct Sampler {
         const u64 sum = whole ? s.pick[4] : static_cast<u64>(mass * static_cast<float>(u64(1) << (44 - weigh.down)));
         int keep = most;
         // (the row's weight is not the survivors' where min_p drops some)
-        bool sure = whole || (tp < 1.0f && least <= -3.402823466e38f);
+        bool sure = whole || (tp < 1.0f && least <= -3.402823466e38f && mass > 0.5f);
         if (tp < 1.0f) {
           const u64 off = whole ? 0 : (sum >> 17) + 1;
           const u64 lo = max(u64(1), part_of(sum - off, tp, true)), hi = max(u64(1), part_of(sum + off, tp, true));
@@ -817,7 +833,7 @@ struct Sampler {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u64 w = 0;
     uint32_t n = 0, e = 0;
-    row.template stream<2>([&](const uint4 &v, int) {
+    row.template in_order<2>([&](const uint4 &v, int, int) {
       e += Row<T>::kept(v, kp.least, [&](float x) {
         w += weight(x);
         ++n;
@@ -966,13 +982,17 @@ struct Sampler {
 
   // ---- 16-bit logits, counted by value: all sums from counts, each value weighed once
   static __device__ __forceinline__ int value_index(float x) {   // -1: another magnitude
-    const uint32_t u = __float_as_uint(x) >> 16, i = (u & 0x7fffu) - kFirstValue;
-    return i >= kEndValue - kFirstValue ? -1 : static_cast<int>(u & 0x8000u ? kHalfValues + i : kHalfValues - 1 - i);
+    return bits_index(__float_as_uint(x) >> 16);
+  }
+  static __device__ __forceinline__ int bits_index(uint32_t u) {
+    const uint32_t i = (u & 0x7fffu) - kFirstValue;
+    return i >= kEndValue - kFirstValue ? -1 : static_cast<int>(i + (u >> 15) * kHalfValues);
   }
   static __device__ __forceinline__ float value_of(int b) {
-    const uint32_t u = b < kHalfValues ? kFirstValue + (kHalfValues - 1 - b) : 0x8000u | (kFirstValue + (b - kHalfValues));
-    return __uint_as_float(u << 16);
+    return __uint_as_float((b < kHalfValues ? kFirstValue + b : 0x8000u | (kFirstValue + (b - kHalfValues))) << 16);
   }
+  // The k-th largest value's index.
+  static __device__ __forceinline__ int ordered(int k) { return k < kHalfValues ? kHalfValues - 1 - k : k; }
   __device__ __forceinline__ u64 value_weight(float x) const {
     const int b = value_index(x);
     return b >= 0 ? s.weight[b] : weigh(x);
@@ -993,16 +1013,23 @@ struct Sampler {
     for (int i = t; i < kValues; i += kSaThreads) s.hist[i] = 0;
     if (t == 0) s.odd_count = 0;
     __syncthreads();
-    row.each_light([&](float x) {
-      if (x >= least) {
-        const int b = value_index(x);
-        if (b >= 0) {
-          atomicAdd(&s.hist[b], 1u);
-        } else {
-          const uint32_t at = atomicAdd(&s.odd_count, 1u);
-          if (at < kOdd) s.odd[at] = x;
-        }
+    row.template stream<4>([&](const uint4 &v, int, int) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+        const int b = bits_index(u);
+        if (b >= 0) atomicAdd(&s.hist[b], 1u);
+        odd |= b < 0 && u != 0xff80u;   // -infinity counts nowhere
       }
+      if (odd)
+        row.elements(v, 0, [&](float x, int) {
+          if (x >= least && value_index(x) < 0) {
+            const uint32_t at = atomicAdd(&s.odd_count, 1u);
+            if (at < kOdd) s.odd[at] = x;
+          }
+        });
     });
     __syncthreads();
     const uint32_t n = s.odd_count;
@@ -1020,8 +1047,9 @@ struct Sampler {
     u64 cn = 0, cw = 0;
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
-      const int b = t * kPer + i;
-      const u64 k = total[b], w = k ? weigh(value_of(b)) : 0;
+      const int b = ordered(t * kPer + i);
+      const float x = value_of(b);
+      const u64 k = x >= least ? total[b] : 0, w = k ? weigh(x) : 0;
       s.weight[b] = w;
       cn += k;
       cw += k * w;
@@ -1049,15 +1077,15 @@ struct Sampler {
     return true;
   }
   // find() over counted values. False: the border lies among those kept aside.
-  __device__ bool find_value(const Counted &c, bool by_weight, u64 target, uint32_t &key, u64 &at, u64 &above,
+  __device__ bool find_value(const Counted &c, float least, bool by_weight, u64 target, uint32_t &key, u64 &at, u64 &above,
                              u64 &above_w) {
     u64 n = c.count, w = c.weight;
     if (threadIdx.x == 0) s.pick[0] = ~u64(0);
     __syncthreads();
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
-      const int b = threadIdx.x * kPer + i;
-      const u64 k = total[b], kw = k * s.weight[b];
+      const int b = ordered(threadIdx.x * kPer + i);
+      const u64 k = value_of(b) >= least ? total[b] : 0, kw = k * s.weight[b];
       if (by_weight ? w < target && w + kw >= target : n < target && n + k >= target) {
         s.pick[0] = b;
         s.pick[1] = n;
@@ -1114,7 +1142,9 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SPara
     for (int c = 0; c < nc; ++c) m = fmaxf(m, __uint_as_float(static_cast<uint32_t>(ld_remote64(remote(&s.sums[0][a.slot], c)))));
     a.slot ^= 1;
   }
-  mass = warp_sum(mass * exp2f((ref - fmaxf(m, -1e30f)) * fmaxf(ch, 1e-30f)));
+  // (a row whose scaled maximum lies below -1e30 has no sum here; such rows do without)
+  // nor does one that overflows when scaled: 1e30 marks it, and its NaNs are looked for below
+  mass = warp_sum(!(ref < INFINITY) ? 1e30f : mass == 0.0f ? 0.0f : mass * exp2f(fmaf(-m, fmaxf(ch, 1e-30f), ref)));
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.fscan[warp] = mass;
   __syncthreads();
@@ -1128,6 +1158,11 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SPara
     a.slot ^= 1;
   }
   const uint32_t best = order_key(m);
+  if (mass > 1e20f && m < INFINITY) {
+    u64 nans = 0;
+    row.each_light([&](float x) { nans += x != x ? 1 : 0; });
+    mass = a.cluster_sum(nans) ? NAN : 0.0f;
+  }
   const bool sound = mass == mass && fabsf(m) < INFINITY;
   float x_tok = m;
   int token = 0;
@@ -1197,7 +1232,7 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SPara
       u64 at, above, above_w, weight = c.all_weight;
       count = c.all_count;
       if (k > 0 && static_cast<u64>(k) < count) {
-        settled = a.find_value(c, false, k, key, at, above, above_w);
+        settled = a.find_value(c, least, false, k, key, at, above, above_w);
         if (settled) {
           cut_k(key, at, above);
           weight = above_w + (static_cast<u64>(k) - above) * a.weigh(least);
@@ -1205,7 +1240,7 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SPara
       }
       if (settled && by_p) {
         const u64 target = max(u64(1), part_of(weight, tp, true)), n_all = count;
-        settled = a.find_value(c, true, target, key, at, above, above_w);
+        settled = a.find_value(c, least0, true, target, key, at, above, above_w);
         if (settled) cut_p(key, at, above, above_w, target, n_all);
       }
       if (!settled) {
