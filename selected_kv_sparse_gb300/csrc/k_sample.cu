@@ -630,7 +630,7 @@ struct Sampler {
     sum = 0.0f;
     tile[0] = tile[1] = -INFINITY;
     const F2 cc = f2(c, c);
-    row.template stream<4>([&](const uint4 &raw, int, int q) {
+    row.template stream<8>([&](const uint4 &raw, int, int q) {
       const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
       float v, s0, s1;
       F2 t[4];
@@ -696,10 +696,12 @@ struct Sampler {
     const uint32_t count_at = remote(&s.few_count, 0);
     auto push = [&](float x, int id) {
       if (x >= low) {
-        const uint32_t at = add_remote32(count_at, 1);
-        if (at < kFew)
-          st_remote64(remote(&s.few.list[at], 0),
-                      (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id)));
+        const u64 e = (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+        const uint32_t at = nc > 1 ? add_remote32(count_at, 1) : atomicAdd(&s.few_count, 1u);
+        if (at < kFew) {
+          if (nc > 1) st_remote64(remote(&s.few.list[at], 0), e);
+          else s.few.list[at] = e;
+        }
       }
     };
 #pragma unroll 1
