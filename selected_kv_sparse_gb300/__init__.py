@@ -23,4 +23,4 @@ from ._binding import (  # noqa: F401
     PrefixGroups, kap_append_kv_norm, kap_attn_verify_shared, kap_sample_tokens, kap_shared_workspace_size,
     rope_freq_axis,
 )
-from .pipeline import DecodeCycle, DecodeLoop, SideFlowDecode  # noqa: F401
+from .pipeline import DecodeCycle, DecodeLoop, QKNorm, SideFlowDecode  # noqa: F401

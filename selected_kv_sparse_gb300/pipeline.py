@@ -15,9 +15,17 @@ tokens on the same stream between the cycle's calls must pass overlap=False.
 With `packed` (a PackedPool whose 16-bit part is `pool`), block tables may name packed 4-bit pages: routing reads the
 packed pool's summaries, appends write the 16-bit pages, and both attentions are the packed calls. A step is then the
 append (which rotates its queries in place, as with fused=False) followed by the attention.
+
+With `norm` (QKNorm) or `rope_offset`, appends are kap_append_kv_norm: queries and keys are normalised a head, and a
+generated token is rotated at its logical position plus its request's offset on every axis (the text after images, whose
+position ids run behind the token count; the offsets are read when the cycle is built). Queries are then rotated in
+place, as with fused=False. With `groups` (kb.PrefixGroups), verification is kap_attn_verify_shared: pages that requests
+share are read once a group.
 """
 from __future__ import annotations
 
+import contextlib
+from dataclasses import dataclass
 from typing import Optional
 
 import torch
@@ -27,18 +35,32 @@ from . import _binding as kb
 PAGE = 16
 
 
+@dataclass
+class QKNorm:
+    """Per-head norms of queries and keys before their rotation: weights [d] fp32 on the device (None: not normalised)."""
+    q_weight: Optional[torch.Tensor]
+    k_weight: Optional[torch.Tensor]
+    eps: float = 1e-6
+
+
 class DecodeCycle:
     def __init__(self, pool: kb.KVPool, block_table: torch.Tensor, ctx_len: torch.Tensor, seq_len0: torch.Tensor,
                  k_prop: int, n_q: torch.Tensor, inv_freq: torch.Tensor, policy: Optional[kb.AccessPolicy] = None,
                  spans: Optional[torch.Tensor] = None, span_offsets: Optional[torch.Tensor] = None,
                  sel_cap: Optional[int] = None, s_max: float = 1.0, fused: bool = True,
                  outputs: Optional[dict] = None, overlap: bool = True,
-                 workspace_pages: Optional[tuple] = None, packed: Optional[kb.PackedPool] = None):
+                 workspace_pages: Optional[tuple] = None, packed: Optional[kb.PackedPool] = None,
+                 norm: Optional[QKNorm] = None, rope_offset: Optional[torch.Tensor] = None,
+                 groups: Optional[kb.PrefixGroups] = None):
         dev = block_table.device
+        if packed is not None and groups is not None:
+            raise ValueError("groups need a pool without packed pages")
         if packed is not None and (packed.pool is not pool or workspace_pages is not None):
             raise ValueError("packed must hold this pool, and has no materialised workspace")
         self.packed = packed
-        self.fused = bool(fused) and packed is None
+        self.norm, self.groups = norm, groups
+        self.fused = bool(fused) and packed is None and norm is None and rope_offset is None
+        self.fused_plan = bool(fused) or packed is not None
         # (first pool page, pages per request) of a materialised compact workspace, or None for the zero-copy view
         self.workspace_pages = tuple(workspace_pages) if workspace_pages is not None else None
         self.overlap = bool(overlap)
@@ -88,12 +110,27 @@ class DecodeCycle:
             self.slots_ver = torch.zeros(self.total_q, dtype=torch.int64, device=dev)
             self.pos_ver = torch.zeros(self.total_q, **i32)
         self.vpol = kb.VerifyPolicy(self.q_offsets, self.q_start, self.max_q, self.total_q)
+        # positions that appends rotate at: the logical ones, or those plus each request's offset
+        self.rope_prop, self.rope_ver = self.pos_prop, self.pos_ver
+        self.offset_prop = self.offset_ver = None
+        if rope_offset is not None:
+            if tuple(rope_offset.shape) != (self.R,) or rope_offset.dtype != torch.int32:
+                raise ValueError("rope_offset must be int32 [R]")
+            self.offset_prop = rope_offset.repeat_interleave(self.horizon)
+            self.rope_prop = torch.zeros_like(self.pos_prop)
+            self.rope_ver = self.rope_prop
+            if not self.window_is_horizon:
+                self.offset_ver = torch.repeat_interleave(rope_offset, torch.tensor(n_q_host, device=dev))
+                self.rope_ver = torch.zeros_like(self.pos_ver)
         # workspaces (zero-filled once)
         mp = int(block_table.shape[1])
         self.ws_score = kb.workspace(kb.kap_score_workspace_size(self.R, self.rows, mp), dev)
         if packed is None:
             self.ws_prop = kb.workspace(kb.kap_propose_workspace_size(self.R, self.Hkv, self.Hq, self.d), dev)
-            self.ws_ver = kb.workspace(kb.kap_verify_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.max_q), dev)
+            self.ws_ver = kb.workspace(
+                kb.kap_verify_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.max_q) if groups is None else
+                kb.kap_shared_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.total_q, groups.prefix_pages.numel()),
+                dev)
         else:
             self.ws_prop = kb.workspace(kb.kap_packed_workspace_size(self.R, self.Hkv, self.Hq, self.d, 1), dev)
             self.ws_ver = kb.workspace(kb.kap_packed_workspace_size(self.R, self.Hkv, self.Hq, self.d, self.max_q), dev)
@@ -123,7 +160,7 @@ class DecodeCycle:
         if self.spans is not None:
             kb.kap_select_spans(self.map_plan, self.spans, self.span_offsets, self.policy, self.sel_ids, self.n_sel,
                                 stream)
-        elif self.fused or self.packed is not None:
+        elif self.fused_plan:
             kb.kap_score_topk_view(self.pool if self.packed is None else self.packed.routing(), self.map_plan, q_route,
                                    self.policy, self.sel_ids, self.n_sel,
                                    self.ws_score, self.horizon, self.view, self.fallback, self.s_max, self.slots_prop,
@@ -131,11 +168,16 @@ class DecodeCycle:
         else:
             kb.kap_score_topk(self.pool, self.map_plan, q_route, self.policy, self.sel_ids, self.n_sel, self.ws_score,
                               stream)
-        if self.spans is not None or not (self.fused or self.packed is not None):
+        if self.spans is not None or not self.fused_plan:
             kb.kap_compile_view(self.map_plan, self.sel_ids, self.n_sel, self.horizon, self.view, self.fallback,
                                 self.s_max, self.slots_prop, self.pos_prop, stream)
         if not self.window_is_horizon:
             kb.kap_slot_mapping(self.map_plan, self.q_offsets, self.q_start, self.slots_ver, self.pos_ver, stream)
+        if self.offset_prop is not None:
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                torch.add(self.pos_prop, self.offset_prop, out=self.rope_prop)
+                if self.offset_ver is not None:
+                    torch.add(self.pos_ver, self.offset_ver, out=self.rope_ver)
         if self.workspace_pages is not None:   # copy the selected pages into the workspace, view rewritten in place
             kb.kap_materialize_view(self.pool, self.map_plan, self.view, self.workspace_pages[0],
                                     self.workspace_pages[1],
@@ -149,10 +191,21 @@ class DecodeCycle:
         self._view_fresh = False
         return s
 
+    def _append(self, q, k_new, v_new, pos, rope, slots, num_tokens, tok_stride, stream):
+        """The KV append of the cycle's kind; q is rotated (and normalised) in place."""
+        if self.norm is None and self.offset_prop is None:
+            kb.kap_append_kv(self.pool, k_new, v_new, q, pos, slots, self.inv_freq, num_tokens=num_tokens,
+                             tok_stride=tok_stride, stream=stream)
+            return
+        n = self.norm if self.norm is not None else QKNorm(None, None)
+        kb.kap_append_kv_norm(self.pool, k_new, v_new, q, q, rope, slots, self.inv_freq, q_weight=n.q_weight,
+                              k_weight=n.k_weight, eps=n.eps, num_tokens=num_tokens, tok_stride=tok_stride,
+                              stream=stream)
+
     def append_step(self, i: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """Proposal step i, first half: the step token's KV at its logical position (q rotated in place)."""
-        kb.kap_append_kv(self.pool, k_new, v_new, q, self.pos_prop[i:], self.slots_prop[i:], self.inv_freq,
-                         num_tokens=self.R, tok_stride=self.horizon, stream=stream)
+        self._append(q, k_new, v_new, self.pos_prop[i:], self.rope_prop[i:], self.slots_prop[i:], self.R, self.horizon,
+                     stream)
         self._view_fresh = False
 
     def propose(self, i: int, q: torch.Tensor, stream=None, settled: Optional[bool] = None):
@@ -180,7 +233,7 @@ class DecodeCycle:
 
     def append_window(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """The verify window's KV into the full-context slots (q rotated in place)."""
-        kb.kap_append_kv(self.pool, k_new, v_new, q, self.pos_ver, self.slots_ver, self.inv_freq, stream=stream)
+        self._append(q, k_new, v_new, self.pos_ver, self.rope_ver, self.slots_ver, None, 1, stream)
         self._view_fresh = False
 
     def verify(self, q: torch.Tensor, k_new: torch.Tensor = None, v_new: torch.Tensor = None, stream=None):
@@ -190,6 +243,9 @@ class DecodeCycle:
         if self.packed is not None:
             kb.kap_attn_verify_packed(self.packed, self.map_full, self.vpol, q, self.o_ver, self.lse_ver, self.ws_ver,
                                       stream)
+        elif self.groups is not None:
+            kb.kap_attn_verify_shared(self.pool, self.map_full, self.vpol, self.groups, q, self.o_ver, self.lse_ver,
+                                      self.ws_ver, stream)
         else:
             kb.kap_attn_verify(self.pool, self.map_full, self.vpol, q, self.o_ver, self.lse_ver, self.ws_ver, stream)
         self._view_fresh = False
@@ -204,12 +260,13 @@ class DecodeCycle:
         """Kernel launches of one run(): selection and view (score + top-K with the view fused in; unfused score,
         top-K and view; or spans and view), a separate window slot mapping when the windows differ from the
         horizon, per step one fused kernel (or an append and a proposal kernel), then the window append and
-        verification; plus the materialisation when a workspace is used."""
-        sel_view = 2 if self.spans is not None else (2 if self.fused or self.packed is not None else 3)
+        verification (two kernels over shared prefixes); plus the materialisation when a workspace is used. PyTorch's
+        addition of rope offsets, one kernel a slot mapping, is not counted."""
+        sel_view = 2 if self.spans is not None or self.fused_plan else 3
         sel_view += 1 if self.workspace_pages is not None else 0
         slots = 0 if self.window_is_horizon else 1
         per_step = 1 if self.fused else 2
-        return sel_view + slots + per_step * self.k_prop + 2
+        return sel_view + slots + per_step * self.k_prop + 2 + (1 if self.groups is not None else 0)
 
 
 class SideFlowDecode:
