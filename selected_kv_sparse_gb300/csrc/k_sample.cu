@@ -173,6 +173,7 @@ struct Shared {
   u64 sums[3][2];   // values for the other CTAs, in turn: a slot is written again two exchanges later
   u64 pick[6];
   float fscan[kSaWarps];
+  u64 own_w[kSaWarps], own_n[kSaWarps], cut;   // candidates above the border: weight, number, and at it, of each warp
   uint32_t few_count, few_done, odd_count;
   uint32_t joined[];   // [kValues] the cluster's histogram, where it has more than one CTA
 };
@@ -509,6 +510,33 @@ struct Sampler {
     return up ? fminf(weigh.m, weigh.m - d + slack) : weigh.m - d - slack;
   }
 
+  // Bounds of a bin's weight: that of one logit at its edge b / 16 octaves down, at most and at least (a logit's bin may be
+  // off by 2^-19 of its distance, so 2^-12 of its weight).
+  __device__ __forceinline__ u64 edge(int b) const {
+    const int e = (b >> 4) + weigh.down;
+    return e < 64 ? weigh.tab->q[(b & 15) * 4] >> e : u64(0);
+  }
+  __device__ __forceinline__ u64 bin_most(int b) const {
+    const u64 w = edge(b);
+    return total[b] * (w + (w >> 12) + 4);
+  }
+  __device__ __forceinline__ u64 bin_least(int b) const {
+    const u64 w = edge(b + 1);
+    return b == kBins - 1 || w < 8 ? u64(0) : total[b] * (w - (w >> 12) - 4);
+  }
+  // The bins in which the running weight can reach a target between `lo` and `hi`, and the interval of keys they can hold.
+  __device__ void border_bins(u64 lo, u64 hi, int &b0, int &b1) {
+    b0 = first_bin(0, lo, [&](int b) { return bin_most(b); });
+    b1 = first_bin(0, hi, [&](int b) { return bin_least(b); });
+  }
+  __device__ void keys_of(int b0, int b1, uint32_t floor, uint32_t top, uint32_t &khi, uint32_t &klo) const {
+    khi = top;
+    klo = floor;
+    if (b0 > 0) khi = min(top, order_key(bin_edge(static_cast<float>(b0), true)));
+    if (b1 < kBins - 1) klo = max(floor, order_key(bin_edge(static_cast<float>(b1 + 1), false)));
+    khi = max(khi, klo);
+  }
+
   // After histogram(key_value(floor)): the least logit of the shortest run of the rank order, among logits whose key is
   // `floor` or more, that holds `target` tokens (by_weight false) or that much weight. Out: its key, how many tokens at it
   // and above it there are, and the weight above (by_weight). The run has to exist.
@@ -516,27 +544,14 @@ struct Sampler {
                        u64 &above_w) {
     int b0, b1;
     if (by_weight) {
-      // the weight at a bin's edge, b / 16 octaves down; a logit's bin may be off by 2^-19 of its distance (2^-12 of a weight)
-      auto edge = [&](int b) {
-        const int e = (b >> 4) + weigh.down;
-        return e < 64 ? weigh.tab->q[(b & 15) * 4] >> e : u64(0);
-      };
-      b0 = first_bin(0, target, [&](int b) {
-        const u64 w = edge(b);
-        return total[b] * (w + (w >> 12) + 4);
-      });
-      b1 = first_bin(0, target, [&](int b) {
-        const u64 w = edge(b + 1);
-        return b == kBins - 1 || w < 8 ? u64(0) : total[b] * (w - (w >> 12) - 4);
-      });
+      border_bins(target, target, b0, b1);
     } else {
       b0 = b1 = first_bin(0, target, [&](int b) { return static_cast<u64>(total[b]); });
     }
-    // the interval of keys that the bins b0 .. b1 can hold
-    uint32_t khi = top, klo = floor;
-    if (b0 > 0) khi = min(top, order_key(bin_edge(static_cast<float>(b0), true)));
-    if (b1 < kBins - 1) klo = max(floor, order_key(bin_edge(static_cast<float>(b1 + 1), false)));
-    khi = max(khi, klo);
+    uint32_t khi, klo;
+    keys_of(b0, b1, floor, top, khi, klo);
+    float known = INFINITY;   // what lies above it is in `above` and `above_w` already: khi only falls
+    above = above_w = 0;
     while (true) {
       const uint32_t range = khi - klo;
       const int sh = max(0, 32 - __clz(range) - 11);
@@ -550,20 +565,23 @@ struct Sampler {
       if (by_weight) {
         row.each([&](float x, int) {
           if (x > vhi) {
-            ++n;
-            w += weigh(x);
+            if (x <= known) {
+              ++n;
+              w += weigh(x);
+            }
           } else {
             place(x);
           }
         });
       } else {
         row.each_light([&](float x) {
-          if (x > vhi) ++n;
+          if (x > vhi) n += x <= known ? 1 : 0;
           else place(x);
         });
       }
-      above = cluster_sum(n);
-      above_w = by_weight ? cluster_sum(w) : 0;
+      above += cluster_sum(n);
+      if (by_weight) above_w += cluster_sum(w);
+      known = vhi;
       join_hist();
       auto hi_key = [&](int b) { return khi - (static_cast<uint32_t>(b) << sh); };
       auto lo_key = [&](int b) {   // the last bin may reach past klo
@@ -668,10 +686,51 @@ struct Sampler {
     });
   }
 
+  // The candidates in s.few.list in the rank order, in the CTA that has them: thread t gets the places 2 t and 2 t + 1 with
+  // their weights (0 below `least`) and the running sums; its number of those from `least` on.
+  __device__ int sort_list(int n, float least, u64 (&e)[2], u64 (&w)[2], u64 (&cum)[2]) {
+    for (int i = threadIdx.x; i < n; i += kSaThreads) {
+      const u64 v = s.few.list[i];
+      int place = 0;
+      for (int q = 0; q < n; ++q) place += s.few.list[q] > v ? 1 : 0;
+      s.few.sorted[place] = v;
+    }
+    __syncthreads();
+    int in = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int i = 2 * threadIdx.x + q;
+      e[q] = i < n ? s.few.sorted[i] : 0;
+      const float x = key_value(static_cast<uint32_t>(e[q] >> 32));
+      const bool is = i < n && x >= least;
+      w[q] = is ? weigh(x) : 0;
+      in += is ? 1 : 0;
+      s.few.w[i] = w[q];
+    }
+    cum[1] = block_inclusive_scan(w[0] + w[1], s.scan);
+    cum[0] = cum[1] - w[1];
+    return in;
+  }
+  __device__ __forceinline__ void push(float x, int id) {
+    const u64 e = (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+    const uint32_t at = nc > 1 ? add_remote32(remote(&s.few_count, 0), 1) : atomicAdd(&s.few_count, 1u);
+    if (at < kFew) {
+      if (nc > 1) st_remote64(remote(&s.few.list[at], 0), e);
+      else s.few.list[at] = e;
+    }
+  }
+
   // The draw from few candidates: all logits at or above a bar that at least `n_bar` logits reach, gathered in the first CTA
   // and sorted there. It decides the row unless there are too many of them, or a border lies past them or within the error of
-  // the row's approximate weight `mass` (2^-17 of it: sums of 32 terms a lane and their joins at 2^-24 each, exponentials
-  // 2^-22). True when the row is done. All of the cluster takes part.
+  // the row's approximate weight. True when the row is done. All of the cluster takes part.
+  // The approximate weight of first_pass() in whole units, and what it is off by at most: 6 * 2^-24 of it for each of a lane's
+  // vectors (a rounding, and where the reference changes an exponential's 2^-22 and a product's rounding), 64 * 2^-24 for
+  // exponents off by 2^-20, joins, and weights cut to units.
+  __device__ void about(float mass, u64 &sum, u64 &off) const {
+    sum = static_cast<u64>(mass * static_cast<float>(u64(1) << (44 - weigh.down)));
+    const u64 vectors = ((row.V / Row<T>::N + 1) / nc + 1) / kSaThreads + 2;
+    off = (sum >> 24) * (6 * vectors + 64) + 1;
+  }
   __device__ bool few(float mx, int n_bar, int k, bool greedy, float least, float tp, float u, float mass, float temp,
                       const SParams &p, int r) {
     const int lane = threadIdx.x & 31, t = threadIdx.x;
@@ -693,16 +752,8 @@ struct Sampler {
     float low = bar > 0x00800000u >> 16 ? key_value(bar << 16) : -INFINITY;   // the keys below are -infinity's and NaN's
     if (row.V <= kFew) low = -3.402823466e38f;   // all of them
     else if (!(low > -1e30f)) return false;
-    const uint32_t count_at = remote(&s.few_count, 0);
-    auto push = [&](float x, int id) {
-      if (x >= low) {
-        const u64 e = (static_cast<u64>(order_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
-        const uint32_t at = nc > 1 ? add_remote32(count_at, 1) : atomicAdd(&s.few_count, 1u);
-        if (at < kFew) {
-          if (nc > 1) st_remote64(remote(&s.few.list[at], 0), e);
-          else s.few.list[at] = e;
-        }
-      }
+    auto gather = [&](float x, int id) {
+      if (x >= low) push(x, id);
     };
 #pragma unroll 1
     for (int q0 = 0; q0 < kTiles; q0 += 32) {
@@ -721,7 +772,7 @@ struct Sampler {
           for (int c = 0; c < 4; ++c) v[c] = row.get_any(j[c] + 32 * kSaWarps * i);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (Row<T>::reaches(v[c], low)) row.elements(v[c], j[c] + 32 * kSaWarps * i, push);
+            if (Row<T>::reaches(v[c], low)) row.elements(v[c], j[c] + 32 * kSaWarps * i, gather);
         }
       }
     }
@@ -731,28 +782,8 @@ struct Sampler {
     if (rank == 0) {
       const int n = s.few_count;
       if (n <= kFew) {
-        for (int i = t; i < n; i += kSaThreads) {
-          const u64 v = s.few.list[i];
-          int place = 0;
-          for (int q = 0; q < n; ++q) place += s.few.list[q] > v ? 1 : 0;
-          s.few.sorted[place] = v;
-        }
-        __syncthreads();
-        // thread t looks at places 2 t and 2 t + 1
         u64 e[2], w[2], cum[2];
-        int in = 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int i = 2 * t + q;
-          e[q] = i < n ? s.few.sorted[i] : 0;
-          const float x = key_value(static_cast<uint32_t>(e[q] >> 32));
-          const bool is = i < n && x >= least;
-          w[q] = is ? weigh(x) : 0;
-          in += is ? 1 : 0;
-          s.few.w[i] = w[q];
-        }
-        cum[1] = block_inclusive_scan(w[0] + w[1], s.scan);
-        cum[0] = cum[1] - w[1];
+        const int in = sort_list(n, least, e, w, cum);
         if (t == 0) s.pick[2] = s.pick[3] = kFew;
         const int survive = static_cast<int>(block_sum(in, s.scan));   // a run from the first on
         const int most = k > 0 ? min(k, survive) : survive;
@@ -760,12 +791,12 @@ struct Sampler {
         const bool whole = k > 0 || least >= low;
         if ((most - 1) / 2 == t) s.pick[4] = (most - 1) & 1 ? cum[1] : cum[0];
         __syncthreads();
-        const u64 sum = whole ? s.pick[4] : static_cast<u64>(mass * static_cast<float>(u64(1) << (44 - weigh.down)));
+        u64 sum = s.pick[4], off = 0;
+        if (!whole) about(mass, sum, off);
         int keep = most;
         // (the row's weight is not the survivors' where min_p drops some)
         bool sure = whole || (tp < 1.0f && least <= -3.402823466e38f && mass > 0.5f);
         if (tp < 1.0f) {
-          const u64 off = whole ? 0 : (sum >> 17) + 1;
           const u64 lo = max(u64(1), part_of(sum - off, tp, true)), hi = max(u64(1), part_of(sum + off, tp, true));
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -832,7 +863,6 @@ struct Sampler {
     u64 mine, before, all, t_before, count;
   };
   template <class W> __device__ Sums sums(const Kept &kp, W &&weight) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     u64 w = 0;
     uint32_t n = 0, e = 0;
     row.template in_order<2>([&](const uint4 &v, int, int) {
@@ -841,6 +871,11 @@ struct Sampler {
         ++n;
       });
     });
+    return join_sums(kp, w, n, e);
+  }
+  // From each lane's weight and number of logits above `least` in its warp's range, and their number at it.
+  __device__ Sums join_sums(const Kept &kp, u64 w, uint32_t n, uint32_t e) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     n = __reduce_add_sync(0xffffffffu, n);
     e = __reduce_add_sync(0xffffffffu, e);
 #pragma unroll
@@ -882,6 +917,138 @@ struct Sampler {
     r.all = w_all + kp.of_ties(0, c_all & kLow);
     r.count = (c_all >> 32) + min(c_all & kLow, kp.ties);
     return r;
+  }
+  // top_p's cut of the logits from `least` on and the sums of what is kept, in a histogram and two passes in the order of ids:
+  // the first weighs every logit once and counts those in the interval of the border, which bounds of the row's weight
+  // (first_pass()'s, or the bins') give ahead of it; the second gathers the part that the border is in, which is sorted.
+  // False: too many logits there (equal ones, mostly).
+  __device__ bool nucleus(float least, float tp, float mass, Kept &kp, Sums &sm) {
+    const int t = threadIdx.x, warp = t >> 5;
+    __syncthreads();   // few_count has been read
+    if (t == 0) s.few_count = 0;
+    histogram(least, false);
+    u64 lo, hi;
+    if (least <= -3.402823466e38f && mass > 0.5f) {
+      u64 off;
+      about(mass, lo, off);
+      hi = lo + off;
+      lo -= min(lo, off);
+    } else {
+      lo = hi = 0;
+      for (int b = t; b < kBins; b += kSaThreads) {
+        lo += bin_least(b);
+        hi += bin_most(b);
+      }
+      lo = block_sum(lo, s.scan);
+      hi = block_sum(hi, s.scan);
+    }
+    // from the top the bins' bounds are apart by 1/16 octave of the share, from the bottom by that of the rest: both
+    int b0, b1;
+    border_bins(max(u64(1), part_of(lo, tp, false)), max(u64(1), part_of(hi, tp, true)), b0, b1);
+    const u64 rest_lo = lo - min(lo, part_of(lo, tp, true) + 1), rest_hi = hi - part_of(hi, tp, false);
+    const int least_up = first_bin(0, rest_hi + 1, [&](int b) { return bin_least(kBins - 1 - b); });
+    const int most_up = first_bin(0, rest_lo + 1, [&](int b) { return bin_most(kBins - 1 - b); });
+    if (least_up < kBins) b0 = max(b0, kBins - 1 - least_up);
+    if (most_up < kBins) b1 = min(b1, kBins - 1 - most_up);
+    b0 = min(b0, kBins - 1);
+    b1 = max(b0, b1);
+    uint32_t khi, klo;
+    keys_of(b0, b1, order_key(least), order_key(weigh.m), khi, klo);
+    const uint32_t range = khi - klo;
+    const int sh = max(0, 32 - __clz(range) - 11);
+    const float vhi = key_value(khi), vlo = key_value(klo);
+    __syncthreads();
+    for (int i = t; i < kBins; i += kSaThreads) s.hist[i] = 0;
+    __syncthreads();
+    u64 all = 0, w = 0;
+    uint32_t n = 0;
+    row.template in_order<2>([&](const uint4 &v, int j, int) {
+      row.elements(v, j, [&](float x, int) {
+        const u64 one = x >= least ? weigh(x) : 0;
+        all += one;
+        if (x > vhi) {
+          w += one;
+          ++n;
+        } else if (x >= vlo) {
+          atomicAdd(&s.hist[(khi - order_key(x)) >> sh], 1u);
+        }
+      });
+    });
+    all = cluster_sum(all);
+    const u64 first = cluster_sum(w), target = max(u64(1), part_of(all, tp, true));
+    join_hist();
+    if (first >= target) return false;
+    auto hi_key = [&](int b) { return khi - (static_cast<uint32_t>(b) << sh); };
+    auto lo_key = [&](int b) {
+      const u64 d = ((static_cast<u64>(b) + 1) << sh) - 1;
+      return d > range ? klo : khi - static_cast<uint32_t>(d);
+    };
+    auto used = [&](int b) { return total[b] != 0 && (static_cast<u64>(b) << sh) <= range; };
+    const u64 more = sh == 0 ? 0 : 4;   // neighbours' weights may be out of order by their rounding
+    b0 = first_bin(first, target, [&](int b) { return used(b) ? total[b] * (weigh(key_value(hi_key(b))) + more) : u64(0); });
+    b1 = first_bin(first, target, [&](int b) {
+      const u64 lw = used(b) ? weigh(key_value(lo_key(b))) : 0;
+      return lw > more ? total[b] * (lw - more) : u64(0);
+    });
+    const int last = static_cast<int>(range >> sh);
+    b1 = min(b1, last);
+    u64 some = 0;
+    for (int b = b0 + t; b <= b1; b += kSaThreads) some += total[b];
+    if (b0 > last || block_sum(some, s.scan) > kFew) return false;
+    const float ghi = key_value(hi_key(b0)), glo = key_value(lo_key(b1));
+    row.template in_order<2>([&](const uint4 &v, int j, int) {
+      row.elements(v, j, [&](float x, int id) {
+        if (x <= vhi && x >= glo) {
+          if (x > ghi) {
+            w += weigh(x);
+            ++n;
+          } else {
+            push(x, id);
+          }
+        }
+      });
+    });
+    const u64 above = cluster_sum(w);
+    if (t < kSaWarps) s.own_w[t] = s.own_n[t] = 0;
+    if (t == 0) s.cut = 0;
+    __syncthreads();
+    if (rank == 0) {
+      u64 e[2], we[2], cum[2];
+      sort_list(min(s.few_count, static_cast<uint32_t>(kFew)), least, e, we, cum);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (above + cum[q] >= target && above + cum[q] - we[q] < target) s.cut = e[q];
+    }
+    if (nc > 1) cluster_sync();
+    else __syncthreads();
+    const u64 cut = ld_remote64(remote(&s.cut, 0));
+    const uint32_t n_list = ld_remote32(remote(&s.few_count, 0));
+    if (cut == 0 || n_list > kFew) return false;
+    // the candidates above the border and at it, to the warps whose they are
+    const int per = (row.c1 - row.c0 + kSaWarps - 1) / kSaWarps;
+    u64 ties = 0;
+    for (uint32_t i = t; i < n_list; i += kSaThreads) {
+      const u64 e = ld_remote64(remote(&s.few.list[i], 0));
+      const bool above_it = e >> 32 > cut >> 32, at_it = e >> 32 == cut >> 32;
+      const int j = (static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)) + row.sh) / Row<T>::N;
+      if (j >= row.c0 && j < row.c1) {
+        const int o = (j - row.c0) / per;
+        if (above_it) atomicAdd(&s.own_w[o], weigh(key_value(static_cast<uint32_t>(e >> 32))));
+        if (above_it || at_it) atomicAdd(&s.own_n[o], above_it ? u64(1) << 32 : u64(1));
+      }
+      ties += at_it && e >= cut ? 1 : 0;
+    }
+    kp.least = key_value(static_cast<uint32_t>(cut >> 32));
+    kp.ties = block_sum(ties, s.scan);
+    kp.w_least = weigh(kp.least);
+    uint32_t at = 0;
+    if ((t & 31) == 0) {
+      w += s.own_w[warp];
+      n += static_cast<uint32_t>(s.own_n[warp] >> 32);
+      at = static_cast<uint32_t>(s.own_n[warp]);
+    }
+    sm = join_sums(kp, w, n, at);
+    return true;
   }
   // The id at which the running kept weight in id order first passes `target`, and its logit; -1 if it never does. Every
   // thread of the cluster gets them.
@@ -1110,8 +1277,106 @@ struct Sampler {
   }
 };
 
+// The draw from rows that few candidates do not decide. Out of line, so that the passes before it have their registers.
 template <class T>
-__global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SParams p) {
+__device__ __noinline__ void draw_kept(const Row<T> row, Shared &s, int slot, const Weigh weigh, int k, float tp, float u,
+                                       float least, float mass, float temp, const SParams &p, int r) {
+  const int rank = cluster_rank(), nc = cluster_size();
+  Sampler<T> a{row, s, rank, nc, slot, weigh, nc > 1 ? s.joined : s.hist, 0};
+  const uint32_t best = order_key(weigh.m);
+  float x_tok = 0.0f;
+  int token = 0;
+  u64 count = 0;
+  // kept: the logits above `least`, and of those at it the first `ties` in id order
+  constexpr u64 kAll = ~u64(0);
+  u64 ties = kAll, total = 0;
+  bool settled = false;
+  const bool by_p = tp < 1.0f;
+  const float least0 = least;
+  // the steps on any way of counting: top_k's cut of `all` tokens, then top_p's
+  auto cut_k = [&](uint32_t key, u64 at, u64 above) {
+    least = key_value(key);
+    ties = static_cast<u64>(k) - above < at ? static_cast<u64>(k) - above : kAll;
+    count = k;
+  };
+  auto cut_p = [&](uint32_t key, u64 at, u64 above, u64 above_w, u64 target, u64 n_all) {
+    const u64 each = a.weigh(key_value(key));
+    const bool last = key_value(key) == least;   // the least logit that top_k left
+    if (last) at = min(at, n_all - above);
+    const u64 need = each ? min(at, (target - above_w + each - 1) / each) : at;
+    count = above + need;
+    ties = need < at || (last && ties != kAll) ? need : kAll;
+    least = key_value(key);
+  };
+  typename Sampler<T>::Counted c;
+  if (sizeof(T) == 2 && ((k > 0 && k < p.V) || by_p) && a.count_values(least, c)) {
+    settled = true;
+    uint32_t key;
+    u64 at, above, above_w, weight = c.all_weight;
+    count = c.all_count;
+    if (k > 0 && static_cast<u64>(k) < count) {
+      settled = a.find_value(c, least, false, k, key, at, above, above_w);
+      if (settled) {
+        cut_k(key, at, above);
+        weight = above_w + (static_cast<u64>(k) - above) * a.weigh(least);
+      }
+    }
+    if (settled && by_p) {
+      const u64 target = max(u64(1), part_of(weight, tp, true)), n_all = count;
+      settled = a.find_value(c, least0, true, target, key, at, above, above_w);
+      if (settled) cut_p(key, at, above, above_w, target, n_all);
+    }
+    if (!settled) {
+      least = least0;
+      ties = kAll;
+    }
+  }
+  const bool by_value = settled;
+  typename Sampler<T>::Kept kp{};
+  typename Sampler<T>::Sums sm{};
+  const bool summed = sizeof(T) == 4 && by_p && !(k > 0 && k < p.V) && a.nucleus(least, tp, mass, kp, sm);
+  if (!settled && !summed) {
+    if (k > 0 && k < p.V) {
+      count = a.histogram(least, false).count;
+      if (static_cast<u64>(k) < count) {
+        uint32_t key;
+        u64 at, above, unused;
+        a.find(false, k, order_key(least), best, key, at, above, unused);
+        cut_k(key, at, above);
+      }
+    }
+    if (by_p) {
+      auto whole = a.histogram(least, true);
+      u64 n_all = whole.count;
+      if (ties != kAll) {   // tokens at the least logit that top_k does not keep
+        whole.weight -= (whole.count - count) * a.weigh(least);
+        n_all = count;
+      }
+      const u64 target = max(u64(1), part_of(whole.weight, tp, true));
+      uint32_t key;
+      u64 at, above, above_w;
+      a.find(true, target, order_key(least), best, key, at, above, above_w);
+      cut_p(key, at, above, above_w, target, n_all);
+    }
+  }
+  if (!summed) kp = {least, ties, a.weigh(least)};
+  auto draw = [&](auto &&weight) {
+    if (!summed) sm = a.sums(kp, weight);
+    count = sm.count;
+    total = sm.all;
+    token = a.pick(sm, kp, part_of(total, u, false), weight, x_tok);
+  };
+  if (by_value) draw([&](float x) { return a.value_weight(x); });
+  else draw([&](float x) { return a.weigh(x); });
+  if (rank == 0 && threadIdx.x == 0) {
+    p.tokens[r] = max(token, 0);
+    if (p.logprob) p.logprob[r] = a.log_share(x_tok, total, temp);
+    if (p.kept) p.kept[r] = static_cast<int32_t>(count);
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const __grid_constant__ SParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared &s = *reinterpret_cast<Shared *>(smem);
   grid_dependency_sync();
@@ -1159,7 +1424,6 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SPara
     for (int c = 0; c < nc; ++c) mass += __uint_as_float(static_cast<uint32_t>(ld_remote64(remote(&s.sums[0][a.slot], c))));
     a.slot ^= 1;
   }
-  const uint32_t best = order_key(m);
   if (mass > 1e20f && m < INFINITY) {
     u64 nans = 0;
     row.each_light([&](float x) { nans += x != x ? 1 : 0; });
@@ -1206,85 +1470,8 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const SPara
     lp = sound ? 0.0f : NAN;
     count = sound ? 1 : 0;
   } else {
-    // kept: the logits above `least`, and of those at it the first `ties` in id order
-    constexpr u64 kAll = ~u64(0);
-    u64 ties = kAll, total = 0;
-    bool settled = false;
-    const bool by_p = tp < 1.0f;
-    const float least0 = least;
-    // the steps on any way of counting: top_k's cut of `all` tokens, then top_p's
-    auto cut_k = [&](uint32_t key, u64 at, u64 above) {
-      least = key_value(key);
-      ties = static_cast<u64>(k) - above < at ? static_cast<u64>(k) - above : kAll;
-      count = k;
-    };
-    auto cut_p = [&](uint32_t key, u64 at, u64 above, u64 above_w, u64 target, u64 n_all) {
-      const u64 each = a.weigh(key_value(key));
-      const bool last = key_value(key) == least;   // the least logit that top_k left
-      if (last) at = min(at, n_all - above);
-      const u64 need = each ? min(at, (target - above_w + each - 1) / each) : at;
-      count = above + need;
-      ties = need < at || (last && ties != kAll) ? need : kAll;
-      least = key_value(key);
-    };
-    typename Sampler<T>::Counted c;
-    if (sizeof(T) == 2 && a.count_values(least, c)) {
-      settled = true;
-      uint32_t key;
-      u64 at, above, above_w, weight = c.all_weight;
-      count = c.all_count;
-      if (k > 0 && static_cast<u64>(k) < count) {
-        settled = a.find_value(c, least, false, k, key, at, above, above_w);
-        if (settled) {
-          cut_k(key, at, above);
-          weight = above_w + (static_cast<u64>(k) - above) * a.weigh(least);
-        }
-      }
-      if (settled && by_p) {
-        const u64 target = max(u64(1), part_of(weight, tp, true)), n_all = count;
-        settled = a.find_value(c, least0, true, target, key, at, above, above_w);
-        if (settled) cut_p(key, at, above, above_w, target, n_all);
-      }
-      if (!settled) {
-        least = least0;
-        ties = kAll;
-      }
-    }
-    const bool by_value = settled;
-    if (!settled) {
-      if (k > 0 && k < p.V) {
-        count = a.histogram(least, false).count;
-        if (static_cast<u64>(k) < count) {
-          uint32_t key;
-          u64 at, above, unused;
-          a.find(false, k, order_key(least), best, key, at, above, unused);
-          cut_k(key, at, above);
-        }
-      }
-      if (by_p) {
-        auto mass = a.histogram(least, true);
-        u64 n_all = mass.count;
-        if (ties != kAll) {   // tokens at the least logit that top_k does not keep
-          mass.weight -= (mass.count - count) * a.weigh(least);
-          n_all = count;
-        }
-        const u64 target = max(u64(1), part_of(mass.weight, tp, true));
-        uint32_t key;
-        u64 at, above, above_w;
-        a.find(true, target, order_key(least), best, key, at, above, above_w);
-        cut_p(key, at, above, above_w, target, n_all);
-      }
-    }
-    const typename Sampler<T>::Kept kp{least, ties, a.weigh(least)};
-    auto draw = [&](auto &&weight) {
-      const auto sm = a.sums(kp, weight);
-      count = sm.count;
-      total = sm.all;
-      token = a.pick(sm, kp, part_of(total, u, false), weight, x_tok);
-    };
-    if (by_value) draw([&](float x) { return a.value_weight(x); });
-    else draw([&](float x) { return a.weigh(x); });
-    if (rank == 0 && threadIdx.x == 0) lp = a.log_share(x_tok, total, temp);
+    draw_kept<T>(row, s, a.slot, a.weigh, k, tp, u, least, mass, temp, p, r);
+    done = true;
   }
   if (!done && rank == 0 && threadIdx.x == 0) {
     p.tokens[r] = max(token, 0);

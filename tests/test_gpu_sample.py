@@ -106,6 +106,21 @@ def test_row_counts_and_settings_a_row(kap, rows, dt):
           mp=np.where(r % 5 == 0, 0.05, 0.0))
 
 
+@pytest.mark.parametrize("rows", [2, 90, 310])
+@pytest.mark.parametrize("steps", [0, 256, 3])
+def test_top_p_of_flat_rows(kap, rows, steps):
+    """Borders that tens of thousands of fp32 logits lie above: all different, in runs of tens of equal ones, and in runs that
+    are longer than any list of candidates."""
+    V = 50021 if rows < 300 else 20011
+    lg = logits(rows, V, torch.float32, rows, scale=1.5, lift=False)
+    if steps:
+        lg = (lg * steps).round() / steps
+    r = np.arange(rows)
+    check(kap, lg, u_of(rows, steps), T=0.8 + 0.2 * (r % 4), p=np.where(r % 5 == 4, 0.0001, 0.3 + 0.23 * (r % 4)),
+          mp=np.where(r % 3 == 1, 1e-3, 0.0), k=np.where(r % 7 == 6, V - 1, 0))
+    assert kap.kap_device_error() == 0
+
+
 def test_a_rows_result_does_not_depend_on_the_batch(kap):
     """The same rows alone (a cluster each) and in a large batch (a CTA each): equal to the bit."""
     lg = logits(8, 128256, torch.float32, 3)
