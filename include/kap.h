@@ -380,7 +380,8 @@ size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
  * window starts inside its group's shared pages, are taken as sharing nothing. The results are those of kap_attn_verify
  * up to rounding: sums and statistics are fp32; over a bf16 pool probabilities enter the product with the values as bf16.
  * A token that a row does not see adds nothing to it, whatever its K and V hold. A row that sees no token gets zeros
- * and lse -infinity. Tokens on a page id outside the pool, or past the table's end, are skipped (device error bit 1).
+ * and lse -infinity; rows of q outside the windows (before q_offsets[0], from q_offsets[R] on) leave out and lse as they
+ * are. Tokens on a page id outside the pool, or past the table's end, are skipped (device error bit 1).
  *   groups: see kap_prefix_groups; group_offsets that do not rise from 0 to num_seqs set device error bit 4 (the results of
  *   the requests concerned are then undefined).
  *   workspace >= kap_shared_workspace_size(R, Hkv, Hq, d, total_q, num_groups) bytes; it needs no clearing. Calls that may

@@ -13,6 +13,10 @@
 // can be a later one of at most one item, that which it starts in). The second kernel joins a row's records and
 // takes the window's tokens by itself, one warp a row: those are the only tokens that some of a request's rows see and
 // others do not.
+//
+// bf16 pools run on tcgen05 (shared_tc_kernel, which says how), fp32 pools in plain arithmetic. In graphs: 32 requests on one
+// prefix of 32768 tokens 66 us (pages alone 25, at the measured copy rate), 64 in 5 groups with windows of 5 156 us (54), 8 on
+// 131072 with windows of 8 264 us (products alone 90, pages 81); kap_attn_verify over the same tables 522, 564 and 687.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 #include "kap_tma.h"
@@ -361,11 +365,13 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
 // an item's block of up to 128 rows gives its even tiles to one and its odd tiles to the other and joins the two at the
 // end; a block of up to 256 rows gives each stream 128 of them, and both read every tile.
 // Warps: 0-3 and 4-7 the streams' softmax (thread = row; they also bring the first segment's queries), 8 and 9 the pages,
-// four of each tile, 8 the tile records, 10 the tcgen05 issuer, 11 the later segments' queries. A page of a head is one TMA request (about 50 ns of its issuing warp each).
+// four of each tile, 8 the tile records, 10 the tcgen05 issuer, 11 the later segments' queries. A page of a head is one TMA
+// request (about 50 ns of its issuing warp each).
 // In shared memory 8 rows of 64 columns are one swizzled block of 1 KB; a K or V tile holds, for each group of 8
 // tokens, the blocks of its d / 64 column halves. K and V tiles share a ring.
 // A barrier's parity tells a phase from its neighbours only to a thread that has seen every phase before it, so the page
-// warps and the issuer watch the ring's places in order and miss none. Every wait is bounded, and no role waits on a block-wide barrier.
+// warps and the issuer watch the ring's places in order and miss none. Every wait is bounded, and no role waits on a
+// block-wide barrier.
 constexpr int kTcThreads = 384;
 constexpr int kTcBlock = 256;
 constexpr float kRescale = 8.0f;  // log2: the reference of a row's weights follows its maximum when 2^8 behind
@@ -480,8 +486,7 @@ __device__ __forceinline__ void store32(float *p, const float *v) {   // 32 byte
                : "memory");
 }
 __device__ __forceinline__ void touch(const int32_t *p) {
-  int v;
-  asm volatile("ld.global.ca.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("{\n\t.reg .b32 v;\n\tld.global.ca.b32 v, [%0];\n\t}" ::"l"(p));
 }
 __device__ __forceinline__ void mbar_arrive8(uint64_t *bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], 8;" ::"r"(smem_u32(bar)) : "memory");
@@ -1043,7 +1048,9 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
   constexpr int WT = 4;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const bool live = wid < static_cast<int64_t>(p.total_q) * p.hq;
+  // rows outside the windows (a batch padded to total_q) are left as they are
+  const bool live = wid < static_cast<int64_t>(p.total_q) * p.hq && wid >= static_cast<int64_t>(p.q_offsets[0]) * p.hq &&
+                    wid < static_cast<int64_t>(p.q_offsets[p.R]) * p.hq;
   float m = -INFINITY, l = 0.0f, o[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.0f;

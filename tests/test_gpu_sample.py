@@ -121,6 +121,14 @@ def test_top_p_of_flat_rows(kap, rows, steps):
     assert kap.kap_device_error() == 0
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_temperatures_past_any_use(kap, dt):
+    """Weights that are all the same, and a step apart, under limits that flat rows meet."""
+    rows, V = 6, 5003
+    check(kap, logits(rows, V, dt, 2, lift=False), u_of(rows), T=np.array([np.inf, 1e30, 1e6, 1e38, 300.0, 1e-30]),
+          p=np.array([0.5, 0.5, 0.9, 0.001, 0.99, 0.9]))
+
+
 def test_a_rows_result_does_not_depend_on_the_batch(kap):
     """The same rows alone (a cluster each) and in a large batch (a CTA each): equal to the bit."""
     lg = logits(8, 128256, torch.float32, 3)

@@ -235,6 +235,30 @@ def test_a_window_inside_the_shared_pages(kap):
     assert kap.kap_device_error() == 0
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_outside_the_windows_are_left_as_they_are(kap, d, dt):
+    """A batch padded to a fixed number of rows, ahead of the first window and behind the last one."""
+    s = make([3, 2], [20, 9], [7, 130, 0, 40, 300], [2, 1, 3, 1, 2], d=d, dt=dt)
+    want, wlse = run(kap, s)
+    before, behind = 2, 60
+    q = torch.cat([torch.randn(before, *s["q"].shape[1:], device="cuda").to(dt), s["q"],
+                   torch.randn(behind, *s["q"].shape[1:], device="cuda").to(dt)])
+    out, lse = torch.full_like(q, 5.0), torch.full(q.shape[:2], 6.0, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    qo = torch.tensor([0, 2, 3, 6, 7, 9], **i32) + before
+    start = torch.tensor(s["starts"], **i32)
+    hkv = s["K"].shape[1]
+    ws = kap.workspace(kap.kap_shared_workspace_size(5, hkv, q.shape[1], d, q.shape[0], 2), "cuda")
+    kap.kap_attn_verify_shared(kap.KVPool(s["K"], s["V"], q.shape[1]), kap.PageMap(s["bt"], start),
+                               kap.VerifyPolicy(qo, start, 3, q.shape[0]), kap.PrefixGroups(s["go"], s["pp"]), q, out, lse, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out[before:before + 9], want) and torch.equal(lse[before:before + 9], wlse)
+    for a, b in ((0, before), (before + 9, before + 9 + behind)):
+        assert (out[a:b] == 5.0).all() and (lse[a:b] == 6.0).all()
+    assert kap.kap_device_error() == 0
+
+
 def test_offsets_that_do_not_cover_the_requests(kap):
     for off in ([0, 3, 5], [1, 3, 6], [0, 4, 2], [0, 9, 6], [-4, 3, 6]):
         s = make([3, 3], [4, 5], [1] * 6, [1] * 6)
