@@ -120,46 +120,46 @@ __device__ const Powers kPowers = make_powers();
 // exp((x - m) / T) as a whole number of 2^-qb, right to about 2^-40 of itself and a half unit, for x <= m that is no NaN:
 // with y = (m - x) log2 e / T as a sum of two fp32, k the nearest whole number to 64 y and r = y - k / 64,
 //   2^-y = 2^(-k/64) (1 - t + t^2/2 - t^3/6 + t^4/24),  t = r ln 2 <= 0.0055, t's leading term again as two fp32.
-// From y = 22 on (weights below 2^-22, units 2^-44) the exponential unit's 2^-22 of the value is below a unit.
+// Every operation is rounded as written, so that the form in line and the one out of line give the same number.
+__device__ __forceinline__ u64 weight_inline(float x, float m, float ch, float cl, int down, const Powers *tab) {
+  auto add = [](float a, float b) { return __fadd_rn(a, b); };
+  auto sub = [](float a, float b) { return __fsub_rn(a, b); };
+  auto mul = [](float a, float b) { return __fmul_rn(a, b); };
+  auto fma = [](float a, float b, float c) { return __fmaf_rn(a, b, c); };
+  // m - x, exactly (two-sum)
+  const float dh = sub(m, x), bb = sub(m, dh), dl = add(sub(m, add(dh, bb)), sub(bb, x));
+  const float yh = mul(dh, ch);
+  const float yl = add(fma(dh, ch, -yh), fma(dh, cl, mul(dl, ch)));
+  const bool some = yh < 62.0f;   // not so for an infinite distance
+  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
+  const float kf = fma(some ? yh : 0.0f, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
+  const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
+  const float r = fma(sub(kf, 12582912.0f), -0.015625f, yh);
+  const float th = mul(r, kLn2h), tl = add(fma(r, kLn2h, -th), fma(r, kLn2l, mul(yl, kLn2h)));
+  const float q = fma(mul(th, th), fma(th, fma(th, 0.0416666679f, -0.166666672f), 0.5f), -tl);
+  const float2 f = tab->f[k & 63];
+  const float ph = mul(f.x, -th);
+  const float pl = add(fma(f.x, -th, -ph), fma(f.x, q, mul(f.y, -th)));
+  // ph + pl in units of 2^-44, through the low bits of sums at 3 (unit 2^-22) and at 3 * 2^-22
+  const float u = add(ph, pl), ub = sub(u, ph), ul = add(sub(ph, sub(u, ub)), sub(pl, ub));
+  const float s1 = add(u, 3.0f);
+  const int i1 = static_cast<int>(__float_as_uint(s1) - 0x40400000u);
+  const float rest = add(sub(u, sub(s1, 3.0f)), ul);
+  const int i2 = static_cast<int>(__float_as_uint(add(rest, 7.152557373046875e-7f)) - 0x35400000u);
+  const u64 w = tab->q[k & 63] + static_cast<u64>(static_cast<int64_t>(i1) * (1 << 22) + i2);
+  const int e = (k >> 6) + down;
+  return some ? (w + ((u64(1) << e) >> 1)) >> e : u64(0);
+}
 // Out of line: passes that weigh logits in several places would not stay in the instruction cache.
 __device__ __noinline__ u64 weight_of(float x, float m, float ch, float cl, int down, const Powers *tab) {
-  // m - x, exactly (two-sum)
-  const float dh = m - x, bb = m - dh, dl = (m - (dh + bb)) + (bb - x);
-  const float yh = dh * ch;
-  const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
-  if (!(yh < 62.0f)) return 0;   // also an infinite distance
-  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
-  u64 w;
-  int e;
-  if (yh >= 22.0f) {
-    float v;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(44.0f - yh));   // the difference is exact
-    v = fmaf(v, -yl * kLn2h, v);
-    return (static_cast<u64>(__float_as_uint(v + 12582912.0f) - 0x4b400000u) + ((1u << down) >> 1)) >> down;
-  }
-  const float kf = fmaf(yh, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
-  const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
-  const float r = fmaf(kf - 12582912.0f, -0.015625f, yh);
-  const float th = r * kLn2h, tl = fmaf(r, kLn2h, -th) + fmaf(r, kLn2l, yl * kLn2h);
-  const float q = th * th * fmaf(th, fmaf(th, 0.0416666679f, -0.166666672f), 0.5f) - tl;
-  const float2 f = tab->f[k & 63];
-  const float ph = f.x * -th;
-  const float pl = fmaf(f.x, -th, -ph) + fmaf(f.x, q, f.y * -th);
-  // ph + pl in units of 2^-44, through the low bits of sums at 3 (unit 2^-22) and at 3 * 2^-22
-  const float u = ph + pl, ub = u - ph, ul = (ph - (u - ub)) + (pl - ub);
-  const float s1 = u + 3.0f;
-  const int i1 = static_cast<int>(__float_as_uint(s1) - 0x40400000u);
-  const float rest = (u - (s1 - 3.0f)) + ul;
-  const int i2 = static_cast<int>(__float_as_uint(rest + 7.152557373046875e-7f) - 0x35400000u);
-  w = tab->q[k & 63] + static_cast<u64>(static_cast<int64_t>(i1) * (1 << 22) + i2);
-  e = (k >> 6) + down;
-  return (w + ((u64(1) << e) >> 1)) >> e;
+  return weight_inline(x, m, ch, cl, down, tab);
 }
 struct Weigh {
   float m, ch, cl;   // largest logit; log2 e / T
   int down;          // 44 - qb
   const Powers *tab;
   __device__ __forceinline__ u64 operator()(float x) const { return weight_of(x, m, ch, cl, down, tab); }
+  __device__ __forceinline__ u64 here(float x) const { return weight_inline(x, m, ch, cl, down, tab); }   // passes over all
 };
 
 constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept, two a lane
@@ -290,6 +290,24 @@ struct Row {
       v.x = v.y;
       v.y = v.z;
       v.z = v.w;
+    }
+  }
+  // f(x) for the logits of a vector, two in line.
+  template <class F> static __device__ __forceinline__ void pairs(uint4 v, F &&f) {
+#pragma unroll 1
+    for (int i = 0; i < (sizeof(T) == 2 ? 4 : 2); ++i) {
+      if (sizeof(T) == 2) {
+        f(__uint_as_float(v.x << 16));
+        f(__uint_as_float(v.x & 0xffff0000u));
+        v.x = v.y;
+        v.y = v.z;
+        v.z = v.w;
+      } else {
+        f(__uint_as_float(v.x));
+        f(__uint_as_float(v.y));
+        v.x = v.z;
+        v.y = v.w;
+      }
     }
   }
   // Vector j; -infinity outside the CTA's range.
@@ -874,9 +892,18 @@ struct Sampler {
   struct Sums {
     u64 mine, before, all, t_before, count;
   };
-  template <class W> __device__ Sums sums(const Kept &kp, W &&weight) {
+  template <bool ALL = false, class W> __device__ Sums sums(const Kept &kp, W &&weight) {
     u64 w = 0;
     uint32_t n = 0, e = 0;
+    if (ALL) {   // nothing but -infinity is left out
+      row.template in_order<2>([&](const uint4 &v, int, int) {
+        row.pairs(v, [&](float x) {
+          w += weigh.here(x);
+          n += x > -INFINITY ? 1 : 0;
+        });
+      });
+      return join_sums(kp, w, n, 0);
+    }
     row.template in_order<2>([&](const uint4 &v, int, int) {
       e += Row<T>::kept(v, kp.least, [&](float x) {
         w += weight(x);
@@ -974,9 +1001,9 @@ struct Sampler {
     __syncthreads();
     u64 all = 0, w = 0;
     uint32_t n = 0;
-    row.template in_order<2>([&](const uint4 &v, int j, int) {
-      row.elements(v, j, [&](float x, int) {
-        const u64 one = x >= least ? weigh(x) : 0;
+    row.template in_order<2>([&](const uint4 &v, int, int) {
+      row.pairs(v, [&](float x) {
+        const u64 one = x >= least ? weigh.here(x) : 0;
         all += one;
         if (x > vhi) {
           w += one;
@@ -1373,13 +1400,20 @@ __device__ __noinline__ void draw_kept(const Row<T> row, Shared &s, int slot, co
   }
   if (!summed) kp = {least, ties, a.weigh(least)};
   auto draw = [&](auto &&weight) {
-    if (!summed) sm = a.sums(kp, weight);
     count = sm.count;
     total = sm.all;
     token = a.pick(sm, kp, part_of(total, u, false), weight, x_tok);
   };
-  if (by_value) draw([&](float x) { return a.value_weight(x); });
-  else draw([&](float x) { return a.weigh(x); });
+  auto counted = [&](float x) { return a.value_weight(x); };
+  auto weighed = [&](float x) { return a.weigh(x); };
+  if (by_value) {
+    sm = a.sums(kp, counted);
+    draw(counted);
+  } else {
+    if (!summed && kp.least <= -3.402823466e38f && ties == kAll) sm = a.template sums<true>(kp, weighed);
+    else if (!summed) sm = a.sums(kp, weighed);
+    draw(weighed);
+  }
   if (rank == 0 && threadIdx.x == 0) {
     p.tokens[r] = max(token, 0);
     if (p.logprob) p.logprob[r] = a.log_share(x_tok, total, temp);
