@@ -493,10 +493,11 @@ size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab);
  *   uniform      u in [0, 1): the token drawn is the first in id order at which the running sum of the kept weights passes
  *                u times their sum. Values outside [0, 1) are taken to its nearest end, NaN to 0.
  * tokens_out [rows]; logprob_out [rows] (may be NULL) = log of the drawn token's share of the kept weight; kept_out [rows]
- * (may be NULL) = how many tokens were kept. Weights are held to 2^-44 of the largest (fewer bits past 2^18 tokens):
- * one that rounds to nothing is never drawn. Sums are whole numbers, so a row's result does not depend on the other rows,
- * on their number or on the order of any addition. A logit of -infinity is never kept. A row with a NaN or +infinity, or
- * with -infinity throughout, has no distribution: it gets the first token of the rank order, NaN and 0.
+ * (may be NULL) = how many tokens were kept. Weights are whole numbers of 2^-44 of the largest (fewer bits past 2^18
+ * tokens), each right to 2^-38 of itself and a unit: one that rounds to nothing is never drawn. Sums are whole numbers, so a
+ * row's result does not depend on the other rows, on their number or on the order of any addition. A logit of -infinity is
+ * never kept. A row with a NaN or +infinity, or with -infinity throughout, has no distribution: it gets the first token of
+ * the rank order, NaN and 0.
  *   logits_dev [rows] rows of `vocab` values (KAP_BF16 or KAP_F32), row_stride elements apart, at any element alignment;
  *   the others [rows] on the device, fp32 but for top_k (int32). No workspace.
  * Errors: KAP_EINVAL for null pointers, rows < 0, vocab < 1, row_stride < vocab; KAP_EUNSUPPORTED for another dtype,

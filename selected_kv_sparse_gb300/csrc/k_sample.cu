@@ -6,7 +6,8 @@
 // above it and the first few ids of those at it. The token drawn is the first in id order at which the running sum of the
 // kept weights passes u times their sum.
 // Weights are whole numbers, 2^-44 of the largest each (fewer bits past 2^18 tokens, so that sums stay below 2^62), so
-// sums do not depend on their order and every border is decided as 64-bit floating point would decide it.
+// sums do not depend on their order. Each is right to 2^-38 of itself and a unit, so a border falls as it would in 64-bit
+// floating point unless it lies that close.
 //
 // A row belongs to a cluster of CTAs, each with a slice of it; they add up their parts through one another's shared
 // memory. One pass over it gives the maximum, the weight to about 2^-16, and the maxima of its tiles. Then, by what the row
@@ -21,10 +22,10 @@
 // The last three end with the kept weight of each warp's range of ids, and the warps then halve the range that the draw
 // falls into.
 //
-// Bound by instructions for flat rows: some 100 a logit that is weighed (the logits' way there included), and for 16-bit
+// Bound by instructions for flat rows: some 70 a logit that is weighed in line, 100 where it is called for, and for 16-bit
 // counts an atomic each, of which a warp's fall into the same banks 3 to 4 times. In graphs: 2048 bf16 rows of 128256 under
-// top_p 506 us (a third of them flat, 110 to 170 us each; the others 25 to 45), where reading them takes 77; 80 fp32 rows
-// with settings of their own 123; 300 bf16 rows of 32000 without limits 60; 4 rows 20, most of it joins and one CTA's sort.
+// top_p 505 us (a third of them flat, 110 to 170 us each; the others 25 to 45), where reading them takes 77; 80 fp32 rows
+// with settings of their own 115; 300 bf16 rows of 32000 without limits 47; 4 rows 20, most of it joins and one CTA's sort.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 
@@ -117,7 +118,7 @@ constexpr Powers make_powers() {
 }
 __device__ const Powers kPowers = make_powers();
 
-// exp((x - m) / T) as a whole number of 2^-qb, right to about 2^-40 of itself and a half unit, for x <= m that is no NaN:
+// exp((x - m) / T) as a whole number of 2^-qb, right to 2^-38 of itself and a unit, for x <= m that is no NaN:
 // with y = (m - x) log2 e / T as a sum of two fp32, k the nearest whole number to 64 y and r = y - k / 64,
 //   2^-y = 2^(-k/64) (1 - t + t^2/2 - t^3/6 + t^4/24),  t = r ln 2 <= 0.0055, t's leading term again as two fp32.
 // Every operation is rounded as written, so that the form in line and the one out of line give the same number.
@@ -135,7 +136,8 @@ __device__ __forceinline__ u64 weight_inline(float x, float m, float ch, float c
   const float kf = fma(some ? yh : 0.0f, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
   const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
   const float r = fma(sub(kf, 12582912.0f), -0.015625f, yh);
-  const float th = mul(r, kLn2h), tl = add(fma(r, kLn2h, -th), fma(r, kLn2l, mul(yl, kLn2h)));
+  const float rh = add(r, yl), rl = add(sub(r, rh), yl);   // y's low part is up to 2^-20: it counts in the square, too
+  const float th = mul(rh, kLn2h), tl = add(fma(rh, kLn2h, -th), fma(rh, kLn2l, mul(rl, kLn2h)));
   const float q = fma(mul(th, th), fma(th, fma(th, 0.0416666679f, -0.166666672f), 0.5f), -tl);
   const float2 f = tab->f[k & 63];
   const float ph = mul(f.x, -th);
@@ -1566,7 +1568,7 @@ cudaError_t launch_sample(const void *logits, int dtype, int V, int64_t stride, 
   while ((int64_t(1) << bits) < V) ++bits;
   const SParams p{logits, V, rows, std::min(44, 62 - bits), stride, u, temp, top_p, min_p, top_k, tokens, logprob, kept};
   // CTAs of a row: as many as fill the GPU once, but no slice below 2048 logits. More of them would spread flat rows among
-  // others that end early (80 mixed fp32 rows: 4 CTAs 115 us, 3 take 131), but rows that few candidates decide then come in
+  // others that end early (80 mixed fp32 rows: 4 CTAs 115 us where 3 took 131), but rows that few candidates decide then come in
   // two turns (51 us, 36).
   int nc = 1;
   nc = std::max(1, std::min({kMaxCluster, kSaCtas * device_sm_count() / rows, V / 2048}));

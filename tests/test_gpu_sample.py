@@ -121,6 +121,25 @@ def test_top_p_of_flat_rows(kap, rows, steps):
     assert kap.kap_device_error() == 0
 
 
+@pytest.mark.parametrize("T", [1.0, 0.7, 1.3])
+def test_borders_that_a_weights_last_bits_decide(kap, T):
+    """Two tokens of weights 1 and w whose share 1 / (1 + w) lies 2^-37 to 2^-33 from a value of top_p. A weight is right to
+    2^-38 of itself and a unit of 2^-44, so the share to w / (1 + w)^2 of 2^-38 and a unit, less than 2^-39: every row falls
+    on its own side."""
+    rng = np.random.default_rng(int(10 * T))
+    T = float(np.float32(T))
+    x = rng.uniform(0.05, 12.0, (1 << 20, 2)).astype(np.float32)
+    x.sort(axis=1)
+    share = 1.0 / (1.0 + np.exp((x[:, 0].astype(np.float64) - x[:, 1]) / T))
+    p = share.astype(np.float32)
+    off = np.abs(p - share)
+    at = np.flatnonzero((off > 2.0 ** -37) & (off < 2.0 ** -33) & (p < 1))[:2000]
+    assert len(at) > 100
+    lg = torch.from_numpy(x[at]).cuda()
+    _, _, kept = call(kap, lg, 0.0, T=T, p=p[at])
+    assert (kept == np.where(share[at] >= p[at], 1, 2)).all()
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_temperatures_past_any_use(kap, dt):
     """Weights that are all the same, and a step apart, under limits that flat rows meet."""
