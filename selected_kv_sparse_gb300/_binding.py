@@ -537,18 +537,19 @@ def kap_append_kv(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, q_inou
                                               _stream(stream)))
 
 
-def _rows_of(t: torch.Tensor, T: int, heads: int, d: int, dt, dev: int, name: str):
+def _rows_of(t: torch.Tensor, shape: tuple, dt, dev: int, name: str):
     """(address, token stride) of [T][heads][d] rows that are contiguous within a token."""
-    if t.shape != (T, heads, d):
-        raise ValueError(f"{name} must be {[T, heads, d]}")
+    if t.shape == shape and t.dtype is dt and t.get_device() == dev:
+        T, heads, d = shape
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == d or heads == 1):
+            return t.data_ptr(), s0 if T > 1 else heads * d
+        raise ValueError(f"{name}: a token's [heads][d] must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
     if t.dtype is not dt:
         raise TypeError(f"{name} must have the pool dtype")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a tensor on the current CUDA device {dev}, got one on {t.device}")
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != d):
-        raise ValueError(f"{name}: a token's [heads][d] must be contiguous")
-    return t.data_ptr(), st[0] if T > 1 else heads * d
+    raise ValueError(f"{name}: expected a tensor on the current CUDA device {dev}, got one on {t.device}")
 
 
 def kap_append_kv_norm(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, q: Optional[torch.Tensor],
@@ -571,24 +572,26 @@ def kap_append_kv_norm(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, q
     P, hkv, _, d = shape
     hq = pool.num_q_heads
     T = k_new.shape[0] if num_tokens is None else int(num_tokens)
-    k, ks = _rows_of(k_new, T, hkv, d, dt, dev, "k_new")
-    v, vs = _rows_of(v_new, T, hkv, d, dt, dev, "v_new")
+    kv, half = (T, hkv, d), d // 2
+    k, ks = _rows_of(k_new, kv, dt, dev, "k_new")
+    v, vs = _rows_of(v_new, kv, dt, dev, "v_new")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     qa = qs = oa = os_ = 0
     if q is not None:
-        qa, qs = _rows_of(q, T, hq, d, dt, dev, "q")
-        oa, os_ = _rows_of(q_out, T, hq, d, dt, dev, "q_out")
+        qa, qs = _rows_of(q, (T, hq, d), dt, dev, "q")
+        oa, os_ = (qa, qs) if q_out is q else _rows_of(q_out, (T, hq, d), dt, dev, "q_out")
     need = (T - 1) * tok_stride + 1 if T > 0 else 0
-    if pos.dim() not in (1, 2) or pos.shape[-1] < need or slots.dim() != 1 or slots.shape[0] < need or tok_stride < 1:
+    ps, n_slots = pos.shape, slots.shape
+    axes, wide = ps if len(ps) == 2 else (1, ps[0] if len(ps) == 1 else -1)
+    if wide < need or len(n_slots) != 1 or n_slots[0] < need or tok_stride < 1:
         raise ValueError("pos must be [axes][T] or [T] and slots [T], with room for every token")
-    axes, wide = (pos.shape[0], pos.shape[1]) if pos.dim() == 2 else (1, pos.shape[0])
-    for t, n, name in ((q_weight, d, "q_weight"), (k_weight, d, "k_weight"), (inv_freq, d // 2, "inv_freq"),
-                       (freq_axis, d // 2, "freq_axis")):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} must have {n} entries")
-    a = _NormAppend(k, v, qa, oa, ks, vs, qs, os_, _at(q_weight, dev, f32, "q_weight"), _at(k_weight, dev, f32, "k_weight"),
-                    eps, axes, _at(pos, dev, i32, "pos"), wide, _at(freq_axis, dev, i32, "freq_axis"),
+    if inv_freq.numel() != half or (q_weight is not None and q_weight.numel() != d) or \
+            (k_weight is not None and k_weight.numel() != d) or (freq_axis is not None and freq_axis.numel() != half):
+        raise ValueError(f"q_weight and k_weight must have {d} entries, inv_freq and freq_axis {half}")
+    a = _NormAppend(k, v, qa, oa, ks, vs, qs, os_, None if q_weight is None else _at(q_weight, dev, f32, "q_weight"),
+                    None if k_weight is None else _at(k_weight, dev, f32, "k_weight"), eps, axes, _at(pos, dev, i32, "pos"),
+                    wide, None if freq_axis is None else _at(freq_axis, dev, i32, "freq_axis"),
                     _at(slots, dev, torch.int64, "slots"), _at(inv_freq, dev, f32, "inv_freq"), T, tok_stride)
     p = _Pool(P, PAGE, hkv, hq, d, KAP_BF16 if dt is torch.bfloat16 else KAP_F32, _at(kp, dev, None, "k_pages"),
               _at(vp, dev, None, "v_pages"), None)
