@@ -139,6 +139,33 @@ def test_widest_windows(kap):
         check(s, out, lse)
 
 
+@pytest.mark.parametrize("d,dt", [(128, torch.bfloat16), (64, torch.bfloat16), (128, torch.float32)])
+def test_requests_without_rows(kap, d, dt):
+    """Windows of no rows: first, last, between others, a group's first request, and all of a group's."""
+    s = make([3, 2, 2, 1, 2], [12, 9, 3, 0, 5], [7, 0, 30, 129, 4, 0, 5, 60, 1, 2], [0, 1, 2, 0, 0, 3, 0, 1, 1, 0], d=d, dt=dt)
+    out, lse = run(kap, s)
+    torch.cuda.synchronize()
+    check(s, out, lse)
+    assert kap.kap_device_error() == 0
+
+
+def test_two_streams_at_once(kap):
+    """Calls with a workspace each, in flight together on two streams."""
+    a, b = make([9], [200], [60] * 9, [2] * 9), make([3, 5], [40, 300], [30] * 8, [1] * 8, d=64, seed=1)
+    ws = [kap.workspace(kap.kap_shared_workspace_size(s["R"], 2, s["hq"], s["K"].shape[3], s["tq"], s["pp"].numel()), "cuda")
+          for s in (a, b)]
+    want = [run(kap, s) for s in (a, b)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(24):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(run(kap, (a, b)[i % 2], ws=ws[i % 2], stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    assert kap.kap_device_error() == 0
+
+
 def test_long_prefix_split_over_all_ctas(kap):
     s = make([6], [2048], [3, 200, 0, 31, 640, 16], [1] * 6, hkv=1, G=8)
     out, lse = run(kap, s)
