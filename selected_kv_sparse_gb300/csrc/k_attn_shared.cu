@@ -22,6 +22,7 @@
 #include "kap_tma.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kap {
 namespace {
@@ -1144,7 +1145,8 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
     const int b0 = owner_cta(es + at[kind], total, nb), b1 = owner_cta(es + end[kind], total, nb);
     Entry x;
     x.q0 = q0[kind];
-    for (int c0 = b0; c0 <= b1; c0 += CH) {   // a chunk's records: all loads first, then one step for all
+    auto take = [&](auto size, int c0) {   // a chunk's records: all loads first, then one step for all
+      constexpr int CH = decltype(size)::value;
       float2 ml[CH];
       float rec[CH][PL];
 #pragma unroll
@@ -1178,7 +1180,10 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
         for (int k = 0; k < PL; ++k) o[k] = fmaf(rec[c][k], w, o[k]);
       }
       m = mn;
-    }
+    };
+    int c0 = b0;
+    for (; c0 + 2 <= b1; c0 += CH) take(std::integral_constant<int, CH>(), c0);
+    if (c0 <= b1) take(std::integral_constant<int, 2>(), c0);   // one or two are left: most own contexts
   }
   T *op = static_cast<T *>(p.out) + (static_cast<size_t>(t) * p.hq + hq) * D + lane * PL;
   const bool none = l == 0.0f && m == -INFINITY;
