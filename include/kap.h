@@ -384,8 +384,8 @@ size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
  * are. Tokens on a page id outside the pool, or past the table's end, are skipped (device error bit 1).
  *   groups: see kap_prefix_groups; group_offsets that do not rise from 0 to num_seqs set device error bit 4 (the results of
  *   the requests concerned are then undefined).
- *   workspace >= kap_shared_workspace_size(R, Hkv, Hq, d, total_q, num_groups) bytes; it needs no clearing. Calls that may
- *   run at the same time, captured graphs among them, need a workspace each.
+ *   workspace >= kap_shared_workspace_size(R, Hkv, Hq, d, total_q, num_groups) bytes, at any multiple of 16 bytes; it needs
+ *   no clearing. Calls that may run at the same time, captured graphs among them, need a workspace each.
  * Errors: those of kap_attn_verify; KAP_EINVAL for num_groups < 0 or null group arrays; KAP_EUNSUPPORTED for more than 2^26
  * table columns, 2^20 groups or 2^31 - 1 query rows (total_q * Hq). */
 kap_status kap_attn_verify_shared(const kap_kv_pool *pool, const kap_page_map *map, const kap_verify_policy *vp,

@@ -481,7 +481,7 @@ __device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *tmap, in
       "l"(tmap), "r"(0), "r"(group), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void store32(float *p, const float *v) {   // 32 bytes, aligned
+__device__ __forceinline__ void store32(float *p, const float *v) {   // 32 bytes, on a multiple of 32
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
@@ -1192,7 +1192,9 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
   if (lane == 0) p.lse[static_cast<size_t>(t) * p.hq + hq] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-size_t up(size_t b) { return (b + 255) / 256 * 256; }
+// Parts of the workspace start on multiples of 256 bytes, whatever its address: records are stored 32 bytes at a time.
+constexpr size_t kPart = 256;
+size_t up(size_t b) { return (b + kPart - 1) / kPart * kPart; }
 
 template <class T, int D> cudaError_t launch_join(const HParams &p, cudaStream_t s) {
   const int64_t warps = static_cast<int64_t>(p.total_q) * p.hq;
@@ -1228,8 +1230,9 @@ template <int D> cudaError_t launch_tc(const PoolArgs &pa, HParams p, cudaStream
 size_t shared_workspace_bytes(int R, int hkv, int hq, int d, int total_q, int num_groups) {
   (void)hkv;
   const size_t rows = static_cast<size_t>(total_q) * hq, extra = static_cast<size_t>(kMaxCtas) * kMaxBlock;
-  return up((static_cast<size_t>(num_groups) + R + 1) * 8) + 2 * up(rows * 8) + 2 * up(rows * d * 4) + up(extra * 8) +
-         up(extra * d * 4);
+  // kPart more: the first part may start that far behind an address that is no multiple of it
+  return kPart + up((static_cast<size_t>(num_groups) + R + 1) * 8) + 2 * up(rows * 8) + 2 * up(rows * d * 4) +
+         up(extra * 8) + up(extra * d * 4);
 }
 
 cudaError_t launch_verify_shared(const PoolArgs &pa, const MapArgs &ma, int total_q, const int32_t *q_offsets,
@@ -1257,7 +1260,7 @@ cudaError_t launch_verify_shared(const PoolArgs &pa, const MapArgs &ma, int tota
   p.lse = lse;
   p.err = err;
   const size_t rows = static_cast<size_t>(total_q) * pa.hq;
-  unsigned char *w = static_cast<unsigned char *>(ws);
+  unsigned char *w = reinterpret_cast<unsigned char *>(up(reinterpret_cast<uintptr_t>(ws)));
   auto take = [&](size_t bytes) {
     unsigned char *at = w;
     w += up(bytes);
