@@ -183,7 +183,7 @@ struct Shared {
   };
   Powers powers;
   float odd[kOdd];
-  u64 scan[kSaWarps], scan2[kSaWarps];
+  u64 scan[kSaWarps], scan2[kSaWarps];   // of block-wide sums: who reads them ends with a barrier, so that the next may write
   u64 sums[3][2];   // values for the other CTAs, in turn: a slot is written again two exchanges later
   u64 pick[6];
   float fscan[kSaWarps];
@@ -213,15 +213,15 @@ __device__ __forceinline__ void st_remote64(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-// Sum over the block, to every thread.
+// Sum over the block, to every thread; ends with a barrier, as block_inclusive_scan does.
 __device__ __forceinline__ u64 block_sum(u64 v, u64 *scratch) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
   u64 t = 0;
   for (int w = 0; w < kSaWarps; ++w) t += scratch[w];
+  __syncthreads();
   return t;
 }
 
@@ -451,10 +451,10 @@ struct Sampler {
   }
   __device__ uint32_t cluster_max(uint32_t v) {
     v = __reduce_max_sync(0xffffffffu, v);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = v;
     __syncthreads();
     for (int w = 0; w < kSaWarps; ++w) v = max(v, static_cast<uint32_t>(s.scan[w]));
+    __syncthreads();
     if (nc == 1) return v;
     if (threadIdx.x == 0) s.sums[0][slot] = v;
     cluster_sync();
@@ -921,7 +921,6 @@ struct Sampler {
     e = __reduce_add_sync(0xffffffffu, e);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-    __syncthreads();
     if (lane == 0) {
       s.scan[warp] = w;
       s.scan2[warp] = (static_cast<u64>(n) << 32) | e;
@@ -934,6 +933,7 @@ struct Sampler {
       w_all += s.scan[i];
       c_all += s.scan2[i];
     }
+    __syncthreads();
     if (nc > 1) {
       if (threadIdx.x == 0) {
         s.sums[0][slot] = w_all;
