@@ -131,7 +131,9 @@ __device__ __forceinline__ u64 weight_inline(float x, float m, float ch, float c
   const float dh = sub(m, x), bb = sub(m, dh), dl = add(sub(m, add(dh, bb)), sub(bb, x));
   const float yh = mul(dh, ch);
   const float yl = add(fma(dh, ch, -yh), fma(dh, cl, mul(dl, ch)));
-  const bool some = yh < 62.0f;   // not so for an infinite distance
+  // weights from 2^-45 on are nothing; up to here no shift below reaches 64 (56 and the 6 of 2^24 tokens). Not so for an
+  // infinite distance
+  const bool some = yh < 56.0f;
   constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.904654323148236017e-9f;
   const float kf = fma(some ? yh : 0.0f, 64.0f, 12582912.0f);   // 1.5 * 2^23: the sum's low bits are the nearest whole number
   const int k = static_cast<int>(__float_as_uint(kf) - 0x4b400000u);
