@@ -494,7 +494,7 @@ size_t kap_logprobs_workspace_size(int32_t rows, int32_t vocab);
  *                u times their sum. Values outside [0, 1) are taken to its nearest end, NaN to 0.
  * tokens_out [rows]; logprob_out [rows] (may be NULL) = log of the drawn token's share of the kept weight; kept_out [rows]
  * (may be NULL) = how many tokens were kept. Weights are whole numbers of 2^-44 of the largest (fewer bits past 2^18
- * tokens), each right to 2^-38 of itself and a unit: one that rounds to nothing is never drawn. Sums are whole numbers, so a
+ * tokens), each right to 2^-37 of itself and a unit: one that rounds to nothing is never drawn. Sums are whole numbers, so a
  * row's result does not depend on the other rows, on their number or on the order of any addition. A logit of -infinity is
  * never kept. A row with a NaN or +infinity, or with -infinity throughout, has no distribution: it gets the first token of
  * the rank order, NaN and 0.

@@ -6,7 +6,7 @@
 // above it and the first few ids of those at it. The token drawn is the first in id order at which the running sum of the
 // kept weights passes u times their sum.
 // Weights are whole numbers, 2^-44 of the largest each (fewer bits past 2^18 tokens, so that sums stay below 2^62), so
-// sums do not depend on their order. Each is right to 2^-38 of itself and a unit, so a border falls as it would in 64-bit
+// sums do not depend on their order. Each is right to 2^-37 of itself and a unit, so a border falls as it would in 64-bit
 // floating point unless it lies that close.
 //
 // A row belongs to a cluster of CTAs, each with a slice of it; they add up their parts through one another's shared
@@ -118,9 +118,11 @@ constexpr Powers make_powers() {
 }
 __device__ const Powers kPowers = make_powers();
 
-// exp((x - m) / T) as a whole number of 2^-qb, right to 2^-38 of itself and a unit, for x <= m that is no NaN:
+// exp((x - m) / T) as a whole number of 2^-qb, right to 2^-37 of itself and a unit, for x <= m that is no NaN:
 // with y = (m - x) log2 e / T as a sum of two fp32, k the nearest whole number to 64 y and r = y - k / 64,
 //   2^-y = 2^(-k/64) (1 - t + t^2/2 - t^3/6 + t^4/24),  t = r ln 2 <= 0.0055, t's leading term again as two fp32.
+// Its largest error is that t's low part (up to 2^-31.2) counts in t but not in t^2/2: 2^-38.7 of the weight, to which the
+// square's and the products' roundings add as much again.
 // Every operation is rounded as written, so that the form in line and the one out of line give the same number.
 __device__ __forceinline__ u64 weight_inline(float x, float m, float ch, float cl, int down, const Powers *tab) {
   auto add = [](float a, float b) { return __fadd_rn(a, b); };
