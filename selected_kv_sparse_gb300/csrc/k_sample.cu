@@ -1487,14 +1487,14 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const __gri
   float lp = 0.0f;
   u64 count = 0;
   bool done = false;
-  const bool greedy = !(temp > 0.0f);
+  const bool greedy = !(temp > 0.0f) || mp > 1.0f;   // no weight reaches a min_p above 1: the first token, which is always kept
   float least = -3.402823466e38f;
   if (sound) {
     a.weigh = Weigh{m, ch, static_cast<float>(cd - static_cast<double>(ch)), 44 - p.qb, &s.powers};
     if (mp > 0.0f && !greedy) {
       if (threadIdx.x == 0)
         s.pick[1] = __float_as_uint(__double2float_ru(
-            static_cast<double>(m) + static_cast<double>(temp) * log(fmin(static_cast<double>(mp), 1.0))));
+            static_cast<double>(m) + static_cast<double>(temp) * log(static_cast<double>(mp))));
       __syncthreads();
       least = fminf(m, fmaxf(least, __uint_as_float(static_cast<uint32_t>(s.pick[1]))));
     }

@@ -34,3 +34,20 @@ def test_flat_rows_under_top_p_and_min_p_repeat(kap, rows):
         for a, b in zip(g, want):
             assert (a.cpu().numpy() == b).all()
     assert kap.kap_device_error() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [3, 900, 5003, 40000])
+def test_min_p_above_one_keeps_the_first_token_alone(kap, V, dt):
+    """No weight reaches it, and the first token is always kept: the lowest id of equal largest logits. At one, all of them."""
+    lg = logits(5, V, dt, V, lift=False)
+    lg[1] = 0.25
+    lg[2, V // 2:] = lg[2].max() + 1.0
+    lg[3, [0, V - 1]] = 30.0
+    lg[4, :V - 2] = -float("inf")
+    for mp in (1.0, 1.0000001, 1.5, 5.0, float("inf")):
+        for kw in ({}, dict(p=0.5), dict(k=2), dict(k=2, p=0.3, T=0.6), dict(k=V - 1), dict(T=3.0)):
+            for u in (0.0, 0.99999994):
+                tok, lp, kept = check(kap, lg, np.full(5, u), mp=mp, **kw)
+                if mp > 1.0:
+                    assert (kept == 1).all() and (lp == 0.0).all() and (tok == lg.float().argmax(1).cpu().numpy()).all()
