@@ -864,7 +864,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mx *= scale2;
           if (had == 0) {
             m = mx;
-          } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
+          } else if (__any_sync(0xffffffffu, mx > m + kRescale && base + trow < f.rows)) {
+            // (rows past the block's are products of whatever an earlier block left in the buffer: they have no say)
             const float mn = fmaxf(m, mx);
             const float a = m == -INFINITY ? 0.0f : exp2f(m - mn);
             l *= a;

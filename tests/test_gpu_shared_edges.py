@@ -21,3 +21,25 @@ def test_a_workspace_at_any_multiple_of_16_bytes(kap, d, dt):
         check(s, out, lse)
         assert (whole[:off] == 255).all() and (whole[off + n:] == 255).all(), off
     assert kap.kap_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 4, 40])
+def test_results_do_not_depend_on_what_ran_before(kap, rows, d):
+    """A block of few query rows fills no more than its part of the 128 rows of a product; what an earlier call left in the
+    others has no part in the results, not even in a rounding."""
+    G = 4 if rows % 4 == 0 else 1
+    s = make([1], [0], [152 * 128 * 6 + 37], [rows // G], hkv=1, G=G, d=d)
+    # rows in all of both query buffers, of every CTA
+    t = make([4], [152 * 16], [3] * 4, [64] * 4, hkv=1, G=1, d=d, seed=1)
+    assert s["tq"] * G == rows and t["tq"] == 256
+    got = []
+    for scale in (0.0, 1e30, -1e30, 1e-3):
+        u = {**t, "q": (t["q"].float() * scale).to(torch.bfloat16)}
+        run(kap, u)
+        got.append(run(kap, s))
+    torch.cuda.synchronize()
+    check(s, *got[0])
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    assert kap.kap_device_error() == 0
