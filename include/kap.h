@@ -382,8 +382,9 @@ size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
  * A token that a row does not see adds nothing to it, whatever its K and V hold. A row that sees no token gets zeros
  * and lse -infinity; rows of q outside the windows (before q_offsets[0], from q_offsets[R] on) leave out and lse as they
  * are. Tokens on a page id outside the pool, or past the table's end, are skipped (device error bit 1).
- *   groups: see kap_prefix_groups; group_offsets that do not rise from 0 to num_seqs set device error bit 4 (the results of
- *   the requests concerned are then undefined).
+ *   groups: see kap_prefix_groups; group_offsets that do not rise from 0 to num_seqs, q_offsets that do not rise within
+ *   0 .. total_q, and a window on more than 32 pages set device error bit 4 (the results of the requests concerned are then
+ *   undefined).
  *   workspace >= kap_shared_workspace_size(R, Hkv, Hq, d, total_q, num_groups) bytes, at any multiple of 16 bytes; it needs
  *   no clearing. Calls that may run at the same time, captured graphs among them, need a workspace each.
  * Errors: those of kap_attn_verify; KAP_EINVAL for num_groups < 0 or null group arrays; KAP_EUNSUPPORTED for more than 2^26

@@ -213,9 +213,13 @@ __device__ __forceinline__ Groups load_groups(const HParams &p, int32_t *s_off) 
   return Groups{s_off};
 }
 
-// CTA 0: offsets have to rise from 0 to R.
-__device__ __forceinline__ void check_groups(const HParams &p, const Groups &gr) {
-  if (blockIdx.x != 0 || p.num_groups == 0) return;
+// CTA 0: a group's offsets have to rise from 0 to R, those of the windows within [0, total_q].
+__device__ __forceinline__ void check_offsets(const HParams &p, const Groups &gr) {
+  if (blockIdx.x != 0) return;
+  for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
+    const int a = p.q_offsets[r], b = p.q_offsets[r + 1];
+    if (a < 0 || a > b || b > p.total_q) set_error(p.err, kErrLength);
+  }
   for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
     const int a = gr.off[g], b = gr.off[g + 1];
     if (a > b || (g == 0 && a != 0) || (g == p.num_groups - 1 && b != p.R)) set_error(p.err, kErrLength);
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
   __shared__ PlanSlots s_slot;
   grid_dependency_sync();
   const Groups gr = load_groups(p, s_off);
-  check_groups(p, gr);
+  check_offsets(p, gr);
   const Plan pl = make_plan(p, gr, s_scratch, &s_slot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float scale = rsqrtf(static_cast<float>(D)) * kLog2e;
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   for (int i = tid; i < p.num_groups; i += kTcThreads) touch(p.prefix_pages + i);
   // the plan's scratch lies where the ring will be
   const Groups gs = load_groups(p, reinterpret_cast<int32_t *>(ring + 512));
-  check_groups(p, gs);
+  check_offsets(p, gs);
   const Plan pl = make_plan(p, gs, reinterpret_cast<int64_t *>(ring), reinterpret_cast<PlanSlots *>(ring + 256));
   fence_proxy_async_smem();
   __syncthreads();
@@ -1071,9 +1075,13 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
     const int r = find_last(p.q_offsets, p.R, t);
     const int start = p.q_start[r], past = p.max_pages * kPage;
     if (start > past && lane == 0) set_error(p.err, kErrPage);   // context past the table's end
-    const int pos0 = max(start, 0), pos1 = start > past ? -1 : start + (t - p.q_offsets[r]);
-    // the window's pages: 64 tokens lie on no more than 5
-    const int page0 = pos0 / kPage;
+    const int pos0 = max(start, 0), page0 = pos0 / kPage;
+    int pos1 = start > past ? -1 : start + (t - p.q_offsets[r]);
+    // the window's pages, one a lane: 64 tokens lie on no more than 5
+    if (pos1 / kPage - page0 > 31) {
+      if (lane == 0) set_error(p.err, kErrLength);
+      pos1 = (page0 + 32) * kPage - 1;
+    }
     int my_page = -1;
     if (lane <= pos1 / kPage - page0 && page0 + lane < p.max_pages)
       my_page = p.bt[static_cast<size_t>(r) * p.max_pages + page0 + lane];
@@ -1130,6 +1138,11 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const HParams p) {
         }
         q0[kind] = x.q0;
         row[kind] = (t - x.q0) * p.G + hq - h * p.G;
+        if (row[kind] < 0 || row[kind] >= x.rows) {   // offsets out of order: the row is none of the group's
+          if (lane == 0) set_error(p.err, kErrLength);
+          ent[kind] = -1;
+          continue;
+        }
         const int block = row[kind] / p.block;
         at[kind] = x.first_tile(p, h, block);
         end[kind] = at[kind] + static_cast<int64_t>(x.tiles - 1) * x.cost(p, block);

@@ -43,3 +43,19 @@ def test_results_do_not_depend_on_what_ran_before(kap, rows, d):
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
     assert kap.kap_device_error() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("qo", [[0, 5000, 10, 5100], [0, 90, 40, 5100], [-7, 3, 9, 5100], [0, 10, 20, 6000], [0, 400, 300, 200]])
+def test_window_offsets_that_do_not_rise(kap, dt, qo):
+    """Rows that no group's records hold are left out and reported, and nothing outside the outputs is written."""
+    s = make([1, 2], [9, 40], [7, 130, 0], [1, 1, 1], hkv=1, G=4, d=64, dt=dt)
+    s["qo"] = torch.tensor(qo, dtype=torch.int32, device="cuda")
+    s["tq"], s["windows"] = 5100, [16, 16, 16]
+    s["q"] = torch.randn(5100, 4, 64, device="cuda").to(dt)
+    n = kap.kap_shared_workspace_size(3, 1, 4, 64, 5100, 2)
+    whole = torch.full((n + 512,), 255, dtype=torch.uint8, device="cuda")
+    run(kap, s, ws=whole[256:256 + n])
+    torch.cuda.synchronize()
+    assert kap.kap_device_error() & 4
+    assert (whole[:256] == 255).all() and (whole[256 + n:] == 255).all()
