@@ -387,6 +387,7 @@ size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
  *   undefined).
  *   workspace >= kap_shared_workspace_size(R, Hkv, Hq, d, total_q, num_groups) bytes, at any multiple of 16 bytes; it needs
  *   no clearing. Calls that may run at the same time, captured graphs among them, need a workspace each.
+ *   total_q == 0: KAP_OK once sizes and groups are checked; outputs, queries, offsets and workspace are not looked at.
  * Errors: those of kap_attn_verify; KAP_EINVAL for num_groups < 0 or null group arrays; KAP_EUNSUPPORTED for more than 2^26
  * table columns, 2^20 groups or 2^31 - 1 query rows (total_q * Hq). */
 kap_status kap_attn_verify_shared(const kap_kv_pool *pool, const kap_page_map *map, const kap_verify_policy *vp,

@@ -125,6 +125,21 @@ def test_shared_attention_is_checked(abi):
 
 
 @cpu_only
+def test_shared_attention_over_no_rows_needs_no_workspace(abi):
+    b, lib = abi
+    pool, m, g = _pool(b), b._Map(2, 4, A, A, None), b._Groups(1, A, A)
+    call = lambda v, ws, n: lib.kap_attn_verify_shared(ctypes.byref(pool), ctypes.byref(m), ctypes.byref(v),  # noqa: E731
+                                                       ctypes.byref(g), None, None, None, ws, n, None)
+    for v in (b._Verify(2, 0, A, A), b._Verify(2, 0, None, None)):
+        for ws, n in ((A, 0), (None, 0), (ODD, 1 << 30)):
+            assert call(v, ws, n) == KAP_OK
+    g = b._Groups(1, None, A)
+    assert call(b._Verify(2, 0, A, A), A, 0) == KAP_EINVAL
+    g = b._Groups((1 << 20) + 1, A, A)
+    assert call(b._Verify(2, 0, A, A), A, 0) == KAP_EUNSUPPORTED
+
+
+@cpu_only
 def test_sampling_is_checked(abi):
     _, lib = abi
     call = lambda lg=A, dt=0, V=100, st=100, rows=3, u=A, tok=A: lib.kap_sample_tokens(  # noqa: E731
