@@ -1482,6 +1482,8 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const __gri
     mass = a.cluster_sum(nans) ? NAN : 0.0f;
   }
   const bool sound = mass == mass && fabsf(m) < INFINITY;
+  // first_pass() took 1e-30 for smaller scales, at which logits of 1e28 and more below the largest still weigh as much
+  if (sound && ch < 1e-30f) mass = 0.0f;
   float x_tok = m;
   int token = 0;
   float lp = 0.0f;

@@ -51,3 +51,15 @@ def test_min_p_above_one_keeps_the_first_token_alone(kap, V, dt):
                 tok, lp, kept = check(kap, lg, np.full(5, u), mp=mp, **kw)
                 if mp > 1.0:
                     assert (kept == 1).all() and (lp == 0.0).all() and (tok == lg.float().argmax(1).cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [-1e9, -3.38e38])
+def test_temperatures_at_which_masked_logits_weigh_as_much(kap, dt, low):
+    """At temperatures past 1e38 a mask of a finite value takes nothing from a token's weight."""
+    rows, V = 4, 10958
+    lg = logits(rows, V, dt, 4, lift=False)
+    lg[:, torch.arange(V) % 97 != 0] = low
+    for T in (float("inf"), 3e38, 1e31):
+        for kw in (dict(p=0.43), dict(p=0.9, mp=1e-6), dict(p=0.004, k=9000), dict(mp=0.3)):
+            check(kap, lg, u_of(rows, 3), T=T, **kw)
