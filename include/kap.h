@@ -378,7 +378,8 @@ size_t kap_verify_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t
  * kap_attn_verify (windows of one row are decode), over the whole table, but the pages that a group shares are read once
  * for all its requests, through the row of the group's first request. A group of one request, and a request whose
  * window starts inside its group's shared pages, are taken as sharing nothing. The results are those of kap_attn_verify
- * up to rounding: sums and statistics are fp32; over a bf16 pool probabilities enter the product with the values as bf16.
+ * up to rounding: sums and statistics are fp32; over a bf16 pool probabilities enter the product with the values as bf16
+ * (those of kap_attn_verify do so at head_dim 128; at 64 they stay in fp32 there).
  * A token that a row does not see adds nothing to it, whatever its K and V hold. A row that sees no token gets zeros
  * and lse -infinity; rows of q outside the windows (before q_offsets[0], from q_offsets[R] on) leave out and lse as they
  * are. Tokens on a page id outside the pool, or past the table's end, are skipped (device error bit 1).

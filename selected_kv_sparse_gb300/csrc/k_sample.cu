@@ -23,7 +23,8 @@
 // falls into.
 //
 // Bound by instructions for flat rows: some 70 a logit that is weighed in line, 100 where it is called for, and for 16-bit
-// counts an atomic each, of which a warp's fall into the same banks 3 to 4 times. In graphs: 2048 bf16 rows of 128256 under
+// counts an atomic each, of which a warp's fall into the same banks 3 to 4 times. (Two CTAs an SM leave 64 registers, and
+// draw_kept spills 300 to 360 bytes, outside its loops: 0.2% of the instructions that run.) In graphs: 2048 bf16 rows of 128256 under
 // top_p 505 us (a third of them flat, 110 to 170 us each; the others 25 to 45), where reading them takes 77; 80 fp32 rows
 // with settings of their own 115; 300 bf16 rows of 32000 without limits 47; 4 rows 20, most of it joins and one CTA's sort.
 #include "kap_device.cuh"
@@ -170,8 +171,13 @@ struct Weigh {
 
 constexpr int kTiles = 64;         // tiles of a warp's range whose maxima are kept, two a lane
 constexpr int kFew = 2 * kSaThreads;   // candidates that are sorted and drawn from directly
-constexpr int kMaxFewK = 256;      // top_k up to which the candidates are gathered: half of the lanes
-constexpr int kFewBar = 64;        // candidates to gather, about, where top_k does not say
+// top_k up to which the candidates are gathered. Gathered / not, bf16 rows of 128256 in graphs: top_k 200 4 rows 26 / 37 us,
+// 80 rows 42 / 63, 2048 rows 462 / 652; top_k 400 42 / 37, 62 / 63 and 960 / 656 (fp32: 42 / 45, 70 / 86).
+constexpr int kMaxFewK = 256;
+// Candidates to gather, about, where top_k does not say. More of them decide more rows but take longer to sort: 4, 80 and
+// 2048 bf16 rows under top_p, a third of them flat: 64 of them 47, 74 and 507 us; 32 46, 73 and 478; 128 47, 78 and 576;
+// 256 50, 85 and 764.
+constexpr int kFewBar = 64;
 // Logits of 16 bits from 2^-10 to 2^10 in magnitude, counted by value: 2560 of either sign, by their bits.
 constexpr int kValues = 5120, kHalfValues = kValues / 2;
 constexpr uint32_t kFirstValue = 0x3A80, kEndValue = 0x4480;   // bits of 2^-10 and 2^10
@@ -1118,7 +1124,7 @@ struct Sampler {
     };
     int a0 = static_cast<int>(s.pick[0] >> 32), a1 = static_cast<int>(s.pick[0] & 0xffffffffu);
     // its CTA: the warps share the range, then the part that the target lies in, until that is 32 vectors
-    for (int step = 0; step < 10 && a1 - a0 > 32; ++step) {   // an eighth each time
+    for (int step = 0; step < 10 && a1 - a0 > 32; ++step) {   // a sixteenth each time, of 32 vectors at least
       const u64 run0 = s.pick[1], ties0 = s.pick[2];
       const int per = ((a1 - a0 + kSaWarps - 1) / kSaWarps + 31) & ~31;
       const int w0 = min(a0 + warp * per, a1), w1 = min(w0 + per, a1);
@@ -1220,7 +1226,8 @@ struct Sampler {
     u64 pos_count, pos_weight;     // of the positive values
     u64 odd_count, odd_weight;
   };
-  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^10 on.
+  // Counts the logits from `least` on. False: too many of other magnitudes, or some from 2^10 on (finite masks such as -1e9
+  // among them: flat rows then take 3.2 ms for 2048 under top_p instead of 0.77 with a mask of -infinity).
   __device__ bool count_values(float least, Counted &c) {
     const int t = threadIdx.x;
     __syncthreads();

@@ -19,8 +19,9 @@ append (which rotates its queries in place, as with fused=False) followed by the
 With `norm` (QKNorm) or `rope_offset`, appends are kap_append_kv_norm: queries and keys are normalised a head, and a
 generated token is rotated at its logical position plus its request's offset on every axis (the text after images, whose
 position ids run behind the token count; the offsets are read when the cycle is built). Queries are then rotated in
-place, as with fused=False. With `groups` (kb.PrefixGroups), verification is kap_attn_verify_shared: pages that requests
-share are read once a group.
+place, as with fused=False: a proposal step is two launches, the append and the attention. DecodeLoop has neither norms nor
+offsets. With `groups` (kb.PrefixGroups, which says where they pay), verification is kap_attn_verify_shared: pages that
+requests share are read once a group. Proposals read their selected pages a request each.
 """
 from __future__ import annotations
 
