@@ -22,11 +22,12 @@
 // The last three end with the kept weight of each warp's range of ids, and the warps then halve the range that the draw
 // falls into.
 //
-// Bound by instructions for flat rows: some 70 a logit that is weighed in line, 100 where it is called for, and for 16-bit
-// counts an atomic each, of which a warp's fall into the same banks 3 to 4 times. (Two CTAs an SM leave 64 registers, and
-// draw_kept spills 300 to 360 bytes, outside its loops: 0.2% of the instructions that run.) In graphs: 2048 bf16 rows of 128256 under
-// top_p 505 us (a third of them flat, 110 to 170 us each; the others 25 to 45), where reading them takes 77; 80 fp32 rows
-// with settings of their own 115; 300 bf16 rows of 32000 without limits 47; 4 rows 20, most of it joins and one CTA's sort.
+// Bound by instructions for flat rows: some 70 a logit that is weighed in line, 100 where it is called for, and for
+// 16-bit counts an atomic each, of which a warp's fall into the same banks 3 to 4 times. (Two CTAs an SM leave 64
+// registers, and draw_kept spills 300 to 360 bytes, outside its loops: 0.2% of the instructions that run.) In graphs:
+// 2048 bf16 rows of 128256 under top_p 505 us (a third of them flat, 110 to 170 us each; the others 25 to 45), where
+// reading them takes 77; 80 fp32 rows with settings of their own 115; 300 bf16 rows of 32000 without limits 47; 4 rows
+// 20, most of it joins and one CTA's sort.
 #include "kap_device.cuh"
 #include "kap_launch.h"
 
@@ -1496,7 +1497,8 @@ __global__ void __launch_bounds__(kSaThreads, kSaCtas) sample_kernel(const __gri
   float lp = 0.0f;
   u64 count = 0;
   bool done = false;
-  const bool greedy = !(temp > 0.0f) || mp > 1.0f;   // no weight reaches a min_p above 1: the first token, which is always kept
+  // no weight reaches a min_p above 1: what is left is the first token, which is always kept
+  const bool greedy = !(temp > 0.0f) || mp > 1.0f;
   float least = -3.402823466e38f;
   if (sound) {
     a.weigh = Weigh{m, ch, static_cast<float>(cd - static_cast<double>(ch)), 44 - p.qb, &s.powers};
